@@ -18,7 +18,8 @@ import threading
 __all__ = ["Epilogue", "Config", "Plan", "GemmError", "gemm_plan", "gemm_run", "gemm_plan_status",
            "gemm_plan_info", "gemm_select_config", "gemm_cache_stats", "gemm_cache_clear",
            "gemm_strerror", "gemm_version", "gemm_run_noalloc", "lib", "load", "matmul", "DTYPES", "ACTS", "LAYOUTS",
-           "KERNELS", "LIB_PATH"]
+           "KERNELS", "LIB_PATH", "FP4_FORMATS", "Fp4Tensor", "Fp4Plan", "fp4_quantize", "fp4_dequantize",
+           "gemm_fp4_plan", "gemm_fp4_run", "gemm_fp4_status", "gemm_fp4_select_config", "fp4_matmul"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm13.so")
 
@@ -27,6 +28,7 @@ ACTS = {"none": 0, "gelu": 1, "relu": 2, "softmax": 3}
 LAYOUTS = {"kn": 0, "nk": 1}
 KERNELS = {"auto": 0, "tc": 1, "ffma": 2, "skinny": 3, "tf32x3": 4}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
+FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
 FLAG_FP32_TENSOR = 0x1         # FP32 inputs may run as 3xTF32 on the tensor cores
 FLAG_TEST_STALL = 0x80000000
 FLAG_TEST_STALL_PEER = 0x40000000   # test only: the second CTA withholds a tile
@@ -115,6 +117,24 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.gemm_run_noalloc.argtypes = [i32, i64, i64, i64, vp, i64, vp, i64, vp, i64,
                                        ctypes.POINTER(_Epilogue), vp, vp, ctypes.c_float, vp]
         L.gemm_run_noalloc.restype = i32
+        L.gemm_fp4_row_bytes.argtypes = [i64]
+        L.gemm_fp4_row_bytes.restype = i64
+        L.gemm_fp4_scales_bytes.argtypes = [i32, i64, i64]
+        L.gemm_fp4_scales_bytes.restype = i64
+        L.gemm_fp4_quantize.argtypes = [i32, i32, i64, i64, vp, i64, vp, vp, vp, vp]
+        L.gemm_fp4_quantize.restype = i32
+        L.gemm_fp4_dequantize.argtypes = [i32, i32, i64, i64, vp, vp, vp, vp, i64, vp]
+        L.gemm_fp4_dequantize.restype = i32
+        L.gemm_fp4_plan.argtypes = [i32, i64, i64, i64, i64, ctypes.POINTER(_Epilogue), ctypes.POINTER(vp)]
+        L.gemm_fp4_plan.restype = i32
+        L.gemm_fp4_run.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, vp]
+        L.gemm_fp4_run.restype = i32
+        L.gemm_fp4_status.argtypes = [vp]
+        L.gemm_fp4_status.restype = i32
+        L.gemm_fp4_destroy.argtypes = [vp]
+        L.gemm_fp4_destroy.restype = None
+        L.gemm_fp4_select_config.argtypes = [i64, i64, i64, ctypes.c_int32, ctypes.POINTER(_Config)]
+        L.gemm_fp4_select_config.restype = i32
         if path is None:
             _lib = L
         return L
@@ -355,4 +375,235 @@ def matmul(A, B, *, b_layout="kn", alpha=1.0, bias=None, act="none", residual=No
         pl = gemm_plan(dt, M, N, K, lda, ldb, ldc, ep)
         _plans[key] = pl
     gemm_run(pl, A, B, out, bias, residual, alpha)
+    return out
+
+
+# ------------------------------------------------------------------ 4-bit floats
+class Fp4Tensor:
+    """A matrix in microscaled 4-bit floats (layout: include/gemm13.h, "4-bit floats").
+
+    codes: uint8 [rows, row_bytes]; scales: uint8, flat; tensor_scale: None (1) or one FP32 value on
+    the same device ("nvfp4" only).
+    """
+
+    __slots__ = ("codes", "scales", "rows", "cols", "format", "tensor_scale")
+
+    def __init__(self, codes, scales, rows, cols, format, tensor_scale=None):
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.format, self.tensor_scale = format, tensor_scale
+
+
+def _refuse(what: str, why: str):
+    e = GemmError(-1, what)
+    e.args = (f"{what}: {why}",)
+    raise e
+
+
+class _On:
+    """Makes a tensor's device the current one for a call, where it is not."""
+
+    __slots__ = ("guard",)
+
+    def __init__(self, torch, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _stream(torch, stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+_TDT: dict = {}
+
+
+def _tdt():
+    """torch dtype -> name of a gemm_dtype_t."""
+    if not _TDT:
+        import torch
+        _TDT.update({torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"})
+    return _TDT
+
+
+def _check_fp4(what: str, t: Fp4Tensor, torch):
+    if t.format not in FP4_FORMATS:
+        _refuse(what, f"unknown format {t.format!r}")
+    L = lib()
+    nrow, nsc = t.rows * L.gemm_fp4_row_bytes(t.cols), L.gemm_fp4_scales_bytes(FP4_FORMATS[t.format], t.rows, t.cols)
+    for name, a, n in (("codes", t.codes, nrow), ("scales", t.scales, nsc)):
+        if a.dtype != torch.uint8 or not a.is_cuda or not a.is_contiguous() or a.numel() != n:
+            _refuse(what, f"{name}: {n} contiguous bytes on the GPU are wanted")
+    _check_scale(what, t.tensor_scale, t.format, t.codes.device, torch)
+    if t.scales.device != t.codes.device:
+        _refuse(what, "codes and scales are on different devices")
+
+
+def _check_scale(what: str, g, format: str, device, torch):
+    if g is None:
+        return
+    if format != "nvfp4":
+        _refuse(what, "only nvfp4 has a scale of the whole tensor")
+    if g.dtype != torch.float32 or g.numel() != 1 or g.device != device:
+        _refuse(what, "tensor_scale: one FP32 value on the matrix's device is wanted")
+
+
+def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp4Tensor:
+    """A 2-D CUDA tensor (FP32, FP16 or BF16, any row stride) in 4-bit floats (gemm_fp4_quantize).
+
+    tensor_scale ("nvfp4"): a positive FP32 CUDA tensor of one value; max|x| / (6 * 448) uses the
+    whole range.  None means 1.
+    """
+    import torch
+    what = "fp4_quantize"
+    if format not in FP4_FORMATS:
+        _refuse(what, f"unknown format {format!r}")
+    dt = _tdt().get(x.dtype)
+    if dt is None or x.dim() != 2 or not x.is_cuda:
+        _refuse(what, "a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
+        x = x.contiguous()
+    _check_scale(what, tensor_scale, format, x.device, torch)
+    L, f = lib(), FP4_FORMATS[format]
+    with _On(torch, x.device):
+        codes = torch.empty((rows, L.gemm_fp4_row_bytes(cols)), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(L.gemm_fp4_scales_bytes(f, rows, cols), dtype=torch.uint8, device=x.device)
+        rc = L.gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), max(x.stride(0) if rows > 1 else cols, 1),
+                                 _ptr(tensor_scale), codes.data_ptr(), scales.data_ptr(), _stream(torch, stream))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return Fp4Tensor(codes, scales, rows, cols, format, tensor_scale)
+
+
+def fp4_dequantize(t: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
+    """The values of a 4-bit matrix as a tensor of `dtype` (gemm_fp4_dequantize)."""
+    import torch
+    what = "fp4_dequantize"
+    if dtype not in DTYPES:
+        _refuse(what, f"unknown dtype {dtype!r}")
+    _check_fp4(what, t, torch)
+    dev = t.codes.device
+    with _On(torch, dev):
+        if out is None:
+            out = torch.empty((t.rows, t.cols), dtype=getattr(torch, _TORCH_NAMES[dtype]), device=dev)
+        elif (tuple(out.shape) != (t.rows, t.cols) or _tdt().get(out.dtype) != dtype or out.device != dev
+              or (t.cols > 1 and out.stride(1) != 1) or (t.rows > 1 and out.stride(0) < t.cols)):
+            _refuse(what, "out: a row-major tensor of the matrix's shape, dtype and device is wanted")
+        rc = lib().gemm_fp4_dequantize(FP4_FORMATS[t.format], DTYPES[dtype], t.rows, t.cols, t.codes.data_ptr(),
+                                       t.scales.data_ptr(), _ptr(t.tensor_scale), out.data_ptr(),
+                                       max(out.stride(0) if t.rows > 1 else t.cols, 1), _stream(torch, stream))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return out
+
+
+_TORCH_NAMES = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}
+
+
+class Fp4Plan:
+    """Owns a gemm_fp4_plan_t; destroyed with the object (or explicitly)."""
+
+    def __init__(self, handle: int, format: str, M: int, N: int, K: int, epilogue: Epilogue):
+        self.handle = handle
+        self.format, self.M, self.N, self.K, self.epilogue = format, M, N, K, epilogue
+
+    def destroy(self):
+        if self.handle:
+            lib().gemm_fp4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def gemm_fp4_plan(format: str, M: int, N: int, K: int, ldc: int, epilogue: Epilogue | None = None) -> Fp4Plan:
+    """gemm_fp4_plan; the epilogue's b_layout must be "nk".  Raises GemmError on a non-OK status."""
+    ep = epilogue or Epilogue(b_layout="nk")
+    h, ce = ctypes.c_void_p(), ep._c()
+    rc = lib().gemm_fp4_plan(FP4_FORMATS[format], M, N, K, ldc, ctypes.byref(ce), ctypes.byref(h))
+    if rc != 0:
+        raise GemmError(rc, "gemm_fp4_plan")
+    return Fp4Plan(h.value, format, M, N, K, ep)
+
+
+def gemm_fp4_run(plan: Fp4Plan, A: Fp4Tensor, B: Fp4Tensor, C, bias=None, residual=None, alpha: float = 1.0,
+                 stream=None) -> int:
+    """Enqueue C = epilogue(A @ B.T) of a plan on `stream` (default: torch's current stream)."""
+    import torch
+    if (A.rows, A.cols, B.rows, B.cols) != (plan.M, plan.K, plan.N, plan.K) or A.format != plan.format \
+            or B.format != plan.format:
+        _refuse("gemm_fp4_run", "the operands do not fit the plan")
+    rc = lib().gemm_fp4_run(plan.handle, _ptr(A.codes), _ptr(A.scales), _ptr(A.tensor_scale), _ptr(B.codes),
+                            _ptr(B.scales), _ptr(B.tensor_scale), _ptr(C), _ptr(bias), _ptr(residual),
+                            float(alpha), _stream(torch, stream))
+    if rc != 0:
+        raise GemmError(rc, "gemm_fp4_run")
+    return rc
+
+
+def gemm_fp4_status(plan: Fp4Plan) -> int:
+    """Synchronise and return the plan's sticky device status (0 or a negative code)."""
+    return int(lib().gemm_fp4_status(plan.handle))
+
+
+def gemm_fp4_select_config(M: int, N: int, K: int, num_sms: int = 152) -> Config:
+    """Host-only query of the 4-bit product's tile (no GPU needed)."""
+    c = _Config()
+    rc = lib().gemm_fp4_select_config(M, N, K, num_sms, ctypes.byref(c))
+    if rc != 0:
+        raise GemmError(rc, "gemm_fp4_select_config")
+    return Config._from(c)
+
+
+_fp4_plans: dict = {}
+
+
+def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", residual=None, beta=1.0,
+               out_dtype="f32", out=None, stream=None):
+    """C = cast(act(alpha * A @ B.T + bias) + beta * residual) of two 4-bit matrices.
+
+    A [M, K] (activations), B [N, K] (a weight as it lies for x @ W.T), both in the same format.
+    bias: FP32 [N]; residual: FP32 [M, N].  Plans are created once per (shape, format, strides,
+    epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.
+    """
+    import torch
+    what = "fp4_matmul"
+    _check_fp4(what, A, torch)
+    _check_fp4(what, B, torch)
+    dev = A.codes.device
+    if A.format != B.format or A.cols != B.cols or B.codes.device != dev:
+        _refuse(what, "A and B need the same format, K and device")
+    if out_dtype not in DTYPES or act not in ("none", "gelu", "relu"):
+        _refuse(what, "out_dtype: f32, f16 or bf16; act: none, gelu or relu")
+    M, N, K = A.rows, B.rows, A.cols
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or bias.device != dev
+                             or not bias.is_contiguous()):
+        _refuse(what, "bias: contiguous FP32 [N] on the operands' device is wanted")
+    for name, t, dt in (("residual", residual, "f32"), ("out", out, out_dtype)):
+        if t is not None and (tuple(t.shape) != (M, N) or _tdt().get(t.dtype) != dt or t.device != dev
+                              or (N > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < N)):
+            _refuse(what, f"{name}: a row-major {dt} [M, N] on the operands' device is wanted")
+    with _On(torch, dev):
+        if out is None:
+            out = torch.empty((M, N), dtype=getattr(torch, _TORCH_NAMES[out_dtype]), device=dev)
+        ldc = max(out.stride(0) if M > 1 else N, 1)
+        ldr = 0 if residual is None else max(residual.stride(0) if M > 1 else N, 1)
+        key = (A.format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, residual is not None, beta, dev.index)
+        pl = _fp4_plans.get(key)
+        if pl is None:
+            ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
+                          residual=residual is not None, beta=beta, ldr=ldr)
+            pl = _fp4_plans[key] = gemm_fp4_plan(A.format, M, N, K, ldc, ep)
+        gemm_fp4_run(pl, A, B, out, bias, residual, alpha, stream)
     return out

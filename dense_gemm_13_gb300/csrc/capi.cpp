@@ -158,6 +158,23 @@ int g13::tmap_encode_3d(CUtensorMap* m, int dtype, const void* base, int64_t col
                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+int g13::tmap_encode_rows_u8(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows,
+                             uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return GEMM_ERR_NO_DEVICE;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows), 1};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
+                                   static_cast<cuuint64_t>(row_bytes * rows)};
+    const cuuint32_t box[3] = {128, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+int g13::cuda_status(cudaError_t e) { return map_cuda_error(e); }
+
 namespace {
 
 bool cfg_is_split_skinny(const gemm_config_t& c) {

@@ -203,6 +203,12 @@ size_t skinny_tma_workspace_bytes(int num_sms);
 int tmap_encode_3d(CUtensorMap* m, int dtype, const void* base, int64_t cols, int64_t rows,
                    int64_t ld, int64_t batches, int64_t bstride, uint32_t box_cols,
                    uint32_t box_rows);
+// Rows of bytes (row_bytes apart, a multiple of 16) in boxes of 128 bytes x
+// box_rows, 128B swizzle.
+int tmap_encode_rows_u8(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows,
+                        uint32_t box_rows);
+// The gemm_status_t of a CUDA error.
+int cuda_status(cudaError_t e);
 
 // Copies [batch][rows][cols] (row stride ld, batch stride bstride, element
 // size esz) into a dense [batch][rows][dst_ld] buffer (dst and dst_ld * esz

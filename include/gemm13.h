@@ -43,6 +43,9 @@ extern "C" {
 
 typedef enum { GEMM_F32 = 0, GEMM_F16 = 1, GEMM_BF16 = 2 } gemm_dtype_t;
 
+/* Microscaled 4-bit formats (see "4-bit floats" below). */
+typedef enum { GEMM_MXFP4 = 0, GEMM_NVFP4 = 1 } gemm_fp4_format_t;
+
 typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_GELU_ERF = 1, /* 0.5*y*(1+erf(y/sqrt(2))) */
@@ -273,6 +276,86 @@ int gemm_run_noalloc(gemm_dtype_t dtype, int64_t M, int64_t N, int64_t K,
                      const void* A, int64_t lda, const void* B, int64_t ldb,
                      void* C, int64_t ldc, const gemm_epilogue_t* epilogue,
                      const void* bias, const void* residual, float alpha, void* stream);
+
+/*
+ * 4-bit floats.  A matrix [rows][cols] in 4 bits is two device arrays, and for
+ * GEMM_NVFP4 an FP32 scale g of the whole tensor:
+ *   codes   E2M1 values (+-0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign), two
+ *           to a byte, the first in the low half; rows of
+ *           gemm_fp4_row_bytes(cols) bytes (cols padded to 32 elements).
+ *   scales  one byte per block of a row, gemm_fp4_scales_bytes() bytes in all,
+ *           in tiles of 128 rows x 4 blocks, 512 bytes each: row r, block c of
+ *           a tile at byte (r % 32) * 16 + (r / 32) * 4 + c; the tiles of a row
+ *           of tiles follow one another.  (The order in which the tensor cores
+ *           take them.)
+ *   GEMM_MXFP4  blocks of 32; byte b is the scale 2^(b - 127) (255: NaN);
+ *               element = code * scale.
+ *   GEMM_NVFP4  blocks of 16; the byte is an E4M3 scale s >= 0 (0x7F: NaN);
+ *               element = code * fl32(s * g), g from a device pointer
+ *               (NULL: 1), positive and finite.
+ * Padding in both arrays is zero; gemm_fp4_quantize writes all of it.  Both
+ * arrays are 16-byte aligned.
+ */
+int64_t gemm_fp4_row_bytes(int64_t cols);
+int64_t gemm_fp4_scales_bytes(gemm_fp4_format_t format, int64_t rows, int64_t cols);
+
+/*
+ * Quantises src (dtype, [rows][ld], any alignment of its element type) into
+ * codes and scales on `stream`.
+ *   GEMM_MXFP4  scale 2^E, E = floor(log2 max|x|) - 2 of the block, kept in
+ *               [-127, 127] (a block of zeros: -127).
+ *   GEMM_NVFP4  s = nearest E4M3 to fl32(max|x| / fl32(6 g)), ties to even, at
+ *               most 448.  g = max|tensor| / (6 * 448) uses the format's whole
+ *               range.
+ *   code        nearest E2M1 value to fl32(x / scale), ties to the even code,
+ *               saturating at 6; all zero where the scale is zero.
+ * A block that holds an infinity or a NaN gets a NaN scale (its codes mean
+ * nothing), so every product that reads it is NaN.
+ * src must not overlap codes or scales.  tensor_scale: g for GEMM_NVFP4 (NULL:
+ * 1); must be NULL for GEMM_MXFP4.  Allocates nothing.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED (sizes), NO_DEVICE, CUDA.
+ */
+int gemm_fp4_quantize(gemm_fp4_format_t format, gemm_dtype_t dtype, int64_t rows, int64_t cols,
+                      const void* src, int64_t ld, const float* tensor_scale, void* codes,
+                      void* scales, void* stream);
+
+/* The values that codes and scales stand for: FP32 code * scale, rounded to
+ * nearest even to dtype, into dst ([rows][ld], any alignment of its element
+ * type; elements past cols are left as they were).  Errors: as
+ * gemm_fp4_quantize. */
+int gemm_fp4_dequantize(gemm_fp4_format_t format, gemm_dtype_t dtype, int64_t rows, int64_t cols,
+                        const void* codes, const void* scales, const float* tensor_scale, void* dst,
+                        int64_t ld, void* stream);
+
+/*
+ * C = cast( act( alpha * A.B^T + bias ) + beta * R ) with A [M][K] and
+ * B [N][K] in 4 bits of one format (a weight as it lies for X.W^T), on the
+ * block-scaled tensor cores with FP32 accumulation; from one row (a token) up.
+ *
+ * gemm_fp4_plan validates the problem, chooses the tile and allocates a status
+ * word on the current device; no workspace.  epilogue: NULL (plain FP32 C), or
+ * as for gemm_plan with b_layout GEMM_B_NK, batch 1 and no row softmax (else
+ * UNSUPPORTED); strides a, b, c, r are ignored.
+ * gemm_fp4_run enqueues on `stream`: arrays as described above, tensor scales
+ * for GEMM_NVFP4 only (NULL: 1); bias, residual and C as for gemm_run; C must
+ * not overlap any input.  Runs of one plan may overlap on the GPU.
+ * Errors: as gemm_plan and gemm_run; MISALIGNED where codes or scales are not
+ * 16-byte aligned.
+ */
+typedef struct gemm_fp4_plan_s* gemm_fp4_plan_t;
+int gemm_fp4_plan(gemm_fp4_format_t format, int64_t M, int64_t N, int64_t K, int64_t ldc,
+                  const gemm_epilogue_t* epilogue, gemm_fp4_plan_t* out_plan);
+int gemm_fp4_run(gemm_fp4_plan_t plan, const void* a_codes, const void* a_scales,
+                 const float* a_tensor_scale, const void* b_codes, const void* b_scales,
+                 const float* b_tensor_scale, void* C, const void* bias, const void* residual,
+                 float alpha, void* stream);
+/* As gemm_plan_status and gemm_plan_destroy. */
+int gemm_fp4_status(gemm_fp4_plan_t plan);
+void gemm_fp4_destroy(gemm_fp4_plan_t plan);
+/* Host-only: the tile that gemm_fp4_plan would choose on a device with num_sms
+ * SMs: rows of A per tile (bn; 128 rows of B), and the CTAs that share a tile's
+ * K (split_k).  Errors: INVALID_ARG. */
+int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gemm_config_t* out);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,304 @@
+"""Microscaled 4-bit floats on the GPU: quantisation byte for byte against the
+definition, products against 64-bit sums, the epilogue, and how calls share a GPU.
+
+Tolerance of a product, with S = sum |a b| of an element: the tensor core adds
+K / 64 partial sums in FP32 (each addition off by at most 2^-22 of a running
+value <= S if it truncates, and one partial sum of 64 products by as much), the
+scales s g of both operands and alpha gA gB round 5 times (2^-24 each):
+    |C - ref| <= ((K / 64 + 2) 2^-22 + 5 2^-24) S      before the epilogue.
+GELU's slope is below 1.13 and its own error below 1e-6 (1 + |y|); each FP32
+step of the epilogue rounds its result (2^-24); the output cast adds half a
+step of its type.
+"""
+import zlib
+
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_13_gb300 as g13
+from tests import fp4_ref as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+FMTS = ["mxfp4", "nvfp4"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from dense_gemm_13_gb300 import _build
+    _build.build()
+    g13.load()
+
+
+def rng(*key):
+    return np.random.default_rng([zlib.crc32(str(k).encode()) for k in key])
+
+
+def matrix(r, rows, cols):
+    """Normal values with blocks of zeros, tiny and large magnitudes."""
+    x = r.standard_normal((rows, cols)).astype(np.float32)
+    x *= np.exp2(r.integers(-12, 12, (rows, -(-cols // 16)))).astype(np.float32).repeat(16, 1)[:, :cols]
+    x[r.random((rows, cols)) < 0.05] = 0
+    x[:, cols // 2: cols // 2 + 32] *= r.random((rows, 1)) < 0.7
+    return x
+
+
+def check_quantised(q, x32, fmt, g):
+    code, byte = ref.quantise(x32, fmt, g)
+    got_s = q.scales.cpu().numpy()
+    want_s = ref.tiles(byte)
+    assert np.array_equal(got_s, want_s), f"{np.sum(got_s != want_s)} scale bytes differ"
+    got, want = q.codes.cpu().numpy(), ref.pack(code)
+    bad = ref.pack(np.broadcast_to((byte == (255 if fmt == "mxfp4" else 127))[..., None] * np.uint8(15),
+                                   byte.shape + (ref.BLOCK[fmt],)).reshape(byte.shape[0], -1)[:, : code.shape[1]])
+    assert np.array_equal(got & ~bad, want & ~bad), f"{np.sum((got ^ want) & ~bad != 0)} code bytes differ"
+
+
+SHAPES = [(1, 1), (1, 16), (3, 17), (1, 4096), (5, 31), (127, 33), (128, 64), (129, 100), (300, 257), (33, 1000),
+          (257, 520)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0]}x{s[1]}")
+def test_quantise_bytes(fmt, dtype, shape):
+    x = torch.from_numpy(matrix(rng(fmt, dtype, shape), *shape)).to(DT[dtype])
+    x32 = x.float().numpy()
+    g = None
+    if fmt == "nvfp4" and shape[0] != 128:
+        g = np.float32(np.abs(x32).max() / np.float32(6 * 448))
+        g = g if g > 0 else np.float32(1)
+    tg = None if g is None else torch.tensor([g], device="cuda")
+    q = g13.fp4_quantize(x.cuda(), fmt, tensor_scale=tg)
+    check_quantised(q, x32, fmt, 1.0 if g is None else g)
+    # back: FP32 products of code and scale, cast once
+    for out in DT:
+        v = torch.from_numpy(ref.values(*ref.quantise(x32, fmt, 1.0 if g is None else g), fmt,
+                                        1.0 if g is None else g)).float()
+        assert torch.equal(g13.fp4_dequantize(q, out).cpu(), v.to(DT[out])), out
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantise_every_tie(fmt):
+    # every midpoint, its neighbours and every magnitude up to 8, under scales whose quotients are exact
+    # and under ones that are not
+    base = np.concatenate([ref.MID, np.nextafter(ref.MID.astype(np.float32), np.float32(9)),
+                           np.nextafter(ref.MID.astype(np.float32), np.float32(0)), ref.E2M1[:8], [7.0, 5.5]])
+    rows = []
+    for s in (1.0, 0.5, 448.0, 2.0 ** -9, 0.4375, 1.875, 3e-3, 26.0):
+        x = np.zeros(32 * len(base), np.float32)
+        x[0::2] = np.repeat(base, 16) * s * np.tile([1, -1], 8 * len(base))
+        x[1::32] = 6 * s  # the block's largest
+        x[17::32] = 6 * s
+        rows.append(x)
+    x = np.stack(rows)
+    check_quantised(g13.fp4_quantize(torch.from_numpy(x).cuda(), fmt), x, fmt, 1.0)
+    if fmt == "nvfp4":
+        for g in (np.float32(0.1), np.float32(3e-39), np.float32(1.7e-30), np.float32(2.0 ** 70)):
+            y = (x * g).astype(np.float32)
+            check_quantised(g13.fp4_quantize(torch.from_numpy(y).cuda(), fmt,
+                                             tensor_scale=torch.tensor([g], device="cuda")), y, fmt, g)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quantise_extremes(fmt):
+    x = np.zeros((6, 100), np.float32)
+    x[0, 3] = 1e-45
+    x[1, :] = np.float32(3.4e38)
+    x[2, 40] = np.inf
+    x[3, 99] = np.nan
+    x[4, :] = np.float32(1.2e-38)
+    x[5, ::3] = -0.0
+    q = g13.fp4_quantize(torch.from_numpy(x).cuda(), fmt)
+    check_quantised(q, x, fmt, 1.0)
+    v = g13.fp4_dequantize(q).cpu().numpy()
+    b = ref.BLOCK[fmt]
+    assert np.isnan(v[2, 40 // b * b: 40 // b * b + b]).all() and np.isnan(v[3, 96:]).all()
+    assert np.isfinite(np.delete(v, [2, 3], 0)).all() and np.isfinite(v[2, : 40 // b * b]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(DT))
+def test_strides_and_offsets(fmt, dtype):
+    # rows and bases that are not 16-byte aligned; a destination inside a larger one keeps its surroundings
+    x = torch.from_numpy(matrix(rng("s", fmt, dtype), 70, 203)).to(DT[dtype]).cuda()
+    for view in (x[1:, 3:150], x[:, 1:], x[::2, 8:40], x.t()[:, :60]):
+        q = g13.fp4_quantize(view, fmt)
+        check_quantised(q, view.float().cpu().numpy(), fmt, 1.0)
+        big = torch.full((view.shape[0] + 2, view.shape[1] + 5), 7.0, dtype=DT[dtype], device="cuda")
+        g13.fp4_dequantize(q, dtype, out=big[1:-1, 3: 3 + view.shape[1]])
+        assert torch.equal(big[1:-1, 3: 3 + view.shape[1]], g13.fp4_dequantize(q, dtype))
+        big[1:-1, 3: 3 + view.shape[1]] = 7
+        assert bool((big == 7).all())
+
+
+def test_empty():
+    for shape in ((0, 5), (4, 0)):
+        q = g13.fp4_quantize(torch.zeros(shape, device="cuda"), "mxfp4")
+        assert tuple(g13.fp4_dequantize(q).shape) == shape
+    A, B = (g13.fp4_quantize(torch.zeros((n, 0), device="cuda"), "mxfp4") for n in (3, 40))
+    bias = torch.arange(40.0, device="cuda")
+    C = torch.full((3, 40), 5.0, device="cuda")
+    g13.fp4_matmul(A, B, bias=bias, out=C)  # K = 0: the epilogue of zero
+    assert torch.equal(C, bias.expand(3, 40))
+    E = g13.fp4_quantize(torch.zeros((0, 64), device="cuda"), "nvfp4")
+    assert tuple(g13.fp4_matmul(E, E).shape) == (0, 0)
+
+
+# ------------------------------------------------------------------ products
+def operand(r, rows, cols, fmt, g=None, ints=False):
+    """(Fp4Tensor, 64-bit values)."""
+    code = r.integers(0, 16, (rows, cols)).astype(np.uint8)
+    nb = -(-cols // ref.BLOCK[fmt])
+    if ints:
+        code = np.array([0, 2, 4, 5, 6, 7, 8, 10, 12, 13, 14, 15], np.uint8)[r.integers(0, 12, (rows, cols))]
+        byte = np.full((rows, nb), 127 if fmt == "mxfp4" else 0x38, np.uint8)
+        byte += r.integers(0, 2, byte.shape).astype(np.uint8) * (1 if fmt == "mxfp4" else 8)  # 1 or 2
+    elif fmt == "mxfp4":
+        byte = r.integers(120, 134, (rows, nb)).astype(np.uint8)
+    else:
+        byte = r.integers(0, 127, (rows, nb)).astype(np.uint8)
+    t = g13.Fp4Tensor(torch.from_numpy(ref.pack(code)).cuda(), torch.from_numpy(ref.tiles(byte)).cuda(), rows,
+                      cols, fmt, None if g is None else torch.tensor([g], dtype=torch.float32, device="cuda"))
+    return t, ref.values(code, byte, fmt, 1.0 if g is None else g)
+
+
+P_SHAPES = [(1, 1, 1), (1, 128, 64), (1, 300, 1000), (7, 129, 65), (16, 128, 256), (17, 200, 257), (32, 64, 512),
+            (33, 500, 96), (64, 130, 300), (65, 257, 700), (127, 384, 1030), (128, 128, 2048), (129, 130, 31),
+            (300, 515, 520), (257, 1000, 64)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("shape", P_SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_product_exact_integers(fmt, shape):
+    # products are multiples of 1 up to 144 and every partial sum stays below 2^24: FP32 is exact in any order
+    M, N, K = shape
+    r = rng("int", fmt, shape)
+    (A, a), (B, b) = operand(r, M, K, fmt, ints=True), operand(r, N, K, fmt, ints=True)
+    want = a @ b.T
+    assert (np.abs(a) @ np.abs(b).T).max() < 2 ** 24
+    big = torch.full((M + 2, N + 3), 7.0, device="cuda")
+    g13.fp4_matmul(A, B, out=big[1:-1, 1: N + 1])
+    got = big[1:-1, 1: N + 1].cpu().numpy()
+    assert np.array_equal(got, want), f"{np.sum(got != want)} of {got.size} differ"
+    big[1:-1, 1: N + 1] = 7
+    assert bool((big == 7).all()), "store outside the M x N window"
+
+
+def check_product(got, A, B, out, bias=None, act="none", R=None, alpha=1.0, beta=1.0):
+    K = A.shape[1]
+    S = np.abs(A) @ np.abs(B).T * abs(alpha)
+    y = alpha * (A @ B.T)
+    tol = ((K / 64 + 2) * 2.0 ** -22 + 5 * 2.0 ** -24) * S
+    if bias is not None:
+        y = y + bias
+        tol = tol + 2.0 ** -24 * np.abs(y)
+    if act == "gelu":
+        from scipy.special import erfc
+        tol = 1.13 * tol + 1e-6 * (1 + np.abs(y))
+        y = 0.5 * y * erfc(-y / np.sqrt(2))
+    elif act == "relu":
+        y = np.maximum(y, 0)
+    if R is not None:
+        y = y + beta * R
+        tol = tol + 2.0 ** -24 * np.abs(y)
+    tol = tol + torch.finfo(DT[out]).eps / 2 * (np.abs(y) + tol) + torch.finfo(DT[out]).smallest_normal * 2.0 ** -10
+    err = np.abs(got.double().cpu().numpy() - y)
+    assert (err <= tol).all(), f"max err/tol {np.max(err / tol):.3g}"
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out", list(DT))
+@pytest.mark.parametrize("shape", [(1, 515, 900), (20, 131, 2000), (50, 300, 333), (100, 129, 4000),
+                                   (200, 300, 770), (600, 9800, 128)], ids=lambda s: "x".join(map(str, s)))
+def test_product_epilogue(fmt, out, shape):
+    M, N, K = shape
+    r = rng("epi", fmt, out, shape)
+    ga, gb = (None, None) if fmt == "mxfp4" else (0.0123, 0.004)
+    (A, a), (B, b) = operand(r, M, K, fmt, ga), operand(r, N, K, fmt, gb)
+    alpha = 1.0 / np.abs(a @ b.T).max()
+    bias, R = r.standard_normal(N).astype(np.float32), r.standard_normal((M, N)).astype(np.float32)
+    tb, tR = torch.from_numpy(bias).cuda(), torch.from_numpy(R).cuda()
+    al = np.float32(alpha)
+    check_product(g13.fp4_matmul(A, B, alpha=al, out_dtype=out), a, b, out, alpha=float(al))
+    check_product(g13.fp4_matmul(A, B, alpha=4 * al, out_dtype=out, bias=tb, act="gelu"), a, b, out, bias, "gelu",
+                  alpha=4 * float(al))
+    check_product(g13.fp4_matmul(A, B, alpha=al, out_dtype=out, bias=tb, act="relu", residual=tR, beta=-0.5), a, b,
+                  out, bias, "relu", R, float(al), -0.5)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_nan_scale_stays_in_its_row(fmt, M):
+    r = rng("nan", fmt, M)
+    x = r.standard_normal((M, 700)).astype(np.float32)
+    x[M // 2, 600] = np.inf
+    A = g13.fp4_quantize(torch.from_numpy(x).cuda(), fmt)
+    w = r.standard_normal((200, 700)).astype(np.float32)
+    w[7, 0] = np.nan
+    C = g13.fp4_matmul(A, g13.fp4_quantize(torch.from_numpy(w).cuda(), fmt)).cpu().numpy()
+    bad = np.zeros(C.shape, bool)
+    bad[M // 2, :] = bad[:, 7] = True
+    assert np.array_equal(np.isnan(C), bad)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_linear_layer(fmt, dtype):
+    # quantise the activations, multiply by a 4-bit weight: as used, on a side stream, repeated
+    r = rng("lin", fmt, dtype)
+    x = torch.from_numpy(r.standard_normal((45, 640)).astype(np.float32)).to(DT[dtype]).cuda()
+    w = torch.from_numpy(r.standard_normal((333, 640)).astype(np.float32)).cuda()
+    g = None if fmt == "mxfp4" else (x.float().abs().max() / (6 * 448)).reshape(1)
+    W = g13.fp4_quantize(w, fmt)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        ys = [g13.fp4_matmul(g13.fp4_quantize(x, fmt, tensor_scale=g), W) for _ in range(3)]
+    torch.cuda.current_stream().wait_stream(st)
+    gv = 1.0 if g is None else np.float32(g.item())
+    a = ref.values(*ref.quantise(x.float().cpu().numpy(), fmt, gv), fmt, gv)
+    b = ref.values(*ref.quantise(w.cpu().numpy(), fmt), fmt)
+    for y in ys:
+        check_product(y, a, b, "f32")
+        assert torch.equal(y, ys[0])
+
+
+@pytest.mark.parametrize("M", [1, 100, 400])
+def test_graph_and_two_streams(M):
+    r = rng("graph", M)
+    ops = [(operand(r, M, 1500, "nvfp4", 0.5), operand(r, 800, 1500, "nvfp4", 0.25)) for _ in range(2)]
+    want = [g13.fp4_matmul(A, B) for (A, _), (B, _) in ops]
+    graphs, outs = [], []
+    for (A, _), (B, _) in ops:
+        out = torch.zeros(M, 800, device="cuda")
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            g13.fp4_matmul(A, B, out=out)
+        graphs.append(gr)
+        outs.append(out)
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(s[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert torch.equal(outs[i], want[i])
+
+
+@pytest.mark.parametrize("M", [1, 200])
+def test_timeout_is_reported(M):
+    # the first CTA withholds one stage: its waits run out, the plan says so, and a new plan works
+    r = rng("stall", M)
+    (A, a), (B, b) = operand(r, M, 2000, "mxfp4", ints=True), operand(r, 300, 2000, "mxfp4", ints=True)
+    C = torch.zeros(M, 300, device="cuda")
+    ep = g13.Epilogue(b_layout="nk", flags=g13.FLAG_TEST_STALL, timeout_ms=50)
+    plan = g13.gemm_fp4_plan("mxfp4", M, 300, 2000, 300, ep)
+    g13.gemm_fp4_run(plan, A, B, C)
+    assert g13.gemm_fp4_status(plan) == -5
+    plan2 = g13.gemm_fp4_plan("mxfp4", M, 300, 2000, 300)
+    g13.gemm_fp4_run(plan2, A, B, C)
+    assert g13.gemm_fp4_status(plan2) == 0
+    assert np.array_equal(C.cpu().numpy(), a @ b.T)
