@@ -158,19 +158,34 @@ int g13::tmap_encode_3d(CUtensorMap* m, int dtype, const void* base, int64_t col
                   CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-int g13::tmap_encode_rows_u8(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows,
-                             uint32_t box_rows) {
+namespace {
+int encode_plain(CUtensorMap* m, CUtensorMapDataType t, const void* base, const cuuint64_t (&dims)[3],
+                 const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swz) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return GEMM_ERR_NO_DEVICE;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows), 1};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes),
-                                   static_cast<cuuint64_t>(row_bytes * rows)};
-    const cuuint32_t box[3] = {128, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
-                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUresult r = fn(m, t, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+}  // namespace
+
+int g13::tmap_encode_rows_u8(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows,
+                             uint32_t box_rows) {
+    return encode_plain(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base,
+                        {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows), 1},
+                        {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(row_bytes * rows)},
+                        {128, box_rows, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int g13::tmap_encode_tiles(CUtensorMap* m, const void* base, int64_t col_tiles, int64_t row_tiles,
+                           int tile_bytes, uint32_t box_cols, uint32_t box_rows) {
+    const uint32_t words = static_cast<uint32_t>(tile_bytes / 4);
+    return encode_plain(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, base,
+                        {words, static_cast<cuuint64_t>(col_tiles), static_cast<cuuint64_t>(row_tiles)},
+                        {static_cast<cuuint64_t>(tile_bytes), static_cast<cuuint64_t>(tile_bytes * col_tiles)},
+                        {words, box_cols, box_rows}, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 int g13::cuda_status(cudaError_t e) { return map_cuda_error(e); }

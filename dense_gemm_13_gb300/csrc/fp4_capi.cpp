@@ -92,7 +92,8 @@ int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
     const Fp4Config c = fp4_choose(M, N, K, num_sms);
     std::memset(out, 0, sizeof(*out));
     out->kernel = GEMM_KERNEL_TC;
-    out->bm = 128;
+    out->bm = c.bn == 256 ? 256 : 128;
+    out->variant = c.bn == 256 ? TC_VARIANT_PAIR : 0;
     out->bn = c.bn;
     out->bk = 256;
     out->split_k = c.splits;
@@ -192,17 +193,11 @@ int gemm_fp4_run(gemm_fp4_plan_t plan, const void* a_codes, const void* a_scales
     lc.num_sms = plan->num_sms;
     lc.stream = static_cast<cudaStream_t>(stream);
 
-    CUtensorMap tmW{}, tmX{};
-    if (p.K > 0) {
-        const int64_t rb = fp4_row_bytes(p.K);
-        int rc = tmap_encode_rows_u8(&tmW, b_codes, rb, p.N, 128);
-        if (rc == GEMM_OK)
-            rc = tmap_encode_rows_u8(&tmX, a_codes, rb, p.M, static_cast<uint32_t>(plan->cfg.bn));
-        if (rc != GEMM_OK) return rc;
-    }
-    return cuda_status(launch_fp4_gemm(plan->cfg, plan->format, tmW, tmX,
-                                       static_cast<const uint8_t*>(b_scales), b_tensor_scale,
-                                       static_cast<const uint8_t*>(a_scales), a_tensor_scale, p.K, e, lc));
+    const Fp4Operand A{static_cast<const uint8_t*>(a_codes), static_cast<const uint8_t*>(a_scales),
+                       a_tensor_scale};
+    const Fp4Operand B{static_cast<const uint8_t*>(b_codes), static_cast<const uint8_t*>(b_scales),
+                       b_tensor_scale};
+    return launch_fp4_gemm(plan->cfg, plan->format, A, B, p.K, e, lc);
 }
 
 int gemm_fp4_status(gemm_fp4_plan_t plan) {

@@ -15,12 +15,20 @@
 // of a row at any alignment, with no transpose through shared memory, and the
 // bias is one value per thread.
 //
-//   warp 0      producer: TMA boxes of both operands' codes and bulk copies of
-//               their scale tiles into a ring, counted by full[s]
-//   warp 1      one thread: tcgen05.cp of the stage's scale tiles to TMEM (in
-//               order with the MMAs that read them), then the MMAs; commits
+//   warp 0      producer: TMA boxes of both operands' codes and scale tiles into
+//               a ring, counted by full[s]
+//   warp 1      tcgen05.cp of the stage's scale tiles to TMEM (in order with the
+//               MMAs that read them), then the MMAs, by one elected lane; commits
 //               free ring stages (empty[s]) and finish accumulators (tfull)
-//   warps 2..5  epilogue, one TMEM lane quarter each
+//   others      epilogue: four warps, one TMEM lane quarter each, or eight, two
+//               to a quarter, taking its 16-column chunks in turn
+//
+// Large products run on CTA pairs (tcgen05 cta_group::2): 256 weight rows x 256
+// tokens, each CTA holding its own 128 weight rows and half of the tokens, so
+// that a stage moves 38 KB through each SM's shared memory instead of 54 KB for
+// 128 x 256.  256 accumulator columns and the scales do not fit TMEM twice: two
+// accumulators overlap by 96 columns, which the epilogue reads first and hands
+// back, so the next tile's MMAs start before the rest is stored.
 //
 // Few tokens leave fewer tiles than SMs: a cluster then splits K, each CTA
 // leaves its partial sums in its own shared memory, and every CTA adds one
@@ -42,34 +50,38 @@ namespace {
 constexpr int FW = 128;            // weight rows (TMEM lanes) of a tile
 constexpr int F_KB = 256;          // K elements per stage: 128 bytes of codes
 constexpr int F_W_TILE = FW * 128;
-constexpr int F_THREADS = 192;
+enum F4Mode { F4_ONE = 0, F4_SPLIT = 1, F4_PAIR = 2 };
 
-template <int BN, int FMT>
+template <int BN, int FMT, int MODE>
 struct F4Layout {
+    static constexpr bool PAIR = MODE == F4_PAIR;
+    static constexpr int EW = BN >= 128 ? 8 : 4;            // epilogue warps
+    static constexpr int THREADS = 64 + 32 * EW;
+    static constexpr int TILE_W = PAIR ? 2 * FW : FW;       // weight rows of a tile
+    static constexpr int X_ROWS = PAIR ? BN / 2 : BN;       // tokens that this CTA loads
     static constexpr int CT = F_KB / (4 * fp4_block(FMT));  // scale tiles per stage along K
     static constexpr int XT = (BN + 127) / 128;             // row tiles of the token side
-    static constexpr int X_TILE = BN * 128;
+    static constexpr int X_TILE = X_ROWS * 128;
     static constexpr int SFW_BYTES = CT * kFp4TileBytes;
     static constexpr int SFX_BYTES = XT * CT * kFp4TileBytes;
     static constexpr int STAGE_BYTES = F_W_TILE + X_TILE + SFW_BYTES + SFX_BYTES;
     static constexpr int STAGE_ALIGN = (STAGE_BYTES + 1023) / 1024 * 1024;
-    // accumulators, then two sets of scale columns (a tile is 4 columns)
-    static constexpr int NBUF = BN > 128 ? 1 : 2;
+    // TMEM columns: two accumulators ACC_STEP apart (side by side, or overlapping
+    // where BN = 256), then two sets of scale columns (a tile is 4 columns)
+    static constexpr int OVERLAP = BN == 256 ? 96 : 0;
+    static constexpr int ACC_STEP = BN - OVERLAP;
     static constexpr int SF_COLS = CT * 4 * (1 + XT);
-    static constexpr int SF_BASE = NBUF * BN;
+    static constexpr int SF_BASE = ACC_STEP + BN;
     static constexpr int COLS = SF_BASE + 2 * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(COLS <= 512, "TMEM");
 };
 
 struct F4Args {
     int64_t M, N, K;
-    const uint8_t* sw;  // scale tiles of the weight side (B) and of the tokens (A)
-    const uint8_t* sx;
-    const float* gw;    // tensor scales, or null
+    const float* gw;             // tensor scales of the weight side (B) and the tokens (A), or null
     const float* gx;
-    int64_t w_tiles, x_tiles;    // row tiles of 128 that exist on each side
     int64_t n_tiles, m_tiles;    // tiles of the product
-    int col_tiles;               // scale tiles along K
     int k_blocks;                // stages along K
     int raster;
     uint32_t idesc;
@@ -88,36 +100,49 @@ __device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
     d |= static_cast<uint64_t>(1) << 46;
     return d;
 }
-// One scale tile (512 bytes) into four TMEM columns of all four lane quarters.
+// One scale tile (512 bytes) into four TMEM columns of all four lane quarters
+// (of both CTAs of a pair, each from its own shared memory).
+template <bool PAIR>
 __device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t sdesc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-template <int FMT>
+#define G13_MMA_F4(group, kind, vec)                                                                    \
+    asm volatile(                                                                                       \
+        "{\n\t.reg .pred p;\n\t"                                                                        \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                                     \
+        "tcgen05.mma.cta_group::" group ".kind::" kind ".block_scale.scale_vec::" vec                   \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                              \
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)                                        \
+        : "memory")
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t acc) {
-    if (FMT == GEMM_MXFP4)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
-            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
-            " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-            : "memory");
+    if (FMT == GEMM_MXFP4) {
+        if (PAIR)
+            G13_MMA_F4("2", "mxf4", "2X");
+        else
+            G13_MMA_F4("1", "mxf4", "2X");
+    } else {
+        if (PAIR)
+            G13_MMA_F4("2", "mxf4nvf4", "4X");
+        else
+            G13_MMA_F4("1", "mxf4nvf4", "4X");
+    }
 }
-// Untiled bulk copy into shared memory (16-byte aligned, a multiple of 16 bytes).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar)
-        : "memory");
+#undef G13_MMA_F4
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// A bounded wait of a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                               unsigned* status, uint64_t timeout_ns) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, timeout_ns));
 }
 // 16 consecutive columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -136,9 +161,12 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -185,9 +213,10 @@ __device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float 
     }
 }
 
-template <int BN, int STAGES, int FMT>
+template <int BN, int STAGES, int FMT, int MODE>
 constexpr int f4_smem() {
-    return 1024 + STAGES * F4Layout<BN, FMT>::STAGE_ALIGN + (2 * STAGES + 5) * 8 + 16;
+    // ring; full / empty per stage; tfull x2, tempty x2, drain, pair exit x2; copy counts; slot, flag
+    return 1024 + STAGES * F4Layout<BN, FMT, MODE>::STAGE_ALIGN + (2 * STAGES + 7) * 8 + 32 + 16;
 }
 
 __device__ __forceinline__ void f4_tile(const F4Args& a, int64_t t, int64_t& mt, int64_t& nt) {
@@ -201,50 +230,65 @@ __device__ __forceinline__ void f4_tile(const F4Args& a, int64_t t, int64_t& mt,
     mt = w / gn;
 }
 
-// SPLIT: one tile per cluster, K divided over its CTAs.  Else persistent, one CTA per tile at a time.
-template <int BN, int STAGES, int FMT, bool SPLIT>
-__global__ void __launch_bounds__(F_THREADS, 1)
+// F4_SPLIT: one tile per cluster, K divided over its CTAs.  Else persistent, a
+// CTA (pair) taking one tile after another.
+template <int BN, int STAGES, int FMT, int MODE>
+__global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                    const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                     const F4Args args) {
-    using L = F4Layout<BN, FMT>;
+    using L = F4Layout<BN, FMT, MODE>;
+    constexpr bool PAIR = L::PAIR, SPLIT = MODE == F4_SPLIT;
+    static_assert(STAGES <= 8, "copy counts hold 8 stages");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * L::STAGE_ALIGN);
     uint64_t* empty = full + STAGES;
-    uint64_t* tfull = empty + STAGES;
-    uint64_t* tempty = tfull + 2;
+    uint64_t* tfull = empty + STAGES;  // [2]
+    uint64_t* tempty = tfull + 2;      // [2] an accumulator is read (overlapping ones: [0], the shared part)
     uint64_t* drain = tempty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* oreport = drain + 1;     // pair exit: the odd CTA's copy counts are ready (even CTA's)
+    uint64_t* pdone = oreport + 1;     // pair exit: the even CTA saw them all land (odd CTA's)
+    uint32_t* uses = reinterpret_cast<uint32_t*>(pdone + 1);  // [8] copies issued per stage
+    uint32_t* tmem_slot = uses + 8;
     volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = MODE == F4_ONE ? 0u : cluster_ctarank();
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&tfull[i]), 1);
-            mbar_init(smem_u32(&tempty[i]), 128);
-        }
+        mbar_init(smem_u32(&tfull[0]), 1);
+        mbar_init(smem_u32(&tfull[1]), 1);
+        for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&tempty[i]), (PAIR ? 2 : 1) * L::EW);
         mbar_init(smem_u32(drain), 1);
+        mbar_init(smem_u32(oreport), 1);
+        mbar_init(smem_u32(pdone), 1);
+        for (int i = 0; i < 8; ++i) uses[i] = 0u;
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    if (warp == 1) tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
+    if (warp == 1) {
+        if (PAIR)
+            tmem_alloc_pair(smem_u32(tmem_slot), L::TMEM_COLS);
+        else
+            tmem_alloc(smem_u32(tmem_slot), L::TMEM_COLS);
+    }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // the peer's barriers are initialised before any remote arrive
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     const uint64_t tmo = args.timeout_ns;
 
-    const uint32_t rank = SPLIT ? cluster_ctarank() : 0u;
     uint32_t splits = 1;
     if (SPLIT) asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(splits));
-    const int64_t t_begin = SPLIT ? blockIdx.x / splits : blockIdx.x;
-    const int64_t t_step = SPLIT ? args.n_tiles * args.m_tiles : gridDim.x;
     const int64_t t_end = args.n_tiles * args.m_tiles;
+    const int64_t t_begin = SPLIT ? blockIdx.x / splits : PAIR ? blockIdx.x >> 1 : blockIdx.x;
+    const int64_t t_step = SPLIT ? t_end : PAIR ? gridDim.x >> 1 : gridDim.x;
     const int kb_lo = SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_blocks) * rank / splits) : 0;
     const int kb_hi = SPLIT ? static_cast<int>(static_cast<int64_t>(args.k_blocks) * (rank + 1) / splits)
                             : args.k_blocks;
@@ -252,14 +296,17 @@ __global__ void __launch_bounds__(F_THREADS, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------ producer
-            const bool stall = (args.flags & GEMM_FLAG_TEST_STALL) && blockIdx.x == 0;
+            const bool stall = ((args.flags & GEMM_FLAG_TEST_STALL) && blockIdx.x == 0) ||
+                               ((args.flags & GEMM_FLAG_TEST_STALL_PEER) && blockIdx.x == 1);
             int s = 0;
             uint32_t ph = 0, armed = 0, armed_par = 0;
             bool ok = true;
             for (int64_t t = t_begin; ok && t < t_end; t += t_step) {
                 int64_t mt, nt;
                 f4_tile(args, t, mt, nt);
-                const int64_t xt0 = mt * BN / 128;  // first row tile of the token side
+                const int32_t wt = static_cast<int32_t>(nt * (L::TILE_W / FW) + (PAIR ? rank : 0));
+                const int32_t x0 = static_cast<int32_t>(mt * BN + (PAIR ? rank * L::X_ROWS : 0));
+                const int32_t xt = static_cast<int32_t>(mt * BN / 128);
                 for (int kb = kb_lo; kb < kb_hi; ++kb) {
                     if (!mbar_wait_bounded(smem_u32(&empty[s]), ph ^ 1u, abort_flag, args.status, tmo)) {
                         ok = false;
@@ -268,22 +315,26 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     armed &= ~(1u << s);
                     if (!(stall && t == t_begin && kb == kb_lo)) {
                         const uint32_t st = smem_u32(smem + s * L::STAGE_ALIGN);
-                        const uint32_t bar = smem_u32(&full[s]);
-                        const int c0 = kb * L::CT;
-                        const uint32_t sf = static_cast<uint32_t>(min(L::CT, args.col_tiles - c0)) * kFp4TileBytes;
-                        const bool two = L::XT == 2 && xt0 + 1 < args.x_tiles;
-                        mbar_arrive_expect_tx(bar, F_W_TILE + L::X_TILE + sf * (two ? 3 : 2));
-                        tma_load_3d(st, &tmW, bar, kb * 128, static_cast<int32_t>(nt * FW), 0);
-                        tma_load_3d(st + F_W_TILE, &tmX, bar, kb * 128, static_cast<int32_t>(mt * BN), 0);
+                        // In a pair, both CTAs' boxes of a stage count on the even CTA's full[s].
+                        const uint32_t bar = PAIR ? mapa_shared(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                        if (!PAIR || rank == 0)
+                            mbar_arrive_expect_tx(smem_u32(&full[s]), (PAIR ? 2 : 1) * L::STAGE_BYTES);
+                        const auto load = [&](uint32_t dst, const CUtensorMap* m, int32_t c0, int32_t c1,
+                                              int32_t c2) {
+                            if (PAIR)
+                                tma_load_3d_pair(dst, m, bar, c0, c1, c2);
+                            else
+                                tma_load_3d(dst, m, bar, c0, c1, c2);
+                        };
+                        load(st, &tmW, kb * 128, wt * FW, 0);
+                        load(st + F_W_TILE, &tmX, kb * 128, x0, 0);
                         const uint32_t dst = st + F_W_TILE + L::X_TILE;
-                        bulk_load(dst, args.sw + (nt * args.col_tiles + c0) * kFp4TileBytes, sf, bar);
-                        bulk_load(dst + L::SFW_BYTES, args.sx + (xt0 * args.col_tiles + c0) * kFp4TileBytes, sf,
-                                  bar);
-                        if (two)
-                            bulk_load(dst + 2 * L::SFW_BYTES,
-                                      args.sx + ((xt0 + 1) * args.col_tiles + c0) * kFp4TileBytes, sf, bar);
+                        // tiles past the matrix arrive as zeros
+                        load(dst, &tmSW, 0, kb * L::CT, wt);
+                        load(dst + L::SFW_BYTES, &tmSX, 0, kb * L::CT, xt);
                         armed |= 1u << s;
                         armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                        if (PAIR) uses[s] += 1u;
                     }
                     if (++s == STAGES) {
                         s = 0;
@@ -291,112 +342,190 @@ __global__ void __launch_bounds__(F_THREADS, 1)
                     }
                 }
             }
-            if (!ok)
+            if (PAIR) {
+                // The pair leaves once every copy that either CTA issued has landed
+                // (they all count on the even CTA's barriers).  A producer issues
+                // use u + 1 of a stage only after use u was consumed, so the
+                // copies in flight belong to each stage's last phase: the odd producer
+                // reports its counts, and the even one makes that phase complete
+                // by accounting for a share that will not come, waits, and answers.
+                const uint64_t lim = 3 * tmo + 1000000ull;
+                if (rank == 1) {
+                    mbar_arrive_cluster(mapa_shared(smem_u32(oreport), 0));
+                    if (!mbar_wait_peer(smem_u32(pdone), 0u, lim) && armed) {
+                        const uint64_t t0 = globaltimer_ns();  // no answer: a fixed 200 us
+                        while (globaltimer_ns() - t0 < 200000ull) {
+                        }
+                    }
+                } else {
+                    const bool got = mbar_wait_peer(smem_u32(oreport), 0u, lim);
+                    for (int i = 0; i < STAGES; ++i) {
+                        if (!got) {
+                            if (!ok && (armed & (1u << i)))
+                                tc_drain(smem_u32(&full[i]), (armed_par >> i) & 1u, tmo);
+                            continue;
+                        }
+                        const uint32_t ne = uses[i];
+                        const uint32_t no = ld_peer_u32(mapa_shared(smem_u32(&uses[i]), 1));
+                        const uint32_t n = ne > no ? ne : no;
+                        if (n == 0) continue;
+                        if (ne == no + 1)
+                            mbar_complete_tx(smem_u32(&full[i]), L::STAGE_BYTES);
+                        else if (no == ne + 1)
+                            mbar_arrive_expect_tx(smem_u32(&full[i]), L::STAGE_BYTES);
+                        else if (ne != no)
+                            continue;
+                        tc_drain(smem_u32(&full[i]), (n - 1) & 1u, tmo);
+                    }
+                    if (got) mbar_arrive_cluster(mapa_shared(smem_u32(pdone), 1));
+                }
+            } else if (!ok) {
                 for (int i = 0; i < STAGES; ++i)
                     if (armed & (1u << i)) tc_drain(smem_u32(&full[i]), (armed_par >> i) & 1u, tmo);
+            }
         }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            // ------------------------------------------------ MMA issuer
-            int s = 0, lt = 0;
-            uint32_t ph = 0, set = 0;
-            bool ok = true, issued = false;
-            for (int64_t t = t_begin; ok && t < t_end; t += t_step, ++lt) {
-                const int buf = L::NBUF == 1 ? 0 : (lt & 1);
-                const uint32_t tph = static_cast<uint32_t>(L::NBUF == 1 ? lt : (lt >> 1)) & 1u;
-                if (!mbar_wait_bounded(smem_u32(&tempty[buf]), tph ^ 1u, abort_flag, args.status, tmo)) {
+        __syncwarp();
+    } else if (warp == 1 && (!PAIR || rank == 0)) {
+        // ---------------------------------------------------- MMA issuer
+        // (in a pair, only the even CTA's warp issues).  The whole warp walks the
+        // stages, so that addresses and descriptors stay in uniform registers; one
+        // elected lane issues.  (With the loop inside a single lane's branch, issuing
+        // was the bound: 470 us at 8192^3 nvfp4 against 276 us, before pairs.)
+        const bool one = elect_one();
+        int s = 0, lt = 0;
+        uint32_t ph = 0, set = 0;
+        bool ok = true, issued = false;
+        // descriptors of ring stage 0; a stage is STAGE_ALIGN bytes further on
+        const uint32_t ring = smem_u32(smem);
+        const uint64_t w_desc = smem_desc_sw128(ring, 16, 1024);
+        const uint64_t x_desc = smem_desc_sw128(ring + F_W_TILE, 16, 1024);
+        const uint64_t s_desc = sf_desc(ring + F_W_TILE + L::X_TILE);
+        const int k_steps = static_cast<int>((args.K + 63) / 64);
+        const auto commit = [&](uint64_t* bar) {
+            if (PAIR)
+                tc_commit_pair(smem_u32(bar), 0x3);
+            else
+                tc_commit(smem_u32(bar));
+        };
+        for (int64_t t = t_begin; ok && t < t_end; t += t_step, ++lt) {
+            // the accumulator's columns are free: overlapping ones once the tile before has
+            // handed back the shared part, else after the tile two before
+            const int n_wait = L::OVERLAP ? lt : lt >> 1;  // phases that must be complete
+            if (!mbar_wait_warp(smem_u32(&tempty[L::OVERLAP ? 0 : lt & 1]), static_cast<uint32_t>(n_wait ^ 1) & 1u,
+                                abort_flag, args.status, tmo)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem_base + static_cast<uint32_t>((lt & 1) * L::ACC_STEP);
+            for (int kb = kb_lo; kb < kb_hi; ++kb) {
+                if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort_flag, args.status, tmo)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(buf * BN);
-                for (int kb = kb_lo; kb < kb_hi; ++kb) {
-                    if (!mbar_wait_bounded(smem_u32(&full[s]), ph, abort_flag, args.status, tmo)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * L::STAGE_ALIGN);
-                    const uint32_t sfs = st + F_W_TILE + L::X_TILE;
-                    const uint32_t sf_t = tmem_base + L::SF_BASE + (set ? L::SF_COLS : 0);
-                    set ^= 1u;
-                    const int ct = min(L::CT, args.col_tiles - kb * L::CT);
-                    // TMEM columns of tile c: weights at 4c, tokens' row tile x at 4 (CT + c XT + x)
-                    for (int c = 0; c < ct; ++c) {
-                        sf_copy(sf_t + 4 * c, sf_desc(sfs + c * kFp4TileBytes));
+                const uint64_t off = static_cast<uint64_t>(s * (L::STAGE_ALIGN >> 4));
+                const uint32_t sf_t = tmem_base + L::SF_BASE + (set ? L::SF_COLS : 0);
+                set ^= 1u;
+                const int steps = k_steps - kb * 4;  // 4 or more: a whole stage
+                if (one) {
+                    // TMEM columns of scale tile c: weights at 4c, tokens' row tile x at
+                    // 4 (CT + c XT + x).  nvfp4: a tile per step; mxfp4: two steps share
+                    // a tile, bytes 0-1 and 2-3
 #pragma unroll
-                        for (int x = 0; x < L::XT; ++x)
-                            sf_copy(sf_t + 4 * (L::CT + c * L::XT + x),
-                                    sf_desc(sfs + L::SFW_BYTES * (1 + x) + c * kFp4TileBytes));
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if (kk > 0 && steps <= kk) break;
+                        constexpr int PER = 4 / L::CT;  // steps per scale tile
+                        const int c = kk / PER;
+                        if (kk % PER == 0) {
+                            sf_copy<PAIR>(sf_t + 4 * c, s_desc + off + c * (kFp4TileBytes >> 4));
+#pragma unroll
+                            for (int x = 0; x < L::XT; ++x)
+                                sf_copy<PAIR>(sf_t + 4 * (L::CT + c * L::XT + x),
+                                              s_desc + off + ((L::SFW_BYTES * (1 + x) + c * kFp4TileBytes) >> 4));
+                        }
+                        const uint32_t id = PER == 2 ? (kk & 1) * 2u : 0u;
+                        mma_f4<FMT, PAIR>(d, w_desc + off + kk * 2, x_desc + off + kk * 2,
+                                          args.idesc | (id << 29) | (id << 4), sf_t + 4 * c,
+                                          sf_t + 4 * (L::CT + c * L::XT), (kb > kb_lo || kk > 0) ? 1u : 0u);
                     }
-                    const int steps = static_cast<int>(min(static_cast<int64_t>(F_KB), args.K - static_cast<int64_t>(kb) * F_KB) + 63) / 64;
-                    for (int kk = 0; kk < steps; ++kk) {
-                        // nvfp4: a tile per step; mxfp4: two steps share a tile, bytes 0-1 and 2-3
-                        const int c = FMT == GEMM_MXFP4 ? kk >> 1 : kk;
-                        const uint32_t id = FMT == GEMM_MXFP4 ? (kk & 1) * 2u : 0u;
-                        mma_f4<FMT>(d, smem_desc_sw128(st + kk * 32, 16, 1024),
-                                    smem_desc_sw128(st + F_W_TILE + kk * 32, 16, 1024),
-                                    args.idesc | (id << 29) | (id << 4), sf_t + 4 * c,
-                                    sf_t + 4 * (L::CT + c * L::XT), (kb > kb_lo || kk > 0) ? 1u : 0u);
-                    }
-                    issued = true;
-                    tc_commit(smem_u32(&empty[s]));
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    commit(&empty[s]);
                 }
-                if (!ok) break;
-                tc_commit(smem_u32(&tfull[buf]));
+                issued = true;
+                if (++s == STAGES) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
-            if (!ok && issued) {
-                tc_commit(smem_u32(drain));
-                tc_drain(smem_u32(drain), 0u, tmo);
-            }
+            if (!ok) break;
+            if (one) commit(&tfull[lt & 1]);
         }
-    } else {
+        if (!ok && issued && one) {
+            if (PAIR)
+                tc_commit_pair(smem_u32(drain), 0x1);
+            else
+                tc_commit(smem_u32(drain));
+            tc_drain(smem_u32(drain), 0u, tmo);
+        }
+        __syncwarp();
+    } else if (warp >= 2) {
         // ---------------------------------------------------- epilogue
         const int q = warp & 3;
+        const int h = (warp - 2) >> 2;         // which of the quarter's warps
+        constexpr int STEP = 16 * (L::EW / 4); // columns from one of its chunks to the next
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
         float alpha = args.e.alpha;
         if (args.gw) alpha *= __ldg(args.gw);
         if (args.gx) alpha *= __ldg(args.gx);
+        // K = 0 issued no MMA: the sum is zero
+        const bool none = kb_lo == kb_hi;
         int lt = 0;
         for (int64_t t = t_begin; t < t_end; t += t_step, ++lt) {
             int64_t mt, nt;
             f4_tile(args, t, mt, nt);
-            const int64_t n = nt * FW + q * 32 + lane;
+            const int64_t n = nt * L::TILE_W + (PAIR ? rank * FW : 0) + q * 32 + lane;
             const float bias = args.e.bias && n < args.N ? __ldg(args.e.bias + n) : 0.0f;
-            const int buf = L::NBUF == 1 ? 0 : (lt & 1);
-            const uint32_t tph = static_cast<uint32_t>(L::NBUF == 1 ? lt : (lt >> 1)) & 1u;
-            // the whole warp goes on or leaves: the TMEM loads are warp-wide
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&tfull[buf]), tph, abort_flag,
-                                                           args.status, tmo)))
+            const int buf = lt & 1;
+            if (!mbar_wait_warp(smem_u32(&tfull[buf]), static_cast<uint32_t>(lt >> 1) & 1u, abort_flag,
+                                args.status, tmo))
                 break;
             tc_fence_after();
-            // K = 0 (or an empty share of K) issued no MMA: the sum is zero
-            const bool none = kb_lo == kb_hi;
+            // Overlapping accumulators: the shared columns come first (the first one's last
+            // 96, the second one's first), and are handed back once they are read.
+            const int start = L::OVERLAP && buf == 0 ? BN - L::OVERLAP : 0;
+            constexpr int LAST = L::OVERLAP ? L::OVERLAP : BN;  // columns to read before the release
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 16) {
-                if (!SPLIT && mt * BN + c >= args.M) break;
+            for (int i = 16 * h; i < BN; i += STEP) {
+                const int c = (start + i) % BN;
+                const bool live = SPLIT || mt * BN + c < args.M;
                 uint32_t r[16];
-                tmem_ld_x16(tmem_base + lane_base + static_cast<uint32_t>(buf * BN + c), r);
+                if (live) tmem_ld_x16(tmem_base + lane_base + static_cast<uint32_t>(buf * L::ACC_STEP + c), r);
+                if (!SPLIT && i < LAST && i + STEP >= LAST) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        uint64_t* bar = &tempty[L::OVERLAP ? 0 : buf];
+                        if (PAIR)
+                            mbar_arrive_cluster(mapa_shared(smem_u32(bar), 0));
+                        else
+                            mbar_arrive(smem_u32(bar));
+                    }
+                }
+                if (!live) continue;
                 float v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = none ? 0.0f : __uint_as_float(r[j]);
                 if (SPLIT) {
-                    // every MMA of this CTA is done: the ring is free for the partial sums [column][lane]
-                    float* part = reinterpret_cast<float*>(smem);
+                    // every MMA of this CTA is done: the ring is free for the partial sums,
+                    // four columns of a lane together
+                    float4* part = reinterpret_cast<float4*>(smem) + (c / 4) * FW + q * 32 + lane;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) part[(c + j) * FW + q * 32 + lane] = v[j];
+                    for (int j = 0; j < 4; ++j)
+                        part[j * FW] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                 } else {
                     f4_store<16>(args.e, alpha, bias, mt * BN + c, n, v);
                     __syncwarp();
                 }
-            }
-            if (!SPLIT) {
-                tc_fence_before();
-                mbar_arrive(smem_u32(&tempty[buf]));
             }
         }
     }
@@ -404,43 +533,63 @@ __global__ void __launch_bounds__(F_THREADS, 1)
         __syncwarp();
         cluster_sync();
         if (warp >= 2) {
+            // (a CTA that gave up leaves its sums undefined; the status says so)
             int64_t mt, nt;
             f4_tile(args, t_begin, mt, nt);
-            const int q = warp & 3;
+            const int q = warp & 3, h = (warp - 2) >> 2;
             const int64_t n = nt * FW + q * 32 + lane;
             float alpha = args.e.alpha;
             if (args.gw) alpha *= __ldg(args.gw);
             if (args.gx) alpha *= __ldg(args.gx);
             const float bias = args.e.bias && n < args.N ? __ldg(args.e.bias + n) : 0.0f;
-            // a CTA that gave up leaves its sums undefined: nothing is written (the status says so)
             const int cols = static_cast<int>(min(static_cast<int64_t>(BN), args.M - mt * BN));
-            const uint32_t part = smem_u32(smem) + (q * 32 + lane) * 4;
-            // pairs of columns in turn over the ranks
-            for (int c = 2 * static_cast<int>(rank); c < cols; c += 2 * static_cast<int>(splits)) {
-                float v[2] = {0.0f, 0.0f};
-                for (uint32_t p = 0; p < splits; ++p) {
-                    const uint32_t src = mapa_shared(part + c * FW * 4, p);
-                    v[0] += ld_cluster_f32(src);
-                    v[1] += ld_cluster_f32(src + FW * 4);
+            const uint32_t part = smem_u32(smem) + (q * 32 + lane) * 16;
+            // four columns at a time in turn over the cluster's warps of this quarter, up to
+            // eight reads of other CTAs in flight
+            const int step = 4 * static_cast<int>(splits) * (L::EW / 4);
+            for (int c = 4 * (static_cast<int>(rank) * (L::EW / 4) + h); c < cols; c += step) {
+                float4 p[8];
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    p[k] = k < splits ? ld_cluster_f4(mapa_shared(part + (c / 4) * FW * 16, k))
+                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float v[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
+#pragma unroll
+                for (int k = 1; k < 8; ++k) {
+                    v[0] += p[k].x;
+                    v[1] += p[k].y;
+                    v[2] += p[k].z;
+                    v[3] += p[k].w;
                 }
-                f4_store<2>(args.e, alpha, bias, mt * BN + c, n, v);
+                f4_store<4>(args.e, alpha, bias, mt * BN + c, n, v);
             }
         }
         __syncwarp();
-        cluster_sync();  // no CTA leaves while others read its shared memory
     }
+    __syncwarp();
+    if (MODE != F4_ONE) cluster_sync();  // no CTA leaves while another reads or signals it
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem_base, L::TMEM_COLS);
+    if (warp == 1) {
+        if (PAIR)
+            tmem_dealloc_pair(tmem_base, L::TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, L::TMEM_COLS);
+    }
 }
 
-template <int BN, int STAGES, int FMT, bool SPLIT>
-cudaError_t launch_f4(const CUtensorMap& tmW, const CUtensorMap& tmX, const F4Args& a, int splits,
-                      int num_sms, cudaStream_t st) {
-    auto k = fp4_gemm_kernel<BN, STAGES, FMT, SPLIT>;
-    constexpr int smem = f4_smem<BN, STAGES, FMT>();
+struct F4Maps {
+    CUtensorMap w, x, sw, sx;
+};
+
+template <int BN, int STAGES, int FMT, int MODE>
+cudaError_t launch_f4(const F4Maps& m, const F4Args& a, int splits, int num_sms, cudaStream_t st) {
+    using L = F4Layout<BN, FMT, MODE>;
+    auto k = fp4_gemm_kernel<BN, STAGES, FMT, MODE>;
+    constexpr int smem = f4_smem<BN, STAGES, FMT, MODE>();
     static_assert(smem <= kMaxDynSmem, "shared memory");
+    static_assert(MODE != F4_SPLIT || STAGES * L::STAGE_ALIGN >= BN * FW * 4, "partial sums fit the ring");
     static std::atomic<unsigned char> ready[kMaxDevices];
     int dev = 0;
     cudaError_t ce = cudaGetDevice(&dev);
@@ -451,78 +600,91 @@ cudaError_t launch_f4(const CUtensorMap& tmW, const CUtensorMap& tmX, const F4Ar
         if (dev < kMaxDevices) ready[dev].store(1, std::memory_order_release);
     }
     const int64_t tiles = a.n_tiles * a.m_tiles;
+    const int64_t grid = MODE == F4_SPLIT  ? tiles * splits
+                         : MODE == F4_PAIR ? 2 * std::min<int64_t>(tiles, num_sms / 2)
+                                           : std::min<int64_t>(tiles, num_sms);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(SPLIT ? tiles * splits : std::min<int64_t>(tiles, num_sms)));
-    cfg.blockDim = dim3(F_THREADS);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
-    if (SPLIT) {
+    if (MODE != F4_ONE) {
         at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = static_cast<unsigned>(splits);
+        at[0].val.clusterDim.x = static_cast<unsigned>(MODE == F4_PAIR ? 2 : splits);
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, k, tmW, tmX, a);
+    return cudaLaunchKernelEx(&cfg, k, m.w, m.x, m.sw, m.sx, a);
 }
 
+template <int BN, int STAGES, int MODE>
+cudaError_t launch_fmt(int fmt, const F4Maps& m, const F4Args& a, int splits, int num_sms, cudaStream_t st) {
+    return fmt == GEMM_MXFP4 ? launch_f4<BN, STAGES, GEMM_MXFP4, MODE>(m, a, splits, num_sms, st)
+                             : launch_f4<BN, STAGES, GEMM_NVFP4, MODE>(m, a, splits, num_sms, st);
+}
 template <int BN, int STAGES>
-cudaError_t launch_fmt(int fmt, const CUtensorMap& tmW, const CUtensorMap& tmX, const F4Args& a, int splits,
-                       int num_sms, cudaStream_t st) {
-    if constexpr (BN <= 128) {
-        if (splits > 1)
-            return fmt == GEMM_MXFP4
-                       ? launch_f4<BN, STAGES, GEMM_MXFP4, true>(tmW, tmX, a, splits, num_sms, st)
-                       : launch_f4<BN, STAGES, GEMM_NVFP4, true>(tmW, tmX, a, splits, num_sms, st);
-    }
-    return fmt == GEMM_MXFP4 ? launch_f4<BN, STAGES, GEMM_MXFP4, false>(tmW, tmX, a, 1, num_sms, st)
-                             : launch_f4<BN, STAGES, GEMM_NVFP4, false>(tmW, tmX, a, 1, num_sms, st);
+cudaError_t launch_bn(int fmt, const F4Maps& m, const F4Args& a, int splits, int num_sms, cudaStream_t st) {
+    return splits > 1 ? launch_fmt<BN, STAGES, F4_SPLIT>(fmt, m, a, splits, num_sms, st)
+                      : launch_fmt<BN, STAGES, F4_ONE>(fmt, m, a, 1, num_sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_fp4_gemm(const Fp4Config& c, int fmt, const CUtensorMap& tmW, const CUtensorMap& tmX,
-                            const uint8_t* sw, const float* gw, const uint8_t* sx, const float* gx, int64_t K,
-                            const EpiParams& e, const LaunchCtx& lc) {
+int launch_fp4_gemm(const Fp4Config& c, int fmt, const Fp4Operand& A, const Fp4Operand& B, int64_t K,
+                    const EpiParams& e, const LaunchCtx& lc) {
+    const bool pair = c.bn == 256;
+    const int tile_w = pair ? 2 * FW : FW;
     F4Args a{};
     a.M = e.M;
     a.N = e.N;
     a.K = K;
-    a.sw = sw;
-    a.sx = sx;
-    a.gw = gw;
-    a.gx = gx;
-    a.w_tiles = fp4_row_tiles(e.N);
-    a.x_tiles = fp4_row_tiles(e.M);
-    a.n_tiles = (e.N + FW - 1) / FW;
+    a.gw = B.tensor_scale;
+    a.gx = A.tensor_scale;
+    a.n_tiles = (e.N + tile_w - 1) / tile_w;
     a.m_tiles = (e.M + c.bn - 1) / c.bn;
-    a.col_tiles = static_cast<int>(fp4_col_tiles(fmt, K));
     a.k_blocks = static_cast<int>((K + F_KB - 1) / F_KB);
     a.raster = 8;
     a.e = e;
     a.status = lc.status;
     a.timeout_ns = lc.timeout_ns;
     a.flags = lc.flags;
-    // instruction descriptor: E2M1 operands (1), scale type (1: UE8M0), N, M = 128
+    // instruction descriptor: E2M1 operands (1), scale type (1: UE8M0), N, M
     a.idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(c.bn >> 3) << 17) |
-              ((fmt == GEMM_MXFP4 ? 1u : 0u) << 23) | (static_cast<uint32_t>(FW >> 7) << 27);
-    switch (c.bn) {
-        case 16: return launch_fmt<16, 8>(fmt, tmW, tmX, a, c.splits, lc.num_sms, lc.stream);
-        case 32: return launch_fmt<32, 8>(fmt, tmW, tmX, a, c.splits, lc.num_sms, lc.stream);
-        case 64: return launch_fmt<64, 7>(fmt, tmW, tmX, a, c.splits, lc.num_sms, lc.stream);
-        case 128: return launch_fmt<128, 6>(fmt, tmW, tmX, a, c.splits, lc.num_sms, lc.stream);
-        case 256: return launch_fmt<256, 4>(fmt, tmW, tmX, a, c.splits, lc.num_sms, lc.stream);
-        default: return cudaErrorInvalidValue;
+              ((fmt == GEMM_MXFP4 ? 1u : 0u) << 23) | (static_cast<uint32_t>(tile_w >> 7) << 27);
+    F4Maps m{};
+    if (K > 0) {
+        const int64_t rb = fp4_row_bytes(K);
+        const int64_t ct = fp4_col_tiles(fmt, K);
+        const uint32_t box_ct = static_cast<uint32_t>(F_KB / (4 * fp4_block(fmt)));
+        int rc = tmap_encode_rows_u8(&m.w, B.codes, rb, e.N, FW);
+        if (rc == GEMM_OK)
+            rc = tmap_encode_rows_u8(&m.x, A.codes, rb, e.M, static_cast<uint32_t>(pair ? c.bn / 2 : c.bn));
+        if (rc == GEMM_OK)
+            rc = tmap_encode_tiles(&m.sw, B.scales, ct, fp4_row_tiles(e.N), kFp4TileBytes, box_ct, 1);
+        if (rc == GEMM_OK)
+            rc = tmap_encode_tiles(&m.sx, A.scales, ct, fp4_row_tiles(e.M), kFp4TileBytes, box_ct,
+                                   static_cast<uint32_t>((c.bn + 127) / 128));
+        if (rc != GEMM_OK) return rc;
     }
+    cudaError_t ce;
+    switch (c.bn) {
+        case 16: ce = launch_bn<16, 8>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
+        case 32: ce = launch_bn<32, 8>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
+        case 64: ce = launch_bn<64, 7>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
+        case 128: ce = launch_bn<128, 6>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
+        case 256: ce = launch_fmt<256, 5, F4_PAIR>(fmt, m, a, 1, lc.num_sms, lc.stream); break;
+        default: return GEMM_ERR_UNSUPPORTED;
+    }
+    return cuda_status(ce);
 }
 
 // Tokens per tile: the narrowest of 16, 32, 64 that holds them all; above 64,
-// 256-wide tiles once they fill the GPU, else 128.  K is split over a cluster
-// while the tiles leave SMs idle.
+// CTA pairs on 256 x 256 tiles once they fill the GPU, else 128.  K is split
+// over a cluster while the tiles leave SMs idle.
 Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
     Fp4Config c{};
-    const int64_t n_tiles = (N + FW - 1) / FW;
     if (M <= 16)
         c.bn = 16;
     else if (M <= 32)
@@ -530,9 +692,9 @@ Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
     else if (M <= 64)
         c.bn = 64;
     else
-        c.bn = ((M + 255) / 256) * n_tiles >= num_sms ? 256 : 128;
+        c.bn = ((M + 255) / 256) * ((N + 255) / 256) * 2 >= num_sms ? 256 : 128;
     c.splits = 1;
-    const int64_t tiles = n_tiles * ((M + c.bn - 1) / c.bn);
+    const int64_t tiles = ((N + FW - 1) / FW) * ((M + c.bn - 1) / c.bn);
     const int64_t kbs = (K + F_KB - 1) / F_KB;
     if (c.bn <= 128 && tiles > 0 && kbs > 1) {
         const int64_t most = std::min<int64_t>(8, kbs);

@@ -207,6 +207,10 @@ int tmap_encode_3d(CUtensorMap* m, int dtype, const void* base, int64_t cols, in
 // box_rows, 128B swizzle.
 int tmap_encode_rows_u8(CUtensorMap* m, const void* base, int64_t row_bytes, int64_t rows,
                         uint32_t box_rows);
+// Tiles of tile_bytes (a multiple of 16, at most 1 KB), [row_tiles][col_tiles], in
+// boxes of box_cols x box_rows whole tiles, not swizzled.
+int tmap_encode_tiles(CUtensorMap* m, const void* base, int64_t col_tiles, int64_t row_tiles, int tile_bytes,
+                      uint32_t box_cols, uint32_t box_rows);
 // The gemm_status_t of a CUDA error.
 int cuda_status(cudaError_t e);
 

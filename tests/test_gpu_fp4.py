@@ -166,7 +166,9 @@ def operand(r, rows, cols, fmt, g=None, ints=False):
 
 P_SHAPES = [(1, 1, 1), (1, 128, 64), (1, 300, 1000), (7, 129, 65), (16, 128, 256), (17, 200, 257), (32, 64, 512),
             (33, 500, 96), (64, 130, 300), (65, 257, 700), (127, 384, 1030), (128, 128, 2048), (129, 130, 31),
-            (300, 515, 520), (257, 1000, 64)]
+            (300, 515, 520), (257, 1000, 64),
+            # CTA pairs: several tiles per pair, ragged in every direction
+            (257, 19700, 320), (1030, 5000, 1100), (2100, 2700, 31)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -211,7 +213,7 @@ def check_product(got, A, B, out, bias=None, act="none", R=None, alpha=1.0, beta
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("out", list(DT))
 @pytest.mark.parametrize("shape", [(1, 515, 900), (20, 131, 2000), (50, 300, 333), (100, 129, 4000),
-                                   (200, 300, 770), (600, 9800, 128)], ids=lambda s: "x".join(map(str, s)))
+                                   (200, 300, 770), (600, 9800, 128), (1300, 3900, 700)], ids=lambda s: "x".join(map(str, s)))
 def test_product_epilogue(fmt, out, shape):
     M, N, K = shape
     r = rng("epi", fmt, out, shape)
@@ -288,17 +290,18 @@ def test_graph_and_two_streams(M):
         assert torch.equal(outs[i], want[i])
 
 
-@pytest.mark.parametrize("M", [1, 200])
-def test_timeout_is_reported(M):
-    # the first CTA withholds one stage: its waits run out, the plan says so, and a new plan works
+@pytest.mark.parametrize("flag", [g13.FLAG_TEST_STALL, g13.FLAG_TEST_STALL_PEER])
+@pytest.mark.parametrize("M,N", [(1, 300), (200, 300), (1200, 4100)])
+def test_timeout_is_reported(M, N, flag):
+    # one CTA withholds one stage: the waits run out, the plan says so, and a new plan works
     r = rng("stall", M)
-    (A, a), (B, b) = operand(r, M, 2000, "mxfp4", ints=True), operand(r, 300, 2000, "mxfp4", ints=True)
-    C = torch.zeros(M, 300, device="cuda")
-    ep = g13.Epilogue(b_layout="nk", flags=g13.FLAG_TEST_STALL, timeout_ms=50)
-    plan = g13.gemm_fp4_plan("mxfp4", M, 300, 2000, 300, ep)
+    (A, a), (B, b) = operand(r, M, 2000, "mxfp4", ints=True), operand(r, N, 2000, "mxfp4", ints=True)
+    C = torch.zeros(M, N, device="cuda")
+    ep = g13.Epilogue(b_layout="nk", flags=flag, timeout_ms=50)
+    plan = g13.gemm_fp4_plan("mxfp4", M, N, 2000, N, ep)
     g13.gemm_fp4_run(plan, A, B, C)
     assert g13.gemm_fp4_status(plan) == -5
-    plan2 = g13.gemm_fp4_plan("mxfp4", M, 300, 2000, 300)
+    plan2 = g13.gemm_fp4_plan("mxfp4", M, N, 2000, N)
     g13.gemm_fp4_run(plan2, A, B, C)
     assert g13.gemm_fp4_status(plan2) == 0
     assert np.array_equal(C.cpu().numpy(), a @ b.T)
