@@ -19,7 +19,8 @@ __all__ = ["Epilogue", "Config", "Plan", "GemmError", "gemm_plan", "gemm_run", "
            "gemm_plan_info", "gemm_select_config", "gemm_cache_stats", "gemm_cache_clear",
            "gemm_strerror", "gemm_version", "gemm_run_noalloc", "lib", "load", "matmul", "DTYPES", "ACTS", "LAYOUTS",
            "KERNELS", "LIB_PATH", "FP4_FORMATS", "Fp4Tensor", "Fp4Plan", "fp4_quantize", "fp4_dequantize",
-           "gemm_fp4_plan", "gemm_fp4_run", "gemm_fp4_status", "gemm_fp4_select_config", "fp4_matmul"]
+           "gemm_fp4_plan", "gemm_fp4_run", "gemm_fp4_status", "gemm_fp4_select_config", "fp4_matmul",
+           "MOE_ACTS", "MoePlan", "gemm_moe_plan", "gemm_moe_run", "gemm_moe_status", "moe_layer"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm13.so")
 
@@ -29,6 +30,7 @@ LAYOUTS = {"kn": 0, "nk": 1}
 KERNELS = {"auto": 0, "tc": 1, "ffma": 2, "skinny": 3, "tf32x3": 4}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 FP4_FORMATS = {"mxfp4": 0, "nvfp4": 1}
+MOE_ACTS = {"gelu": 0, "relu": 1, "swiglu": 2}
 FLAG_FP32_TENSOR = 0x1         # FP32 inputs may run as 3xTF32 on the tensor cores
 FLAG_TEST_STALL = 0x80000000
 FLAG_TEST_STALL_PEER = 0x40000000   # test only: the second CTA withholds a tile
@@ -67,6 +69,14 @@ class _PlanInfo(ctypes.Structure):
     _fields_ = [("config", _Config), ("workspace_bytes", ctypes.c_int64),
                 ("num_sms", ctypes.c_int32), ("device", ctypes.c_int32),
                 ("cache_hit", ctypes.c_int32), ("kernels_per_run", ctypes.c_int32)]
+
+
+class _MoeDesc(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("T", ctypes.c_int64), ("E", ctypes.c_int64), ("top_k", ctypes.c_int64),
+                ("H", ctypes.c_int64), ("I", ctypes.c_int64), ("act", ctypes.c_int), ("normalize", ctypes.c_int),
+                ("ldx", ctypes.c_int64), ("ld_router", ctypes.c_int64), ("ld_w1", ctypes.c_int64),
+                ("stride_w1", ctypes.c_int64), ("ld_w2", ctypes.c_int64), ("stride_w2", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("flags", ctypes.c_uint32), ("timeout_ms", ctypes.c_uint32)]
 
 
 _lock = threading.Lock()
@@ -135,6 +145,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.gemm_fp4_destroy.restype = None
         L.gemm_fp4_select_config.argtypes = [i64, i64, i64, ctypes.c_int32, ctypes.POINTER(_Config)]
         L.gemm_fp4_select_config.restype = i32
+        L.gemm_moe_desc_init.argtypes = [ctypes.POINTER(_MoeDesc)]
+        L.gemm_moe_desc_init.restype = None
+        L.gemm_moe_plan.argtypes = [ctypes.POINTER(_MoeDesc), ctypes.POINTER(vp)]
+        L.gemm_moe_plan.restype = i32
+        L.gemm_moe_workspace_bytes.argtypes = [vp]
+        L.gemm_moe_workspace_bytes.restype = i64
+        L.gemm_moe_run.argtypes = [vp] * 10
+        L.gemm_moe_run.restype = i32
+        L.gemm_moe_status.argtypes = [vp]
+        L.gemm_moe_status.restype = i32
+        L.gemm_moe_destroy.argtypes = [vp]
+        L.gemm_moe_destroy.restype = None
         if path is None:
             _lib = L
         return L
@@ -607,3 +629,110 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
             pl = _fp4_plans[key] = gemm_fp4_plan(A.format, M, N, K, ldc, ep)
         gemm_fp4_run(pl, A, B, out, bias, residual, alpha, stream)
     return out
+
+
+# ------------------------------------------------------------------ mixture of experts
+class MoePlan:
+    """Owns a gemm_moe_plan_t; destroyed with the object (or explicitly)."""
+
+    def __init__(self, handle: int, workspace_bytes: int):
+        self.handle, self.workspace_bytes = handle, workspace_bytes
+
+    def destroy(self):
+        if self.handle:
+            lib().gemm_moe_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def gemm_moe_plan(dtype: str, T: int, E: int, top_k: int, H: int, I: int, act: str = "swiglu",
+                  normalize: bool = True, **fields) -> MoePlan:
+    """gemm_moe_plan; `fields`: the other members of gemm_moe_desc_t.  Raises GemmError on a non-OK status."""
+    d, h = _MoeDesc(), ctypes.c_void_p()
+    lib().gemm_moe_desc_init(ctypes.byref(d))
+    d.dtype, d.T, d.E, d.top_k, d.H, d.I = DTYPES[dtype], T, E, top_k, H, I
+    d.act, d.normalize = MOE_ACTS[act], int(bool(normalize))
+    for k, v in fields.items():
+        setattr(d, k, int(v))
+    rc = lib().gemm_moe_plan(ctypes.byref(d), ctypes.byref(h))
+    if rc != 0:
+        raise GemmError(rc, "gemm_moe_plan")
+    return MoePlan(h.value, lib().gemm_moe_workspace_bytes(h))
+
+
+def gemm_moe_run(plan: MoePlan, X, router, W1, W2, Y, workspace, expert_ids=None, expert_weights=None,
+                 stream=None) -> int:
+    """Enqueue one layer on `stream` (default: torch's current stream); raises on error."""
+    import torch
+    rc = lib().gemm_moe_run(plan.handle, _ptr(X), _ptr(router), _ptr(W1), _ptr(W2), _ptr(Y), _ptr(expert_ids),
+                            _ptr(expert_weights), _ptr(workspace), _stream(torch, stream))
+    if rc != 0:
+        raise GemmError(rc, "gemm_moe_run")
+    return rc
+
+
+def gemm_moe_status(plan: MoePlan) -> int:
+    """Synchronise and return the plan's sticky device status (0 or a negative code)."""
+    return int(lib().gemm_moe_status(plan.handle))
+
+
+_moe_plans: dict = {}
+
+
+def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: bool = True, out=None,
+              return_routing: bool = False, stream=None):
+    """A mixture-of-experts layer for 1 to 64 tokens (include/gemm13.h, gemm_moe_run).
+
+    x [T, H], router [E, H], w1 [E, I, H] ("gelu", "relu") or [E, 2I, H] ("swiglu": gate rows, then up
+    rows), w2 [E, H, I], all FP16 or all BF16, rows contiguous.  Returns y [T, H], or with
+    return_routing (y, expert ids int32 [T, top_k], their weights FP32 [T, top_k]).  Plans are kept per
+    shape, strides and device; every call has a workspace of its own from torch's allocator, on the
+    stream that it runs on.
+    """
+    import torch
+    what = "moe_layer"
+    dt = _tdt().get(x.dtype)
+    if dt not in ("f16", "bf16") or act not in MOE_ACTS:
+        _refuse(what, "FP16 or BF16 tensors and act gelu, relu or swiglu are wanted")
+    if x.dim() != 2 or router.dim() != 2 or w1.dim() != 3 or w2.dim() != 3:
+        _refuse(what, "x [T, H], router [E, H], w1 [E, I or 2I, H], w2 [E, H, I] are wanted")
+    (T, H), E, I, dev = x.shape, router.shape[0], w2.shape[2], x.device
+    rows = 2 * I if act == "swiglu" else I
+    if tuple(router.shape) != (E, H) or tuple(w1.shape) != (E, rows, H) or tuple(w2.shape) != (E, H, I):
+        _refuse(what, "the shapes of x, router, w1 and w2 do not fit one another")
+    for name, t in (("x", x), ("router", router), ("w1", w1), ("w2", w2), ("out", out)):
+        if t is not None and (t.dtype != x.dtype or t.device != dev or not t.is_cuda or
+                              (t.shape[-1] > 1 and t.stride(-1) != 1) or
+                              (t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]) or
+                              (t.dim() == 3 and t.shape[0] > 1 and t.stride(0) == 0)):
+            _refuse(what, f"{name}: x's dtype and device and rows that are contiguous and not shared are wanted")
+    if out is not None and tuple(out.shape) != (T, H):
+        _refuse(what, "out: [T, H] is wanted")
+    with _On(torch, dev):
+        if out is None:
+            out = torch.empty((T, H), dtype=x.dtype, device=dev)
+        ldx, ldr, ldy = (t.stride(0) if t.shape[0] > 1 else H for t in (x, router, out))
+        ld1, ld2 = w1.stride(1) if rows > 1 else H, w2.stride(1) if H > 1 else I
+        st1, st2 = (w1.stride(0), w2.stride(0)) if E > 1 else (rows * ld1, H * ld2)
+        key = (dt, T, E, top_k, H, I, act, normalize, ldx, ldr, ld1, st1, ld2, st2, ldy, dev.index)
+        pl = _moe_plans.get(key)
+        if pl is None:
+            pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=ldx, ld_router=ldr,
+                                                 ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=ldy)
+        ids = wts = None
+        if return_routing:
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+            wts = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        if stream is None:
+            ws = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
+        else:  # the workspace belongs to the stream that uses it
+            s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                ws = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
+        gemm_moe_run(pl, x, router, w1, w2, out, ws, ids, wts, stream)
+    return (out, ids, wts) if return_routing else out

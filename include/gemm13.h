@@ -357,6 +357,78 @@ void gemm_fp4_destroy(gemm_fp4_plan_t plan);
  * K (split_k).  Errors: INVALID_ARG. */
 int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gemm_config_t* out);
 
+/*
+ * A mixture-of-experts layer for a few tokens, all of it: router, choice of
+ * experts, both products of each chosen expert, and their weighted sum.
+ *
+ *     z = X.Wr^T                          [T][E], FP32
+ *     p = softmax(z) over all E experts
+ *     the top_k experts of a token are those with the largest z (equal ones:
+ *     the lowest index; NaN comes last); their weights are p, or, with
+ *     normalize, p divided by its sum over them
+ *     Y[t] = cast( sum_j weight_j * W2[e_j] . h_j ),  h_j = cast( act(W1[e_j] . X[t]) )
+ *
+ * in FP32 accumulation; cast rounds to nearest even to `dtype`, that of X, Wr,
+ * W1, W2 and Y (GEMM_F16 or GEMM_BF16; an h beyond FP16's range becomes an
+ * infinity).  Every weight of a chosen expert is read once.  A token with
+ * a NaN or an infinite logit gets NaN rows, and no other token's row changes.
+ */
+typedef enum {
+    GEMM_MOE_GELU = 0,  /* GELU (erf form) of W1[e] . x, W1[e] [I][H] */
+    GEMM_MOE_RELU = 1,  /* max(W1[e] . x, 0) */
+    GEMM_MOE_SWIGLU = 2 /* silu(gate) * up, W1[e] [2I][H]: gate rows, then up rows */
+} gemm_moe_act_t;
+
+typedef struct {
+    gemm_dtype_t dtype;  /* GEMM_BF16 (default) or GEMM_F16 */
+    int64_t T;           /* tokens, 0 to 64 */
+    int64_t E;           /* experts, 1 to 512 */
+    int64_t top_k;       /* experts per token, 1 to min(E, 32) */
+    int64_t H;           /* length of a token, 1 to 16384 */
+    int64_t I;           /* inner length of an expert, 1 to 2^20 */
+    gemm_moe_act_t act;  /* default GEMM_MOE_SWIGLU */
+    int normalize;       /* 1 (default): weights of a token sum to one */
+    /* strides in elements; 0 means contiguous (H; H; H and rows of W1 times
+       ld_w1; I and H * ld_w2; H) */
+    int64_t ldx;                /* X [T][ldx] */
+    int64_t ld_router;          /* Wr [E][ld_router] */
+    int64_t ld_w1, stride_w1;   /* W1 [E][I or 2I][ld_w1], experts stride_w1 apart */
+    int64_t ld_w2, stride_w2;   /* W2 [E][H][ld_w2], experts stride_w2 apart */
+    int64_t ldy;                /* Y [T][ldy] */
+    uint32_t flags;             /* GEMM_FLAG_TEST_STALL, or 0 */
+    uint32_t timeout_ms;        /* bound on the device-side wait; 0 means 2000 ms */
+} gemm_moe_desc_t;
+
+typedef struct gemm_moe_plan_s* gemm_moe_plan_t;
+
+/* Fills *d with the defaults listed above. */
+void gemm_moe_desc_init(gemm_moe_desc_t* d);
+
+/* Validates the layer and allocates a status word on the current device.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes, FP32), NO_DEVICE, OUT_OF_MEMORY, CUDA. */
+int gemm_moe_plan(const gemm_moe_desc_t* desc, gemm_moe_plan_t* out_plan);
+
+/* Device bytes that each run needs as its workspace; 0 for a bad plan. */
+int64_t gemm_moe_workspace_bytes(gemm_moe_plan_t plan);
+
+/*
+ * Enqueues the layer (two kernels) on `stream`.  All pointers are device pointers,
+ * aligned to their element type; any other alignment is accepted, but weights whose
+ * rows all start on 16 bytes and whose H and I are multiples of 8 load fastest.
+ * (Other rows are read in whole 16-byte pieces of memory, each of which holds at
+ * least one of their elements.)  expert_ids (int32 [T][top_k], largest weight first)
+ * and expert_weights (FP32 [T][top_k]) may be NULL.  workspace: 256-byte aligned,
+ * gemm_moe_workspace_bytes() long, any contents; it belongs to the run until the run
+ * has finished on the GPU.  Runs with workspaces of their own may overlap.  No output
+ * may overlap an input, the workspace or another output.  Allocates nothing.
+ * Errors: BAD_PLAN, INVALID_ARG, MISALIGNED, CUDA.
+ */
+int gemm_moe_run(gemm_moe_plan_t plan, const void* X, const void* Wr, const void* W1, const void* W2,
+                 void* Y, int32_t* expert_ids, float* expert_weights, void* workspace, void* stream);
+/* As gemm_plan_status and gemm_plan_destroy. */
+int gemm_moe_status(gemm_moe_plan_t plan);
+void gemm_moe_destroy(gemm_moe_plan_t plan);
+
 #ifdef __cplusplus
 }
 #endif
