@@ -11,14 +11,14 @@
 // loads in flight.  Two kernels:
 //
 //   router   z in FP32 (one warp per expert and four tokens); copies x into rows
-//            padded to 32 elements; clears the counters of the second kernel
+//            padded to 64 elements; clears the counters of the second kernel
 //   experts  one CTA of 16 warps per SM, cooperative.  Every CTA works out the
 //            routing for itself from z (softmax, top-k by warp-wide maximum
 //            reductions, a 64-bit mask of tokens per expert), which is cheaper than
 //            another trip through memory.  Then the two products, with one grid
 //            barrier between them:
 //     up     work units of 16 weight rows of a chosen expert (SwiGLU: 8 gate rows
-//            and their 8 up rows, so one thread holds both factors) x 32-element
+//            and their 8 up rows, so one thread holds both factors) x 64-element
 //            steps along H.  A CTA takes an equal share of the units and its warps
 //            equal shares of the units' steps; a unit cut between warps is joined
 //            through shared memory, in warp order.
@@ -30,7 +30,7 @@
 //
 // Products: mma.sync m16n8k16, weights as the 16 rows and a group of 8 tokens as
 // the columns.  The order of k within a step is free as long as both operands share
-// it, so a thread takes 16 consecutive bytes of a row (8 values: two MMAs' worth)
+// it, so a thread takes 32 consecutive bytes of a row (16 values: four MMAs' worth)
 // straight from global memory as its fragments; no shared memory, no barrier.
 // (tcgen05 would need the weights staged through shared memory, to do arithmetic
 // that is far from the bound.)  FP32 accumulation; h = act(...) is rounded to
@@ -60,6 +60,10 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                  : "l"(p));
     return v;
 }
+
+// How the rows of a weight lie: all on 32 bytes with lengths a multiple of 16 elements, all
+// on 16 bytes with multiples of 8, or anyhow.
+enum Rows { ROWS_32 = 0, ROWS_16 = 1, ROWS_ANY = 2 };
 
 // Eight consecutive 16-bit values at p, of which the first n (0 to 8) exist; the rest
 // are zero.  VEC: p is 16-byte aligned and n is 0 or 8.  Else two aligned 16-byte loads
@@ -93,6 +97,39 @@ __device__ __forceinline__ uint4 ld_row8(const uint16_t* p, int n) {
     }
     return a;
 }
+// Sixteen of them.
+struct Row16 {
+    uint32_t v[8];
+};
+template <int ROWS>
+__device__ __forceinline__ Row16 ld_row16(const uint16_t* p, int n) {
+    Row16 r;
+    if (ROWS == ROWS_32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.v[i] = 0u;
+        if (n > 0)
+            asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=r"(r.v[0]), "=r"(r.v[1]), "=r"(r.v[2]), "=r"(r.v[3]), "=r"(r.v[4]), "=r"(r.v[5]),
+                           "=r"(r.v[6]), "=r"(r.v[7])
+                         : "l"(p));
+    } else {
+        const uint4 a = ld_row8<ROWS == ROWS_16>(p, n), b = ld_row8<ROWS == ROWS_16>(p + 8, n - 8);
+        r = Row16{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+    }
+    return r;
+}
+
+// Equal shares of `total` for `parts` takers, the first ones one longer.
+struct Share {
+    int q, r;
+    __device__ __forceinline__ Share(int total, int parts) : q(total / parts), r(total % parts) {}
+    __device__ __forceinline__ int lo(int i) const { return i * q + min(i, r); }
+    // The taker of item u (shares that are not empty).
+    __device__ __forceinline__ int owner(int u) const {
+        const int longer = r * (q + 1);
+        return u < longer ? u / (q + 1) : r + (u - longer) / max(q, 1);
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ float2 unpack2(uint32_t v);
@@ -144,29 +181,29 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
     const gemm_moe_desc_t& d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t tid = static_cast<int64_t>(blockIdx.x) * RT + threadIdx.x;
-    const int64_t nthreads = static_cast<int64_t>(gridDim.x) * RT;
+    // (every count here stays below 2^31; 64-bit divisions would cost microseconds)
+    const int tid = static_cast<int>(blockIdx.x) * RT + threadIdx.x;
+    const int nthreads = static_cast<int>(gridDim.x) * RT;
     // counters, padded x, and the padding of h (never written by the up product)
     unsigned* ctr = reinterpret_cast<unsigned*>(a.ws + a.w.bar);
-    const int64_t n_ctr = (a.w.logits - a.w.bar) / 4;
-    for (int64_t i = tid; i < n_ctr; i += nthreads) ctr[i] = 0u;
+    const int n_ctr = static_cast<int>((a.w.logits - a.w.bar) / 4);
+    for (int i = tid; i < n_ctr; i += nthreads) ctr[i] = 0u;
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     uint16_t* xp = reinterpret_cast<uint16_t*>(a.ws + a.w.x);
     const int hp = static_cast<int>(a.w.hp), H = static_cast<int>(d.H);
-    for (int64_t i = tid; i < d.T * hp; i += nthreads) {
-        const int64_t t = i / hp;
-        const int k = static_cast<int>(i - t * hp);
+    for (int i = tid; i < static_cast<int>(d.T) * hp; i += nthreads) {
+        const int t = i / hp, k = i - t * hp;
         xp[i] = k < H ? x[t * d.ldx + k] : uint16_t(0);
     }
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws + a.w.h);
     const int pad = static_cast<int>(a.w.ip - d.I);
-    for (int64_t i = tid; i < d.T * d.top_k * pad; i += nthreads)
-        h[i / pad * a.w.ip + d.I + i % pad] = 0;
+    for (int i = tid; i < static_cast<int>(d.T * d.top_k) * pad; i += nthreads)
+        h[static_cast<int64_t>(i / pad) * a.w.ip + d.I + i % pad] = 0;
 
     // z: a warp takes one expert and four tokens
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (RT / 32) + warp;
-    const int64_t e = unit % d.E;
-    const int t0 = static_cast<int>(unit / d.E) * 4;
+    const int unit = static_cast<int>(blockIdx.x) * (RT / 32) + warp;
+    const int t0 = unit / static_cast<int>(d.E) * 4;
+    const int64_t e = unit % static_cast<int>(d.E);
     if (t0 >= d.T) return;
     const int nt = min(4, static_cast<int>(d.T) - t0);
     const uint16_t* r = static_cast<const uint16_t*>(a.router) + e * d.ld_router;
@@ -202,6 +239,7 @@ struct MoeShared {
     int off[kMoeMaxExperts];                  // first slot of each expert
     int active[kMoeMaxExperts];               // experts that have tokens
     int n_active;
+    int warp_first[kMoeWarps], warp_last[kMoeWarps];  // output blocks that each warp adds to
     int last[2];                              // this CTA joins its first / last output block
     int gave_up;
     int slot_token[kMoeMaxTokens * kMoeMaxTopK];
@@ -217,9 +255,9 @@ __device__ __forceinline__ uint32_t order_key(float z) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Top-k of one token by a warp: writes pick[] and pick_weight[] at t * top_k.
+// Top-k of one token by a warp, PER logits a lane: writes pick[] and pick_weight[] at t * top_k.
+template <int PER>
 __device__ __forceinline__ void route_token(const MoeArgs& a, MoeShared& s, int t, int lane) {
-    constexpr int PER = kMoeMaxExperts / 32;
     const int E = static_cast<int>(a.d.E), k = static_cast<int>(a.d.top_k);
     const float* z = reinterpret_cast<const float*>(a.ws + a.w.logits) + static_cast<int64_t>(t) * E;
     float v[PER];
@@ -266,32 +304,36 @@ __device__ __forceinline__ void route_token(const MoeArgs& a, MoeShared& s, int 
         for (int j = lane; j < k; j += 32) s.pick_weight[t * k + j] /= total;
 }
 
-// One warp, steps [s0, s1) of 32 elements: acc[16 rows x 8 NT columns] += W x^T.  w0, w1: this
+// One warp, steps [s0, s1) of 64 elements: acc[16 rows x 8 NT columns] += W x^T.  w0, w1: this
 // lane's two weight rows (null: zeros), xr: its token rows (padded), K valid elements of a weight row.
-template <typename T, bool VEC, int NT>
+template <typename T, int ROWS, int NT>
 __device__ __forceinline__ void mma_steps(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT],
                                           int s0, int s1, int K, int t4, float (&acc)[NT][4]) {
-    constexpr int U = NT <= 2 ? 4 : 2;  // steps of loads in flight (two batches)
-    uint4 wa[2][U], wb[2][U];
+    constexpr int U = NT <= 2 ? 2 : 1;  // steps of loads in a batch (two batches in flight)
+    Row16 wa[2][U], wb[2][U];
     const auto load = [&](int b, int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int k = (s + u) * 32 + t4 * 8;
+            const int k = (s + u) * 64 + t4 * 16;
             const int n = s + u < s1 ? K - k : 0;
-            wa[b][u] = ld_row8<VEC>(w0 + k, w0 ? n : 0);
-            wb[b][u] = ld_row8<VEC>(w1 + k, w1 ? n : 0);
+            wa[b][u] = ld_row16<ROWS>(w0 + k, w0 ? n : 0);
+            wb[b][u] = ld_row16<ROWS>(w1 + k, w1 ? n : 0);
         }
     };
     const auto compute = [&](int b, int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s + u >= s1) break;
-            const int k = (s + u) * 32 + t4 * 8;
+            const int k = (s + u) * 64 + t4 * 16;
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const uint4 xv = *reinterpret_cast<const uint4*>(xr[j] + k);
-                mma16816<T>(acc[j], wa[b][u].x, wb[b][u].x, wa[b][u].y, wb[b][u].y, xv.x, xv.y);
-                mma16816<T>(acc[j], wa[b][u].z, wb[b][u].z, wa[b][u].w, wb[b][u].w, xv.z, xv.w);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 xv = *reinterpret_cast<const uint4*>(xr[j] + k + 8 * i);
+                    const uint32_t *p = wa[b][u].v + 4 * i, *q = wb[b][u].v + 4 * i;
+                    mma16816<T>(acc[j], p[0], q[0], p[1], q[1], xv.x, xv.y);
+                    mma16816<T>(acc[j], p[2], q[2], p[3], q[3], xv.z, xv.w);
+                }
             }
         }
     };
@@ -306,7 +348,7 @@ __device__ __forceinline__ void mma_steps(const uint16_t* w0, const uint16_t* w1
 
 // As mma_steps for n columns (1 to 8 NTMAX) of the slots at `off`: rows of `x` of xld elements, indexed
 // by token (by_token) or by slot.
-template <typename T, bool VEC, int NTMAX>
+template <typename T, int ROWS, int NTMAX>
 __device__ __forceinline__ void mma_cols(const MoeShared& s, const uint16_t* w0, const uint16_t* w1,
                                          const uint16_t* x, int64_t xld, bool by_token, int off, int n, int s0,
                                          int s1, int K, int lane, float (&acc)[NTMAX][4]) {
@@ -322,7 +364,7 @@ __device__ __forceinline__ void mma_cols(const MoeShared& s, const uint16_t* w0,
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[j][i] = 0.0f;
         }
-        mma_steps<T, VEC, NT>(w0, w1, xr, s0, s1, K, lane & 3, c);
+        mma_steps<T, ROWS, NT>(w0, w1, xr, s0, s1, K, lane & 3, c);
 #pragma unroll
         for (int j = 0; j < NTMAX; ++j)
 #pragma unroll
@@ -340,7 +382,7 @@ __device__ __forceinline__ void mma_cols(const MoeShared& s, const uint16_t* w0,
     run(std::integral_constant<int, 1>{});
 }
 
-template <typename T, bool VEC, int NTMAX>
+template <typename T, int ROWS, int NTMAX>
 __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     extern __shared__ __align__(16) char moe_smem[];
     MoeShared& s = *reinterpret_cast<MoeShared*>(moe_smem);
@@ -348,13 +390,18 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     const gemm_moe_desc_t& d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tok = static_cast<int>(d.T), E = static_cast<int>(d.E), top_k = static_cast<int>(d.top_k);
-    const int64_t G = gridDim.x, cta = blockIdx.x;
+    const int G = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
 
     // ---------------------------------------------------------------- routing
     for (int e = threadIdx.x; e < E; e += MT) s.mask[e] = 0ull;
     if (threadIdx.x == 0) s.gave_up = 0;
     __syncthreads();
-    for (int t = warp; t < tok; t += kMoeWarps) route_token(a, s, t, lane);
+    for (int t = warp; t < tok; t += kMoeWarps) {
+        if (E <= 64)
+            route_token<2>(a, s, t, lane);
+        else
+            route_token<kMoeMaxExperts / 32>(a, s, t, lane);
+    }
     __syncthreads();
     if (warp == 0) {
         int n = 0, slots = 0;
@@ -397,15 +444,17 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     {
         const bool gated = d.act == GEMM_MOE_SWIGLU;
         const int per = gated ? 8 : 16;  // values of h per unit
-        const int64_t UB = (d.I + per - 1) / per, U = UB * A;
-        const int KS = static_cast<int>(a.w.hp / 32);
-        const int64_t u_lo = cta * U / G, n_u = (cta + 1) * U / G - u_lo;
-        const int64_t total = n_u * KS;
-        const int64_t lo = warp * total / kMoeWarps, hi = (warp + 1) * total / kMoeWarps;
+        // (the host keeps these counts below 2^31)
+        const int UB = static_cast<int>((d.I + per - 1) / per), U = UB * A;
+        const int KS = static_cast<int>(a.w.hp / 64);
+        const Share ctas(U, G);
+        const int u_lo = ctas.lo(cta), total = (ctas.lo(cta + 1) - u_lo) * KS;
+        const Share warps(total, kMoeWarps);
+        const int lo = warps.lo(warp), hi = warps.lo(warp + 1);
         const uint16_t* w1 = static_cast<const uint16_t*>(a.w1);
-        const auto finish = [&](int64_t u, const float (&acc)[NTMAX][4]) {
+        const auto finish = [&](int u, const float (&acc)[NTMAX][4]) {
             const int e = s.active[u / UB];
-            const int64_t i0 = u % UB * per;
+            const int i0 = u % UB * per;
             const int n = __popcll(s.mask[e]), off = s.off[e];
 #pragma unroll
             for (int j = 0; j < NTMAX; ++j) {
@@ -424,10 +473,9 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                 }
             }
         };
-        for (int64_t cur = lo; cur < hi;) {
-            const int64_t u = u_lo + cur / KS;
-            const int s0 = static_cast<int>(cur % KS);
-            const int s1 = static_cast<int>(min(static_cast<int64_t>(KS), s0 + hi - cur));
+        for (int cur = lo; cur < hi;) {
+            const int u = u_lo + cur / KS;
+            const int s0 = cur % KS, s1 = min(KS, s0 + hi - cur);
             const int e = s.active[u / UB];
             const int64_t i = u % UB * per + g;
             const uint16_t* base = w1 + e * d.stride_w1;
@@ -435,7 +483,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
             const uint16_t* r1 = gated ? (r0 ? r0 + d.I * d.ld_w1 : nullptr)
                                        : (i + 8 < d.I ? base + (i + 8) * d.ld_w1 : nullptr);
             float acc[NTMAX][4];
-            mma_cols<T, VEC, NTMAX>(s, r0, r1, xp, a.w.hp, true, s.off[e], __popcll(s.mask[e]), s0, s1,
+            mma_cols<T, ROWS, NTMAX>(s, r0, r1, xp, a.w.hp, true, s.off[e], __popcll(s.mask[e]), s0, s1,
                                     static_cast<int>(d.H), lane, acc);
             if (s0 == 0 && s1 == KS) {
                 finish(u, acc);
@@ -453,7 +501,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         __syncthreads();
         // the warp in which a cut unit begins joins it
         if (lo < hi) {
-            const int64_t u = (hi - 1) / KS;
+            const int u = (hi - 1) / KS;
             if (u * KS >= lo && (u + 1) * KS > hi) {
                 float acc[NTMAX][4];
 #pragma unroll
@@ -462,9 +510,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                     for (int c = 0; c < 4; ++c)
                         acc[j][c] = my_tile[16 * 8 * NTMAX + (j * 4 + c) * 32 + lane];
                 for (int w = warp + 1; w < kMoeWarps; ++w) {
-                    const int64_t wlo = w * total / kMoeWarps, whi = (w + 1) * total / kMoeWarps;
-                    if (wlo >= (u + 1) * KS) break;
-                    if (wlo == whi) continue;
+                    if (warps.lo(w) >= (u + 1) * KS || warps.lo(w) == warps.lo(w + 1)) break;
                     const float* slot = tiles + w * 2 * (16 * 8 * NTMAX);
 #pragma unroll
                     for (int j = 0; j < NTMAX; ++j)
@@ -477,6 +523,22 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     }
 
     // ---------------------------------------------------------------- grid barrier
+    // This warp's share of the down product is known already: its first weights are
+    // asked into L2 while the barrier is waited for.
+    const int OB = static_cast<int>((d.H + 15) / 16), V = OB * A;
+    const int KS = static_cast<int>(a.w.ip / 64);
+    const Share ctas(V, G);
+    const int v_lo = ctas.lo(cta), v_hi = ctas.lo(cta + 1);
+    const Share warps((v_hi - v_lo) * KS, kMoeWarps);
+    const int lo = warps.lo(warp), hi = warps.lo(warp + 1);
+    const uint16_t* w2 = static_cast<const uint16_t*>(a.w2);
+    if (lo < hi) {
+        const int v = v_lo + lo / KS, k = (lo % KS + t4) * 64;
+        const int64_t o = v / A * 16 + g;
+        const uint16_t* p = w2 + s.active[v % A] * d.stride_w2 + o * d.ld_w2 + k;
+        if (k < d.I && o < d.H) prefetch_l2(p);
+        if (k < d.I && o + 8 < d.H) prefetch_l2(p + 8 * d.ld_w2);
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
         unsigned* bar = reinterpret_cast<unsigned*>(a.ws + a.w.bar);
@@ -496,22 +558,19 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     if (s.gave_up) return;
 
     // ---------------------------------------------------------------- down
-    const int64_t OB = (d.H + 15) / 16, V = OB * A;
-    const int KS = static_cast<int>(a.w.ip / 32);
-    const int64_t v_lo = cta * V / G, v_hi = (cta + 1) * V / G;
-    const int64_t total = (v_hi - v_lo) * KS;
-    const int64_t lo = warp * total / kMoeWarps, hi = (warp + 1) * total / kMoeWarps;
-    const uint16_t* w2 = static_cast<const uint16_t*>(a.w2);
     const int ytile = 16 * tok;  // [row][token]
     float* yt = tiles + warp * 2 * ytile;
     for (int i = lane; i < 2 * ytile; i += 32) yt[i] = 0.0f;
     __syncwarp();
-    const int64_t first_ob = (v_lo + lo / KS) / A;
-    for (int64_t cur = lo; cur < hi;) {
-        const int64_t v = v_lo + cur / KS;
-        const int s0 = static_cast<int>(cur % KS);
-        const int s1 = static_cast<int>(min(static_cast<int64_t>(KS), s0 + hi - cur));
-        const int64_t ob = v / A;
+    const int first_ob = (v_lo + lo / KS) / A;
+    if (lane == 0) {
+        s.warp_first[warp] = first_ob;
+        s.warp_last[warp] = lo < hi ? (v_lo + (hi - 1) / KS) / A : -1;
+    }
+    for (int cur = lo; cur < hi;) {
+        const int v = v_lo + cur / KS;
+        const int s0 = cur % KS, s1 = min(KS, s0 + hi - cur);
+        const int ob = v / A;
         const int e = s.active[v - ob * A];
         const int64_t o = ob * 16 + g;
         const uint16_t* base = w2 + e * d.stride_w2;
@@ -519,7 +578,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         const uint16_t* r1 = o + 8 < d.H ? base + (o + 8) * d.ld_w2 : nullptr;
         const int n = __popcll(s.mask[e]), off = s.off[e];
         float acc[NTMAX][4];
-        mma_cols<T, VEC, NTMAX>(s, r0, r1, reinterpret_cast<const uint16_t*>(h), a.w.ip, false, off, n, s0, s1,
+        mma_cols<T, ROWS, NTMAX>(s, r0, r1, reinterpret_cast<const uint16_t*>(h), a.w.ip, false, off, n, s0, s1,
                                 static_cast<int>(d.I), lane, acc);
         float* tile = yt + (ob == first_ob ? 0 : ytile);
 #pragma unroll
@@ -542,65 +601,60 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     // Output blocks of this CTA: the sums of its warps, in order.
     T* y = static_cast<T*>(a.y);
     float* partial = reinterpret_cast<float*>(a.ws + a.w.partial);
-    if (v_lo < v_hi) {
-        const int64_t ob_lo = v_lo / A, ob_hi = (v_hi - 1) / A;
-        for (int64_t i = threadIdx.x; i < (ob_hi - ob_lo + 1) * ytile; i += MT) {
-            const int64_t ob = ob_lo + i / ytile;
-            const int el = static_cast<int>(i % ytile);
+    if (v_lo >= v_hi) return;
+    const int ob_lo = v_lo / A, ob_hi = (v_hi - 1) / A;
+    for (int i = threadIdx.x; i < (ob_hi - ob_lo + 1) * ytile; i += MT) {
+        const int ob = ob_lo + i / ytile, el = i % ytile;
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kMoeWarps; ++w)
+            if (ob >= s.warp_first[w] && ob <= s.warp_last[w])
+                sum += tiles[(w * 2 + (ob == s.warp_first[w] ? 0 : 1)) * ytile + el];
+        if (ob * A >= v_lo && (ob + 1) * A <= v_hi) {
+            const int o = ob * 16 + el / tok;
+            if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
+        } else {
+            partial[(cta * 2 + (ob == ob_lo ? 0 : 1)) * ytile + el] = sum;
+        }
+    }
+    // The first and the last block: whoever arrives last at a cut one joins it.
+    if (ob_lo * A >= v_lo && (ob_hi + 1) * A <= v_hi) return;  // neither is cut
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        const int ob = threadIdx.x == 0 ? ob_lo : ob_hi;
+        const bool whole = ob * A >= v_lo && (ob + 1) * A <= v_hi;
+        int last = 0;
+        if (!whole && (threadIdx.x == 0 || ob_hi != ob_lo)) {
+            // blocks are cut between neighbours, none of which is empty
+            const unsigned parts = ctas.owner(ob * A + A - 1) - ctas.owner(ob * A) + 1;
+            unsigned* ctr = reinterpret_cast<unsigned*>(a.ws + a.w.counters);
+            last = atomicAdd(ctr + ob, 1u) == parts - 1;
+            __threadfence();
+        }
+        s.last[threadIdx.x] = last;
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+        if (!s.last[k]) continue;
+        const int ob = k == 0 ? ob_lo : ob_hi;
+        const int c_lo = ctas.owner(ob * A), c_hi = ctas.owner(ob * A + A - 1);
+        for (int el = threadIdx.x; el < ytile; el += MT) {
             float sum = 0.0f;
-            for (int w = 0; w < kMoeWarps; ++w) {
-                const int64_t wlo = w * total / kMoeWarps, whi = (w + 1) * total / kMoeWarps;
-                if (wlo == whi) continue;
-                const int64_t f = (v_lo + wlo / KS) / A, l = (v_lo + (whi - 1) / KS) / A;
-                if (ob >= f && ob <= l) sum += tiles[(w * 2 + (ob == f ? 0 : 1)) * ytile + el];
-            }
-            if (ob * A >= v_lo && (ob + 1) * A <= v_hi) {
-                const int64_t o = ob * 16 + el / tok;
-                if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
-            } else {
-                partial[((cta * 2) + (ob == ob_lo ? 0 : 1)) * ytile + el] = sum;
-            }
-        }
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x < 2) {
-            // the first and the last block: whoever arrives last at a cut one joins it
-            const int64_t ob = threadIdx.x == 0 ? ob_lo : ob_hi;
-            s.last[threadIdx.x] = 0;
-            const bool whole = ob * A >= v_lo && (ob + 1) * A <= v_hi;
-            if (!whole && (threadIdx.x == 0 || ob_hi != ob_lo)) {
-                unsigned parts = 0;
-                for (int64_t c = ((ob * A + 1) * G - 1) / V; c <= ((ob * A + A) * G - 1) / V; ++c)
-                    parts += c * V / G < (c + 1) * V / G;
-                unsigned* ctr = reinterpret_cast<unsigned*>(a.ws + a.w.counters);
-                s.last[threadIdx.x] = atomicAdd(ctr + ob, 1u) == parts - 1;
-                __threadfence();
-            }
-        }
-        __syncthreads();
-        for (int k = 0; k < 2; ++k) {
-            if (!s.last[k]) continue;
-            const int64_t ob = k == 0 ? ob_lo : ob_hi;
-            const int64_t c_lo = ((ob * A + 1) * G - 1) / V, c_hi = ((ob * A + A) * G - 1) / V;
-            for (int el = threadIdx.x; el < ytile; el += MT) {
-                float sum = 0.0f;
-                for (int64_t c = c_lo; c <= c_hi; ++c) {
-                    const int64_t b = c * V / G, f = (c + 1) * V / G;
-                    if (b == f) continue;
-                    sum += __ldcg(partial + (c * 2 + (ob == b / A ? 0 : 1)) * ytile + el);
-                }
-                const int64_t o = ob * 16 + el / tok;
-                if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
-            }
+            // the first of them may have begun in an earlier block: then this one is its last
+            for (int c = c_lo; c <= c_hi; ++c)
+                sum += __ldcg(partial + (c * 2 + (c > c_lo || ctas.lo(c) >= ob * A ? 0 : 1)) * ytile + el);
+            const int o = ob * 16 + el / tok;
+            if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
         }
     }
 }
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-template <typename T, bool VEC, int NTMAX>
+template <typename T, int ROWS, int NTMAX>
 cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
-    auto k = moe_experts_kernel<T, VEC, NTMAX>;
+    auto k = moe_experts_kernel<T, ROWS, NTMAX>;
     const size_t smem = (sizeof(MoeShared) + 15) / 16 * 16 +
                         static_cast<size_t>(kMoeWarps) * 2 * 16 * 8 * NTMAX * sizeof(float);
     static std::atomic<unsigned char> ready[kMaxDevices];
@@ -625,7 +679,7 @@ cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <typename T, bool VEC>
+template <typename T, int ROWS>
 cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
     const int64_t units = a.d.E * ((a.d.T + 3) / 4);
     const unsigned blocks = static_cast<unsigned>((units + RT / 32 - 1) / (RT / 32));
@@ -639,18 +693,18 @@ cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
     cudaError_t ce = cudaGetLastError();
     if (ce != cudaSuccess) return ce;
     // groups of 8 tokens that one expert can be given: 1, 2, 4 or 8
-    if (a.d.T <= 8) return launch_experts<T, VEC, 1>(a, grid, st);
-    if (a.d.T <= 16) return launch_experts<T, VEC, 2>(a, grid, st);
-    if (a.d.T <= 32) return launch_experts<T, VEC, 4>(a, grid, st);
-    return launch_experts<T, VEC, 8>(a, grid, st);
+    if (a.d.T <= 8) return launch_experts<T, ROWS, 1>(a, grid, st);
+    if (a.d.T <= 16) return launch_experts<T, ROWS, 2>(a, grid, st);
+    if (a.d.T <= 32) return launch_experts<T, ROWS, 4>(a, grid, st);
+    return launch_experts<T, ROWS, 8>(a, grid, st);
 }
 
 }  // namespace
 
 MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid) {
     MoeWorkspace w{};
-    w.hp = round_up(d.H, 32);
-    w.ip = round_up(d.I, 32);
+    w.hp = round_up(d.H, 64);
+    w.ip = round_up(d.I, 64);
     w.bar = 0;
     w.counters = 256;
     w.logits = w.counters + round_up((d.H + 15) / 16 * 4, 256);
@@ -662,12 +716,15 @@ MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid) {
 }
 
 cudaError_t launch_moe(const MoeArgs& a, int grid, cudaStream_t st) {
-    const bool vec = reinterpret_cast<uintptr_t>(a.w1) % 16 == 0 && reinterpret_cast<uintptr_t>(a.w2) % 16 == 0 &&
-                     a.d.ld_w1 % 8 == 0 && a.d.ld_w2 % 8 == 0 && a.d.stride_w1 % 8 == 0 &&
-                     a.d.stride_w2 % 8 == 0 && a.d.H % 8 == 0 && a.d.I % 8 == 0;
-    if (a.d.dtype == GEMM_F16)
-        return vec ? launch_t<__half, true>(a, grid, st) : launch_t<__half, false>(a, grid, st);
-    return vec ? launch_t<__nv_bfloat16, true>(a, grid, st) : launch_t<__nv_bfloat16, false>(a, grid, st);
+    const auto all = [&](int64_t n) {  // every row on n elements, rows a multiple of n long
+        return reinterpret_cast<uintptr_t>(a.w1) % (2 * n) == 0 && reinterpret_cast<uintptr_t>(a.w2) % (2 * n) == 0 &&
+               a.d.ld_w1 % n == 0 && a.d.ld_w2 % n == 0 && a.d.stride_w1 % n == 0 && a.d.stride_w2 % n == 0 &&
+               a.d.H % n == 0 && a.d.I % n == 0;
+    };
+    const bool f16 = a.d.dtype == GEMM_F16;
+    if (all(16)) return f16 ? launch_t<__half, ROWS_32>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_32>(a, grid, st);
+    if (all(8)) return f16 ? launch_t<__half, ROWS_16>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_16>(a, grid, st);
+    return f16 ? launch_t<__half, ROWS_ANY>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_ANY>(a, grid, st);
 }
 
 }  // namespace g13

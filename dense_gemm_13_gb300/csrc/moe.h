@@ -13,7 +13,7 @@ constexpr int kMoeWarps = 16;
 // Byte offsets of the parts of a run's workspace.
 struct MoeWorkspace {
     int64_t bar, counters, logits, x, h, partial, bytes;
-    int64_t hp, ip;  // row lengths of the padded copies of x and of h (multiples of 32)
+    int64_t hp, ip;  // row lengths of the padded copies of x and of h (multiples of 64)
 };
 MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid);
 

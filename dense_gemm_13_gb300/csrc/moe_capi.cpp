@@ -53,6 +53,10 @@ int check_desc(gemm_moe_desc_t& d) {
     if (d.stride_w2 == 0) d.stride_w2 = d.H * d.ld_w2;
     if (d.stride_w1 < 0 || d.stride_w2 < 0) return GEMM_ERR_INVALID_ARG;
     if (d.stride_w1 > (int64_t(1) << 52) || d.stride_w2 > (int64_t(1) << 52)) return GEMM_ERR_UNSUPPORTED;
+    // the kernel counts pieces of 16 rows x 64 elements in 32 bits
+    if (d.E * ((rows + 15) / 16 + 1) * ((d.H + 63) / 64) >= (int64_t(1) << 30) ||
+        d.E * ((d.H + 15) / 16) * ((d.I + 63) / 64) >= (int64_t(1) << 30))
+        return GEMM_ERR_UNSUPPORTED;
     if (d.timeout_ms == 0) d.timeout_ms = 2000;
     return GEMM_OK;
 }

@@ -39,13 +39,14 @@ def test_invalid(lib, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(dtype=0), dict(T=65), dict(E=513), dict(E=512, top_k=33), dict(H=16385),
-                                dict(I=(1 << 20) + 1), dict(ldx=(1 << 40) + 1), dict(stride_w1=1 << 53)], ids=str)
+                                dict(I=(1 << 20) + 1),
+                                dict(T=64, E=512, top_k=32, H=16384, I=1 << 20), dict(ldx=(1 << 40) + 1), dict(stride_w1=1 << 53)], ids=str)
 def test_unsupported(lib, kw):
     assert plan(lib, **kw) == -2
 
 
 def test_valid_needs_a_device(lib):
-    for kw in (dict(), dict(T=0), dict(T=64, E=512, top_k=32, H=16384, I=1 << 20), dict(dtype=1, act=0, normalize=0)):
+    for kw in (dict(), dict(T=0), dict(T=64, E=512, top_k=32, H=16384, I=1 << 15), dict(dtype=1, act=0, normalize=0)):
         assert plan(lib, **kw) in (0, -7), kw
     assert lib.gemm_moe_plan(None, None) == -1
     h = ctypes.c_void_p()
