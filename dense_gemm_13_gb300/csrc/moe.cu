@@ -10,7 +10,7 @@
 // experts' weights once is the cost, so everything is laid out to keep those
 // loads in flight.  Two kernels:
 //
-//   router   z in FP32 (one warp per expert and four tokens); copies x into rows
+//   router   z in FP32 (a CTA per two experts and four tokens); copies x into rows
 //            padded to 64 elements; clears the counters of the second kernel
 //   experts  one CTA of 16 warps per SM, cooperative.  Every CTA works out the
 //            routing for itself from z (softmax, top-k by warp-wide maximum
@@ -19,22 +19,27 @@
 //            barrier between them:
 //     up     work units of 16 weight rows of a chosen expert (SwiGLU: 8 gate rows
 //            and their 8 up rows, so one thread holds both factors) x 64-element
-//            steps along H.  A CTA takes an equal share of the units and its warps
-//            equal shares of the units' steps; a unit cut between warps is joined
-//            through shared memory, in warp order.
-//     down   units (16 output columns, chosen expert), column block major, cut
-//            the same way; each warp adds weight * product to its own tile of the
-//            output in shared memory.  A block cut between CTAs leaves partial sums
-//            in the workspace, and the CTA that arrives last adds them in
-//            CTA order: the result does not depend on timing.
+//            steps along H.  A CTA takes an equal share of the units; its warps take
+//            whole units in turn, and equal shares of the steps of those left over,
+//            joined through shared memory in warp order.
+//     down   units (64 output columns, chosen expert), column block major; CTAs, and
+//            their teams of four warps, take equal shares of all units' steps; each
+//            warp adds weight * product to its own tile of the output in shared
+//            memory.  A block cut between CTAs leaves partial sums in the workspace,
+//            and the CTA that arrives last adds them in CTA order.
+//   No sum depends on timing.
+//
+// Weights go from global memory straight into registers, two batches ahead.  (Through a
+// ring in shared memory, cp.async per warp, they took 118 us where this takes 113 with 16 tokens,
+// and 600 against 445 with 64: the ring's space is what L1 keeps the tokens' values in.)  Rows
+// that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Products: mma.sync m16n8k16, weights as the 16 rows and a group of 8 tokens as
 // the columns.  The order of k within a step is free as long as both operands share
-// it, so a thread takes 32 consecutive bytes of a row (16 values: four MMAs' worth)
-// straight from global memory as its fragments; no shared memory, no barrier.
-// (tcgen05 would need the weights staged through shared memory, to do arithmetic
-// that is far from the bound.)  FP32 accumulation; h = act(...) is rounded to
-// the operands' 16-bit type, which the second product needs as its operand.
+// it, so a thread takes 16 consecutive values of a row (four MMAs' worth) as its
+// fragments.  (tcgen05 would need a 128-row tile and TMEM round trips, to do
+// arithmetic that is far from the bound.)  FP32 accumulation; h = act(...) is rounded
+// to the operands' 16-bit type, which the second product needs as its operand.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -50,6 +55,7 @@ namespace g13 {
 namespace {
 
 constexpr int MT = kMoeWarps * 32;   // threads per CTA
+constexpr int kMoeTeams = kMoeWarps / 4;  // down product: teams of four warps
 constexpr int RT = 256;              // threads per router CTA
 constexpr int kMaxDevices = 64;
 
@@ -60,10 +66,6 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
                  : "l"(p));
     return v;
 }
-
-// How the rows of a weight lie: all on 32 bytes with lengths a multiple of 16 elements, all
-// on 16 bytes with multiples of 8, or anyhow.
-enum Rows { ROWS_32 = 0, ROWS_16 = 1, ROWS_ANY = 2 };
 
 // Eight consecutive 16-bit values at p, of which the first n (0 to 8) exist; the rest
 // are zero.  VEC: p is 16-byte aligned and n is 0 or 8.  Else two aligned 16-byte loads
@@ -97,7 +99,12 @@ __device__ __forceinline__ uint4 ld_row8(const uint16_t* p, int n) {
     }
     return a;
 }
-// Sixteen of them.
+// How the rows of a weight lie: all on 32 bytes with lengths a multiple of 16 elements, all
+// on 16 bytes with multiples of 8, or anyhow.
+enum Rows { ROWS_32 = 0, ROWS_16 = 1, ROWS_ANY = 2 };
+
+// Sixteen values of an aligned row, n of which exist (n <= 0: none; else, with the row's
+// length, 8 or 16 at least).
 struct Row16 {
     uint32_t v[8];
 };
@@ -113,10 +120,39 @@ __device__ __forceinline__ Row16 ld_row16(const uint16_t* p, int n) {
                            "=r"(r.v[6]), "=r"(r.v[7])
                          : "l"(p));
     } else {
-        const uint4 a = ld_row8<ROWS == ROWS_16>(p, n), b = ld_row8<ROWS == ROWS_16>(p + 8, n - 8);
+        const uint4 a = ld_row8<true>(p, n), b = ld_row8<true>(p + 8, n - 8);
         r = Row16{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
     }
     return r;
+}
+
+// Sixteen values of a row that lies anyhow, as they are loaded: the three 16-byte granules
+// that hold them (two, where they are aligned), to be shifted when they are used.
+struct Raw16 {
+    uint32_t v[12];
+};
+// (`on` false: nothing is loaded and r keeps what it holds.  The predicate sits inside the
+// assembly: a branch, or zeros for the other case, cost the loop its schedule.)
+__device__ __forceinline__ void ld_raw16(Raw16& r, const char* p, bool on, unsigned o) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+            "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+            : "+r"(r.v[4 * i]), "+r"(r.v[4 * i + 1]), "+r"(r.v[4 * i + 2]), "+r"(r.v[4 * i + 3])
+            : "l"(p + 16 * i), "r"(static_cast<int>(on && (i < 2 || o != 0))));
+}
+// The values themselves; o: their offset in bytes in the first granule.
+__device__ __forceinline__ void use_raw16(const Raw16& r, unsigned o, uint32_t (&w)[8]) {
+    uint32_t v[12];
+#pragma unroll
+    for (int i = 0; i < 12; ++i) v[i] = r.v[i];
+#pragma unroll
+    for (int i = 0; i < 10; ++i) v[i] = o & 8 ? v[i + 2] : v[i];
+#pragma unroll
+    for (int i = 0; i < 9; ++i) v[i] = o & 4 ? v[i + 1] : v[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(v[i], v[i + 1], (o & 2) * 8);
 }
 
 // Equal shares of `total` for `parts` takers, the first ones one longer.
@@ -177,75 +213,94 @@ __device__ __forceinline__ float moe_act(int act, float y) {
 }
 
 // ------------------------------------------------------------------ router
+// A CTA takes two experts and four tokens; its threads take 8 elements of H each, so that
+// everything a CTA reads is in flight at once.
+constexpr int RE = 2, RTOK = 4;
+
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
+    griddep_launch();  // the experts' kernel may take its place; it waits for this one's results
+    __shared__ float sums[RT / 32][RE * RTOK];
     const gemm_moe_desc_t& d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int E = static_cast<int>(d.E), H = static_cast<int>(d.H), tok = static_cast<int>(d.T);
+    const int groups = (E + RE - 1) / RE;
+    const int e0 = static_cast<int>(blockIdx.x) % groups * RE, t0 = static_cast<int>(blockIdx.x) / groups * RTOK;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+    const uint16_t* r = static_cast<const uint16_t*>(a.router);
+    float acc[RE][RTOK] = {};
+    for (int k = threadIdx.x * 8; k < H; k += RT * 8) {
+        uint4 w[RE], v[RTOK];
+#pragma unroll
+        for (int e = 0; e < RE; ++e) w[e] = ld_row8<VEC>(r + (e0 + e) * d.ld_router + k, e0 + e < E ? H - k : 0);
+#pragma unroll
+        for (int t = 0; t < RTOK; ++t) v[t] = ld_row8<VEC>(x + (t0 + t) * d.ldx + k, t0 + t < tok ? H - k : 0);
+#pragma unroll
+        for (int e = 0; e < RE; ++e)
+#pragma unroll
+            for (int t = 0; t < RTOK; ++t) {
+                const uint32_t ww[4] = {w[e].x, w[e].y, w[e].z, w[e].w};
+                const uint32_t vv[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = unpack2<T>(ww[i]), g = unpack2<T>(vv[i]);
+                    acc[e][t] = fmaf(f.x, g.x, acc[e][t]);
+                    acc[e][t] = fmaf(f.y, g.y, acc[e][t]);
+                }
+            }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < RE * RTOK; ++i)
+            acc[i / RTOK][i % RTOK] += __shfl_xor_sync(0xFFFFFFFFu, acc[i / RTOK][i % RTOK], o);
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < RE * RTOK; ++i) sums[warp][i] = acc[i / RTOK][i % RTOK];
+    __syncthreads();
+    const int e = e0 + static_cast<int>(threadIdx.x) / RTOK, t = t0 + static_cast<int>(threadIdx.x) % RTOK;
+    if (threadIdx.x < RE * RTOK && e < E && t < tok) {
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < RT / 32; ++w) z += sums[w][threadIdx.x];
+        reinterpret_cast<float*>(a.ws + a.w.logits)[t * E + e] = z;
+    }
+
+    // the counters, the padded copy of x, and the padding of h (which the up product does not write)
     // (every count here stays below 2^31; 64-bit divisions would cost microseconds)
     const int tid = static_cast<int>(blockIdx.x) * RT + threadIdx.x;
     const int nthreads = static_cast<int>(gridDim.x) * RT;
-    // counters, padded x, and the padding of h (never written by the up product)
     unsigned* ctr = reinterpret_cast<unsigned*>(a.ws + a.w.bar);
     const int n_ctr = static_cast<int>((a.w.logits - a.w.bar) / 4);
     for (int i = tid; i < n_ctr; i += nthreads) ctr[i] = 0u;
-    const uint16_t* x = static_cast<const uint16_t*>(a.x);
     uint16_t* xp = reinterpret_cast<uint16_t*>(a.ws + a.w.x);
-    const int hp = static_cast<int>(a.w.hp), H = static_cast<int>(d.H);
-    for (int i = tid; i < static_cast<int>(d.T) * hp; i += nthreads) {
-        const int t = i / hp, k = i - t * hp;
-        xp[i] = k < H ? x[t * d.ldx + k] : uint16_t(0);
+    const int hp8 = static_cast<int>(a.w.hp / 8);
+    for (int i = tid; i < tok * hp8; i += nthreads) {
+        const int row = i / hp8, k = (i - row * hp8) * 8;
+        reinterpret_cast<uint4*>(xp)[i] = ld_row8<VEC>(x + row * d.ldx + k, H - k);
     }
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws + a.w.h);
     const int pad = static_cast<int>(a.w.ip - d.I);
     for (int i = tid; i < static_cast<int>(d.T * d.top_k) * pad; i += nthreads)
         h[static_cast<int64_t>(i / pad) * a.w.ip + d.I + i % pad] = 0;
-
-    // z: a warp takes one expert and four tokens
-    const int unit = static_cast<int>(blockIdx.x) * (RT / 32) + warp;
-    const int t0 = unit / static_cast<int>(d.E) * 4;
-    const int64_t e = unit % static_cast<int>(d.E);
-    if (t0 >= d.T) return;
-    const int nt = min(4, static_cast<int>(d.T) - t0);
-    const uint16_t* r = static_cast<const uint16_t*>(a.router) + e * d.ld_router;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = lane * 8; k < H; k += 256) {
-        const uint4 w = ld_row8<VEC>(r + k, H - k);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            if (t >= nt) break;
-            const uint4 v = ld_row8<VEC>(x + (t0 + t) * d.ldx + k, H - k);
-            const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2<T>(ww[i]), g = unpack2<T>(vv[i]);
-                acc[t] = fmaf(f.x, g.x, acc[t]);
-                acc[t] = fmaf(f.y, g.y, acc[t]);
-            }
-        }
-    }
-    float* z = reinterpret_cast<float*>(a.ws + a.w.logits);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xFFFFFFFFu, acc[t], o);
-        if (lane == 0 && t < nt) z[(t0 + t) * d.E + e] = acc[t];
-    }
 }
 
 // ------------------------------------------------------------------ experts
 struct MoeShared {
     unsigned long long mask[kMoeMaxExperts];  // tokens of each expert
-    int off[kMoeMaxExperts];                  // first slot of each expert
-    int active[kMoeMaxExperts];               // experts that have tokens
+    short off[kMoeMaxExperts];                // first slot of each expert
+    short active[kMoeMaxExperts];             // experts that have tokens
+    float slot_weight[kMoeMaxTokens * kMoeMaxTopK];
+    uint8_t slot_token[kMoeMaxTokens * kMoeMaxTopK];
     int n_active;
-    int warp_first[kMoeWarps], warp_last[kMoeWarps];  // output blocks that each warp adds to
+    int team_first[kMoeTeams], team_last[kMoeTeams];  // output blocks that each team adds to
     int last[2];                              // this CTA joins its first / last output block
     int gave_up;
-    int slot_token[kMoeMaxTokens * kMoeMaxTopK];
-    float slot_weight[kMoeMaxTokens * kMoeMaxTopK];
-    short pick[kMoeMaxTokens * kMoeMaxTopK];
-    float pick_weight[kMoeMaxTokens * kMoeMaxTopK];
+};
+// While the routing is worked out, each token's choice lies where the tiles of sums are later.
+struct MoePicks {
+    float weight[kMoeMaxTokens * kMoeMaxTopK];
+    short expert[kMoeMaxTokens * kMoeMaxTopK];
 };
 
 // Order-preserving key of a logit; NaN below every number, 0 is free for "not there".
@@ -255,86 +310,164 @@ __device__ __forceinline__ uint32_t order_key(float z) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// Top-k of one token by a warp, PER logits a lane: writes pick[] and pick_weight[] at t * top_k.
-template <int PER>
-__device__ __forceinline__ void route_token(const MoeArgs& a, MoeShared& s, int t, int lane) {
-    const int E = static_cast<int>(a.d.E), k = static_cast<int>(a.d.top_k);
-    const float* z = reinterpret_cast<const float*>(a.ws + a.w.logits) + static_cast<int64_t>(t) * E;
-    float v[PER];
-    uint32_t key[PER];
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = i * 32 + lane;
-        v[i] = e < E ? __ldcg(z + e) : 0.0f;
-        key[i] = e < E ? order_key(v[i]) : 0u;
-        if (e < E) top = fmaxf(top, v[i]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (i * 32 + lane < E) sum += expf(v[i] - top);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    float total = 0.0f;
-    for (int j = 0; j < k; ++j) {
-        uint32_t best = 0;
-        int at = 0;
-        float bv = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) best = key[i], at = i * 32 + lane, bv = v[i];
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-        const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, best == m ? static_cast<uint32_t>(at) : 0xFFFFu);
-        const float p = expf(__shfl_sync(0xFFFFFFFFu, bv, e & 31) - top) / sum;
-        total += p;
-        if (lane == 0) {
-            s.pick[t * k + j] = static_cast<short>(e);
-            s.pick_weight[t * k + j] = p;
-            atomicOr(&s.mask[e], 1ull << t);
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (static_cast<uint32_t>(i * 32 + lane) == e) key[i] = 0u;
-    }
-    __syncwarp();
-    if (a.d.normalize)
-        for (int j = lane; j < k; j += 32) s.pick_weight[t * k + j] /= total;
+// The logit that a key stands for (-0 as +0).
+__device__ __forceinline__ float key_value(uint32_t key) {
+    if (key == 1u) return __uint_as_float(0x7FFFFFFFu);
+    return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
 
-// One warp, steps [s0, s1) of 64 elements: acc[16 rows x 8 NT columns] += W x^T.  w0, w1: this
-// lane's two weight rows (null: zeros), xr: its token rows (padded), K valid elements of a weight row.
-template <typename T, int ROWS, int NT>
-__device__ __forceinline__ void mma_steps(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT],
-                                          int s0, int s1, int K, int t4, float (&acc)[NT][4]) {
-    constexpr int U = NT <= 2 ? 2 : 1;  // steps of loads in a batch (two batches in flight)
+// Top-k of N tokens t0, t0 + step, ... (those below `tok`) by a warp, PER logits a lane:
+// writes its picks at t * top_k.  A round finds the largest key, then
+// the lowest index that has it; the tokens' rounds are independent and overlap.
+template <int PER, int N>
+__device__ __forceinline__ void route_tokens(const MoeArgs& a, MoeShared& s, MoePicks& picks, int t0, int step, int tok, int lane) {
+    const int E = static_cast<int>(a.d.E), k = static_cast<int>(a.d.top_k);
+    const float* z = reinterpret_cast<const float*>(a.ws + a.w.logits);
+    uint32_t key[N][PER];
+    float top[N], sum[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * 32 + lane, t = min(t0 + n * step, tok - 1);
+            key[n][i] = e < E ? order_key(__ldcg(z + t * E + e)) : 0u;
+        }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) m = max(m, key[n][i]);
+        top[n] = key_value(__reduce_max_sync(0xFFFFFFFFu, m));  // (NaN only if every logit is NaN)
+        sum[n] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (i * 32 + lane < E) sum[n] += expf(key_value(key[n][i]) - top[n]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) sum[n] += __shfl_xor_sync(0xFFFFFFFFu, sum[n], o);
+    // lane j keeps pick j
+    uint32_t my_key[N], my_e[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) my_key[n] = 1u, my_e[n] = 0u;
+    for (int j = 0; j < k; ++j) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) m = max(m, key[n][i]);
+            m = __reduce_max_sync(0xFFFFFFFFu, m);
+            uint32_t e = 0xFFFFu;
+#pragma unroll
+            for (int i = PER - 1; i >= 0; --i)
+                if (key[n][i] == m) e = i * 32 + lane;
+            e = __reduce_min_sync(0xFFFFFFFFu, e);
+            if (lane == j) my_key[n] = m, my_e[n] = e;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i * 32 + lane == e) key[n][i] = 0u;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        float p = lane < k ? expf(key_value(my_key[n]) - top[n]) / sum[n] : 0.0f;
+        if (a.d.normalize) {
+            float total = p;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+            p /= total;
+        }
+        const int t = t0 + n * step;
+        if (lane < k && t < tok) {
+            picks.expert[t * k + lane] = static_cast<short>(my_e[n]);
+            picks.weight[t * k + lane] = p;
+            atomicOr(&s.mask[my_e[n]], 1ull << t);
+        }
+    }
+}
+
+// acc[16 rows x 8 NT columns] += 16 values of rows g and g + 8 (p, q) times the tokens' values at k
+// (from L1 or L2; asking for them a step ahead took registers from the weights and was slower).
+template <typename T, int NT, int NTMAX>
+__device__ __forceinline__ void mma_step(const uint32_t (&p)[8], const uint32_t (&q)[8],
+                                         const uint16_t* const (&xr)[NT], int k, float (&acc)[NTMAX][4]) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(xr[j] + k + 8 * i);
+            mma16816<T>(acc[j], p[4 * i], q[4 * i], p[4 * i + 1], q[4 * i + 1], v.x, v.y);
+            mma16816<T>(acc[j], p[4 * i + 2], q[4 * i + 2], p[4 * i + 3], q[4 * i + 3], v.z, v.w);
+        }
+}
+
+// One warp, steps [s0, s1) of a unit whose rows lie anyhow.  w0, w1: this lane's two weight
+// rows, xr: its token rows (padded), K elements of a weight row.
+template <typename T, int NT, int NTMAX>
+__device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT],
+                                          int s0, int s1, int K, int t4, float (&acc)[NTMAX][4]) {
+    const int sf = min(s1, K / 64);  // steps before it are whole
+    w0 += t4 * 16;
+    w1 += t4 * 16;
+    const unsigned o0 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(w0) & 15);
+    const unsigned o1 = static_cast<unsigned>(reinterpret_cast<uintptr_t>(w1) & 15);
+    const char* p0 = reinterpret_cast<const char*>(w0) - o0;
+    const char* p1 = reinterpret_cast<const char*>(w1) - o1;
+    Raw16 ra[2] = {}, rb[2] = {};
+    const auto load = [&](int b, int s) {
+        ld_raw16(ra[b], p0 + s * 128, s < sf, o0);
+        ld_raw16(rb[b], p1 + s * 128, s < sf, o1);
+    };
+    const auto compute = [&](int b, int s) {
+        if (s >= sf) return;
+        uint32_t p[8], q[8];
+        use_raw16(ra[b], o0, p);
+        use_raw16(rb[b], o1, q);
+        mma_step<T, NT, NTMAX>(p, q, xr, s * 64 + t4 * 16, acc);
+    };
+    load(0, s0);
+    for (int s = s0; s < sf; s += 2) {
+        load(1, s + 1);
+        compute(0, s);
+        load(0, s + 2);
+        compute(1, s + 1);
+    }
+    if (sf < s1) {  // the row's end
+        const int k = sf * 64, n = K - k - t4 * 16;
+        uint32_t p[8], q[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 a = ld_row8<false>(w0 + k + 8 * i, n - 8 * i);
+            const uint4 b = ld_row8<false>(w1 + k + 8 * i, n - 8 * i);
+            p[4 * i] = a.x, p[4 * i + 1] = a.y, p[4 * i + 2] = a.z, p[4 * i + 3] = a.w;
+            q[4 * i] = b.x, q[4 * i + 1] = b.y, q[4 * i + 2] = b.z, q[4 * i + 3] = b.w;
+        }
+        mma_step<T, NT, NTMAX>(p, q, xr, k + t4 * 16, acc);
+    }
+}
+
+// The same for rows that all lie on 16 bytes (ROWS_16) or 32 (ROWS_32) and are a multiple of
+// that long: two batches of U steps in flight in registers, 64 KB per SM and batch at U = 2.
+template <typename T, int ROWS, int NT, int NTMAX>
+__device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT],
+                                              int s0, int s1, int K, int t4, float (&acc)[NTMAX][4]) {
+    constexpr int U = NT <= 2 ? 2 : 1;
     Row16 wa[2][U], wb[2][U];
     const auto load = [&](int b, int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s + u) * 64 + t4 * 16;
             const int n = s + u < s1 ? K - k : 0;
-            wa[b][u] = ld_row16<ROWS>(w0 + k, w0 ? n : 0);
-            wb[b][u] = ld_row16<ROWS>(w1 + k, w1 ? n : 0);
+            wa[b][u] = ld_row16<ROWS>(w0 + k, n);
+            wb[b][u] = ld_row16<ROWS>(w1 + k, n);
         }
     };
     const auto compute = [&](int b, int s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s + u >= s1) break;
-            const int k = (s + u) * 64 + t4 * 16;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 xv = *reinterpret_cast<const uint4*>(xr[j] + k + 8 * i);
-                    const uint32_t *p = wa[b][u].v + 4 * i, *q = wb[b][u].v + 4 * i;
-                    mma16816<T>(acc[j], p[0], q[0], p[1], q[1], xv.x, xv.y);
-                    mma16816<T>(acc[j], p[2], q[2], p[3], q[3], xv.z, xv.w);
-                }
-            }
+            mma_step<T, NT, NTMAX>(wa[b][u].v, wb[b][u].v, xr, (s + u) * 64 + t4 * 16, acc);
         }
     };
     load(0, s0);
@@ -346,47 +479,45 @@ __device__ __forceinline__ void mma_steps(const uint16_t* w0, const uint16_t* w1
     }
 }
 
-// As mma_steps for n columns (1 to 8 NTMAX) of the slots at `off`: rows of `x` of xld elements, indexed
-// by token (by_token) or by slot.
-template <typename T, int ROWS, int NTMAX>
-__device__ __forceinline__ void mma_cols(const MoeShared& s, const uint16_t* w0, const uint16_t* w1,
-                                         const uint16_t* x, int64_t xld, bool by_token, int off, int n, int s0,
-                                         int s1, int K, int lane, float (&acc)[NTMAX][4]) {
-    const auto run = [&](auto tag) {
-        constexpr int NT = decltype(tag)::value;
-        const uint16_t* xr[NT];
-        float c[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            // columns past the last read its row: their sums are not used
-            const int slot = off + min(j * 8 + (lane >> 2), n - 1);
-            xr[j] = x + (by_token ? s.slot_token[slot] : slot) * xld;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) c[j][i] = 0.0f;
-        }
-        mma_steps<T, ROWS, NT>(w0, w1, xr, s0, s1, K, lane & 3, c);
-#pragma unroll
-        for (int j = 0; j < NTMAX; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = j < NT ? c[j < NT ? j : 0][i] : 0.0f;
-    };
+template <typename T, int ROWS, int NT, int NTMAX>
+__device__ __forceinline__ void steps(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT], int s0,
+                                      int s1, int K, int t4, float (&acc)[NTMAX][4]) {
+    if constexpr (ROWS == ROWS_ANY)
+        steps_any<T, NT, NTMAX>(w0, w1, xr, s0, s1, K, t4, acc);
+    else
+        steps_aligned<T, ROWS, NT, NTMAX>(w0, w1, xr, s0, s1, K, t4, acc);
+}
+
+// Runs f with the least of 1, 2, 4, 8 (at most NTMAX) groups of 8 columns that hold n.
+template <int NTMAX, typename F>
+__device__ __forceinline__ void with_groups(int n, const F& f) {
     if constexpr (NTMAX >= 8) {
-        if (n > 32) return run(std::integral_constant<int, 8>{});
+        if (n > 32) return f(std::integral_constant<int, 8>{});
     }
     if constexpr (NTMAX >= 4) {
-        if (n > 16) return run(std::integral_constant<int, 4>{});
+        if (n > 16) return f(std::integral_constant<int, 4>{});
     }
     if constexpr (NTMAX >= 2) {
-        if (n > 8) return run(std::integral_constant<int, 2>{});
+        if (n > 8) return f(std::integral_constant<int, 2>{});
     }
-    run(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 1>{});
 }
+
+template <int NTMAX>
+constexpr int kMoeTileBytes = 2 * kMoeWarps * 16 * 8 * NTMAX * 4;
+template <int NTMAX>
+constexpr int kMoeSmem = (static_cast<int>(sizeof(MoeShared)) + 127) / 128 * 128 +
+                         (kMoeTileBytes<NTMAX> > static_cast<int>(sizeof(MoePicks))
+                              ? kMoeTileBytes<NTMAX>
+                              : static_cast<int>(sizeof(MoePicks)));
 
 template <typename T, int ROWS, int NTMAX>
 __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
-    extern __shared__ __align__(16) char moe_smem[];
+    constexpr int TILE = 16 * 8 * NTMAX;  // a warp's tile of sums
+    extern __shared__ __align__(128) uint8_t moe_smem[];
     MoeShared& s = *reinterpret_cast<MoeShared*>(moe_smem);
-    float* tiles = reinterpret_cast<float*>(moe_smem + (sizeof(MoeShared) + 15) / 16 * 16);
+    float* tiles = reinterpret_cast<float*>(moe_smem + (sizeof(MoeShared) + 127) / 128 * 128);
+    MoePicks& picks = *reinterpret_cast<MoePicks*>(tiles);
     const gemm_moe_desc_t& d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tok = static_cast<int>(d.T), E = static_cast<int>(d.E), top_k = static_cast<int>(d.top_k);
@@ -395,12 +526,16 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     // ---------------------------------------------------------------- routing
     for (int e = threadIdx.x; e < E; e += MT) s.mask[e] = 0ull;
     if (threadIdx.x == 0) s.gave_up = 0;
+    griddep_wait();  // the router's results
     __syncthreads();
-    for (int t = warp; t < tok; t += kMoeWarps) {
-        if (E <= 64)
-            route_token<2>(a, s, t, lane);
-        else
-            route_token<kMoeMaxExperts / 32>(a, s, t, lane);
+    static_assert(kMoeMaxTopK <= 32, "a lane for each pick");
+    if (E > 64) {
+        for (int t = warp; t < tok; t += kMoeWarps)
+            route_tokens<kMoeMaxExperts / 32, 1>(a, s, picks, t, kMoeWarps, tok, lane);
+    } else if (tok > kMoeWarps) {
+        for (int t = warp; t < tok; t += 4 * kMoeWarps) route_tokens<2, 4>(a, s, picks, t, kMoeWarps, tok, lane);
+    } else if (warp < tok) {
+        route_tokens<2, 1>(a, s, picks, warp, kMoeWarps, tok, lane);
     }
     __syncthreads();
     if (warp == 0) {
@@ -415,8 +550,8 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                 const int up = __shfl_up_sync(0xFFFFFFFFu, pre, o);
                 if (lane >= o) pre += up;
             }
-            if (e < E) s.off[e] = slots + pre - c;
-            if (c > 0) s.active[n + __popc(has & ((1u << lane) - 1u))] = e;
+            if (e < E) s.off[e] = static_cast<short>(slots + pre - c);
+            if (c > 0) s.active[n + __popc(has & ((1u << lane) - 1u))] = static_cast<short>(e);
             n += __popc(has);
             slots += __shfl_sync(0xFFFFFFFFu, pre, 31);
         }
@@ -424,13 +559,13 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     }
     __syncthreads();
     for (int i = threadIdx.x; i < tok * top_k; i += MT) {
-        const int t = i / top_k, e = s.pick[i];
+        const int t = i / top_k, e = picks.expert[i];
         const int slot = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1ull));
-        s.slot_token[slot] = t;
-        s.slot_weight[slot] = s.pick_weight[i];
+        s.slot_token[slot] = static_cast<uint8_t>(t);
+        s.slot_weight[slot] = picks.weight[i];
         if (cta == 0) {
             if (a.ids) a.ids[i] = e;
-            if (a.weights) a.weights[i] = s.pick_weight[i];
+            if (a.weights) a.weights[i] = picks.weight[i];
         }
     }
     __syncthreads();
@@ -440,7 +575,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     const uint16_t* xp = reinterpret_cast<const uint16_t*>(a.ws + a.w.x);
     T* h = reinterpret_cast<T*>(a.ws + a.w.h);
     const int g = lane >> 2, t4 = lane & 3;
-    float* my_tile = tiles + warp * 2 * (16 * 8 * NTMAX);
+    float* my_tile = tiles + warp * 2 * TILE;
     {
         const bool gated = d.act == GEMM_MOE_SWIGLU;
         const int per = gated ? 8 : 16;  // values of h per unit
@@ -448,8 +583,11 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         const int UB = static_cast<int>((d.I + per - 1) / per), U = UB * A;
         const int KS = static_cast<int>(a.w.hp / 64);
         const Share ctas(U, G);
-        const int u_lo = ctas.lo(cta), total = (ctas.lo(cta + 1) - u_lo) * KS;
-        const Share warps(total, kMoeWarps);
+        const int u_lo = ctas.lo(cta), n_u = ctas.lo(cta + 1) - u_lo;
+        // Whole units go to the warps in turn: all warps walk H together and find the tokens'
+        // values in L1 (each x row comes from L2 once per 16 units).  The units left over are cut.
+        const int whole = n_u / kMoeWarps, u_cut = u_lo + whole * kMoeWarps;
+        const Share warps(n_u % kMoeWarps * KS, kMoeWarps);
         const int lo = warps.lo(warp), hi = warps.lo(warp + 1);
         const uint16_t* w1 = static_cast<const uint16_t*>(a.w1);
         const auto finish = [&](int u, const float (&acc)[NTMAX][4]) {
@@ -473,77 +611,100 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                 }
             }
         };
-        for (int cur = lo; cur < hi;) {
-            const int u = u_lo + cur / KS;
-            const int s0 = cur % KS, s1 = min(KS, s0 + hi - cur);
+        // Position in the warp's stream of steps -> unit, step.
+        const auto at = [&](int pos, int& u, int& s0) {
+            if (pos < whole * KS) {
+                u = u_lo + pos / KS * kMoeWarps + warp;
+                s0 = pos % KS;
+            } else {
+                const int q = pos - whole * KS + lo;
+                u = u_cut + q / KS;
+                s0 = q % KS;
+            }
+        };
+        // Row r of a unit (rows past the last read it again: their sums are not used).
+        const auto row = [&](int u, int r) {
+            const int64_t i = u % UB * per + (gated ? r & 7 : r);
+            return w1 + s.active[u / UB] * d.stride_w1 +
+                   (min(i, d.I - 1) + (gated && r >= 8 ? d.I : 0)) * d.ld_w1;
+        };
+        const int total = whole * KS + hi - lo;
+        int u = 0, s0 = 0, s1 = 0;
+        for (int pos = 0; pos < total; pos += s1 - s0) {
+            float acc[NTMAX][4] = {};
+            at(pos, u, s0);
+            s1 = min(KS, s0 + total - pos);
             const int e = s.active[u / UB];
-            const int64_t i = u % UB * per + g;
-            const uint16_t* base = w1 + e * d.stride_w1;
-            const uint16_t* r0 = i < d.I ? base + i * d.ld_w1 : nullptr;
-            const uint16_t* r1 = gated ? (r0 ? r0 + d.I * d.ld_w1 : nullptr)
-                                       : (i + 8 < d.I ? base + (i + 8) * d.ld_w1 : nullptr);
-            float acc[NTMAX][4];
-            mma_cols<T, ROWS, NTMAX>(s, r0, r1, xp, a.w.hp, true, s.off[e], __popcll(s.mask[e]), s0, s1,
-                                    static_cast<int>(d.H), lane, acc);
+            const int n = __popcll(s.mask[e]), off = s.off[e];
+            with_groups<NTMAX>(n, [&](auto tag) {
+                constexpr int NT = decltype(tag)::value;
+                const uint16_t* xr[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j)  // columns past the last read its row: their sums are not used
+                    xr[j] = xp + s.slot_token[off + min(j * 8 + g, n - 1)] * a.w.hp;
+                steps<T, ROWS, NT, NTMAX>(row(u, g), row(u, g + 8), xr, s0, s1, static_cast<int>(d.H), t4, acc);
+            });
             if (s0 == 0 && s1 == KS) {
                 finish(u, acc);
             } else {
-                // a unit that began in an earlier warp goes to slot 0, one that goes on in a later
-                // warp to slot 1
-                float* slot = my_tile + (s0 > 0 ? 0 : 16 * 8 * NTMAX);
+                // a unit that began in an earlier warp goes to this warp's first tile, one that
+                // goes on in a later one to its second
+                float* tile = my_tile + (s0 > 0 ? 0 : TILE);
 #pragma unroll
                 for (int j = 0; j < NTMAX; ++j)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) slot[(j * 4 + c) * 32 + lane] = acc[j][c];
+                    for (int c = 0; c < 4; ++c) tile[(j * 4 + c) * 32 + lane] = acc[j][c];
             }
-            cur += s1 - s0;
         }
         __syncthreads();
-        // the warp in which a cut unit begins joins it
-        if (lo < hi) {
-            const int u = (hi - 1) / KS;
-            if (u * KS >= lo && (u + 1) * KS > hi) {
-                float acc[NTMAX][4];
+        if (total > 0 && s0 == 0 && s1 < KS) {
+            // this warp's last unit goes on in later ones: their sums, in order
+            float acc[NTMAX][4];
+#pragma unroll
+            for (int j = 0; j < NTMAX; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[j][c] = my_tile[TILE + (j * 4 + c) * 32 + lane];
+            for (int w = warp + 1; w < kMoeWarps; ++w) {
+                if (warps.lo(w) >= (u - u_cut + 1) * KS || warps.lo(w) == warps.lo(w + 1)) break;
+                const float* tile = tiles + w * 2 * TILE;
 #pragma unroll
                 for (int j = 0; j < NTMAX; ++j)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        acc[j][c] = my_tile[16 * 8 * NTMAX + (j * 4 + c) * 32 + lane];
-                for (int w = warp + 1; w < kMoeWarps; ++w) {
-                    if (warps.lo(w) >= (u + 1) * KS || warps.lo(w) == warps.lo(w + 1)) break;
-                    const float* slot = tiles + w * 2 * (16 * 8 * NTMAX);
-#pragma unroll
-                    for (int j = 0; j < NTMAX; ++j)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) acc[j][c] += slot[(j * 4 + c) * 32 + lane];
-                }
-                finish(u_lo + u, acc);
+                    for (int c = 0; c < 4; ++c) acc[j][c] += tile[(j * 4 + c) * 32 + lane];
             }
+            finish(u, acc);
         }
     }
 
     // ---------------------------------------------------------------- grid barrier
-    // This warp's share of the down product is known already: its first weights are
-    // asked into L2 while the barrier is waited for.
-    const int OB = static_cast<int>((d.H + 15) / 16), V = OB * A;
+    // Four warps side by side take 16 of a block's columns each and walk the same steps
+    // (sharing h in L1); four such teams share the CTA's steps.  The weights do not depend on
+    // h: the first of them are asked into L2 before the barrier.
+    const int sub = warp & 3, team = warp >> 2;
+    const int OB = static_cast<int>((d.H + kMoeBlock - 1) / kMoeBlock);
     const int KS = static_cast<int>(a.w.ip / 64);
-    const Share ctas(V, G);
-    const int v_lo = ctas.lo(cta), v_hi = ctas.lo(cta + 1);
-    const Share warps((v_hi - v_lo) * KS, kMoeWarps);
-    const int lo = warps.lo(warp), hi = warps.lo(warp + 1);
+    const int block = A * KS;  // steps of an output block
+    const Share ctas(OB * block, G);
+    const int c_lo = ctas.lo(cta), c_hi = ctas.lo(cta + 1);
+    const Share teams(c_hi - c_lo, kMoeTeams);
+    const int lo = c_lo + teams.lo(team), hi = c_lo + teams.lo(team + 1);
     const uint16_t* w2 = static_cast<const uint16_t*>(a.w2);
+    const auto row = [&](int v, int r) {
+        const int64_t o = v / A * kMoeBlock + sub * 16 + r;
+        return w2 + s.active[v % A] * d.stride_w2 + min(o, d.H - 1) * d.ld_w2;
+    };
     if (lo < hi) {
-        const int v = v_lo + lo / KS, k = (lo % KS + t4) * 64;
-        const int64_t o = v / A * 16 + g;
-        const uint16_t* p = w2 + s.active[v % A] * d.stride_w2 + o * d.ld_w2 + k;
-        if (k < d.I && o < d.H) prefetch_l2(p);
-        if (k < d.I && o + 8 < d.H) prefetch_l2(p + 8 * d.ld_w2);
+        const int k = (lo % KS + t4) * 64;  // four steps of the warp's rows
+        if (k < d.I) {
+            prefetch_l2(row(lo / KS, g) + k);
+            prefetch_l2(row(lo / KS, g + 8) + k);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0) {
         unsigned* bar = reinterpret_cast<unsigned*>(a.ws + a.w.bar);
-        __threadfence();
-        if (!((d.flags & GEMM_FLAG_TEST_STALL) && cta == 0)) atomicAdd(bar, 1u);
+        if (!((d.flags & GEMM_FLAG_TEST_STALL) && cta == 0))
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
         const uint64_t t0 = globaltimer_ns();
         while (ld_acquire_gpu(bar) < static_cast<unsigned>(G)) {
             if (globaltimer_ns() - t0 > a.timeout_ns) {
@@ -552,35 +713,45 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                 break;
             }
         }
-        __threadfence();
     }
     __syncthreads();
     if (s.gave_up) return;
 
     // ---------------------------------------------------------------- down
-    const int ytile = 16 * tok;  // [row][token]
-    float* yt = tiles + warp * 2 * ytile;
-    for (int i = lane; i < 2 * ytile; i += 32) yt[i] = 0.0f;
+    const int ytile = 16 * tok;  // [row][token] of a warp
+    float* yt = my_tile;
+    float* flushed = reinterpret_cast<float*>(a.ws + a.w.flushed) + ((cta * kMoeTeams + team) * kMoeBlock + sub * 16) * tok;
+    for (int i = lane; i < ytile; i += 32) yt[i] = 0.0f;
     __syncwarp();
-    const int first_ob = (v_lo + lo / KS) / A;
-    if (lane == 0) {
-        s.warp_first[warp] = first_ob;
-        s.warp_last[warp] = lo < hi ? (v_lo + (hi - 1) / KS) / A : -1;
+    const int first_ob = lo / block;
+    if (sub == 0 && lane == 0) {
+        s.team_first[team] = first_ob;
+        s.team_last[team] = lo < hi ? (hi - 1) / block : -1;
     }
-    for (int cur = lo; cur < hi;) {
-        const int v = v_lo + cur / KS;
+    for (int cur = lo, ob_now = first_ob; cur < hi;) {
+        const int v = cur / KS;
         const int s0 = cur % KS, s1 = min(KS, s0 + hi - cur);
         const int ob = v / A;
         const int e = s.active[v - ob * A];
-        const int64_t o = ob * 16 + g;
-        const uint16_t* base = w2 + e * d.stride_w2;
-        const uint16_t* r0 = o < d.H ? base + o * d.ld_w2 : nullptr;
-        const uint16_t* r1 = o + 8 < d.H ? base + (o + 8) * d.ld_w2 : nullptr;
         const int n = __popcll(s.mask[e]), off = s.off[e];
-        float acc[NTMAX][4];
-        mma_cols<T, ROWS, NTMAX>(s, r0, r1, reinterpret_cast<const uint16_t*>(h), a.w.ip, false, off, n, s0, s1,
-                                static_cast<int>(d.I), lane, acc);
-        float* tile = yt + (ob == first_ob ? 0 : ytile);
+        if (ob != ob_now) {
+            // a team enters a second block at most: its sums of the first go to the workspace
+            for (int i = lane; i < ytile; i += 32) {
+                flushed[i] = yt[i];
+                yt[i] = 0.0f;
+            }
+            ob_now = ob;
+            __syncwarp();
+        }
+        float acc[NTMAX][4] = {};
+        with_groups<NTMAX>(n, [&](auto tag) {
+            constexpr int NT = decltype(tag)::value;
+            const uint16_t* xr[NT];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                xr[j] = reinterpret_cast<const uint16_t*>(h) + (off + min(j * 8 + g, n - 1)) * a.w.ip;
+            steps<T, ROWS, NT, NTMAX>(row(v, g), row(v, g + 8), xr, s0, s1, static_cast<int>(d.I), t4, acc);
+        });
 #pragma unroll
         for (int j = 0; j < NTMAX; ++j) {
 #pragma unroll
@@ -589,8 +760,8 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                 if (col >= n) continue;
                 const int t = s.slot_token[off + col];
                 const float wgt = s.slot_weight[off + col];
-                tile[g * tok + t] += wgt * acc[j][c];
-                tile[(g + 8) * tok + t] += wgt * acc[j][2 + c];
+                yt[g * tok + t] += wgt * acc[j][c];
+                yt[(g + 8) * tok + t] += wgt * acc[j][2 + c];
             }
         }
         __syncwarp();
@@ -601,33 +772,38 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     // Output blocks of this CTA: the sums of its warps, in order.
     T* y = static_cast<T*>(a.y);
     float* partial = reinterpret_cast<float*>(a.ws + a.w.partial);
-    if (v_lo >= v_hi) return;
-    const int ob_lo = v_lo / A, ob_hi = (v_hi - 1) / A;
-    for (int i = threadIdx.x; i < (ob_hi - ob_lo + 1) * ytile; i += MT) {
-        const int ob = ob_lo + i / ytile, el = i % ytile;
+    if (c_lo >= c_hi) return;
+    const int ob_lo = c_lo / block, ob_hi = (c_hi - 1) / block;
+    const int ysize = kMoeBlock * tok;
+    const float* all_flushed = reinterpret_cast<const float*>(a.ws + a.w.flushed) + cta * kMoeTeams * ysize;
+    for (int i = threadIdx.x; i < (ob_hi - ob_lo + 1) * ysize; i += MT) {
+        const int ob = ob_lo + i / ysize, el = i % ysize;
+        const int el_sub = el / ytile, el_in = el - el_sub * ytile;
         float sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kMoeWarps; ++w)
-            if (ob >= s.warp_first[w] && ob <= s.warp_last[w])
-                sum += tiles[(w * 2 + (ob == s.warp_first[w] ? 0 : 1)) * ytile + el];
-        if (ob * A >= v_lo && (ob + 1) * A <= v_hi) {
-            const int o = ob * 16 + el / tok;
+        for (int w = 0; w < kMoeTeams; ++w)
+            if (ob == s.team_last[w])
+                sum += tiles[(w * 4 + el_sub) * 2 * TILE + el_in];
+            else if (ob == s.team_first[w] && ob < s.team_last[w])
+                sum += all_flushed[w * ysize + el];
+        if (ob * block >= c_lo && (ob + 1) * block <= c_hi) {
+            const int o = ob * kMoeBlock + el / tok;
             if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
         } else {
-            partial[(cta * 2 + (ob == ob_lo ? 0 : 1)) * ytile + el] = sum;
+            partial[(cta * 2 + (ob == ob_lo ? 0 : 1)) * ysize + el] = sum;
         }
     }
     // The first and the last block: whoever arrives last at a cut one joins it.
-    if (ob_lo * A >= v_lo && (ob_hi + 1) * A <= v_hi) return;  // neither is cut
+    if (ob_lo * block >= c_lo && (ob_hi + 1) * block <= c_hi) return;  // neither is cut
     __threadfence();
     __syncthreads();
     if (threadIdx.x < 2) {
         const int ob = threadIdx.x == 0 ? ob_lo : ob_hi;
-        const bool whole = ob * A >= v_lo && (ob + 1) * A <= v_hi;
+        const bool whole = ob * block >= c_lo && (ob + 1) * block <= c_hi;
         int last = 0;
         if (!whole && (threadIdx.x == 0 || ob_hi != ob_lo)) {
             // blocks are cut between neighbours, none of which is empty
-            const unsigned parts = ctas.owner(ob * A + A - 1) - ctas.owner(ob * A) + 1;
+            const unsigned parts = ctas.owner((ob + 1) * block - 1) - ctas.owner(ob * block) + 1;
             unsigned* ctr = reinterpret_cast<unsigned*>(a.ws + a.w.counters);
             last = atomicAdd(ctr + ob, 1u) == parts - 1;
             __threadfence();
@@ -638,13 +814,13 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     for (int k = 0; k < 2; ++k) {
         if (!s.last[k]) continue;
         const int ob = k == 0 ? ob_lo : ob_hi;
-        const int c_lo = ctas.owner(ob * A), c_hi = ctas.owner(ob * A + A - 1);
-        for (int el = threadIdx.x; el < ytile; el += MT) {
+        const int from = ctas.owner(ob * block), to = ctas.owner((ob + 1) * block - 1);
+        for (int el = threadIdx.x; el < ysize; el += MT) {
             float sum = 0.0f;
             // the first of them may have begun in an earlier block: then this one is its last
-            for (int c = c_lo; c <= c_hi; ++c)
-                sum += __ldcg(partial + (c * 2 + (c > c_lo || ctas.lo(c) >= ob * A ? 0 : 1)) * ytile + el);
-            const int o = ob * 16 + el / tok;
+            for (int c = from; c <= to; ++c)
+                sum += __ldcg(partial + (c * 2 + (c > from || ctas.lo(c) >= ob * block ? 0 : 1)) * ysize + el);
+            const int o = ob * kMoeBlock + el / tok;
             if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
         }
     }
@@ -655,14 +831,14 @@ int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 template <typename T, int ROWS, int NTMAX>
 cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
     auto k = moe_experts_kernel<T, ROWS, NTMAX>;
-    const size_t smem = (sizeof(MoeShared) + 15) / 16 * 16 +
-                        static_cast<size_t>(kMoeWarps) * 2 * 16 * 8 * NTMAX * sizeof(float);
+    constexpr int smem = kMoeSmem<NTMAX>;
+    static_assert(smem <= 232448, "shared memory");
     static std::atomic<unsigned char> ready[kMaxDevices];
     int dev = 0;
     cudaError_t ce = cudaGetDevice(&dev);
     if (ce != cudaSuccess) return ce;
     if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_acquire)) {
-        ce = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        ce = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (ce != cudaSuccess) return ce;
         if (dev < kMaxDevices) ready[dev].store(1, std::memory_order_release);
     }
@@ -671,18 +847,19 @@ cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
     cfg.blockDim = dim3(MT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeCooperative;  // the grid barrier needs every CTA resident
     at[0].val.cooperative = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
 template <typename T, int ROWS>
 cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
-    const int64_t units = a.d.E * ((a.d.T + 3) / 4);
-    const unsigned blocks = static_cast<unsigned>((units + RT / 32 - 1) / (RT / 32));
+    const unsigned blocks = static_cast<unsigned>((a.d.E + RE - 1) / RE * ((a.d.T + RTOK - 1) / RTOK));
     // the router's rows and x take vector loads on their own terms
     const bool rvec = reinterpret_cast<uintptr_t>(a.router) % 16 == 0 && a.d.ld_router % 8 == 0 &&
                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.d.ldx % 8 == 0 && a.d.H % 8 == 0;
@@ -707,11 +884,12 @@ MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid) {
     w.ip = round_up(d.I, 64);
     w.bar = 0;
     w.counters = 256;
-    w.logits = w.counters + round_up((d.H + 15) / 16 * 4, 256);
+    w.logits = w.counters + round_up((d.H + kMoeBlock - 1) / kMoeBlock * 4, 256);
     w.x = w.logits + round_up(d.T * d.E * 4, 256);
     w.h = w.x + round_up(d.T * w.hp * 2, 256);
     w.partial = w.h + round_up(d.T * d.top_k * w.ip * 2, 256);
-    w.bytes = w.partial + static_cast<int64_t>(grid) * 2 * 16 * d.T * 4;
+    w.flushed = w.partial + static_cast<int64_t>(grid) * 2 * kMoeBlock * d.T * 4;
+    w.bytes = w.flushed + static_cast<int64_t>(grid) * kMoeTeams * kMoeBlock * d.T * 4;
     return w;
 }
 

@@ -9,10 +9,11 @@ namespace g13 {
 
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32, kMoeMaxH = 16384;
 constexpr int kMoeWarps = 16;
+constexpr int kMoeBlock = 64;  // output columns that the down product's CTAs share or cut
 
 // Byte offsets of the parts of a run's workspace.
 struct MoeWorkspace {
-    int64_t bar, counters, logits, x, h, partial, bytes;
+    int64_t bar, counters, logits, x, h, partial, flushed, bytes;
     int64_t hp, ip;  // row lengths of the padded copies of x and of h (multiples of 64)
 };
 MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid);

@@ -89,9 +89,9 @@ int gemm_moe_plan(const gemm_moe_desc_t* desc, gemm_moe_plan_t* out_plan) {
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || major != 10 ||
         minor != 3)
         return GEMM_ERR_NO_DEVICE;
-    // a warp's share of the down product touches at most two output blocks: with
-    // 16 warps a CTA, that needs fewer than 15 blocks per CTA
-    if ((d.H + 15) / 16 > int64_t(15) * sms) return GEMM_ERR_UNSUPPORTED;
+    // a warp's share of the down product (a quarter of a CTA's) touches at most two output
+    // blocks: that needs fewer than four blocks per CTA
+    if ((d.H + kMoeBlock - 1) / kMoeBlock > int64_t(3) * sms) return GEMM_ERR_UNSUPPORTED;
     gemm_moe_plan_s* pl = new (std::nothrow) gemm_moe_plan_s();
     if (!pl) return GEMM_ERR_OUT_OF_MEMORY;
     pl->d = d;
