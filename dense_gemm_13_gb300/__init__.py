@@ -163,7 +163,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
 
 
 def lib() -> ctypes.CDLL:
-    return load()
+    return _lib or load()
 
 
 def _strerror(status: int) -> str:
@@ -421,60 +421,74 @@ def _refuse(what: str, why: str):
     raise e
 
 
-class _On:
-    """Makes a tensor's device the current one for a call, where it is not."""
+class _Torch:
+    """torch, its dtypes by name and its current device and stream, looked up once (a call of a few
+    microseconds on the GPU waits for every attribute lookup on the host)."""
 
-    __slots__ = ("guard",)
+    torch = None
 
-    def __init__(self, torch, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    def __init__(self):
+        import torch
+        self.torch = torch
+        self.name = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+        self.dtype = {v: k for k, v in self.name.items()}
+        self.u8, self.f32, self.i32 = torch.uint8, torch.float32, torch.int32
+        self.empty = torch.empty
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.raw_stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+        self.device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
 
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+_torch_cache: list = []
 
 
-def _stream(torch, stream) -> int:
+def _t() -> _Torch:
+    if not _torch_cache:
+        _torch_cache.append(_Torch())
+    return _torch_cache[0]
+
+
+def _stream(t: _Torch, index: int, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return t.raw_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-_TDT: dict = {}
+def _rows_ok(x) -> bool:
+    """Row-major, rows not overlapping: what a C entry point takes as [rows][ld]."""
+    rows, cols = x.shape
+    return (cols <= 1 or x.stride(1) == 1) and (rows <= 1 or x.stride(0) >= cols)
 
 
-def _tdt():
-    """torch dtype -> name of a gemm_dtype_t."""
-    if not _TDT:
-        import torch
-        _TDT.update({torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"})
-    return _TDT
+def _ld(x) -> int:
+    rows, cols = x.shape
+    return x.stride(0) if rows > 1 else max(cols, 1)
 
 
-def _check_fp4(what: str, t: Fp4Tensor, torch):
-    if t.format not in FP4_FORMATS:
-        _refuse(what, f"unknown format {t.format!r}")
-    L = lib()
-    nrow, nsc = t.rows * L.gemm_fp4_row_bytes(t.cols), L.gemm_fp4_scales_bytes(FP4_FORMATS[t.format], t.rows, t.cols)
-    for name, a, n in (("codes", t.codes, nrow), ("scales", t.scales, nsc)):
-        if a.dtype != torch.uint8 or not a.is_cuda or not a.is_contiguous() or a.numel() != n:
-            _refuse(what, f"{name}: {n} contiguous bytes on the GPU are wanted")
-    _check_scale(what, t.tensor_scale, t.format, t.codes.device, torch)
-    if t.scales.device != t.codes.device:
-        _refuse(what, "codes and scales are on different devices")
-
-
-def _check_scale(what: str, g, format: str, device, torch):
-    if g is None:
-        return
+def _check_scale(t: _Torch, what: str, g, format: str, device):
     if format != "nvfp4":
         _refuse(what, "only nvfp4 has a scale of the whole tensor")
-    if g.dtype != torch.float32 or g.numel() != 1 or g.device != device:
+    if g.dtype is not t.f32 or g.numel() != 1 or g.device != device:
         _refuse(what, "tensor_scale: one FP32 value on the matrix's device is wanted")
+
+
+def _check_fp4(t: _Torch, what: str, q: Fp4Tensor):
+    """Refuses arrays that are shorter than the kernels read; returns their device."""
+    codes, scales = q.codes, q.scales
+    block = 32 if q.format == "mxfp4" else 16 if q.format == "nvfp4" else _refuse(what, f"unknown format {q.format!r}")
+    rows, cols = q.rows, q.cols
+    if rows < 0 or cols < 0:
+        _refuse(what, "negative sizes")
+    tiles = (rows + 127) // 128 * ((cols + 4 * block - 1) // (4 * block))
+    for name, a, n in (("codes", codes, rows * ((cols + 31) // 32 * 16)), ("scales", scales, tiles * 512)):
+        if a.dtype is not t.u8 or not a.is_cuda or a.numel() != n or not a.is_contiguous():
+            _refuse(what, f"{name}: {n} contiguous bytes on the GPU are wanted")
+    dev = codes.device
+    if scales.device != dev:
+        _refuse(what, "codes and scales are on different devices")
+    if q.tensor_scale is not None:
+        _check_scale(t, what, q.tensor_scale, q.format, dev)
+    return dev
 
 
 def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp4Tensor:
@@ -483,51 +497,53 @@ def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp
     tensor_scale ("nvfp4"): a positive FP32 CUDA tensor of one value; max|x| / (6 * 448) uses the
     whole range.  None means 1.
     """
-    import torch
-    what = "fp4_quantize"
-    if format not in FP4_FORMATS:
+    what, t = "fp4_quantize", _t()
+    f = FP4_FORMATS.get(format)
+    if f is None:
         _refuse(what, f"unknown format {format!r}")
-    dt = _tdt().get(x.dtype)
+    dt = t.name.get(x.dtype)
     if dt is None or x.dim() != 2 or not x.is_cuda:
         _refuse(what, "a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
-    rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1 or rows > 1 and x.stride(0) < cols:
+    dev = x.device
+    if dev.index != t.device_index():
+        with t.torch.cuda.device(dev):
+            return fp4_quantize(x, format, tensor_scale, stream)
+    if not _rows_ok(x):
         x = x.contiguous()
-    _check_scale(what, tensor_scale, format, x.device, torch)
-    L, f = lib(), FP4_FORMATS[format]
-    with _On(torch, x.device):
-        codes = torch.empty((rows, L.gemm_fp4_row_bytes(cols)), dtype=torch.uint8, device=x.device)
-        scales = torch.empty(L.gemm_fp4_scales_bytes(f, rows, cols), dtype=torch.uint8, device=x.device)
-        rc = L.gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), max(x.stride(0) if rows > 1 else cols, 1),
-                                 _ptr(tensor_scale), codes.data_ptr(), scales.data_ptr(), _stream(torch, stream))
+    if tensor_scale is not None:
+        _check_scale(t, what, tensor_scale, format, dev)
+    rows, cols = x.shape
+    block4 = 128 if f == 0 else 64
+    codes = t.empty((rows, (cols + 31) // 32 * 16), dtype=t.u8, device=dev)
+    scales = t.empty((rows + 127) // 128 * ((cols + block4 - 1) // block4) * 512, dtype=t.u8, device=dev)
+    rc = lib().gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), _ld(x), _ptr(tensor_scale),
+                                 codes.data_ptr(), scales.data_ptr(), _stream(t, dev.index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return Fp4Tensor(codes, scales, rows, cols, format, tensor_scale)
 
 
-def fp4_dequantize(t: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
+def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
     """The values of a 4-bit matrix as a tensor of `dtype` (gemm_fp4_dequantize)."""
-    import torch
-    what = "fp4_dequantize"
-    if dtype not in DTYPES:
+    what, t = "fp4_dequantize", _t()
+    code = DTYPES.get(dtype)
+    if code is None:
         _refuse(what, f"unknown dtype {dtype!r}")
-    _check_fp4(what, t, torch)
-    dev = t.codes.device
-    with _On(torch, dev):
-        if out is None:
-            out = torch.empty((t.rows, t.cols), dtype=getattr(torch, _TORCH_NAMES[dtype]), device=dev)
-        elif (tuple(out.shape) != (t.rows, t.cols) or _tdt().get(out.dtype) != dtype or out.device != dev
-              or (t.cols > 1 and out.stride(1) != 1) or (t.rows > 1 and out.stride(0) < t.cols)):
-            _refuse(what, "out: a row-major tensor of the matrix's shape, dtype and device is wanted")
-        rc = lib().gemm_fp4_dequantize(FP4_FORMATS[t.format], DTYPES[dtype], t.rows, t.cols, t.codes.data_ptr(),
-                                       t.scales.data_ptr(), _ptr(t.tensor_scale), out.data_ptr(),
-                                       max(out.stride(0) if t.rows > 1 else t.cols, 1), _stream(torch, stream))
+    dev = _check_fp4(t, what, q)
+    if dev.index != t.device_index():
+        with t.torch.cuda.device(dev):
+            return fp4_dequantize(q, dtype, out, stream)
+    if out is None:
+        out = t.empty((q.rows, q.cols), dtype=t.dtype[dtype], device=dev)
+    elif (tuple(out.shape) != (q.rows, q.cols) or t.name.get(out.dtype) != dtype or out.device != dev
+          or not _rows_ok(out)):
+        _refuse(what, "out: a row-major tensor of the matrix's shape, dtype and device is wanted")
+    rc = lib().gemm_fp4_dequantize(FP4_FORMATS[q.format], code, q.rows, q.cols, q.codes.data_ptr(),
+                                   q.scales.data_ptr(), _ptr(q.tensor_scale), out.data_ptr(), _ld(out),
+                                   _stream(t, dev.index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return out
-
-
-_TORCH_NAMES = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}
 
 
 class Fp4Plan:
@@ -562,13 +578,13 @@ def gemm_fp4_plan(format: str, M: int, N: int, K: int, ldc: int, epilogue: Epilo
 def gemm_fp4_run(plan: Fp4Plan, A: Fp4Tensor, B: Fp4Tensor, C, bias=None, residual=None, alpha: float = 1.0,
                  stream=None) -> int:
     """Enqueue C = epilogue(A @ B.T) of a plan on `stream` (default: torch's current stream)."""
-    import torch
     if (A.rows, A.cols, B.rows, B.cols) != (plan.M, plan.K, plan.N, plan.K) or A.format != plan.format \
             or B.format != plan.format:
         _refuse("gemm_fp4_run", "the operands do not fit the plan")
-    rc = lib().gemm_fp4_run(plan.handle, _ptr(A.codes), _ptr(A.scales), _ptr(A.tensor_scale), _ptr(B.codes),
-                            _ptr(B.scales), _ptr(B.tensor_scale), _ptr(C), _ptr(bias), _ptr(residual),
-                            float(alpha), _stream(torch, stream))
+    t = _t()
+    rc = lib().gemm_fp4_run(plan.handle, A.codes.data_ptr(), A.scales.data_ptr(), _ptr(A.tensor_scale),
+                            B.codes.data_ptr(), B.scales.data_ptr(), _ptr(B.tensor_scale), _ptr(C), _ptr(bias),
+                            _ptr(residual), alpha, _stream(t, t.device_index(), stream))
     if rc != 0:
         raise GemmError(rc, "gemm_fp4_run")
     return rc
@@ -599,35 +615,39 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     bias: FP32 [N]; residual: FP32 [M, N].  Plans are created once per (shape, format, strides,
     epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.
     """
-    import torch
-    what = "fp4_matmul"
-    _check_fp4(what, A, torch)
-    _check_fp4(what, B, torch)
-    dev = A.codes.device
-    if A.format != B.format or A.cols != B.cols or B.codes.device != dev:
+    what, t = "fp4_matmul", _t()
+    dev = _check_fp4(t, what, A)
+    devB = _check_fp4(t, what, B)
+    if A.format != B.format or A.cols != B.cols or devB != dev:
         _refuse(what, "A and B need the same format, K and device")
+    if dev.index != t.device_index():
+        with t.torch.cuda.device(dev):
+            return fp4_matmul(A, B, alpha=alpha, bias=bias, act=act, residual=residual, beta=beta,
+                              out_dtype=out_dtype, out=out, stream=stream)
     if out_dtype not in DTYPES or act not in ("none", "gelu", "relu"):
         _refuse(what, "out_dtype: f32, f16 or bf16; act: none, gelu or relu")
     M, N, K = A.rows, B.rows, A.cols
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (N,) or bias.device != dev
+    if bias is not None and (bias.dtype is not t.f32 or tuple(bias.shape) != (N,) or bias.device != dev
                              or not bias.is_contiguous()):
         _refuse(what, "bias: contiguous FP32 [N] on the operands' device is wanted")
-    for name, t, dt in (("residual", residual, "f32"), ("out", out, out_dtype)):
-        if t is not None and (tuple(t.shape) != (M, N) or _tdt().get(t.dtype) != dt or t.device != dev
-                              or (N > 1 and t.stride(1) != 1) or (M > 1 and t.stride(0) < N)):
+    for name, x, dt in (("residual", residual, "f32"), ("out", out, out_dtype)):
+        if x is not None and (tuple(x.shape) != (M, N) or t.name.get(x.dtype) != dt or x.device != dev
+                              or not _rows_ok(x)):
             _refuse(what, f"{name}: a row-major {dt} [M, N] on the operands' device is wanted")
-    with _On(torch, dev):
-        if out is None:
-            out = torch.empty((M, N), dtype=getattr(torch, _TORCH_NAMES[out_dtype]), device=dev)
-        ldc = max(out.stride(0) if M > 1 else N, 1)
-        ldr = 0 if residual is None else max(residual.stride(0) if M > 1 else N, 1)
-        key = (A.format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, residual is not None, beta, dev.index)
-        pl = _fp4_plans.get(key)
-        if pl is None:
-            ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
-                          residual=residual is not None, beta=beta, ldr=ldr)
-            pl = _fp4_plans[key] = gemm_fp4_plan(A.format, M, N, K, ldc, ep)
-        gemm_fp4_run(pl, A, B, out, bias, residual, alpha, stream)
+    if out is None:
+        out = t.empty((M, N), dtype=t.dtype[out_dtype], device=dev)
+    ldc, ldr = _ld(out), 0 if residual is None else _ld(residual)
+    key = (A.format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, dev.index)
+    pl = _fp4_plans.get(key)
+    if pl is None:
+        ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
+                      residual=residual is not None, beta=beta, ldr=ldr)
+        pl = _fp4_plans[key] = gemm_fp4_plan(A.format, M, N, K, ldc, ep)
+    rc = lib().gemm_fp4_run(pl.handle, A.codes.data_ptr(), A.scales.data_ptr(), _ptr(A.tensor_scale),
+                            B.codes.data_ptr(), B.scales.data_ptr(), _ptr(B.tensor_scale), out.data_ptr(),
+                            _ptr(bias), _ptr(residual), alpha, _stream(t, dev.index, stream))
+    if rc != 0:
+        raise GemmError(rc, what)
     return out
 
 
@@ -668,9 +688,9 @@ def gemm_moe_plan(dtype: str, T: int, E: int, top_k: int, H: int, I: int, act: s
 def gemm_moe_run(plan: MoePlan, X, router, W1, W2, Y, workspace, expert_ids=None, expert_weights=None,
                  stream=None) -> int:
     """Enqueue one layer on `stream` (default: torch's current stream); raises on error."""
-    import torch
+    t = _t()
     rc = lib().gemm_moe_run(plan.handle, _ptr(X), _ptr(router), _ptr(W1), _ptr(W2), _ptr(Y), _ptr(expert_ids),
-                            _ptr(expert_weights), _ptr(workspace), _stream(torch, stream))
+                            _ptr(expert_weights), _ptr(workspace), _stream(t, t.device_index(), stream))
     if rc != 0:
         raise GemmError(rc, "gemm_moe_run")
     return rc
@@ -694,45 +714,52 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     shape, strides and device; every call has a workspace of its own from torch's allocator, on the
     stream that it runs on.
     """
-    import torch
-    what = "moe_layer"
-    dt = _tdt().get(x.dtype)
+    what, t = "moe_layer", _t()
+    dt = t.name.get(x.dtype)
     if dt not in ("f16", "bf16") or act not in MOE_ACTS:
         _refuse(what, "FP16 or BF16 tensors and act gelu, relu or swiglu are wanted")
     if x.dim() != 2 or router.dim() != 2 or w1.dim() != 3 or w2.dim() != 3:
         _refuse(what, "x [T, H], router [E, H], w1 [E, I or 2I, H], w2 [E, H, I] are wanted")
-    (T, H), E, I, dev = x.shape, router.shape[0], w2.shape[2], x.device
+    (T, H), (E, I), dev, dtype = x.shape, (router.shape[0], w2.shape[2]), x.device, x.dtype
     rows = 2 * I if act == "swiglu" else I
-    if tuple(router.shape) != (E, H) or tuple(w1.shape) != (E, rows, H) or tuple(w2.shape) != (E, H, I):
+    if router.shape != (E, H) or w1.shape != (E, rows, H) or w2.shape != (E, H, I):
         _refuse(what, "the shapes of x, router, w1 and w2 do not fit one another")
-    for name, t in (("x", x), ("router", router), ("w1", w1), ("w2", w2), ("out", out)):
-        if t is not None and (t.dtype != x.dtype or t.device != dev or not t.is_cuda or
-                              (t.shape[-1] > 1 and t.stride(-1) != 1) or
-                              (t.shape[-2] > 1 and t.stride(-2) < t.shape[-1]) or
-                              (t.dim() == 3 and t.shape[0] > 1 and t.stride(0) == 0)):
-            _refuse(what, f"{name}: x's dtype and device and rows that are contiguous and not shared are wanted")
-    if out is not None and tuple(out.shape) != (T, H):
+    if out is not None and out.shape != (T, H):
         _refuse(what, "out: [T, H] is wanted")
-    with _On(torch, dev):
-        if out is None:
-            out = torch.empty((T, H), dtype=x.dtype, device=dev)
-        ldx, ldr, ldy = (t.stride(0) if t.shape[0] > 1 else H for t in (x, router, out))
-        ld1, ld2 = w1.stride(1) if rows > 1 else H, w2.stride(1) if H > 1 else I
-        st1, st2 = (w1.stride(0), w2.stride(0)) if E > 1 else (rows * ld1, H * ld2)
-        key = (dt, T, E, top_k, H, I, act, normalize, ldx, ldr, ld1, st1, ld2, st2, ldy, dev.index)
-        pl = _moe_plans.get(key)
-        if pl is None:
-            pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=ldx, ld_router=ldr,
-                                                 ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=ldy)
-        ids = wts = None
-        if return_routing:
-            ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-            wts = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-        if stream is None:
-            ws = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
-        else:  # the workspace belongs to the stream that uses it
-            s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-            with torch.cuda.stream(s):
-                ws = torch.empty(pl.workspace_bytes, dtype=torch.uint8, device=dev)
-        gemm_moe_run(pl, x, router, w1, w2, out, ws, ids, wts, stream)
+    if not x.is_cuda or router.device != dev or w1.device != dev or w2.device != dev or router.dtype is not dtype \
+            or w1.dtype is not dtype or w2.dtype is not dtype \
+            or (out is not None and (out.device != dev or out.dtype is not dtype)):
+        _refuse(what, "tensors of x's dtype on x's device, a GPU, are wanted")
+    if dev.index != t.device_index():
+        with t.torch.cuda.device(dev):
+            return moe_layer(x, router, w1, w2, top_k, act=act, normalize=normalize, out=out,
+                             return_routing=return_routing, stream=stream)
+    if out is None:
+        out = t.empty((T, H), dtype=dtype, device=dev)
+    (st1, ld1, c1), (st2, ld2, c2) = w1.stride(), w2.stride()
+    if not (_rows_ok(x) and _rows_ok(router) and _rows_ok(out)) or (H > 1 and c1 != 1) or (I > 1 and c2 != 1) \
+            or (rows > 1 and ld1 < H) or (H > 1 and ld2 < I) or (E > 1 and (st1 == 0 or st2 == 0)):
+        _refuse(what, "rows that are contiguous and not shared are wanted")
+    # strides that no element uses may be anything
+    ld1, ld2 = ld1 if rows > 1 else H, ld2 if H > 1 else I
+    st1, st2 = (st1, st2) if E > 1 else (rows * ld1, H * ld2)
+    key = (dt, T, E, top_k, H, I, act, normalize, _ld(x), _ld(router), ld1, st1, ld2, st2, _ld(out), dev.index)
+    pl = _moe_plans.get(key)
+    if pl is None:
+        pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=_ld(x), ld_router=_ld(router),
+                                             ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=_ld(out))
+    ids = wts = None
+    if return_routing:
+        ids = t.empty((T, top_k), dtype=t.i32, device=dev)
+        wts = t.empty((T, top_k), dtype=t.f32, device=dev)
+    if stream is None:
+        ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
+    else:  # the workspace belongs to the stream that uses it
+        s = t.torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
+        with t.torch.cuda.stream(s):
+            ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
+    rc = lib().gemm_moe_run(pl.handle, x.data_ptr(), router.data_ptr(), w1.data_ptr(), w2.data_ptr(), out.data_ptr(),
+                            _ptr(ids), _ptr(wts), ws.data_ptr(), _stream(t, dev.index, stream))
+    if rc != 0:
+        raise GemmError(rc, what)
     return (out, ids, wts) if return_routing else out

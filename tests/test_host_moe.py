@@ -68,8 +68,8 @@ def test_python_refusals(lib):
     for bad, why in (((z(2, 8, dt=torch.float32),) + good[1:], "FP16 or BF16"),
                      ((z(8),) + good[1:], "are wanted"),
                      (good[:2] + (z(4, 6, 8), good[3]), "do not fit"),
-                     ((good[0], z(4, 8, dt=torch.float16)) + good[2:], "dtype and device"),
-                     (good, "dtype and device")):  # on the CPU
+                     ((good[0], z(4, 8, dt=torch.float16)) + good[2:], "dtype on x's device"),
+                     (good, "dtype on x's device")):  # on the CPU
         with pytest.raises(g13.GemmError, match=why):
             g13.moe_layer(*bad, 2)
     with pytest.raises(g13.GemmError, match="act"):
