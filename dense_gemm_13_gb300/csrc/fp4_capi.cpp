@@ -119,7 +119,8 @@ int gemm_fp4_plan(gemm_fp4_format_t format, int64_t M, int64_t N, int64_t K, int
     if (rc != GEMM_OK) return rc;
     if (p.epi.b_layout != GEMM_B_NK || p.epi.act == GEMM_ACT_SOFTMAX) return GEMM_ERR_UNSUPPORTED;
     if (!sizes_ok(M, K) || !sizes_ok(N, K)) return GEMM_ERR_UNSUPPORTED;
-    // tile counts are 32-bit in the kernel
+    // tile counts, and byte offsets along a row of C, are 32-bit in the kernel
+    if (N >= (int64_t(1) << 30)) return GEMM_ERR_UNSUPPORTED;
     if (M > 0 && N > 0 && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 27))
         return GEMM_ERR_UNSUPPORTED;
 

@@ -20,8 +20,8 @@
 //   warp 1      tcgen05.cp of the stage's scale tiles to TMEM (in order with the
 //               MMAs that read them), then the MMAs, by one elected lane; commits
 //               free ring stages (empty[s]) and finish accumulators (tfull)
-//   others      epilogue: four warps, one TMEM lane quarter each, or eight, two
-//               to a quarter, taking its 16-column chunks in turn
+//   others      epilogue: four warps, one TMEM lane quarter each, or 16, four to a
+//               quarter, taking its 16-column chunks in turn
 //
 // Large products run on CTA pairs (tcgen05 cta_group::2): 256 weight rows x 256
 // tokens, each CTA holding its own 128 weight rows and half of the tokens, so
@@ -55,7 +55,7 @@ enum F4Mode { F4_ONE = 0, F4_SPLIT = 1, F4_PAIR = 2 };
 template <int BN, int FMT, int MODE>
 struct F4Layout {
     static constexpr bool PAIR = MODE == F4_PAIR;
-    static constexpr int EW = BN >= 128 ? 8 : 4;            // epilogue warps
+    static constexpr int EW = BN >= 128 ? 16 : 4;           // epilogue warps
     static constexpr int THREADS = 64 + 32 * EW;
     static constexpr int TILE_W = PAIR ? 2 * FW : FW;       // weight rows of a tile
     static constexpr int X_ROWS = PAIR ? BN / 2 : BN;       // tokens that this CTA loads
@@ -170,20 +170,26 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-// alpha' acc + bias -> act -> + beta R -> cast of CN columns of C rows m0..: one element per lane and row.
+// alpha' acc + bias -> act -> + beta R -> cast of C rows m0 .. m0 + CN - 1 (those below M) at this lane's
+// column n: the rows' addresses are the warp's, a lane adds its own offset (32 bits: N stays below 2^30).
 template <int CN>
-__device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float bias, int64_t m0,
-                                         int64_t n, float* v) {
-    if (n >= e.N) return;
+__device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float bias, int64_t m0, uint32_t n,
+                                         float (&v)[CN]) {
+    static_assert(CN % 2 == 0, "pairs");
+    if (n >= static_cast<uint32_t>(e.N)) return;
     const int live = static_cast<int>(min(static_cast<int64_t>(CN), e.M - m0));
     float r[CN];
     if (e.R) {
+        const char* p = reinterpret_cast<const char*>(e.R + m0 * e.ldr);
 #pragma unroll
-        for (int j = 0; j < CN; ++j)
-            r[j] = j < live ? __ldg(e.R + (m0 + j) * e.ldr + n) : 0.0f;
+        for (int j = 0; j < CN; ++j) {
+            r[j] = j < live ? __ldg(reinterpret_cast<const float*>(p + n * 4u)) : 0.0f;
+            p += e.ldr * 4;
+        }
     }
+    const uint64_t a2 = f2_pack(alpha, alpha), b2 = f2_pack(bias, bias);
 #pragma unroll
-    for (int j = 0; j < CN; ++j) v[j] = fmaf(v[j], alpha, bias);
+    for (int j = 0; j < CN; j += 2) f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), a2, b2), v[j], v[j + 1]);
     if (e.act == GEMM_ACT_GELU_ERF) {
 #pragma unroll
         for (int j = 0; j < CN; j += 2) gelu2_as7126(v[j], v[j + 1]);
@@ -195,21 +201,40 @@ __device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float 
 #pragma unroll
         for (int j = 0; j < CN; ++j) v[j] = fmaf(e.beta, r[j], v[j]);
     }
-    if (e.out_dtype == GEMM_F32) {
-        float* c = static_cast<float*>(e.C) + m0 * e.ldc + n;
+    const int64_t size = e.out_dtype == GEMM_F32 ? 4 : 2;
+    char* c = static_cast<char*>(e.C) + m0 * e.ldc * size;
+    const int64_t step = e.ldc * size;
+    if (size == 4) {
+        if (live == CN) {
 #pragma unroll
-        for (int j = 0; j < CN; ++j)
-            if (j < live) c[j * e.ldc] = v[j];
-    } else if (e.out_dtype == GEMM_BF16) {
-        __nv_bfloat16* c = static_cast<__nv_bfloat16*>(e.C) + m0 * e.ldc + n;
+            for (int j = 0; j < CN; ++j, c += step) *reinterpret_cast<float*>(c + n * 4u) = v[j];
+        } else {
 #pragma unroll
-        for (int j = 0; j < CN; ++j)
-            if (j < live) c[j * e.ldc] = __float2bfloat16_rn(v[j]);
+            for (int j = 0; j < CN; ++j, c += step)
+                if (j < live) *reinterpret_cast<float*>(c + n * 4u) = v[j];
+        }
     } else {
-        __half* c = static_cast<__half*>(e.C) + m0 * e.ldc + n;
+        uint32_t w[CN / 2];  // two values in 16 bits each
 #pragma unroll
-        for (int j = 0; j < CN; ++j)
-            if (j < live) c[j * e.ldc] = __float2half_rn(v[j]);
+        for (int j = 0; j < CN; j += 2) {
+            if (e.out_dtype == GEMM_BF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[j], v[j + 1]);
+                w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(v[j], v[j + 1]);
+                w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+        if (live == CN) {
+#pragma unroll
+            for (int j = 0; j < CN; ++j, c += step)
+                *reinterpret_cast<uint16_t*>(c + n * 2u) = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+        } else {
+#pragma unroll
+            for (int j = 0; j < CN; ++j, c += step)
+                if (j < live)
+                    *reinterpret_cast<uint16_t*>(c + n * 2u) = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+        }
     }
 }
 
@@ -483,8 +508,8 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
         for (int64_t t = t_begin; t < t_end; t += t_step, ++lt) {
             int64_t mt, nt;
             f4_tile(args, t, mt, nt);
-            const int64_t n = nt * L::TILE_W + (PAIR ? rank * FW : 0) + q * 32 + lane;
-            const float bias = args.e.bias && n < args.N ? __ldg(args.e.bias + n) : 0.0f;
+            const uint32_t n = static_cast<uint32_t>(nt * L::TILE_W + (PAIR ? rank * FW : 0)) + q * 32 + lane;
+            const float bias = args.e.bias && n < static_cast<uint32_t>(args.N) ? __ldg(args.e.bias + n) : 0.0f;
             const int buf = lt & 1;
             if (!mbar_wait_warp(smem_u32(&tfull[buf]), static_cast<uint32_t>(lt >> 1) & 1u, abort_flag,
                                 args.status, tmo))
@@ -537,15 +562,14 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
             int64_t mt, nt;
             f4_tile(args, t_begin, mt, nt);
             const int q = warp & 3, h = (warp - 2) >> 2;
-            const int64_t n = nt * FW + q * 32 + lane;
+            const uint32_t n = static_cast<uint32_t>(nt * FW) + q * 32 + lane;
             float alpha = args.e.alpha;
             if (args.gw) alpha *= __ldg(args.gw);
             if (args.gx) alpha *= __ldg(args.gx);
-            const float bias = args.e.bias && n < args.N ? __ldg(args.e.bias + n) : 0.0f;
+            const float bias = args.e.bias && n < static_cast<uint32_t>(args.N) ? __ldg(args.e.bias + n) : 0.0f;
             const int cols = static_cast<int>(min(static_cast<int64_t>(BN), args.M - mt * BN));
             const uint32_t part = smem_u32(smem) + (q * 32 + lane) * 16;
-            // four columns at a time in turn over the cluster's warps of this quarter, up to
-            // eight reads of other CTAs in flight
+            // four columns at a time in turn over the cluster's warps of this quarter
             const int step = 4 * static_cast<int>(splits) * (L::EW / 4);
             for (int c = 4 * (static_cast<int>(rank) * (L::EW / 4) + h); c < cols; c += step) {
                 float4 p[8];
@@ -682,7 +706,7 @@ int launch_fp4_gemm(const Fp4Config& c, int fmt, const Fp4Operand& A, const Fp4O
 
 // Tokens per tile: the narrowest of 16, 32, 64 that holds them all; above 64,
 // CTA pairs on 256 x 256 tiles once they fill the GPU, else 128.  K is split
-// over a cluster while the tiles leave SMs idle.
+// over a cluster of 2, 4 or 8 while the tiles leave SMs idle.
 Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
     Fp4Config c{};
     if (M <= 16)
@@ -696,10 +720,8 @@ Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
     c.splits = 1;
     const int64_t tiles = ((N + FW - 1) / FW) * ((M + c.bn - 1) / c.bn);
     const int64_t kbs = (K + F_KB - 1) / F_KB;
-    if (c.bn <= 128 && tiles > 0 && kbs > 1) {
-        const int64_t most = std::min<int64_t>(8, kbs);
-        c.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, num_sms / tiles)));
-    }
+    if (c.bn <= 128 && tiles > 0)
+        while (c.splits < 8 && 2 * c.splits <= kbs && tiles * c.splits * 2 <= num_sms) c.splits *= 2;
     return c;
 }
 
