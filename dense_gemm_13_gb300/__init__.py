@@ -465,30 +465,30 @@ def _ld(x) -> int:
     return x.stride(0) if rows > 1 else max(cols, 1)
 
 
-def _check_scale(t: _Torch, what: str, g, format: str, device):
+def _check_scale(t: _Torch, what: str, g, format: str, index: int):
     if format != "nvfp4":
         _refuse(what, "only nvfp4 has a scale of the whole tensor")
-    if g.dtype is not t.f32 or g.numel() != 1 or g.device != device:
+    if g.dtype is not t.f32 or g.numel() != 1 or g.get_device() != index:
         _refuse(what, "tensor_scale: one FP32 value on the matrix's device is wanted")
 
 
-def _check_fp4(t: _Torch, what: str, q: Fp4Tensor):
-    """Refuses arrays that are shorter than the kernels read; returns their device."""
-    codes, scales = q.codes, q.scales
-    block = 32 if q.format == "mxfp4" else 16 if q.format == "nvfp4" else _refuse(what, f"unknown format {q.format!r}")
-    rows, cols = q.rows, q.cols
-    if rows < 0 or cols < 0:
-        _refuse(what, "negative sizes")
-    tiles = (rows + 127) // 128 * ((cols + 4 * block - 1) // (4 * block))
-    for name, a, n in (("codes", codes, rows * ((cols + 31) // 32 * 16)), ("scales", scales, tiles * 512)):
-        if a.dtype is not t.u8 or not a.is_cuda or a.numel() != n or not a.is_contiguous():
-            _refuse(what, f"{name}: {n} contiguous bytes on the GPU are wanted")
-    dev = codes.device
-    if scales.device != dev:
-        _refuse(what, "codes and scales are on different devices")
+def _check_fp4(t: _Torch, what: str, q: Fp4Tensor) -> int:
+    """Refuses arrays that are shorter than the kernels read; returns their device's index."""
+    codes, scales, format, rows, cols = q.codes, q.scales, q.format, q.rows, q.cols
+    if format not in FP4_FORMATS:
+        _refuse(what, f"unknown format {format!r}")
+    per = 128 if format == "mxfp4" else 64  # elements of four blocks
+    n_codes = rows * ((cols + 31) // 32 * 16)
+    n_scales = (rows + 127) // 128 * ((cols + per - 1) // per) * 512
+    index, u8 = codes.get_device(), t.u8
+    if (index < 0 or scales.get_device() != index or codes.dtype is not u8 or scales.dtype is not u8 or rows < 0
+            or cols < 0 or codes.numel() != n_codes or scales.numel() != n_scales or not codes.is_contiguous()
+            or not scales.is_contiguous()):
+        _refuse(what, f"{rows} x {cols} in {format}: codes ({n_codes} bytes) and scales ({n_scales} bytes), contiguous "
+                      "uint8 on the GPU, are wanted")
     if q.tensor_scale is not None:
-        _check_scale(t, what, q.tensor_scale, q.format, dev)
-    return dev
+        _check_scale(t, what, q.tensor_scale, format, index)
+    return index
 
 
 def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp4Tensor:
@@ -501,23 +501,27 @@ def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp
     f = FP4_FORMATS.get(format)
     if f is None:
         _refuse(what, f"unknown format {format!r}")
-    dt = t.name.get(x.dtype)
-    if dt is None or x.dim() != 2 or not x.is_cuda:
+    dt, index = t.name.get(x.dtype), x.get_device()
+    if dt is None or x.dim() != 2 or index < 0:
         _refuse(what, "a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
-    dev = x.device
-    if dev.index != t.device_index():
-        with t.torch.cuda.device(dev):
+    if index != t.device_index():
+        with t.torch.cuda.device(index):
             return fp4_quantize(x, format, tensor_scale, stream)
-    if not _rows_ok(x):
-        x = x.contiguous()
     if tensor_scale is not None:
-        _check_scale(t, what, tensor_scale, format, dev)
+        _check_scale(t, what, tensor_scale, format, index)
     rows, cols = x.shape
-    block4 = 128 if f == 0 else 64
+    ld, step = x.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
+        x = x.contiguous()
+        ld = cols
+    if rows <= 1 or ld < 1:
+        ld = max(cols, 1)
+    per = 128 if f == 0 else 64  # elements of four blocks
+    dev = x.device
     codes = t.empty((rows, (cols + 31) // 32 * 16), dtype=t.u8, device=dev)
-    scales = t.empty((rows + 127) // 128 * ((cols + block4 - 1) // block4) * 512, dtype=t.u8, device=dev)
-    rc = lib().gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), _ld(x), _ptr(tensor_scale),
-                                 codes.data_ptr(), scales.data_ptr(), _stream(t, dev.index, stream))
+    scales = t.empty((rows + 127) // 128 * ((cols + per - 1) // per) * 512, dtype=t.u8, device=dev)
+    rc = lib().gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), ld, _ptr(tensor_scale),
+                                 codes.data_ptr(), scales.data_ptr(), _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return Fp4Tensor(codes, scales, rows, cols, format, tensor_scale)
@@ -529,18 +533,18 @@ def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
     code = DTYPES.get(dtype)
     if code is None:
         _refuse(what, f"unknown dtype {dtype!r}")
-    dev = _check_fp4(t, what, q)
-    if dev.index != t.device_index():
-        with t.torch.cuda.device(dev):
+    index = _check_fp4(t, what, q)
+    if index != t.device_index():
+        with t.torch.cuda.device(index):
             return fp4_dequantize(q, dtype, out, stream)
     if out is None:
-        out = t.empty((q.rows, q.cols), dtype=t.dtype[dtype], device=dev)
-    elif (tuple(out.shape) != (q.rows, q.cols) or t.name.get(out.dtype) != dtype or out.device != dev
+        out = t.empty((q.rows, q.cols), dtype=t.dtype[dtype], device=q.codes.device)
+    elif (tuple(out.shape) != (q.rows, q.cols) or t.name.get(out.dtype) != dtype or out.get_device() != index
           or not _rows_ok(out)):
         _refuse(what, "out: a row-major tensor of the matrix's shape, dtype and device is wanted")
     rc = lib().gemm_fp4_dequantize(FP4_FORMATS[q.format], code, q.rows, q.cols, q.codes.data_ptr(),
                                    q.scales.data_ptr(), _ptr(q.tensor_scale), out.data_ptr(), _ld(out),
-                                   _stream(t, dev.index, stream))
+                                   _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return out
@@ -616,28 +620,31 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.
     """
     what, t = "fp4_matmul", _t()
-    dev = _check_fp4(t, what, A)
-    devB = _check_fp4(t, what, B)
-    if A.format != B.format or A.cols != B.cols or devB != dev:
+    index = _check_fp4(t, what, A)
+    if _check_fp4(t, what, B) != index or A.format != B.format or A.cols != B.cols:
         _refuse(what, "A and B need the same format, K and device")
-    if dev.index != t.device_index():
-        with t.torch.cuda.device(dev):
+    if index != t.device_index():
+        with t.torch.cuda.device(index):
             return fp4_matmul(A, B, alpha=alpha, bias=bias, act=act, residual=residual, beta=beta,
                               out_dtype=out_dtype, out=out, stream=stream)
     if out_dtype not in DTYPES or act not in ("none", "gelu", "relu"):
         _refuse(what, "out_dtype: f32, f16 or bf16; act: none, gelu or relu")
     M, N, K = A.rows, B.rows, A.cols
-    if bias is not None and (bias.dtype is not t.f32 or tuple(bias.shape) != (N,) or bias.device != dev
+    if bias is not None and (bias.dtype is not t.f32 or tuple(bias.shape) != (N,) or bias.get_device() != index
                              or not bias.is_contiguous()):
         _refuse(what, "bias: contiguous FP32 [N] on the operands' device is wanted")
-    for name, x, dt in (("residual", residual, "f32"), ("out", out, out_dtype)):
-        if x is not None and (tuple(x.shape) != (M, N) or t.name.get(x.dtype) != dt or x.device != dev
-                              or not _rows_ok(x)):
-            _refuse(what, f"{name}: a row-major {dt} [M, N] on the operands' device is wanted")
+    if residual is not None and (tuple(residual.shape) != (M, N) or residual.dtype is not t.f32
+                                 or residual.get_device() != index or not _rows_ok(residual)):
+        _refuse(what, "residual: a row-major f32 [M, N] on the operands' device is wanted")
     if out is None:
-        out = t.empty((M, N), dtype=t.dtype[out_dtype], device=dev)
-    ldc, ldr = _ld(out), 0 if residual is None else _ld(residual)
-    key = (A.format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, dev.index)
+        out, ldc = t.empty((M, N), dtype=t.dtype[out_dtype], device=A.codes.device), max(N, 1)
+    else:
+        if tuple(out.shape) != (M, N) or t.name.get(out.dtype) != out_dtype or out.get_device() != index \
+                or not _rows_ok(out):
+            _refuse(what, f"out: a row-major {out_dtype} [M, N] on the operands' device is wanted")
+        ldc = _ld(out)
+    ldr = 0 if residual is None else _ld(residual)
+    key = (A.format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, index)
     pl = _fp4_plans.get(key)
     if pl is None:
         ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
@@ -645,7 +652,7 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
         pl = _fp4_plans[key] = gemm_fp4_plan(A.format, M, N, K, ldc, ep)
     rc = lib().gemm_fp4_run(pl.handle, A.codes.data_ptr(), A.scales.data_ptr(), _ptr(A.tensor_scale),
                             B.codes.data_ptr(), B.scales.data_ptr(), _ptr(B.tensor_scale), out.data_ptr(),
-                            _ptr(bias), _ptr(residual), alpha, _stream(t, dev.index, stream))
+                            _ptr(bias), _ptr(residual), alpha, _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return out
@@ -720,34 +727,42 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
         _refuse(what, "FP16 or BF16 tensors and act gelu, relu or swiglu are wanted")
     if x.dim() != 2 or router.dim() != 2 or w1.dim() != 3 or w2.dim() != 3:
         _refuse(what, "x [T, H], router [E, H], w1 [E, I or 2I, H], w2 [E, H, I] are wanted")
-    (T, H), (E, I), dev, dtype = x.shape, (router.shape[0], w2.shape[2]), x.device, x.dtype
-    rows = 2 * I if act == "swiglu" else I
-    if router.shape != (E, H) or w1.shape != (E, rows, H) or w2.shape != (E, H, I):
+    (T, H), (E, Hr), (E1, rows, H1), (E2, H2, I), dtype = x.shape, router.shape, w1.shape, w2.shape, x.dtype
+    if not (Hr == H1 == H2 == H and E1 == E2 == E and rows == (2 * I if act == "swiglu" else I)):
         _refuse(what, "the shapes of x, router, w1 and w2 do not fit one another")
-    if out is not None and out.shape != (T, H):
+    if out is not None and tuple(out.shape) != (T, H):
         _refuse(what, "out: [T, H] is wanted")
-    if not x.is_cuda or router.device != dev or w1.device != dev or w2.device != dev or router.dtype is not dtype \
-            or w1.dtype is not dtype or w2.dtype is not dtype \
-            or (out is not None and (out.device != dev or out.dtype is not dtype)):
+    index = x.get_device()
+    if index < 0 or router.get_device() != index or w1.get_device() != index or w2.get_device() != index \
+            or router.dtype is not dtype or w1.dtype is not dtype or w2.dtype is not dtype \
+            or (out is not None and (out.get_device() != index or out.dtype is not dtype)):
         _refuse(what, "tensors of x's dtype on x's device, a GPU, are wanted")
-    if dev.index != t.device_index():
-        with t.torch.cuda.device(dev):
+    if index != t.device_index():
+        with t.torch.cuda.device(index):
             return moe_layer(x, router, w1, w2, top_k, act=act, normalize=normalize, out=out,
                              return_routing=return_routing, stream=stream)
+    dev = x.device
     if out is None:
         out = t.empty((T, H), dtype=dtype, device=dev)
+    (ldx, cx), (ldr, cr), (ldy, cy) = x.stride(), router.stride(), out.stride()
     (st1, ld1, c1), (st2, ld2, c2) = w1.stride(), w2.stride()
-    if not (_rows_ok(x) and _rows_ok(router) and _rows_ok(out)) or (H > 1 and c1 != 1) or (I > 1 and c2 != 1) \
-            or (rows > 1 and ld1 < H) or (H > 1 and ld2 < I) or (E > 1 and (st1 == 0 or st2 == 0)):
+    if (H > 1 and not cx == cr == cy == c1 == 1) or (I > 1 and c2 != 1) or (T > 1 and (ldx < H or ldy < H)) \
+            or (E > 1 and (ldr < H or st1 == 0 or st2 == 0)) or (rows > 1 and ld1 < H) or (H > 1 and ld2 < I):
         _refuse(what, "rows that are contiguous and not shared are wanted")
     # strides that no element uses may be anything
-    ld1, ld2 = ld1 if rows > 1 else H, ld2 if H > 1 else I
-    st1, st2 = (st1, st2) if E > 1 else (rows * ld1, H * ld2)
-    key = (dt, T, E, top_k, H, I, act, normalize, _ld(x), _ld(router), ld1, st1, ld2, st2, _ld(out), dev.index)
+    if T <= 1:
+        ldx = ldy = H
+    if rows <= 1:
+        ld1 = H
+    if H <= 1:
+        ld2 = I
+    if E <= 1:
+        ldr, st1, st2 = H, rows * ld1, H * ld2
+    key = (dt, T, E, top_k, H, I, act, normalize, ldx, ldr, ld1, st1, ld2, st2, ldy, index)
     pl = _moe_plans.get(key)
     if pl is None:
-        pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=_ld(x), ld_router=_ld(router),
-                                             ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=_ld(out))
+        pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=ldx, ld_router=ldr,
+                                             ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=ldy)
     ids = wts = None
     if return_routing:
         ids = t.empty((T, top_k), dtype=t.i32, device=dev)
@@ -759,7 +774,7 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
         with t.torch.cuda.stream(s):
             ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
     rc = lib().gemm_moe_run(pl.handle, x.data_ptr(), router.data_ptr(), w1.data_ptr(), w2.data_ptr(), out.data_ptr(),
-                            _ptr(ids), _ptr(wts), ws.data_ptr(), _stream(t, dev.index, stream))
+                            _ptr(ids), _ptr(wts), ws.data_ptr(), _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return (out, ids, wts) if return_routing else out

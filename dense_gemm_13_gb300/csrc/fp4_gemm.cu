@@ -704,25 +704,41 @@ int launch_fp4_gemm(const Fp4Config& c, int fmt, const Fp4Operand& A, const Fp4O
     return cuda_status(ce);
 }
 
-// Tokens per tile: the narrowest of 16, 32, 64 that holds them all; above 64,
-// CTA pairs on 256 x 256 tiles once they fill the GPU, else 128.  K is split
-// over a cluster of 2, 4 or 8 while the tiles leave SMs idle.
+// Clusters of `splits` CTAs (one CTA per SM) that run at a time: a cluster stays within a
+// part of the GPU, so the larger ones leave SMs over (152 SMs hold 76, 36 and 15 of 2, 4 and 8).
+int64_t clusters_at_once(int splits, int num_sms) {
+    return splits == 1 ? num_sms : splits == 2 ? num_sms / 2 : splits == 4 ? num_sms / 4 - num_sms / 76 : num_sms / 10;
+}
+
+// Up to 64 tokens: the narrowest of 16, 32, 64 that holds them all (a stage streams the same
+// weights with any of them), K split over a cluster of 2, 4 or 8 while all tiles run at once.
+// Above: the cheapest of 128 x 128 tiles, those with K split, and CTA pairs on 256 x 256, by a
+// model in ns: a stage of 256 K elements takes 300 on 128 x 128 (the bytes from L2 bound it: 36 KB
+// per SM) and 360 on a pair for four times the area (38 KB per SM); a tile's stages hide the one
+// before's epilogue, or wait for it (1500, 3000); launch, fill and last epilogue as measured.
 Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
-    Fp4Config c{};
-    if (M <= 16)
-        c.bn = 16;
-    else if (M <= 32)
-        c.bn = 32;
-    else if (M <= 64)
-        c.bn = 64;
-    else
-        c.bn = ((M + 255) / 256) * ((N + 255) / 256) * 2 >= num_sms ? 256 : 128;
-    c.splits = 1;
-    const int64_t tiles = ((N + FW - 1) / FW) * ((M + c.bn - 1) / c.bn);
-    const int64_t kbs = (K + F_KB - 1) / F_KB;
-    if (c.bn <= 128 && tiles > 0)
-        while (c.splits < 8 && 2 * c.splits <= kbs && tiles * c.splits * 2 <= num_sms) c.splits *= 2;
-    return c;
+    Fp4Config best{};
+    best.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    best.splits = 1;
+    const int64_t n_tiles = (N + FW - 1) / FW, kbs = (K + F_KB - 1) / F_KB;
+    const int64_t tiles = n_tiles * ((M + best.bn - 1) / best.bn);
+    if (tiles == 0) return best;
+    const auto waves = [](int64_t t, int64_t at_once) { return (t + at_once - 1) / at_once; };
+    int64_t cost = waves(tiles, num_sms) * std::max<int64_t>(300 * kbs, 1500) + 2500;
+    for (int s = 2; s <= 8 && s <= kbs; s *= 2) {
+        if (tiles > clusters_at_once(s, num_sms)) break;
+        const int64_t c = 300 * ((kbs + s - 1) / s) + 3500;
+        if (c < cost || M <= 64) {
+            cost = c;
+            best.splits = s;
+        }
+    }
+    if (M > 64) {
+        const int64_t pairs = ((N + 255) / 256) * ((M + 255) / 256);
+        const int64_t c = waves(pairs, num_sms / 2) * std::max<int64_t>(360 * kbs, 3000) + 3500;
+        if (num_sms >= 2 && c < cost) return Fp4Config{256, 1};
+    }
+    return best;
 }
 
 }  // namespace g13

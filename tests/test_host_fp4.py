@@ -83,12 +83,21 @@ def test_tile_choice(lib):
         assert c(M, 6144, 6144).bn == bn, M
     for M, N, K in ((1, 128, 64), (1, 1, 256), (0, 5, 1000), (5, 0, 1000), (5, 5, 0)):
         assert c(M, N, K).split_k == 1, (M, N, K)
+    held = {1: 152, 2: 76, 4: 36, 8: 15}  # clusters that run at a time
     for M in (1, 20, 60, 100):
         for N in (1, 128, 1000, 6144, 152 * 128, 153 * 128):
             for K in (300, 600, 6144):
-                s = c(M, N, K).split_k
-                tiles = -(-N // 128) * -(-M // c(M, N, K).bn)
-                assert 1 <= s <= min(8, -(-K // 256)) and (s == 1 or s * tiles <= 152), (M, N, K)
+                f = c(M, N, K)
+                tiles = -(-N // 128) * -(-M // f.bn)
+                s = f.split_k
+                assert s in held and s <= -(-K // 256), (M, N, K)
+                assert s == 1 or tiles <= held[s], (M, N, K)
+                if M <= 64 and s < 8 and 2 * s <= -(-K // 256):
+                    assert tiles > held[2 * s], (M, N, K)
+    # pairs where one wave of them replaces two of 128 x 128, or fills the GPU; not where they leave most of it idle
+    assert c(8192, 8192, 8192).bn == 256 and c(8192, 8192, 8192).variant == 2 and c(8192, 8192, 8192).bm == 256
+    assert c(1000, 3001, 4097).bn == 256 and c(512, 6144, 6144).bn == 256
+    assert c(200, 300, 770).bn == 128 and c(128, 6144, 6144).bn == 128
     with pytest.raises(g13.GemmError):
         c(-1, 1, 1)
 
