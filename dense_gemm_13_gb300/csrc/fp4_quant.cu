@@ -7,12 +7,17 @@
 //   code   = nearest E2M1 value to fl32(x / d), ties to even, saturating at 6
 //
 // Both directions move every byte once, so memory bounds them.  A thread takes
-// 16 elements (an nvfp4 block; half an mxfp4 block, joined by one shuffle):
-// 32 bytes of 16-bit input, 8 bytes of codes.  The scale bytes of a row are
-// 512 bytes apart in the stored tiles; a quantising CTA therefore takes the 32
+// 16 elements at a time (an nvfp4 block; half an mxfp4 block, joined by one
+// shuffle): 32 bytes of 16-bit input, 8 bytes of codes.  The scale bytes of a row
+// are 512 bytes apart in the stored tiles; a quantising CTA therefore takes the 32
 // rows r, r + 32, r + 64, r + 96 (r = 8 consecutive rows) that share 128
 // consecutive bytes of a tile, gathers their scales in shared memory and
-// writes whole sectors.
+// writes whole sectors.  Rows that are not 16-byte aligned go through shared
+// memory, so that global accesses stay coalesced.
+// Measured on 8192 x 8192 (bytes of both sides over time): quantising FP32 6.6 TB/s,
+// BF16 6.2 (mxfp4) and 4.9 (nvfp4: 15 instructions an element, latency at 64 warps per SM;
+// 40 us instead of 35 at 4 CTAs per SM), reading back 6.6 (FP32) and 6.0 (BF16).  The FP32
+// form holds 5 CTAs per SM (at 8 its 32 loaded registers spill: 68 us instead of 46).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -23,7 +28,7 @@ namespace g13 {
 namespace {
 
 constexpr int QT = 256;       // threads per CTA
-constexpr int QCOLS = 256;    // columns per quantising CTA
+constexpr int QCOLS = 256;    // columns that a CTA's threads take at a time
 constexpr int QROWS = 32;     // rows per quantising CTA
 
 template <typename T>
@@ -95,91 +100,156 @@ __device__ __forceinline__ float ue8m0_value(uint32_t byte) {
     return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
 }
 
-// 16 consecutive elements as FP32: 16-byte loads, or (VEC false, or the row's
-// end) one by one with zeros past `n`.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const T* p, int64_t n, float* x) {
-    if (VEC && n >= 16) {
-        constexpr int W = 16 / sizeof(T);
-        uint4 v[16 / W];
+// 16 consecutive elements of a row.
+template <typename T>
+struct __align__(16) Sixteen {
+    T v[16];
+};
+// Of which n exist (the rest are zero); 16-byte loads where all do.
+template <typename T>
+__device__ __forceinline__ Sixteen<T> load16(const T* p, int64_t n) {
+    Sixteen<T> x;
+    if (n >= 16) {
 #pragma unroll
-        for (int i = 0; i < 16 / W; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = to_f32<T>(reinterpret_cast<const T*>(v)[i]);
+        for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+            reinterpret_cast<uint4*>(x.v)[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = i < n ? to_f32<T>(p[i]) : 0.0f;
+        for (int i = 0; i < 16; ++i) x.v[i] = i < n ? p[i] : from_f32<T>(0.0f);
     }
+    return x;
 }
 
+// The largest magnitude as the bits of an FP32 number; infinities and NaN compare above
+// every number.
+__device__ __forceinline__ uint32_t top16(const Sixteen<float>& x) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x.v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+template <typename T, typename T2>
+__device__ __forceinline__ uint32_t top16_packed(const Sixteen<T>& x) {
+    const T2* p = reinterpret_cast<const T2*>(x.v);
+    T2 m = __habs2(p[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(p[i]));
+    return max(__float_as_uint(to_f32<T>(m.x)) & 0x7FFFFFFFu, __float_as_uint(to_f32<T>(m.y)) & 0x7FFFFFFFu);
+}
+__device__ __forceinline__ uint32_t top16(const Sixteen<__half>& x) { return top16_packed<__half, __half2>(x); }
+__device__ __forceinline__ uint32_t top16(const Sixteen<__nv_bfloat16>& x) {
+    return top16_packed<__nv_bfloat16, __nv_bfloat162>(x);
+}
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// VEC: rows are 16-byte aligned.
 template <int FMT, typename T, bool VEC>
-__global__ void __launch_bounds__(QT)
+__global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
     fp4_quantize_kernel(const T* __restrict__ src, int64_t rows, int64_t cols, int64_t ld,
                         const float* __restrict__ gscale, uint8_t* __restrict__ codes,
                         uint8_t* __restrict__ scales, int64_t col_blocks) {
     constexpr int BLK = fp4_block(FMT);
-    constexpr int TILES = QCOLS / (4 * BLK);  // scale tiles along the CTA's columns
+    constexpr int TILES = QCOLS / (4 * BLK);      // scale tiles along the CTA's columns
+    constexpr int LINE = QCOLS + 16 / sizeof(T);  // a staged row
     __shared__ __align__(16) uint8_t sc[TILES][128];
+    __shared__ __align__(16) T stage[VEC ? 1 : QROWS * LINE];
     const int64_t rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
     const int64_t rt = rb >> 2;          // row tile of 128
     const int sub = static_cast<int>(rb & 3);
     const int64_t row_bytes = fp4_row_bytes(cols);
     const int64_t ctiles = fp4_col_tiles(FMT, cols);
     const float g = FMT == GEMM_NVFP4 && gscale ? __ldg(gscale) : 1.0f;
-    const int tc = threadIdx.x & 15;
-    const int64_t c0 = cb * QCOLS + tc * 16;
+    const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
+    // slot 0..31 of the CTA -> row
+    const auto row_of = [&](int slot) { return rt * 128 + (slot >> 3) * 32 + sub * 8 + (slot & 7); };
 
-    float x[2][16];
+    Sixteen<T> x[2];
+    if constexpr (VEC) {
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        const int slot = pass * 16 + (threadIdx.x >> 4);
-        const int64_t row = rt * 128 + (slot >> 3) * 32 + sub * 8 + (slot & 7);
-        load16<T, VEC>(src + row * ld + c0, row < rows ? cols - c0 : 0, x[pass]);
+        for (int p = 0; p < 2; ++p) {
+            const int64_t row = row_of(p * 16 + tr), c0 = cb * QCOLS + tc * 16;
+            x[p] = load16<T>(src + row * ld + c0, row < rows ? cols - c0 : 0);
+        }
+    } else {
+        const int64_t c = cb * QCOLS + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < QROWS; ++i) {
+            const int64_t row = row_of(i);
+            stage[i * LINE + threadIdx.x] = row < rows && c < cols ? src[row * ld + c] : from_f32<T>(0.0f);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+            x[p] = *reinterpret_cast<const Sixteen<T>*>(&stage[(p * 16 + tr) * LINE + tc * 16]);
     }
 #pragma unroll
-    for (int pass = 0; pass < 2; ++pass) {
-        const int slot = pass * 16 + (threadIdx.x >> 4);
-        const int64_t row = rt * 128 + (slot >> 3) * 32 + sub * 8 + (slot & 7);
-        // the largest magnitude as bits: infinities and NaN compare above every number
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[pass][i]) & 0x7FFFFFFFu);
+    for (int p = 0; p < 2; ++p) {
+        const int slot = p * 16 + tr;
+        const int64_t row = row_of(slot), c0 = cb * QCOLS + tc * 16;
+        uint32_t top = top16(x[p]);
         if (FMT == GEMM_MXFP4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         uint32_t byte;
-        float y[16];
+        float d = 1.0f, inv;
         if (FMT == GEMM_MXFP4) {
             // floor(log2) of a normal number is its exponent field; below the
             // normal range the result is kept at -127 anyway
             const int e = static_cast<int>(top >> 23) - 127 - 2;
             byte = top >= 0x7F800000u ? 0xFFu : static_cast<uint32_t>(max(e, -127) + 127);
-            // 2^-E; exact products, apart from results far below the least code
-            const float inv = ue8m0_value(254u - min(byte, 254u));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) y[i] = x[pass][i] * inv;
+            inv = ue8m0_value(254u - min(byte, 254u));  // 2^-E
         } else {
             const float r = fminf(__fdiv_rn(__uint_as_float(top), 6.0f * g), 448.0f);
             byte = top >= 0x7F800000u ? 0x7Fu : e4m3_byte(r);
-            const float d = e4m3_value(byte) * g;
-            if (d > 0x1p-60f && d < 0x1p60f) {
+            d = e4m3_value(byte) * g;
+            inv = __frcp_rn(d);
+        }
+        uint32_t code[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float v[8], y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(x[p].v[8 * h + i]);
+            if (FMT == GEMM_MXFP4) {
+                // exact products, apart from results far below the least code
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
+            } else if (d > 0x1p-60f && d < 0x1p60f) {
                 // fl32(x / d): q = x (1/d) corrected by its exact remainder, which gives the
                 // rounded quotient (P. Markstein, "Computation of elementary functions on the
-                // IBM RISC System/6000 processor", 1990); three operations an element where
-                // a division each would take longer than the memory
-                const float inv = __frcp_rn(d);
+                // IBM RISC System/6000 processor", 1990); one and a half instructions an element
+                // where a division each would take longer than the memory
+                const uint64_t inv2 = pack2(inv, inv), nd2 = pack2(-d, -d);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float q = x[pass][i] * inv;
+                for (int i = 0; i < 8; i += 2) {
+                    const uint64_t v2 = pack2(v[i], v[i + 1]), q = mul2(v2, inv2);
+                    const uint64_t r = fma2(fma2(q, nd2, v2), inv2, q);
+                    asm("mov.b64 {%0, %1}, %2;" : "=f"(y[i]), "=f"(y[i + 1]) : "l"(r));
                     // (the remainder of -0 is +0: the sign is put back)
-                    y[i] = copysignf(fmaf(fmaf(-q, d, x[pass][i]), inv, q), x[pass][i]);
+                    y[i] = copysignf(y[i], v[i]);
+                    y[i + 1] = copysignf(y[i + 1], v[i + 1]);
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = d > 0.0f ? __fdiv_rn(x[pass][i], d) : 0.0f * x[pass][i];
+                for (int i = 0; i < 8; ++i) y[i] = d > 0.0f ? __fdiv_rn(v[i], d) : 0.0f * v[i];
             }
+            code[h] = e2m1x8(y);
         }
         if (row < rows && c0 / 2 < row_bytes)
-            *reinterpret_cast<uint2*>(codes + row * row_bytes + c0 / 2) =
-                make_uint2(e2m1x8(y), e2m1x8(y + 8));
+            *reinterpret_cast<uint2*>(codes + row * row_bytes + c0 / 2) = make_uint2(code[0], code[1]);
         // blocks past the row's end and rows past the matrix: zeros
         if (row >= rows || c0 / BLK >= (cols + BLK - 1) / BLK) byte = 0;
         const int blk = tc * 16 / BLK;  // block within the CTA
@@ -194,39 +264,73 @@ __global__ void __launch_bounds__(QT)
             *reinterpret_cast<const uint4*>(&sc[t >> 3][(t & 7) * 16]);
 }
 
-// One thread per 16 elements.
-template <int FMT, typename T, bool VEC>
+// One thread per 16 elements.  ALIGN: bytes that every row of dst starts on (32: whole
+// sectors per store; 16; else through shared memory, 32 neighbouring elements a store).
+template <int FMT, typename T, int ALIGN>
 __global__ void __launch_bounds__(QT)
     fp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                           const float* __restrict__ gscale, T* __restrict__ dst, int64_t rows,
                           int64_t cols, int64_t ld, int64_t groups) {
+    __shared__ __align__(16) T stage[ALIGN >= 16 ? 1 : QT * 16];
     const int64_t i = static_cast<int64_t>(blockIdx.x) * QT + threadIdx.x;
     const int64_t row = i / groups;
-    if (row >= rows) return;
     const int64_t c0 = (i - row * groups) * 16;
-    const int64_t row_bytes = fp4_row_bytes(cols);
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + row * row_bytes + c0 / 2));
-    const int64_t blk = c0 / fp4_block(FMT);
-    const int r = static_cast<int>(row & 127);
-    const uint32_t byte = __ldg(scales + ((row >> 7) * fp4_col_tiles(FMT, cols) + (blk >> 2)) * kFp4TileBytes +
-                                (r & 31) * 16 + (r >> 5) * 4 + (blk & 3));
-    const float d = FMT == GEMM_MXFP4 ? ue8m0_value(byte)
-                                      : e4m3_value(byte) * (gscale ? __ldg(gscale) : 1.0f);
-    float y[16];
-    e2m1x8_values(w.x, y);
-    e2m1x8_values(w.y, y + 8);
-    __align__(16) T out[16];
+    __align__(32) T out[16];
+    if (row < rows) {
+        const int64_t row_bytes = fp4_row_bytes(cols);
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + row * row_bytes + c0 / 2));
+        const int64_t blk = c0 / fp4_block(FMT);
+        const int r = static_cast<int>(row & 127);
+        const uint32_t byte =
+            __ldg(scales + ((row >> 7) * fp4_col_tiles(FMT, cols) + (blk >> 2)) * kFp4TileBytes +
+                  (r & 31) * 16 + (r >> 5) * 4 + (blk & 3));
+        const float d = FMT == GEMM_MXFP4 ? ue8m0_value(byte)
+                                          : e4m3_value(byte) * (gscale ? __ldg(gscale) : 1.0f);
+        float y[16];
+        e2m1x8_values(w.x, y);
+        e2m1x8_values(w.y, y + 8);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) out[j] = from_f32<T>(y[j] * d);
-    T* p = dst + row * ld + c0;
-    if (VEC && c0 + 16 <= cols) {
+        for (int j = 0; j < 16; ++j) out[j] = from_f32<T>(y[j] * d);
+    }
+    if constexpr (ALIGN >= 16) {
+        if (row >= rows) return;
+        T* p = dst + row * ld + c0;
+        const uint32_t* o = reinterpret_cast<const uint32_t*>(out);
+        if (c0 + 16 <= cols) {
+            if constexpr (ALIGN == 32) {
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)) / 2; ++j)
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                     reinterpret_cast<char*>(p) + 32 * j),
+                                 "r"(o[8 * j]), "r"(o[8 * j + 1]), "r"(o[8 * j + 2]), "r"(o[8 * j + 3]),
+                                 "r"(o[8 * j + 4]), "r"(o[8 * j + 5]), "r"(o[8 * j + 6]), "r"(o[8 * j + 7])
+                                 : "memory");
+            } else {
+#pragma unroll
+                for (int j = 0; j < static_cast<int>(sizeof(T)); ++j)
+                    reinterpret_cast<uint4*>(p)[j] = reinterpret_cast<const uint4*>(out)[j];
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c0 + j < cols) p[j] = out[j];
+        }
+    } else {
+        // a warp's 32 groups: element j of the warp's 512 by lane j % 32
+        const int lane = threadIdx.x & 31;
+        T* mine = stage + (threadIdx.x >> 5) * 512;
 #pragma unroll
         for (int j = 0; j < static_cast<int>(sizeof(T)); ++j)
-            reinterpret_cast<uint4*>(p)[j] = reinterpret_cast<const uint4*>(out)[j];
-    } else {
+            reinterpret_cast<uint4*>(mine + lane * 16)[j] = reinterpret_cast<const uint4*>(out)[j];
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (c0 + j < cols) p[j] = out[j];
+        for (int j = 0; j < 16; ++j) {
+            // the group that element 32 j + lane belongs to, as its thread sees it
+            const int src = 2 * j + (lane >> 4);
+            const int64_t r = __shfl_sync(0xFFFFFFFFu, row, src);
+            const int64_t c = __shfl_sync(0xFFFFFFFFu, c0, src) + (lane & 15);
+            if (r < rows && c < cols) dst[r * ld + c] = mine[32 * j + lane];
+        }
     }
 }
 
@@ -245,10 +349,12 @@ cudaError_t quantize_t(const void* src, int64_t rows, int64_t cols, int64_t ld, 
 template <int FMT, typename T>
 cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, const float* g, void* dst,
                          int64_t rows, int64_t cols, int64_t ld, cudaStream_t st) {
-    const bool vec = reinterpret_cast<uintptr_t>(dst) % 16 == 0 && ld * sizeof(T) % 16 == 0;
+    const auto on = [&](uintptr_t n) { return reinterpret_cast<uintptr_t>(dst) % n == 0 && ld * sizeof(T) % n == 0; };
     const int64_t groups = (cols + 15) / 16;
     const int64_t grid = (rows * groups + QT - 1) / QT;
-    auto k = vec ? fp4_dequantize_kernel<FMT, T, true> : fp4_dequantize_kernel<FMT, T, false>;
+    auto k = on(32)   ? fp4_dequantize_kernel<FMT, T, 32>
+             : on(16) ? fp4_dequantize_kernel<FMT, T, 16>
+                      : fp4_dequantize_kernel<FMT, T, 0>;
     k<<<static_cast<unsigned>(grid), QT, 0, st>>>(codes, scales, g, static_cast<T*>(dst), rows, cols, ld,
                                                   groups);
     return cudaGetLastError();
