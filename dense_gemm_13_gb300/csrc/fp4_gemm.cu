@@ -21,7 +21,7 @@
 //               MMAs that read them), then the MMAs, by one elected lane; commits
 //               free ring stages (empty[s]) and finish accumulators (tfull)
 //   others      epilogue: four warps, one TMEM lane quarter each, or 16, four to a
-//               quarter, taking its 16-column chunks in turn
+//               quarter, taking its 32-column chunks in turn
 //
 // Large products run on CTA pairs (tcgen05 cta_group::2): 256 weight rows x 256
 // tokens, each CTA holding its own 128 weight rows and half of the tokens, so
@@ -67,12 +67,15 @@ struct F4Layout {
     static constexpr int STAGE_BYTES = F_W_TILE + X_TILE + SFW_BYTES + SFX_BYTES;
     static constexpr int STAGE_ALIGN = (STAGE_BYTES + 1023) / 1024 * 1024;
     // TMEM columns: two accumulators ACC_STEP apart (side by side, or overlapping
-    // where BN = 256), then two sets of scale columns (a tile is 4 columns)
+    // where BN = 256), then sets of scale columns (a tile is 4 columns), one per stage in
+    // turn: up to one less than the ring's stages, or the two that 256 x 256 tiles leave room
+    // for in nvfp4
     static constexpr int OVERLAP = BN == 256 ? 96 : 0;
     static constexpr int ACC_STEP = BN - OVERLAP;
     static constexpr int SF_COLS = CT * 4 * (1 + XT);
     static constexpr int SF_BASE = ACC_STEP + BN;
-    static constexpr int COLS = SF_BASE + 2 * SF_COLS;
+    static constexpr int SETS = BN <= 32 ? 7 : BN == 64 ? 6 : SF_BASE + 4 * SF_COLS <= 512 ? 4 : 2;
+    static constexpr int COLS = SF_BASE + SETS * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(COLS <= 512, "TMEM");
 };
@@ -144,8 +147,8 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
                                                unsigned* status, uint64_t timeout_ns) {
     return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, timeout_ns));
 }
-// 16 consecutive columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+// 16 or 32 consecutive columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -160,6 +163,40 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
                    "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
+}
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) {
+    tmem_ld_32x32b_x32(taddr, r);
+    tmem_ld_wait_regs(r);
+}
+// GELU of two values, 0.5 y (1 + erf(y / sqrt 2)), with erf from Abramowitz & Stegun, Handbook
+// of Mathematical Functions, formula 7.1.28 (|error| <= 3e-7): for x >= 0
+//     1 - erf(x) = (1 + a1 x + ... + a6 x^6)^-16,
+//     a1..a6 = 0.0705230784, 0.0422820123, 0.0092705272, 0.0001520143, 0.0002765672, 0.0000430638
+// (here with x = |y| / sqrt 2 and the powers of 1 / sqrt 2 in the constants).  One special-function
+// operation a value, the reciprocal; formula 7.1.26 takes two, which alone took a third of a
+// 256 x 256 tile's epilogue.  |y| is kept at 30, where the result is max(y, 0) to the last bit, so that
+// an infinity gives one; NaN stays NaN.
+__device__ __forceinline__ void gelu2_as7128(float& y0, float& y1) {
+    const float c0 = fminf(fabsf(y0), 30.0f), c1 = fminf(fabsf(y1), 30.0f);
+    const uint64_t x = f2_pack(c0, c1);
+    const auto two = [](float v) { return f2_pack(v, v); };
+    uint64_t p = f2_fma(two(5.3829750e-06f), x, two(4.8890639e-05f));
+    p = f2_fma(p, x, two(3.8003575e-05f));
+    p = f2_fma(p, x, two(3.2776264e-03f));
+    p = f2_fma(p, x, two(2.1141006e-02f));
+    p = f2_fma(p, x, two(4.9867347e-02f));
+    p = f2_fma(p, x, two(1.0f));
+    p = f2_mul(p, p);
+    p = f2_mul(p, p);
+    p = f2_mul(p, p);
+    p = f2_mul(p, p);
+    float p0, p1, h0, h1, m0, m1;
+    f2_unpack(p, p0, p1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(h0) : "f"(p0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(h1) : "f"(p1));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m0) : "f"(y0));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m1) : "f"(y1));
+    f2_unpack(f2_fma(f2_mul(x, f2_pack(h0, h1)), two(-0.5f), f2_pack(m0, m1)), y0, y1);
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
@@ -176,8 +213,8 @@ template <int CN>
 __device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float bias, int64_t m0, uint32_t n,
                                          float (&v)[CN]) {
     static_assert(CN % 2 == 0, "pairs");
-    if (n >= static_cast<uint32_t>(e.N)) return;
     const int live = static_cast<int>(min(static_cast<int64_t>(CN), e.M - m0));
+    if (n >= static_cast<uint32_t>(e.N) || live <= 0) return;
     float r[CN];
     if (e.R) {
         const char* p = reinterpret_cast<const char*>(e.R + m0 * e.ldr);
@@ -192,7 +229,7 @@ __device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float 
     for (int j = 0; j < CN; j += 2) f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), a2, b2), v[j], v[j + 1]);
     if (e.act == GEMM_ACT_GELU_ERF) {
 #pragma unroll
-        for (int j = 0; j < CN; j += 2) gelu2_as7126(v[j], v[j + 1]);
+        for (int j = 0; j < CN; j += 2) gelu2_as7128(v[j], v[j + 1]);
     } else if (e.act == GEMM_ACT_RELU) {
 #pragma unroll
         for (int j = 0; j < CN; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];
@@ -417,7 +454,7 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
         // elected lane issues.  (With the loop inside a single lane's branch, issuing
         // was the bound: 470 us at 8192^3 nvfp4 against 276 us, before pairs.)
         const bool one = elect_one();
-        int s = 0, lt = 0;
+        int s = 0, lt = 0, done = 0;
         uint32_t ph = 0, set = 0;
         bool ok = true, issued = false;
         // descriptors of ring stage 0; a stage is STAGE_ALIGN bytes further on
@@ -450,8 +487,21 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
                 }
                 tc_fence_after();
                 const uint64_t off = static_cast<uint64_t>(s * (L::STAGE_ALIGN >> 4));
-                const uint32_t sf_t = tmem_base + L::SF_BASE + (set ? L::SF_COLS : 0);
-                set ^= 1u;
+                const uint32_t sf_t = tmem_base + L::SF_BASE + set * L::SF_COLS;
+                set = set + 1 == L::SETS ? 0 : set + 1;
+                // The copies below overwrite the scale columns of SETS stages ago: its MMAs must
+                // have read them (the stages since keep the tensor cores busy meanwhile).
+                static_assert(L::SETS < STAGES, "the stage's barrier has not gone round");
+                if (done >= L::SETS) {
+                    const int sp = s >= L::SETS ? s - L::SETS : s + STAGES - L::SETS;
+                    if (!mbar_wait_warp(smem_u32(&empty[sp]), s >= L::SETS ? ph : ph ^ 1u, abort_flag, args.status,
+                                        tmo)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                ++done;
                 const int steps = k_steps - kb * 4;  // 4 or more: a whole stage
                 if (one) {
                     // TMEM columns of scale tile c: weights at 4c, tokens' row tile x at
@@ -497,7 +547,8 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
         // ---------------------------------------------------- epilogue
         const int q = warp & 3;
         const int h = (warp - 2) >> 2;         // which of the quarter's warps
-        constexpr int STEP = 16 * (L::EW / 4); // columns from one of its chunks to the next
+        constexpr int CH = BN >= 32 ? 32 : 16;  // columns of a chunk
+        constexpr int STEP = CH * (L::EW / 4);  // from one of its chunks to the next
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
         float alpha = args.e.alpha;
         if (args.gw) alpha *= __ldg(args.gw);
@@ -516,16 +567,17 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
                 break;
             tc_fence_after();
             // Overlapping accumulators: the shared columns come first (the first one's last
-            // 96, the second one's first), and are handed back once they are read.
+            // 96, the second one's first), within every warp's first chunk, and are handed back as
+            // soon as that is read; else the accumulator is, after the last.
             const int start = L::OVERLAP && buf == 0 ? BN - L::OVERLAP : 0;
-            constexpr int LAST = L::OVERLAP ? L::OVERLAP : BN;  // columns to read before the release
+            static_assert(L::OVERLAP <= STEP, "the shared columns lie in the first chunks");
 #pragma unroll 1
-            for (int i = 16 * h; i < BN; i += STEP) {
+            for (int i = CH * h; i < BN; i += STEP) {
                 const int c = (start + i) % BN;
                 const bool live = SPLIT || mt * BN + c < args.M;
-                uint32_t r[16];
-                if (live) tmem_ld_x16(tmem_base + lane_base + static_cast<uint32_t>(buf * L::ACC_STEP + c), r);
-                if (!SPLIT && i < LAST && i + STEP >= LAST) {
+                uint32_t r[CH];
+                if (live) tmem_ld_cols(tmem_base + lane_base + static_cast<uint32_t>(buf * L::ACC_STEP + c), r);
+                if (!SPLIT && (L::OVERLAP ? i < STEP : i + STEP >= BN)) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -537,19 +589,22 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
                     }
                 }
                 if (!live) continue;
-                float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = none ? 0.0f : __uint_as_float(r[j]);
-                if (SPLIT) {
-                    // every MMA of this CTA is done: the ring is free for the partial sums,
-                    // four columns of a lane together
-                    float4* part = reinterpret_cast<float4*>(smem) + (c / 4) * FW + q * 32 + lane;
+                for (int k = 0; k < CH; k += 16) {
+                    float v[16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        part[j * FW] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                } else {
-                    f4_store<16>(args.e, alpha, bias, mt * BN + c, n, v);
-                    __syncwarp();
+                    for (int j = 0; j < 16; ++j) v[j] = none ? 0.0f : __uint_as_float(r[k + j]);
+                    if (SPLIT) {
+                        // every MMA of this CTA is done: the ring is free for the partial sums,
+                        // four columns of a lane together
+                        float4* part = reinterpret_cast<float4*>(smem) + ((c + k) / 4) * FW + q * 32 + lane;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            part[j * FW] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    } else {
+                        f4_store<16>(args.e, alpha, bias, mt * BN + c + k, n, v);
+                        __syncwarp();
+                    }
                 }
             }
         }
