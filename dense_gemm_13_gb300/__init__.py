@@ -402,17 +402,45 @@ def matmul(A, B, *, b_layout="kn", alpha=1.0, bias=None, act="none", residual=No
 
 # ------------------------------------------------------------------ 4-bit floats
 class Fp4Tensor:
-    """A matrix in microscaled 4-bit floats (layout: include/gemm13.h, "4-bit floats").
+    """A matrix in microscaled 4-bit floats (layout: include/gemm13.h, "4-bit floats"); read-only.
 
     codes: uint8 [rows, row_bytes]; scales: uint8, flat; tensor_scale: None (1) or one FP32 value on
-    the same device ("nvfp4" only).
+    the same device ("nvfp4" only).  Arrays that do not fit the sizes are refused here, once.
     """
 
-    __slots__ = ("codes", "scales", "rows", "cols", "format", "tensor_scale")
+    __slots__ = ("_codes", "_scales", "_rows", "_cols", "_format", "_g", "_index", "_both")
 
     def __init__(self, codes, scales, rows, cols, format, tensor_scale=None):
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
-        self.format, self.tensor_scale = format, tensor_scale
+        self._index = _check_fp4(_t(), codes, scales, rows, cols, format, tensor_scale)
+        self._codes, self._scales, self._rows, self._cols = codes, scales, rows, cols
+        self._format, self._g, self._both = format, tensor_scale, None
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            row = (self._cols + 31) // 32 * 16
+            self._codes = self._both[: self._rows * row].view(self._rows, row)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._scales = self._both[self._rows * ((self._cols + 31) // 32 * 16):]
+        return self._scales
+
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    format = property(lambda self: self._format)
+    tensor_scale = property(lambda self: self._g)
+
+    def _ptrs(self):
+        """Addresses of codes, scales and tensor scale."""
+        g = self._g
+        g = None if g is None else g.data_ptr()
+        if self._both is not None:
+            p = self._both.data_ptr()
+            return p, p + self._rows * ((self._cols + 31) // 32 * 16), g
+        return self._codes.data_ptr(), self._scales.data_ptr(), g
 
 
 def _refuse(what: str, why: str):
@@ -434,9 +462,17 @@ class _Torch:
         self.dtype = {v: k for k, v in self.name.items()}
         self.u8, self.f32, self.i32 = torch.uint8, torch.float32, torch.int32
         self.empty = torch.empty
+        self._devices: dict = {}
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.raw_stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
         self.device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+    def device(self, index: int):
+        d = self._devices.get(index)
+        if d is None:
+            d = self._devices[index] = self.torch.device("cuda", index)
+        return d
 
 
 _torch_cache: list = []
@@ -472,9 +508,9 @@ def _check_scale(t: _Torch, what: str, g, format: str, index: int):
         _refuse(what, "tensor_scale: one FP32 value on the matrix's device is wanted")
 
 
-def _check_fp4(t: _Torch, what: str, q: Fp4Tensor) -> int:
+def _check_fp4(t: _Torch, codes, scales, rows: int, cols: int, format: str, g) -> int:
     """Refuses arrays that are shorter than the kernels read; returns their device's index."""
-    codes, scales, format, rows, cols = q.codes, q.scales, q.format, q.rows, q.cols
+    what = "Fp4Tensor"
     if format not in FP4_FORMATS:
         _refuse(what, f"unknown format {format!r}")
     per = 128 if format == "mxfp4" else 64  # elements of four blocks
@@ -486,8 +522,8 @@ def _check_fp4(t: _Torch, what: str, q: Fp4Tensor) -> int:
             or not scales.is_contiguous()):
         _refuse(what, f"{rows} x {cols} in {format}: codes ({n_codes} bytes) and scales ({n_scales} bytes), contiguous "
                       "uint8 on the GPU, are wanted")
-    if q.tensor_scale is not None:
-        _check_scale(t, what, q.tensor_scale, format, index)
+    if g is not None:
+        _check_scale(t, what, g, format, index)
     return index
 
 
@@ -516,15 +552,19 @@ def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp
         ld = cols
     if rows <= 1 or ld < 1:
         ld = max(cols, 1)
+    # codes and scales in one allocation (codes are a multiple of 16 bytes)
     per = 128 if f == 0 else 64  # elements of four blocks
-    dev = x.device
-    codes = t.empty((rows, (cols + 31) // 32 * 16), dtype=t.u8, device=dev)
-    scales = t.empty((rows + 127) // 128 * ((cols + per - 1) // per) * 512, dtype=t.u8, device=dev)
-    rc = lib().gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), ld, _ptr(tensor_scale),
-                                 codes.data_ptr(), scales.data_ptr(), _stream(t, index, stream))
+    n_codes = rows * ((cols + 31) // 32 * 16)
+    both = t.empty(n_codes + (rows + 127) // 128 * ((cols + per - 1) // per) * 512, dtype=t.u8, device=x.device)
+    p = both.data_ptr()
+    rc = (_lib or load()).gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), ld, _ptr(tensor_scale), p,
+                                            p + n_codes, _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
-    return Fp4Tensor(codes, scales, rows, cols, format, tensor_scale)
+    q = Fp4Tensor.__new__(Fp4Tensor)
+    q._codes = q._scales = None
+    q._rows, q._cols, q._format, q._g, q._index, q._both = rows, cols, format, tensor_scale, index, both
+    return q
 
 
 def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
@@ -533,18 +573,20 @@ def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
     code = DTYPES.get(dtype)
     if code is None:
         _refuse(what, f"unknown dtype {dtype!r}")
-    index = _check_fp4(t, what, q)
+    index, rows, cols = q._index, q._rows, q._cols
     if index != t.device_index():
         with t.torch.cuda.device(index):
             return fp4_dequantize(q, dtype, out, stream)
     if out is None:
-        out = t.empty((q.rows, q.cols), dtype=t.dtype[dtype], device=q.codes.device)
-    elif (tuple(out.shape) != (q.rows, q.cols) or t.name.get(out.dtype) != dtype or out.get_device() != index
-          or not _rows_ok(out)):
-        _refuse(what, "out: a row-major tensor of the matrix's shape, dtype and device is wanted")
-    rc = lib().gemm_fp4_dequantize(FP4_FORMATS[q.format], code, q.rows, q.cols, q.codes.data_ptr(),
-                                   q.scales.data_ptr(), _ptr(q.tensor_scale), out.data_ptr(), _ld(out),
-                                   _stream(t, index, stream))
+        out, ld = t.empty((rows, cols), dtype=t.dtype[dtype], device=t.device(index)), cols or 1
+    else:
+        if (tuple(out.shape) != (rows, cols) or t.name.get(out.dtype) != dtype or out.get_device() != index
+                or not _rows_ok(out)):
+            _refuse(what, "out: a row-major tensor of the matrix's shape, dtype and device is wanted")
+        ld = _ld(out)
+    codes, scales, g = q._ptrs()
+    rc = (_lib or load()).gemm_fp4_dequantize(FP4_FORMATS[q._format], code, rows, cols, codes, scales, g,
+                                              out.data_ptr(), ld, _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return out
@@ -582,13 +624,12 @@ def gemm_fp4_plan(format: str, M: int, N: int, K: int, ldc: int, epilogue: Epilo
 def gemm_fp4_run(plan: Fp4Plan, A: Fp4Tensor, B: Fp4Tensor, C, bias=None, residual=None, alpha: float = 1.0,
                  stream=None) -> int:
     """Enqueue C = epilogue(A @ B.T) of a plan on `stream` (default: torch's current stream)."""
-    if (A.rows, A.cols, B.rows, B.cols) != (plan.M, plan.K, plan.N, plan.K) or A.format != plan.format \
-            or B.format != plan.format:
+    if (A._rows, A._cols, B._rows, B._cols) != (plan.M, plan.K, plan.N, plan.K) or A._format != plan.format \
+            or B._format != plan.format:
         _refuse("gemm_fp4_run", "the operands do not fit the plan")
     t = _t()
-    rc = lib().gemm_fp4_run(plan.handle, A.codes.data_ptr(), A.scales.data_ptr(), _ptr(A.tensor_scale),
-                            B.codes.data_ptr(), B.scales.data_ptr(), _ptr(B.tensor_scale), _ptr(C), _ptr(bias),
-                            _ptr(residual), alpha, _stream(t, t.device_index(), stream))
+    rc = (_lib or load()).gemm_fp4_run(plan.handle, *A._ptrs(), *B._ptrs(), _ptr(C), _ptr(bias), _ptr(residual), alpha,
+                                       _stream(t, t.device_index(), stream))
     if rc != 0:
         raise GemmError(rc, "gemm_fp4_run")
     return rc
@@ -620,8 +661,8 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.
     """
     what, t = "fp4_matmul", _t()
-    index = _check_fp4(t, what, A)
-    if _check_fp4(t, what, B) != index or A.format != B.format or A.cols != B.cols:
+    index, format, M, K, N = A._index, A._format, A._rows, A._cols, B._rows
+    if B._index != index or B._format != format or B._cols != K:
         _refuse(what, "A and B need the same format, K and device")
     if index != t.device_index():
         with t.torch.cuda.device(index):
@@ -629,7 +670,6 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
                               out_dtype=out_dtype, out=out, stream=stream)
     if out_dtype not in DTYPES or act not in ("none", "gelu", "relu"):
         _refuse(what, "out_dtype: f32, f16 or bf16; act: none, gelu or relu")
-    M, N, K = A.rows, B.rows, A.cols
     if bias is not None and (bias.dtype is not t.f32 or tuple(bias.shape) != (N,) or bias.get_device() != index
                              or not bias.is_contiguous()):
         _refuse(what, "bias: contiguous FP32 [N] on the operands' device is wanted")
@@ -637,22 +677,21 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
                                  or residual.get_device() != index or not _rows_ok(residual)):
         _refuse(what, "residual: a row-major f32 [M, N] on the operands' device is wanted")
     if out is None:
-        out, ldc = t.empty((M, N), dtype=t.dtype[out_dtype], device=A.codes.device), max(N, 1)
+        out, ldc = t.empty((M, N), dtype=t.dtype[out_dtype], device=t.device(index)), N or 1
     else:
         if tuple(out.shape) != (M, N) or t.name.get(out.dtype) != out_dtype or out.get_device() != index \
                 or not _rows_ok(out):
             _refuse(what, f"out: a row-major {out_dtype} [M, N] on the operands' device is wanted")
         ldc = _ld(out)
     ldr = 0 if residual is None else _ld(residual)
-    key = (A.format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, index)
+    key = (format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, index)
     pl = _fp4_plans.get(key)
     if pl is None:
         ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
                       residual=residual is not None, beta=beta, ldr=ldr)
-        pl = _fp4_plans[key] = gemm_fp4_plan(A.format, M, N, K, ldc, ep)
-    rc = lib().gemm_fp4_run(pl.handle, A.codes.data_ptr(), A.scales.data_ptr(), _ptr(A.tensor_scale),
-                            B.codes.data_ptr(), B.scales.data_ptr(), _ptr(B.tensor_scale), out.data_ptr(),
-                            _ptr(bias), _ptr(residual), alpha, _stream(t, index, stream))
+        pl = _fp4_plans[key] = gemm_fp4_plan(format, M, N, K, ldc, ep)
+    rc = (_lib or load()).gemm_fp4_run(pl.handle, *A._ptrs(), *B._ptrs(), out.data_ptr(), _ptr(bias), _ptr(residual),
+                                       alpha, _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)
     return out
@@ -773,7 +812,7 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
         s = t.torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
         with t.torch.cuda.stream(s):
             ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
-    rc = lib().gemm_moe_run(pl.handle, x.data_ptr(), router.data_ptr(), w1.data_ptr(), w2.data_ptr(), out.data_ptr(),
+    rc = (_lib or load()).gemm_moe_run(pl.handle, x.data_ptr(), router.data_ptr(), w1.data_ptr(), w2.data_ptr(), out.data_ptr(),
                             _ptr(ids), _ptr(wts), ws.data_ptr(), _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, what)

@@ -305,3 +305,40 @@ def test_timeout_is_reported(M, N, flag):
     g13.gemm_fp4_run(plan2, A, B, C)
     assert g13.gemm_fp4_status(plan2) == 0
     assert np.array_equal(C.cpu().numpy(), a @ b.T)
+
+
+def test_python_refusals():
+    x = torch.randn(5, 70, device="cuda")
+    q = g13.fp4_quantize(x, "nvfp4")
+    p = g13.fp4_quantize(x, "mxfp4")
+    assert tuple(q.codes.shape) == (5, 48) and q.scales.numel() == 1024
+    g = torch.ones(1, device="cuda")
+    same = g13.Fp4Tensor(q.codes, q.scales, 5, 70, "nvfp4", None)
+    assert torch.equal(g13.fp4_dequantize(same), g13.fp4_dequantize(q))
+    with pytest.raises(AttributeError):
+        q.codes = x
+    E = g13.GemmError
+    for args in ((q.codes, q.scales[:512], 5, 70, "nvfp4"), (q.codes, q.scales, 6, 70, "nvfp4"),
+                 (q.codes, q.scales, 5, 70, "mxfp4"), (q.codes[:, :32], q.scales, 5, 70, "nvfp4"),
+                 (q.codes.int(), q.scales, 5, 70, "nvfp4"), (q.codes, q.scales, -5, 70, "nvfp4"),
+                 (q.codes, q.scales, 5, 70, "nvfp4", g.double()), (q.codes, q.scales, 5, 70, "nvfp4", g.cpu()),
+                 (p.codes, p.scales, 5, 70, "mxfp4", g)):
+        with pytest.raises(E):
+            g13.Fp4Tensor(*args)
+    with pytest.raises(E):
+        g13.fp4_quantize(x, "mxfp4", tensor_scale=g)
+    bad = dict(A=q, B=q)
+    for kw in (dict(B=p), dict(B=g13.fp4_quantize(x[:, :60], "nvfp4")), dict(act="softmax"), dict(out_dtype="f64"),
+               dict(bias=torch.zeros(4, device="cuda")), dict(bias=torch.zeros(5)), dict(bias=g.bfloat16().expand(5)),
+               dict(residual=torch.zeros(5, 5)), dict(residual=torch.zeros(5, 6, device="cuda")),
+               dict(residual=torch.zeros(1, 5, device="cuda").expand(5, 5)),
+               dict(out=torch.zeros(5, 5, device="cuda").t()[:, :4]),
+               dict(out=torch.zeros(5, 5, device="cuda", dtype=torch.float16))):
+        with pytest.raises(E):
+            c = dict(bad, **kw)
+            g13.fp4_matmul(c.pop("A"), c.pop("B"), **c)
+    with pytest.raises(E):
+        g13.fp4_dequantize(q, out=torch.zeros(5, 71, device="cuda"))
+    plan = g13.gemm_fp4_plan("nvfp4", 5, 5, 64, 5)
+    with pytest.raises(E):
+        g13.gemm_fp4_run(plan, q, q, x)
