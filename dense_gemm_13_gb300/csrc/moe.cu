@@ -220,6 +220,7 @@ constexpr int RE = 2, RTOK = 4;
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
     griddep_launch();  // the experts' kernel may take its place; it waits for this one's results
+    griddep_wait();    // what came before has written its inputs, and is done with the workspace
     __shared__ float sums[RT / 32][RE * RTOK];
     const gemm_moe_desc_t& d = a.d;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -815,13 +816,32 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         if (!s.last[k]) continue;
         const int ob = k == 0 ? ob_lo : ob_hi;
         const int from = ctas.owner(ob * block), to = ctas.owner((ob + 1) * block - 1);
-        for (int el = threadIdx.x; el < ysize; el += MT) {
-            float sum = 0.0f;
-            // the first of them may have begun in an earlier block: then this one is its last
-            for (int c = from; c <= to; ++c)
-                sum += __ldcg(partial + (c * 2 + (c > from || ctas.lo(c) >= ob * block ? 0 : 1)) * ysize + el);
-            const int o = ob * kMoeBlock + el / tok;
-            if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(sum);
+        // (the first of them may have begun in an earlier block: then this one is its last)
+        const int first = from * 2 + (ctas.lo(from) >= ob * block ? 0 : 1);
+        for (int i = threadIdx.x; i < ysize / 4; i += MT) {
+            const auto part = [&](int slot) {
+                return __ldcg(reinterpret_cast<const float4*>(partial + static_cast<int64_t>(slot) * ysize) + i);
+            };
+            float4 sum = part(first);
+            for (int c = from + 1; c <= to; c += 8) {  // eight reads in flight, added in order
+                float4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = part(min(c + j, to) * 2);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j <= to) {
+                        sum.x += v[j].x;
+                        sum.y += v[j].y;
+                        sum.z += v[j].z;
+                        sum.w += v[j].w;
+                    }
+            }
+            const float out[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int el = 4 * i + j, o = ob * kMoeBlock + el / tok;
+                if (o < d.H) y[(el % tok) * d.ldy + o] = cast16<T>(out[j]);
+            }
         }
     }
 }
@@ -863,11 +883,16 @@ cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
     // the router's rows and x take vector loads on their own terms
     const bool rvec = reinterpret_cast<uintptr_t>(a.router) % 16 == 0 && a.d.ld_router % 8 == 0 &&
                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.d.ldx % 8 == 0 && a.d.H % 8 == 0;
-    if (rvec)
-        moe_router_kernel<T, true><<<blocks, RT, 0, st>>>(a);
-    else
-        moe_router_kernel<T, false><<<blocks, RT, 0, st>>>(a);
-    cudaError_t ce = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(RT);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // (it waits before its first read)
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t ce = cudaLaunchKernelEx(&cfg, rvec ? moe_router_kernel<T, true> : moe_router_kernel<T, false>, a);
     if (ce != cudaSuccess) return ce;
     // groups of 8 tokens that one expert can be given: 1, 2, 4 or 8
     if (a.d.T <= 8) return launch_experts<T, ROWS, 1>(a, grid, st);
