@@ -468,6 +468,14 @@ class _Torch:
         self.device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+    def on(self, stream, index: int):
+        """Context in which `stream` (a torch stream or a handle) is the current one: what a call allocates then
+        belongs to the stream that uses it."""
+        cuda = self.torch.cuda
+        if not isinstance(stream, int) and stream.device.index != index:
+            _refuse("stream", "it belongs to another device than the tensors")
+        return cuda.stream(cuda.ExternalStream(stream, device=index) if isinstance(stream, int) else stream)
+
     def device(self, index: int):
         d = self._devices.get(index)
         if d is None:
@@ -488,6 +496,12 @@ def _stream(t: _Torch, index: int, stream) -> int:
     if stream is None:
         return t.raw_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _no_capture(t: _Torch, what: str):
+    """A plan allocates, which would break a graph capture."""
+    if t.torch.cuda.is_current_stream_capturing():
+        _refuse(what, "no plan for this shape yet: call it once before capturing a graph")
 
 
 def _rows_ok(x) -> bool:
@@ -540,9 +554,12 @@ def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp
     dt, index = t.name.get(x.dtype), x.get_device()
     if dt is None or x.dim() != 2 or index < 0:
         _refuse(what, "a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
+    if stream is not None:
+        with t.on(stream, index):
+            return fp4_quantize(x, format, tensor_scale)
     if index != t.device_index():
         with t.torch.cuda.device(index):
-            return fp4_quantize(x, format, tensor_scale, stream)
+            return fp4_quantize(x, format, tensor_scale)
     if tensor_scale is not None:
         _check_scale(t, what, tensor_scale, format, index)
     rows, cols = x.shape
@@ -558,7 +575,7 @@ def fp4_quantize(x, format: str = "nvfp4", tensor_scale=None, stream=None) -> Fp
     both = t.empty(n_codes + (rows + 127) // 128 * ((cols + per - 1) // per) * 512, dtype=t.u8, device=x.device)
     p = both.data_ptr()
     rc = (_lib or load()).gemm_fp4_quantize(f, DTYPES[dt], rows, cols, x.data_ptr(), ld, _ptr(tensor_scale), p,
-                                            p + n_codes, _stream(t, index, stream))
+                                            p + n_codes, t.raw_stream(index))
     if rc != 0:
         raise GemmError(rc, what)
     q = Fp4Tensor.__new__(Fp4Tensor)
@@ -574,9 +591,12 @@ def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
     if code is None:
         _refuse(what, f"unknown dtype {dtype!r}")
     index, rows, cols = q._index, q._rows, q._cols
+    if stream is not None:
+        with t.on(stream, index):
+            return fp4_dequantize(q, dtype, out)
     if index != t.device_index():
         with t.torch.cuda.device(index):
-            return fp4_dequantize(q, dtype, out, stream)
+            return fp4_dequantize(q, dtype, out)
     if out is None:
         out, ld = t.empty((rows, cols), dtype=t.dtype[dtype], device=t.device(index)), cols or 1
     else:
@@ -586,7 +606,7 @@ def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
         ld = _ld(out)
     codes, scales, g = q._ptrs()
     rc = (_lib or load()).gemm_fp4_dequantize(FP4_FORMATS[q._format], code, rows, cols, codes, scales, g,
-                                              out.data_ptr(), ld, _stream(t, index, stream))
+                                              out.data_ptr(), ld, t.raw_stream(index))
     if rc != 0:
         raise GemmError(rc, what)
     return out
@@ -658,16 +678,18 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
 
     A [M, K] (activations), B [N, K] (a weight as it lies for x @ W.T), both in the same format.
     bias: FP32 [N]; residual: FP32 [M, N].  Plans are created once per (shape, format, strides,
-    epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.
+    epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.  (The
+    first call of a shape makes its plan, and is refused while a graph is being captured.)  With
+    `stream`, the call runs, and allocates, as if that were the current stream.
     """
     what, t = "fp4_matmul", _t()
     index, format, M, K, N = A._index, A._format, A._rows, A._cols, B._rows
     if B._index != index or B._format != format or B._cols != K:
         _refuse(what, "A and B need the same format, K and device")
-    if index != t.device_index():
-        with t.torch.cuda.device(index):
+    if stream is not None or index != t.device_index():
+        with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
             return fp4_matmul(A, B, alpha=alpha, bias=bias, act=act, residual=residual, beta=beta,
-                              out_dtype=out_dtype, out=out, stream=stream)
+                              out_dtype=out_dtype, out=out)
     if out_dtype not in DTYPES or act not in ("none", "gelu", "relu"):
         _refuse(what, "out_dtype: f32, f16 or bf16; act: none, gelu or relu")
     if bias is not None and (bias.dtype is not t.f32 or tuple(bias.shape) != (N,) or bias.get_device() != index
@@ -687,11 +709,12 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     key = (format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, index)
     pl = _fp4_plans.get(key)
     if pl is None:
+        _no_capture(t, what)
         ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
                       residual=residual is not None, beta=beta, ldr=ldr)
         pl = _fp4_plans[key] = gemm_fp4_plan(format, M, N, K, ldc, ep)
     rc = (_lib or load()).gemm_fp4_run(pl.handle, *A._ptrs(), *B._ptrs(), out.data_ptr(), _ptr(bias), _ptr(residual),
-                                       alpha, _stream(t, index, stream))
+                                       alpha, t.raw_stream(index))
     if rc != 0:
         raise GemmError(rc, what)
     return out
@@ -757,8 +780,9 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     x [T, H], router [E, H], w1 [E, I, H] ("gelu", "relu") or [E, 2I, H] ("swiglu": gate rows, then up
     rows), w2 [E, H, I], all FP16 or all BF16, rows contiguous.  Returns y [T, H], or with
     return_routing (y, expert ids int32 [T, top_k], their weights FP32 [T, top_k]).  Plans are kept per
-    shape, strides and device; every call has a workspace of its own from torch's allocator, on the
-    stream that it runs on.
+    shape, strides and device (the first call makes its plan, and is refused while a graph is being
+    captured); every call has a workspace of its own from torch's allocator.  With
+    `stream`, the call runs, and allocates, as if that were the current stream.
     """
     what, t = "moe_layer", _t()
     dt = t.name.get(x.dtype)
@@ -776,10 +800,10 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
             or router.dtype is not dtype or w1.dtype is not dtype or w2.dtype is not dtype \
             or (out is not None and (out.get_device() != index or out.dtype is not dtype)):
         _refuse(what, "tensors of x's dtype on x's device, a GPU, are wanted")
-    if index != t.device_index():
-        with t.torch.cuda.device(index):
+    if stream is not None or index != t.device_index():
+        with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
             return moe_layer(x, router, w1, w2, top_k, act=act, normalize=normalize, out=out,
-                             return_routing=return_routing, stream=stream)
+                             return_routing=return_routing)
     dev = x.device
     if out is None:
         out = t.empty((T, H), dtype=dtype, device=dev)
@@ -800,20 +824,16 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     key = (dt, T, E, top_k, H, I, act, normalize, ldx, ldr, ld1, st1, ld2, st2, ldy, index)
     pl = _moe_plans.get(key)
     if pl is None:
+        _no_capture(t, what)
         pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=ldx, ld_router=ldr,
                                              ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=ldy)
     ids = wts = None
     if return_routing:
         ids = t.empty((T, top_k), dtype=t.i32, device=dev)
         wts = t.empty((T, top_k), dtype=t.f32, device=dev)
-    if stream is None:
-        ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
-    else:  # the workspace belongs to the stream that uses it
-        s = t.torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-        with t.torch.cuda.stream(s):
-            ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
+    ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=dev)
     rc = (_lib or load()).gemm_moe_run(pl.handle, x.data_ptr(), router.data_ptr(), w1.data_ptr(), w2.data_ptr(), out.data_ptr(),
-                            _ptr(ids), _ptr(wts), ws.data_ptr(), _stream(t, index, stream))
+                            _ptr(ids), _ptr(wts), ws.data_ptr(), t.raw_stream(index))
     if rc != 0:
         raise GemmError(rc, what)
     return (out, ids, wts) if return_routing else out

@@ -60,10 +60,10 @@ int check_convert(int format, int dtype, int64_t rows, int64_t cols, int64_t ld,
 
 extern "C" {
 
-int64_t gemm_fp4_row_bytes(int64_t cols) { return cols < 0 ? 0 : fp4_row_bytes(cols); }
+int64_t gemm_fp4_row_bytes(int64_t cols) { return cols < 0 || !sizes_ok(0, cols) ? 0 : fp4_row_bytes(cols); }
 
 int64_t gemm_fp4_scales_bytes(gemm_fp4_format_t format, int64_t rows, int64_t cols) {
-    if (!format_ok(format) || rows < 0 || cols < 0) return 0;
+    if (!format_ok(format) || rows < 0 || cols < 0 || !sizes_ok(rows, cols)) return 0;
     return fp4_row_tiles(rows) * fp4_col_tiles(format, cols) * kFp4TileBytes;
 }
 

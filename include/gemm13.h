@@ -294,7 +294,8 @@ int gemm_run_noalloc(gemm_dtype_t dtype, int64_t M, int64_t N, int64_t K,
  *               element = code * fl32(s * g), g from a device pointer
  *               (NULL: 1), positive and finite.
  * Padding in both arrays is zero; gemm_fp4_quantize writes all of it.  Both
- * arrays are 16-byte aligned.
+ * arrays are 16-byte aligned.  The two calls below return 0 for sizes or formats
+ * that the library does not take.
  */
 int64_t gemm_fp4_row_bytes(int64_t cols);
 int64_t gemm_fp4_scales_bytes(gemm_fp4_format_t format, int64_t rows, int64_t cols);
@@ -405,7 +406,8 @@ typedef struct gemm_moe_plan_s* gemm_moe_plan_t;
 void gemm_moe_desc_init(gemm_moe_desc_t* d);
 
 /* Validates the layer and allocates a status word on the current device.
- * Errors: INVALID_ARG, UNSUPPORTED (sizes, FP32), NO_DEVICE, OUT_OF_MEMORY, CUDA. */
+ * Errors: INVALID_ARG, UNSUPPORTED (FP32; sizes beyond those above; 2^30 or more
+ * pieces of 16 rows x 64 elements in W1 or W2), NO_DEVICE, OUT_OF_MEMORY, CUDA. */
 int gemm_moe_plan(const gemm_moe_desc_t* desc, gemm_moe_plan_t* out_plan);
 
 /* Device bytes that each run needs as its workspace; 0 for a bad plan. */
@@ -413,10 +415,9 @@ int64_t gemm_moe_workspace_bytes(gemm_moe_plan_t plan);
 
 /*
  * Enqueues the layer (two kernels) on `stream`.  All pointers are device pointers,
- * aligned to their element type; any other alignment is accepted, but weights whose
- * rows all start on 16 bytes and whose H and I are multiples of 8 load fastest.
- * (Other rows are read in whole 16-byte pieces of memory, each of which holds at
- * least one of their elements.)  expert_ids (int32 [T][top_k], largest weight first)
+ * aligned to their element type; weights whose rows all start on 32 bytes (16) and
+ * whose H and I are multiples of 16 (8) load fastest.  (Rows anyhow are read in whole
+ * 16-byte pieces of memory, each of which holds at least one of their elements.)  expert_ids (int32 [T][top_k], largest weight first)
  * and expert_weights (FP32 [T][top_k]) may be NULL.  workspace: 256-byte aligned,
  * gemm_moe_workspace_bytes() long, any contents; it belongs to the run until the run
  * has finished on the GPU.  Runs with workspaces of their own may overlap.  No output

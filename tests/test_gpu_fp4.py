@@ -342,3 +342,20 @@ def test_python_refusals():
     plan = g13.gemm_fp4_plan("nvfp4", 5, 5, 64, 5)
     with pytest.raises(E):
         g13.gemm_fp4_run(plan, q, q, x)
+
+
+def test_stream_argument():
+    # a stream or its handle: the same results, in order on that stream, whatever the current one does
+    x = torch.randn(300, 640, device="cuda")
+    w = g13.fp4_quantize(torch.randn(500, 640, device="cuda"), "nvfp4")
+    want = g13.fp4_matmul(g13.fp4_quantize(x, "nvfp4"), w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for s in (side, side.cuda_stream):
+        for _ in range(4):
+            torch.randn(300, 500, device="cuda")  # allocations of the current stream in between
+            q = g13.fp4_quantize(x, "nvfp4", stream=s)
+            y = g13.fp4_matmul(q, w, stream=s)
+            v = g13.fp4_dequantize(q, "bf16", stream=s)
+        side.synchronize()
+        assert torch.equal(y, want) and torch.equal(v, g13.fp4_dequantize(g13.fp4_quantize(x, "nvfp4"), "bf16"))

@@ -202,3 +202,32 @@ def test_with_4bit_layers():
     for _ in range(5):
         gr.replay()
     assert torch.equal(out, y)
+
+
+def test_first_call_in_a_capture_is_refused():
+    # a plan allocates: the call is refused, and the capture goes on
+    x, router, w1, w2 = on_gpu(inputs("capture", 3, 4, 88, 24, "relu", "f16"))
+    q = g13.fp4_quantize(torch.randn(3, 88, device="cuda"))
+    gr, y = torch.cuda.CUDAGraph(), torch.zeros(4, device="cuda")
+    with torch.cuda.graph(gr):
+        with pytest.raises(g13.GemmError, match="before capturing"):
+            g13.moe_layer(x, router, w1, w2, 2, act="relu")
+        with pytest.raises(g13.GemmError, match="before capturing"):
+            g13.fp4_matmul(q, q, act="relu")
+        y += 1
+    gr.replay()
+    torch.cuda.synchronize()
+    assert bool((y == 1).all())
+    assert g13.moe_layer(x, router, w1, w2, 2, act="relu").shape == (3, 88)
+
+
+def test_stream_argument():
+    T, E, k, H, I = 6, 8, 3, 200, 64
+    s = on_gpu(inputs("stream", T, E, H, I, "swiglu", "bf16", top_k=k))
+    want = g13.moe_layer(*s, k)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for st in (side, side.cuda_stream):
+        ys = [g13.moe_layer(*s, k, stream=st) for _ in range(4)]
+        side.synchronize()
+        assert all(torch.equal(y, want) for y in ys)

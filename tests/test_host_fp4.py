@@ -27,6 +27,7 @@ def test_sizes(lib):
             assert lib.gemm_fp4_scales_bytes(f, rows, cols) == -(-rows // 128) * -(-nb // 4) * 512
     assert lib.gemm_fp4_scales_bytes(7, 10, 10) == 0
     assert lib.gemm_fp4_scales_bytes(0, -1, 10) == 0
+    assert lib.gemm_fp4_scales_bytes(0, 2 ** 62, 2 ** 62) == 0 and lib.gemm_fp4_row_bytes(2 ** 63 - 1) == 0
 
 
 P = 1 << 20  # an aligned address that no refused call reads
