@@ -25,11 +25,15 @@
 //
 // Large products run on CTA pairs (tcgen05 cta_group::2): 256 weight rows x 256
 // tokens, each CTA holding its own 128 weight rows and half of the tokens, so
-// that a stage moves 38 KB through each SM's shared memory instead of 54 KB for
-// 128 x 256.  256 accumulator columns and the scales do not fit TMEM twice: two
+// that a stage brings 38 KB into each SM instead of 54 KB for 128 x 256.  At
+// 8192^3 (nvfp4) that is 185-190 us, 5.8-5.9 PFLOP/s: the tensor cores are busy 66 %
+// of the cycles, and 14 TB/s come from L2, close to the 15 TB/s that the same loads
+// reached with nothing else running.  256 accumulator columns and the scales do not fit TMEM twice: two
 // accumulators overlap by 96 columns, which the epilogue reads first and hands
 // back, so the next tile's MMAs start before the rest is stored.
 //
+// Up to 64 tokens the weights' bytes are the cost (1 x 6144 x 6144: 8.0 us, of
+// which 3.2 would be HBM's share and 3 the launch, set-up and cluster barriers).
 // Few tokens leave fewer tiles than SMs: a cluster then splits K, each CTA
 // leaves its partial sums in its own shared memory, and every CTA adds one
 // share of the columns through distributed shared memory, in rank order (the
@@ -753,7 +757,10 @@ int launch_fp4_gemm(const Fp4Config& c, int fmt, const Fp4Operand& A, const Fp4O
         case 32: ce = launch_bn<32, 8>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
         case 64: ce = launch_bn<64, 7>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
         case 128: ce = launch_bn<128, 6>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
-        case 256: ce = launch_fmt<256, 5, F4_PAIR>(fmt, m, a, 1, lc.num_sms, lc.stream); break;
+        case 256:  // as many stages as shared memory holds (mxfp4's 35 KB: 6, 184 us at 8192^3 instead of 187)
+            ce = fmt == GEMM_MXFP4 ? launch_f4<256, 6, GEMM_MXFP4, F4_PAIR>(m, a, 1, lc.num_sms, lc.stream)
+                                   : launch_f4<256, 5, GEMM_NVFP4, F4_PAIR>(m, a, 1, lc.num_sms, lc.stream);
+            break;
         default: return GEMM_ERR_UNSUPPORTED;
     }
     return cuda_status(ce);
