@@ -296,6 +296,14 @@ __device__ __forceinline__ void f4_tile(const F4Args& a, int64_t t, int64_t& mt,
     mt = w / gn;
 }
 
+// alpha gA gB, rounded once (a partial product may lie outside FP32).
+__device__ __forceinline__ float f4_alpha(const F4Args& a) {
+    double f = a.e.alpha;
+    if (a.gw) f *= static_cast<double>(__ldg(a.gw));
+    if (a.gx) f *= static_cast<double>(__ldg(a.gx));
+    return static_cast<float>(f);
+}
+
 // F4_SPLIT: one tile per cluster, K divided over its CTAs.  Else persistent, a
 // CTA (pair) taking one tile after another.
 template <int BN, int STAGES, int FMT, int MODE>
@@ -554,9 +562,7 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
         constexpr int CH = BN >= 32 ? 32 : 16;  // columns of a chunk
         constexpr int STEP = CH * (L::EW / 4);  // from one of its chunks to the next
         const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
-        float alpha = args.e.alpha;
-        if (args.gw) alpha *= __ldg(args.gw);
-        if (args.gx) alpha *= __ldg(args.gx);
+        const float alpha = f4_alpha(args);
         // K = 0 issued no MMA: the sum is zero
         const bool none = kb_lo == kb_hi;
         int lt = 0;
@@ -622,9 +628,7 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
             f4_tile(args, t_begin, mt, nt);
             const int q = warp & 3, h = (warp - 2) >> 2;
             const uint32_t n = static_cast<uint32_t>(nt * FW) + q * 32 + lane;
-            float alpha = args.e.alpha;
-            if (args.gw) alpha *= __ldg(args.gw);
-            if (args.gx) alpha *= __ldg(args.gx);
+            const float alpha = f4_alpha(args);
             const float bias = args.e.bias && n < static_cast<uint32_t>(args.N) ? __ldg(args.e.bias + n) : 0.0f;
             const int cols = static_cast<int>(min(static_cast<int64_t>(BN), args.M - mt * BN));
             const uint32_t part = smem_u32(smem) + (q * 32 + lane) * 16;

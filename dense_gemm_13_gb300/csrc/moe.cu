@@ -38,7 +38,9 @@
 // 112 us, 5.7 TB/s (0.85 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 446 us,
 // 5.4 TB/s (the tokens' values take a third of what the SMs read); one token, 2 of 8
 // experts of 768 x 3072: 16 us, of which 3 are bytes and the rest a chain of two
-// kernels, the routing, the barrier and the join, each a trip or two to L2.
+// kernels, the routing, the barrier and the join, each a trip or two to L2.  (Blocks of
+// 16 columns instead of 64 in the down product cut fewer of them between CTAs and
+// still took 17 us: sixteen teams' sums are slower to add than four's.)
 //
 // Products: mma.sync m16n8k16, weights as the 16 rows and a group of 8 tokens as
 // the columns.  The order of k within a step is free as long as both operands share
@@ -807,7 +809,6 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     }
     // The first and the last block: whoever arrives last at a cut one joins it.
     if (ob_lo * block >= c_lo && (ob_hi + 1) * block <= c_hi) return;  // neither is cut
-    __threadfence();
     __syncthreads();
     if (threadIdx.x < 2) {
         const int ob = threadIdx.x == 0 ? ob_lo : ob_hi;
@@ -817,8 +818,10 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
             // blocks are cut between neighbours, none of which is empty
             const unsigned parts = ctas.owner((ob + 1) * block - 1) - ctas.owner(ob * block) + 1;
             unsigned* ctr = reinterpret_cast<unsigned*>(a.ws + a.w.counters);
-            last = atomicAdd(ctr + ob, 1u) == parts - 1;
-            __threadfence();
+            // releases the CTA's partial sums (written before the barrier), acquires the others'
+            unsigned before;
+            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(ctr + ob) : "memory");
+            last = before == parts - 1;
         }
         s.last[threadIdx.x] = last;
     }

@@ -188,6 +188,35 @@ def test_product_exact_integers(fmt, shape):
     assert bool((big == 7).all()), "store outside the M x N window"
 
 
+@pytest.mark.parametrize("shape", [(100001, 3, 70), (3, 100001, 70), (5, 130, 70000), (130, 130, 20000)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_product_long_sides(shape):
+    M, N, K = shape
+    r = rng("long", shape)
+    (A, a), (B, b) = operand(r, M, K, "nvfp4", ints=True), operand(r, N, K, "nvfp4", ints=True)
+    assert 144 * K < 2 ** 24
+    assert np.array_equal(g13.fp4_matmul(A, B).cpu().numpy(), a @ b.T)
+
+
+def test_scales_whose_partial_product_overflows():
+    r = rng("range")
+    (A, a), (B, b) = operand(r, 20, 64, "nvfp4", ints=True), operand(r, 40, 64, "nvfp4", ints=True)
+
+    def scaled(q, g):
+        return g13.Fp4Tensor(q.codes, q.scales, q.rows, q.cols, "nvfp4", torch.tensor([g], device="cuda"))
+
+    # alpha gB lies beyond FP32, alpha gA gB does not: powers of two, so the result is exact
+    y = g13.fp4_matmul(scaled(A, 2.0 ** -100), scaled(B, 2.0 ** 90), alpha=2.0 ** 60)
+    assert np.array_equal(y.cpu().numpy(), (a @ b.T * 2.0 ** 50).astype(np.float32))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("shape", [(200003, 17), (2, 300007)], ids=lambda s: f"{s[0]}x{s[1]}")
+def test_quantise_long_sides(fmt, shape):
+    x = matrix(rng("ql", fmt, shape), *shape)
+    check_quantised(g13.fp4_quantize(torch.from_numpy(x).cuda(), fmt), x, fmt, 1.0)
+
+
 def check_product(got, A, B, out, bias=None, act="none", R=None, alpha=1.0, beta=1.0):
     K = A.shape[1]
     S = np.abs(A) @ np.abs(B).T * abs(alpha)

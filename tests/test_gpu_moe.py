@@ -94,6 +94,17 @@ def test_strides(T, pad):
     assert torch.equal(g13.moe_layer(x, router, w1t, w2, k), g13.moe_layer(x, router, w1, w2, k))
 
 
+@pytest.mark.parametrize("case", [(64, 2, 2, 16384, 24), (8, 3, 2, 16384, 17), (1, 1, 1, 16, 100000),
+                                  (9, 2, 1, 40, 30001), (64, 512, 32, 48, 8), (1, 512, 32, 8, 640)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_extremes(case):
+    T, E, k, H, I = case
+    ts = on_gpu(inputs((case, "ends"), T, E, H, I, "swiglu", "bf16", top_k=k))
+    y, ids, wts = g13.moe_layer(*ts, k, return_routing=True)
+    check(*ts, k, "swiglu", True, y, ids, wts)
+    assert torch.equal(y, g13.moe_layer(*ts, k))
+
+
 def test_ties_go_to_the_lowest_index():
     T, E, k, H, I = 6, 40, 5, 96, 16
     x, router, w1, w2 = on_gpu(inputs("ties", T, E, H, I, "gelu", "bf16"))
