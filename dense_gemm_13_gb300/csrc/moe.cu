@@ -35,8 +35,9 @@
 // that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Measured (bytes of the chosen experts over time): 16 tokens, 64 experts of 2048 x 1024:
-// 112 us, 5.7 TB/s (0.85 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 446 us,
-// 5.4 TB/s (the tokens' values take a third of what the SMs read); one token, 2 of 8
+// 112 us, 5.7 TB/s (0.85 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 452 us,
+// 5.3 TB/s (the tokens' values take a third of what the SMs read; where an expert
+// has 32 tokens or more they take most of it, and 2.5 TB/s remain); one token, 2 of 8
 // experts of 768 x 3072: 16 us, of which 3 are bytes and the rest a chain of two
 // kernels, the routing, the barrier and the join, each a trip or two to L2.  (Blocks of
 // 16 columns instead of 64 in the down product cut fewer of them between CTAs and
@@ -399,25 +400,55 @@ __device__ __forceinline__ void route_tokens(const MoeArgs& a, MoeShared& s, Moe
     }
 }
 
-// acc[16 rows x 8 NT columns] += 16 values of rows g and g + 8 (p, q) times the tokens' values at k
+// The tokens of a unit's columns: this lane's rows (padded to whole steps of 128 bytes).  Up to
+// 16 columns as pointers, read in 16-byte pieces; more as 32-bit offsets in steps, read in
+// 32-byte pieces, which leaves registers (64 tokens on 8 of 16 experts each, 4096 x 1536: 237 us
+// instead of 266; with few columns the address arithmetic stands before every load: 489 us
+// instead of 452 with 64 tokens on 8 of 64 experts).
+template <int NT>
+struct Columns {
+    static constexpr bool FEW = NT <= 2;
+    const uint16_t* base;
+    const uint16_t* ptr[FEW ? NT : 1];
+    uint32_t row[FEW ? 1 : NT];
+    __device__ __forceinline__ void set(int j, uint32_t first_step) {
+        if constexpr (FEW)
+            ptr[j] = base + static_cast<uint64_t>(first_step) * 64;
+        else
+            row[j] = first_step;
+    }
+};
+// acc[16 rows x 8 NT columns] += 16 values of rows g and g + 8 (p, q) times the tokens' values of step s
 // (from L1 or L2; asking for them a step ahead took registers from the weights and was slower).
 template <typename T, int NT, int NTMAX>
-__device__ __forceinline__ void mma_step(const uint32_t (&p)[8], const uint32_t (&q)[8],
-                                         const uint16_t* const (&xr)[NT], int k, float (&acc)[NTMAX][4]) {
+__device__ __forceinline__ void mma_step(const uint32_t (&p)[8], const uint32_t (&q)[8], const Columns<NT>& x, int s,
+                                         int t4, float (&acc)[NTMAX][4]) {
+    const int k = s * 64 + t4 * 16;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; ++j) {
+        if constexpr (Columns<NT>::FEW) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(xr[j] + k + 8 * i);
-            mma16816<T>(acc[j], p[4 * i], q[4 * i], p[4 * i + 1], q[4 * i + 1], v.x, v.y);
-            mma16816<T>(acc[j], p[4 * i + 2], q[4 * i + 2], p[4 * i + 3], q[4 * i + 3], v.z, v.w);
+            for (int i = 0; i < 2; ++i) {
+                const uint4 v = *reinterpret_cast<const uint4*>(x.ptr[j] + k + 8 * i);
+                mma16816<T>(acc[j], p[4 * i], q[4 * i], p[4 * i + 1], q[4 * i + 1], v.x, v.y);
+                mma16816<T>(acc[j], p[4 * i + 2], q[4 * i + 2], p[4 * i + 3], q[4 * i + 3], v.z, v.w);
+            }
+        } else {
+            const ulonglong4_32a v = *reinterpret_cast<const ulonglong4_32a*>(
+                x.base + static_cast<uint64_t>(x.row[j] + s) * 64 + t4 * 16);
+            const unsigned long long w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                mma16816<T>(acc[j], p[2 * i], q[2 * i], p[2 * i + 1], q[2 * i + 1], static_cast<uint32_t>(w[i]),
+                            static_cast<uint32_t>(w[i] >> 32));
         }
+    }
 }
 
 // One warp, steps [s0, s1) of a unit whose rows lie anyhow.  w0, w1: this lane's two weight
-// rows, xr: its token rows (padded), K elements of a weight row.
+// rows, x: its token rows, K elements of a weight row.
 template <typename T, int NT, int NTMAX>
-__device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT],
+__device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x,
                                           int s0, int s1, int K, int t4, float (&acc)[NTMAX][4]) {
     const int sf = min(s1, K / 64);  // steps before it are whole
     w0 += t4 * 16;
@@ -436,7 +467,7 @@ __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1
         uint32_t p[8], q[8];
         use_raw16(ra[b], o0, p);
         use_raw16(rb[b], o1, q);
-        mma_step<T, NT, NTMAX>(p, q, xr, s * 64 + t4 * 16, acc);
+        mma_step<T, NT, NTMAX>(p, q, x, s, t4, acc);
     };
     load(0, s0);
     for (int s = s0; s < sf; s += 2) {
@@ -455,14 +486,14 @@ __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1
             p[4 * i] = a.x, p[4 * i + 1] = a.y, p[4 * i + 2] = a.z, p[4 * i + 3] = a.w;
             q[4 * i] = b.x, q[4 * i + 1] = b.y, q[4 * i + 2] = b.z, q[4 * i + 3] = b.w;
         }
-        mma_step<T, NT, NTMAX>(p, q, xr, k + t4 * 16, acc);
+        mma_step<T, NT, NTMAX>(p, q, x, sf, t4, acc);
     }
 }
 
 // The same for rows that all lie on 16 bytes (ROWS_16) or 32 (ROWS_32) and are a multiple of
 // that long: two batches of U steps in flight in registers, 64 KB per SM and batch at U = 2.
 template <typename T, int ROWS, int NT, int NTMAX>
-__device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT],
+__device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x,
                                               int s0, int s1, int K, int t4, float (&acc)[NTMAX][4]) {
     constexpr int U = NT <= 2 ? 2 : 1;
     Row16 wa[2][U], wb[2][U];
@@ -479,7 +510,7 @@ __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s + u >= s1) break;
-            mma_step<T, NT, NTMAX>(wa[b][u].v, wb[b][u].v, xr, (s + u) * 64 + t4 * 16, acc);
+            mma_step<T, NT, NTMAX>(wa[b][u].v, wb[b][u].v, x, s + u, t4, acc);
         }
     };
     load(0, s0);
@@ -492,12 +523,12 @@ __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t
 }
 
 template <typename T, int ROWS, int NT, int NTMAX>
-__device__ __forceinline__ void steps(const uint16_t* w0, const uint16_t* w1, const uint16_t* const (&xr)[NT], int s0,
+__device__ __forceinline__ void steps(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x, int s0,
                                       int s1, int K, int t4, float (&acc)[NTMAX][4]) {
     if constexpr (ROWS == ROWS_ANY)
-        steps_any<T, NT, NTMAX>(w0, w1, xr, s0, s1, K, t4, acc);
+        steps_any<T, NT, NTMAX>(w0, w1, x, s0, s1, K, t4, acc);
     else
-        steps_aligned<T, ROWS, NT, NTMAX>(w0, w1, xr, s0, s1, K, t4, acc);
+        steps_aligned<T, ROWS, NT, NTMAX>(w0, w1, x, s0, s1, K, t4, acc);
 }
 
 // Runs f with the least of 1, 2, 4, 8 (at most NTMAX) groups of 8 columns that hold n.
@@ -652,11 +683,12 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
             const int n = __popcll(s.mask[e]), off = s.off[e];
             with_groups<NTMAX>(n, [&](auto tag) {
                 constexpr int NT = decltype(tag)::value;
-                const uint16_t* xr[NT];
+                Columns<NT> x;
+                x.base = xp;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)  // columns past the last read its row: their sums are not used
-                    xr[j] = xp + s.slot_token[off + min(j * 8 + g, n - 1)] * a.w.hp;
-                steps<T, ROWS, NT, NTMAX>(row(u, g), row(u, g + 8), xr, s0, s1, static_cast<int>(d.H), t4, acc);
+                    x.set(j, s.slot_token[off + min(j * 8 + g, n - 1)] * static_cast<uint32_t>(KS));
+                steps<T, ROWS, NT, NTMAX>(row(u, g), row(u, g + 8), x, s0, s1, static_cast<int>(d.H), t4, acc);
             });
             if (s0 == 0 && s1 == KS) {
                 finish(u, acc);
@@ -760,11 +792,11 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         float acc[NTMAX][4] = {};
         with_groups<NTMAX>(n, [&](auto tag) {
             constexpr int NT = decltype(tag)::value;
-            const uint16_t* xr[NT];
+            Columns<NT> x;
+            x.base = reinterpret_cast<const uint16_t*>(h);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                xr[j] = reinterpret_cast<const uint16_t*>(h) + (off + min(j * 8 + g, n - 1)) * a.w.ip;
-            steps<T, ROWS, NT, NTMAX>(row(v, g), row(v, g + 8), xr, s0, s1, static_cast<int>(d.I), t4, acc);
+            for (int j = 0; j < NT; ++j) x.set(j, static_cast<uint32_t>(off + min(j * 8 + g, n - 1)) * KS);
+            steps<T, ROWS, NT, NTMAX>(row(v, g), row(v, g + 8), x, s0, s1, static_cast<int>(d.I), t4, acc);
         });
 #pragma unroll
         for (int j = 0; j < NTMAX; ++j) {
