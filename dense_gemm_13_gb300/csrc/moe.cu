@@ -35,10 +35,10 @@
 // that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Measured (bytes of the chosen experts over time): 16 tokens, 64 experts of 2048 x 1024:
-// 112 us, 5.7 TB/s (0.85 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 452 us,
-// 5.3 TB/s (the tokens' values take a third of what the SMs read; where an expert
-// has 32 tokens or more they take most of it, and 2.5 TB/s remain); one token, 2 of 8
-// experts of 768 x 3072: 16 us, of which 3 are bytes and the rest a chain of two
+// 116 us, 5.5 TB/s (0.82 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 486 us,
+// 5.0 TB/s (the tokens' values take half of what the SMs read; where an expert has 32
+// tokens or more they take most of it, and 2.5 TB/s remain); one token, 2 of 8
+// experts of 768 x 3072: 16.8 us, of which 3 are bytes and the rest a chain of two
 // kernels, the routing, the barrier and the join, each a trip or two to L2.  (Blocks of
 // 16 columns instead of 64 in the down product cut fewer of them between CTAs and
 // still took 17 us: sixteen teams' sums are slower to add than four's.)
@@ -47,8 +47,10 @@
 // the columns.  The order of k within a step is free as long as both operands share
 // it, so a thread takes 16 consecutive values of a row (four MMAs' worth) as its
 // fragments.  (tcgen05 would need a 128-row tile and TMEM round trips, to do
-// arithmetic that is far from the bound.)  FP32 accumulation; h = act(...) is rounded
-// to the operands' 16-bit type, which the second product needs as its operand.
+// arithmetic that is far from the bound.)  FP32 accumulation; h = act(...) goes into the
+// second product, whose operands are 16-bit, as two numbers of that type, its rounding and
+// the rest.  (Rounded once, it made the output's error 1.4 times that of the output's own
+// rounding, and the layers took 112, 452 and 16 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -196,6 +198,9 @@ __device__ __forceinline__ __half cast16(float v) { return __float2half_rn(v); }
 template <>
 __device__ __forceinline__ __nv_bfloat16 cast16(float v) { return __float2bfloat16_rn(v); }
 
+__device__ __forceinline__ float as_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1);
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
     }
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws + a.w.h);
     const int pad = static_cast<int>(a.w.ip - d.I);
-    for (int i = tid; i < static_cast<int>(d.T * d.top_k) * pad; i += nthreads)
+    for (int i = tid; i < static_cast<int>(d.T * d.top_k) * 2 * pad; i += nthreads)  // both parts of each h
         h[static_cast<int64_t>(i / pad) * a.w.ip + d.I + i % pad] = 0;
 }
 
@@ -419,37 +424,41 @@ struct Columns {
     }
 };
 // acc[16 rows x 8 NT columns] += 16 values of rows g and g + 8 (p, q) times the tokens' values of step s
-// (from L1 or L2; asking for them a step ahead took registers from the weights and was slower).
-template <typename T, int NT, int NTMAX>
+// (from L1 or L2; asking for them a step ahead took registers from the weights and was slower).  PARTS = 2:
+// and times their second parts, KS steps further on.
+template <typename T, int NT, int NTMAX, int PARTS>
 __device__ __forceinline__ void mma_step(const uint32_t (&p)[8], const uint32_t (&q)[8], const Columns<NT>& x, int s,
-                                         int t4, float (&acc)[NTMAX][4]) {
-    const int k = s * 64 + t4 * 16;
+                                         int KS, int t4, float (&acc)[NTMAX][4]) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        if constexpr (Columns<NT>::FEW) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint4 v = *reinterpret_cast<const uint4*>(x.ptr[j] + k + 8 * i);
-                mma16816<T>(acc[j], p[4 * i], q[4 * i], p[4 * i + 1], q[4 * i + 1], v.x, v.y);
-                mma16816<T>(acc[j], p[4 * i + 2], q[4 * i + 2], p[4 * i + 3], q[4 * i + 3], v.z, v.w);
+        for (int part = 0; part < PARTS; ++part) {
+            const int k = (s + part * KS) * 64 + t4 * 16;
+            if constexpr (Columns<NT>::FEW) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(x.ptr[j] + k + 8 * i);
+                    mma16816<T>(acc[j], p[4 * i], q[4 * i], p[4 * i + 1], q[4 * i + 1], v.x, v.y);
+                    mma16816<T>(acc[j], p[4 * i + 2], q[4 * i + 2], p[4 * i + 3], q[4 * i + 3], v.z, v.w);
+                }
+            } else {
+                const ulonglong4_32a v =
+                    *reinterpret_cast<const ulonglong4_32a*>(x.base + static_cast<uint64_t>(x.row[j]) * 64 + k);
+                const unsigned long long w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma16816<T>(acc[j], p[2 * i], q[2 * i], p[2 * i + 1], q[2 * i + 1], static_cast<uint32_t>(w[i]),
+                                static_cast<uint32_t>(w[i] >> 32));
             }
-        } else {
-            const ulonglong4_32a v = *reinterpret_cast<const ulonglong4_32a*>(
-                x.base + static_cast<uint64_t>(x.row[j] + s) * 64 + t4 * 16);
-            const unsigned long long w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mma16816<T>(acc[j], p[2 * i], q[2 * i], p[2 * i + 1], q[2 * i + 1], static_cast<uint32_t>(w[i]),
-                            static_cast<uint32_t>(w[i] >> 32));
         }
     }
 }
 
 // One warp, steps [s0, s1) of a unit whose rows lie anyhow.  w0, w1: this lane's two weight
 // rows, x: its token rows, K elements of a weight row.
-template <typename T, int NT, int NTMAX>
+template <typename T, int NT, int NTMAX, int PARTS>
 __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x,
-                                          int s0, int s1, int K, int t4, float (&acc)[NTMAX][4]) {
+                                          int s0, int s1, int K, int KS, int t4, float (&acc)[NTMAX][4]) {
     const int sf = min(s1, K / 64);  // steps before it are whole
     w0 += t4 * 16;
     w1 += t4 * 16;
@@ -467,7 +476,7 @@ __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1
         uint32_t p[8], q[8];
         use_raw16(ra[b], o0, p);
         use_raw16(rb[b], o1, q);
-        mma_step<T, NT, NTMAX>(p, q, x, s, t4, acc);
+        mma_step<T, NT, NTMAX, PARTS>(p, q, x, s, KS, t4, acc);
     };
     load(0, s0);
     for (int s = s0; s < sf; s += 2) {
@@ -486,15 +495,15 @@ __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1
             p[4 * i] = a.x, p[4 * i + 1] = a.y, p[4 * i + 2] = a.z, p[4 * i + 3] = a.w;
             q[4 * i] = b.x, q[4 * i + 1] = b.y, q[4 * i + 2] = b.z, q[4 * i + 3] = b.w;
         }
-        mma_step<T, NT, NTMAX>(p, q, x, sf, t4, acc);
+        mma_step<T, NT, NTMAX, PARTS>(p, q, x, sf, KS, t4, acc);
     }
 }
 
 // The same for rows that all lie on 16 bytes (ROWS_16) or 32 (ROWS_32) and are a multiple of
 // that long: two batches of U steps in flight in registers, 64 KB per SM and batch at U = 2.
-template <typename T, int ROWS, int NT, int NTMAX>
+template <typename T, int ROWS, int NT, int NTMAX, int PARTS>
 __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x,
-                                              int s0, int s1, int K, int t4, float (&acc)[NTMAX][4]) {
+                                              int s0, int s1, int K, int KS, int t4, float (&acc)[NTMAX][4]) {
     constexpr int U = NT <= 2 ? 2 : 1;
     Row16 wa[2][U], wb[2][U];
     const auto load = [&](int b, int s) {
@@ -510,7 +519,7 @@ __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (s + u >= s1) break;
-            mma_step<T, NT, NTMAX>(wa[b][u].v, wb[b][u].v, x, s + u, t4, acc);
+            mma_step<T, NT, NTMAX, PARTS>(wa[b][u].v, wb[b][u].v, x, s + u, KS, t4, acc);
         }
     };
     load(0, s0);
@@ -522,13 +531,13 @@ __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t
     }
 }
 
-template <typename T, int ROWS, int NT, int NTMAX>
+template <typename T, int ROWS, int NT, int NTMAX, int PARTS>
 __device__ __forceinline__ void steps(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x, int s0,
-                                      int s1, int K, int t4, float (&acc)[NTMAX][4]) {
+                                      int s1, int K, int KS, int t4, float (&acc)[NTMAX][4]) {
     if constexpr (ROWS == ROWS_ANY)
-        steps_any<T, NT, NTMAX>(w0, w1, x, s0, s1, K, t4, acc);
+        steps_any<T, NT, NTMAX, PARTS>(w0, w1, x, s0, s1, K, KS, t4, acc);
     else
-        steps_aligned<T, ROWS, NT, NTMAX>(w0, w1, x, s0, s1, K, t4, acc);
+        steps_aligned<T, ROWS, NT, NTMAX, PARTS>(w0, w1, x, s0, s1, K, KS, t4, acc);
 }
 
 // Runs f with the least of 1, 2, 4, 8 (at most NTMAX) groups of 8 columns that hold n.
@@ -635,6 +644,13 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         const Share warps(n_u % kMoeWarps * KS, kMoeWarps);
         const int lo = warps.lo(warp), hi = warps.lo(warp + 1);
         const uint16_t* w1 = static_cast<const uint16_t*>(a.w1);
+        // An h in two parts (an infinity, or NaN, in the first alone).
+        const auto put = [&](T* p, float v) {
+            const T hi = cast16<T>(v);
+            const float f = as_float(hi);
+            p[0] = hi;
+            p[a.w.ip] = cast16<T>(fabsf(f) < INFINITY ? v - f : 0.0f);
+        };
         const auto finish = [&](int u, const float (&acc)[NTMAX][4]) {
             const int e = s.active[u / UB];
             const int i0 = u % UB * per;
@@ -645,13 +661,13 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                 for (int c = 0; c < 2; ++c) {
                     const int col = j * 8 + t4 * 2 + c;
                     if (col >= n) continue;
-                    T* row = h + (off + col) * a.w.ip;
+                    T* row = h + (off + col) * 2 * a.w.ip;
                     const float v0 = acc[j][c], v1 = acc[j][2 + c];
                     if (gated) {
-                        if (i0 + g < d.I) row[i0 + g] = cast16<T>(v0 / (1.0f + expf(-v0)) * v1);
+                        if (i0 + g < d.I) put(row + i0 + g, v0 / (1.0f + expf(-v0)) * v1);
                     } else {
-                        if (i0 + g < d.I) row[i0 + g] = cast16<T>(moe_act(d.act, v0));
-                        if (i0 + g + 8 < d.I) row[i0 + g + 8] = cast16<T>(moe_act(d.act, v1));
+                        if (i0 + g < d.I) put(row + i0 + g, moe_act(d.act, v0));
+                        if (i0 + g + 8 < d.I) put(row + i0 + g + 8, moe_act(d.act, v1));
                     }
                 }
             }
@@ -688,7 +704,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j)  // columns past the last read its row: their sums are not used
                     x.set(j, s.slot_token[off + min(j * 8 + g, n - 1)] * static_cast<uint32_t>(KS));
-                steps<T, ROWS, NT, NTMAX>(row(u, g), row(u, g + 8), x, s0, s1, static_cast<int>(d.H), t4, acc);
+                steps<T, ROWS, NT, NTMAX, 1>(row(u, g), row(u, g + 8), x, s0, s1, static_cast<int>(d.H), KS, t4, acc);
             });
             if (s0 == 0 && s1 == KS) {
                 finish(u, acc);
@@ -795,8 +811,8 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
             Columns<NT> x;
             x.base = reinterpret_cast<const uint16_t*>(h);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) x.set(j, static_cast<uint32_t>(off + min(j * 8 + g, n - 1)) * KS);
-            steps<T, ROWS, NT, NTMAX>(row(v, g), row(v, g + 8), x, s0, s1, static_cast<int>(d.I), t4, acc);
+            for (int j = 0; j < NT; ++j) x.set(j, static_cast<uint32_t>(off + min(j * 8 + g, n - 1)) * 2 * KS);
+            steps<T, ROWS, NT, NTMAX, 2>(row(v, g), row(v, g + 8), x, s0, s1, static_cast<int>(d.I), KS, t4, acc);
         });
 #pragma unroll
         for (int j = 0; j < NTMAX; ++j) {
@@ -958,7 +974,7 @@ MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid) {
     w.logits = w.counters + round_up((d.H + kMoeBlock - 1) / kMoeBlock * 4, 256);
     w.x = w.logits + round_up(d.T * d.E * 4, 256);
     w.h = w.x + round_up(d.T * w.hp * 2, 256);
-    w.partial = w.h + round_up(d.T * d.top_k * w.ip * 2, 256);
+    w.partial = w.h + round_up(d.T * d.top_k * 2 * w.ip * 2, 256);
     w.flushed = w.partial + static_cast<int64_t>(grid) * 2 * kMoeBlock * d.T * 4;
     w.bytes = w.flushed + static_cast<int64_t>(grid) * kMoeTeams * kMoeBlock * d.T * 4;
     return w;

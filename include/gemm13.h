@@ -367,10 +367,11 @@ int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  *     the top_k experts of a token are those with the largest z (equal ones:
  *     the lowest index; NaN comes last); their weights are p, or, with
  *     normalize, p divided by its sum over them
- *     Y[t] = cast( sum_j weight_j * W2[e_j] . h_j ),  h_j = cast( act(W1[e_j] . X[t]) )
+ *     Y[t] = cast( sum_j weight_j * W2[e_j] . h_j ),  h_j = act(W1[e_j] . X[t])
  *
  * in FP32 accumulation; cast rounds to nearest even to `dtype`, that of X, Wr,
- * W1, W2 and Y (GEMM_F16 or GEMM_BF16; an h beyond FP16's range becomes an
+ * W1, W2 and Y (GEMM_F16 or GEMM_BF16).  Between the products h is held as two
+ * numbers of that type, its rounding and the rest (beyond FP16's range: an
  * infinity).  Every weight of a chosen expert is read once.  A token with
  * a NaN or an infinite logit gets NaN rows, and no other token's row changes.
  */

@@ -21,7 +21,7 @@ def layer(x, router, w1, w2, k, act, normalize, u):
 
     The bound follows the computation: FP32 sums of n exact products are off by at most n 2^-24 times
     the sum of magnitudes in any order (2^-23 where the tensor core truncates), expf by 2 units in the last
-    place; h and y are rounded once to 16 bits.  gap: the least difference between a chosen and a
+    place; h is held in two 16-bit parts (off by u of the second, which is at most u of h), and y is rounded once.  gap: the least difference between a chosen and a
     passed-over logit, less what both may be off by (a choice is certain where it is positive).
     """
     T, H = x.shape
@@ -36,7 +36,7 @@ def layer(x, router, w1, w2, k, act, normalize, u):
     # weights: every exponent off by its logit and the maximum's, the sums by E additions
     dw = w * (4 * dz.max(1, keepdims=True) + (E + 16) * 2.0 ** -23)
     y, b = np.zeros((T, H)), np.zeros((T, H))
-    n1, n2 = (H + 64) * 2.0 ** -23, (I + 64) * 2.0 ** -23
+    n1, n2 = (H + 64) * 2.0 ** -23, (2 * I + 64) * 2.0 ** -23
     for e in range(E):
         t, j = np.nonzero(ids == e)
         if not len(t):
@@ -54,7 +54,7 @@ def layer(x, router, w1, w2, k, act, normalize, u):
             dh = 1.13 * da + 2.0 ** -21 * np.abs(a)
         else:
             h, dh = np.maximum(a, 0), da
-        dh = dh + u * (np.abs(h) + dh) + 2.0 ** -24  # (FP16: below the normal range a step is 2^-24)
+        dh = dh + u * u * (np.abs(h) + dh) + 2.0 ** -24  # (FP16: below the normal range a step is 2^-24)
         o = h @ w2[e].T
         do = dh @ np.abs(w2[e]).T + n2 * ((np.abs(h) + dh) @ np.abs(w2[e]).T)
         y[t] += w[t, j][:, None] * o
