@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
         if (FMT == GEMM_MXFP4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         uint32_t byte;
         float d = 1.0f, inv;
+        bool near = true;  // the block's quotients x / d stay far inside FP32
         if (FMT == GEMM_MXFP4) {
             // floor(log2) of a normal number is its exponent field; below the
             // normal range the result is kept at -127 anyway
@@ -212,8 +213,9 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
             byte = top >= 0x7F800000u ? 0xFFu : static_cast<uint32_t>(max(e, -127) + 127);
             inv = ue8m0_value(254u - min(byte, 254u));  // 2^-E
         } else {
-            const float r = fminf(__fdiv_rn(__uint_as_float(top), 6.0f * g), 448.0f);
-            byte = top >= 0x7F800000u ? 0x7Fu : e4m3_byte(r);
+            const float r = __fdiv_rn(__uint_as_float(top), 6.0f * g);
+            near = r < 0x1p60f;
+            byte = top >= 0x7F800000u ? 0x7Fu : e4m3_byte(fminf(r, 448.0f));
             d = e4m3_value(byte) * g;
             inv = __frcp_rn(d);
         }
@@ -227,11 +229,11 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
                 // exact products, apart from results far below the least code
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
-            } else if (d > 0x1p-60f && d < 0x1p60f) {
+            } else if (d > 0x1p-60f && d < 0x1p60f && near) {
                 // fl32(x / d): q = x (1/d) corrected by its exact remainder, which gives the
                 // rounded quotient (P. Markstein, "Computation of elementary functions on the
-                // IBM RISC System/6000 processor", 1990); one and a half instructions an element
-                // where a division each would take longer than the memory
+                // IBM RISC System/6000 processor", 1990) as long as q is finite; one and a half
+                // instructions an element where a division each would take longer than the memory
                 const uint64_t inv2 = pack2(inv, inv), nd2 = pack2(-d, -d);
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {

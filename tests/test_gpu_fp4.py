@@ -118,6 +118,20 @@ def test_quantise_extremes(fmt):
     assert np.isfinite(np.delete(v, [2, 3], 0)).all() and np.isfinite(v[2, : 40 // b * b]).all()
 
 
+@pytest.mark.parametrize("g", [1e-15, 3e-19])
+def test_quantise_saturates_with_its_sign(g):
+    # quotients past FP32's range, next to ordinary ones: the scale of the whole tensor is far too small
+    x = np.zeros((4, 64), np.float32)
+    x[0], x[1, ::2], x[1, 1::2] = -1e30, 3e38, -3e38
+    x[2] = np.linspace(-1, 1, 64) * np.float32(g) * 2000
+    x[3, :16], x[3, 16:] = -1e30, np.linspace(-3, 3, 48) * np.float32(g)
+    q = g13.fp4_quantize(torch.from_numpy(x).cuda(), "nvfp4", tensor_scale=torch.tensor([g], device="cuda"))
+    with np.errstate(over="ignore"):
+        check_quantised(q, x, "nvfp4", np.float32(g))
+    v = g13.fp4_dequantize(q).cpu().numpy()
+    assert np.array_equal(np.sign(v[:2]), np.sign(x[:2]))
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", list(DT))
 def test_strides_and_offsets(fmt, dtype):
