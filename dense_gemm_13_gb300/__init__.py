@@ -467,7 +467,6 @@ class _Torch:
         self.raw_stream = raw or (lambda i: torch.cuda.current_stream(i).cuda_stream)
         self.device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
-
     def on(self, stream, index: int):
         """Context in which `stream` (a torch stream or a handle) is the current one: what a call allocates then
         belongs to the stream that uses it."""
@@ -677,7 +676,7 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     """C = cast(act(alpha * A @ B.T + bias) + beta * residual) of two 4-bit matrices.
 
     A [M, K] (activations), B [N, K] (a weight as it lies for x @ W.T), both in the same format.
-    bias: FP32 [N]; residual: FP32 [M, N].  Plans are created once per (shape, format, strides,
+    bias: FP32 [N]; residual: FP32 [M, N]; out overlaps none of the inputs.  Plans are created once per (shape, format, strides,
     epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.  (The
     first call of a shape makes its plan, and is refused while a graph is being captured.)  With
     `stream`, the call runs, and allocates, as if that were the current stream.
@@ -781,7 +780,7 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     rows), w2 [E, H, I], all FP16 or all BF16, rows contiguous.  Returns y [T, H], or with
     return_routing (y, expert ids int32 [T, top_k], their weights FP32 [T, top_k]).  Plans are kept per
     shape, strides and device (the first call makes its plan, and is refused while a graph is being
-    captured); every call has a workspace of its own from torch's allocator.  With
+    captured); every call has a workspace of its own from torch's allocator.  out overlaps no input.  With
     `stream`, the call runs, and allocates, as if that were the current stream.
     """
     what, t = "moe_layer", _t()

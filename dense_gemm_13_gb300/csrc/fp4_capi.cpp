@@ -172,6 +172,9 @@ int gemm_fp4_run(gemm_fp4_plan_t plan, const void* a_codes, const void* a_scales
     if ((ep.has_residual != 0) != (residual != nullptr)) return GEMM_ERR_INVALID_ARG;
     if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales))
         return GEMM_ERR_MISALIGNED;
+    if (reinterpret_cast<uintptr_t>(C) % dtype_size(ep.out_dtype) != 0) return GEMM_ERR_MISALIGNED;
+    for (const void* f : {bias, residual, static_cast<const void*>(a_tensor_scale), static_cast<const void*>(b_tensor_scale)})
+        if (reinterpret_cast<uintptr_t>(f) % 4 != 0) return GEMM_ERR_MISALIGNED;
     int cur = -1;
     if (cudaGetDevice(&cur) != cudaSuccess || cur != plan->device) return GEMM_ERR_INVALID_ARG;
 

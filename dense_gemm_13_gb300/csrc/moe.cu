@@ -30,8 +30,8 @@
 //   No sum depends on timing.
 //
 // Weights go from global memory straight into registers, two batches ahead.  (Through a
-// ring in shared memory, cp.async per warp, they took 118 us where this takes 113 with 16 tokens,
-// and 600 against 445 with 64: the ring's space is what L1 keeps the tokens' values in.)  Rows
+// ring in shared memory, cp.async per warp, they took 118 us where this took 113 with 16 tokens,
+// and 600 against 445 with 64, h in one part: the ring's space is what L1 keeps the tokens' values in.)  Rows
 // that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Measured (bytes of the chosen experts over time): 16 tokens, 64 experts of 2048 x 1024:
@@ -72,7 +72,7 @@ constexpr int kMaxDevices = 64;
 
 // A 16-byte piece of a row.  (Two loads meet in most 32-byte sectors: without room in L1 the second
 // would fetch it again; 132 us instead of 144 with 16 tokens and unaligned rows, 525 instead of 659
-// with 64.)
+// with 64, h still in one part; 136 and 550 now.)
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::evict_first.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -409,7 +409,7 @@ __device__ __forceinline__ void route_tokens(const MoeArgs& a, MoeShared& s, Moe
 // 16 columns as pointers, read in 16-byte pieces; more as 32-bit offsets in steps, read in
 // 32-byte pieces, which leaves registers (64 tokens on 8 of 16 experts each, 4096 x 1536: 237 us
 // instead of 266; with few columns the address arithmetic stands before every load: 489 us
-// instead of 452 with 64 tokens on 8 of 64 experts).
+// instead of 452 with 64 tokens on 8 of 64 experts; h still in one part, 241 and 486 now).
 template <int NT>
 struct Columns {
     static constexpr bool FEW = NT <= 2;

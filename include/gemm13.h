@@ -341,7 +341,7 @@ int gemm_fp4_dequantize(gemm_fp4_format_t format, gemm_dtype_t dtype, int64_t ro
  * for GEMM_NVFP4 only (NULL: 1); bias, residual and C as for gemm_run; C must
  * not overlap any input.  Runs of one plan may overlap on the GPU.
  * Errors: as gemm_plan and gemm_run; MISALIGNED where codes or scales are not
- * 16-byte aligned.
+ * 16-byte aligned, or another array not to its element type.
  */
 typedef struct gemm_fp4_plan_s* gemm_fp4_plan_t;
 int gemm_fp4_plan(gemm_fp4_format_t format, int64_t M, int64_t N, int64_t K, int64_t ldc,
@@ -372,8 +372,10 @@ int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  * in FP32 accumulation; cast rounds to nearest even to `dtype`, that of X, Wr,
  * W1, W2 and Y (GEMM_F16 or GEMM_BF16).  Between the products h is held as two
  * numbers of that type, its rounding and the rest (beyond FP16's range: an
- * infinity).  Every weight of a chosen expert is read once.  A token with
- * a NaN or an infinite logit gets NaN rows, and no other token's row changes.
+ * infinity; an infinite weight in W2 may give NaN where h alone gives an
+ * infinity).  Every weight of a chosen expert is read once.  A token with a
+ * logit that is NaN or +infinity, or with none above -infinity, gets a row of
+ * NaN, and no other token's row changes.
  */
 typedef enum {
     GEMM_MOE_GELU = 0,  /* GELU (erf form) of W1[e] . x, W1[e] [I][H] */

@@ -402,3 +402,21 @@ def test_stream_argument():
             v = g13.fp4_dequantize(q, "bf16", stream=s)
         side.synchronize()
         assert torch.equal(y, want) and torch.equal(v, g13.fp4_dequantize(g13.fp4_quantize(x, "nvfp4"), "bf16"))
+
+
+def test_misaligned_arrays_are_refused():
+    # an address off its type is refused before anything is enqueued
+    lib, M, N, K = g13.load(), 2, 32, 64
+    q = [g13.fp4_quantize(torch.ones(r, K, device="cuda"), "nvfp4", tensor_scale=torch.ones(1, device="cuda"))
+         for r in (M, N)]
+    f = torch.zeros(M * N + 8, device="cuda").data_ptr()
+    for out, size in (("f32", 4), ("bf16", 2)):
+        pl = g13.gemm_fp4_plan("nvfp4", M, N, K, N, g13.Epilogue(b_layout="nk", out_dtype=out, bias=True,
+                                                                residual=True, ldr=N))
+        (ac, as_, ag), (bc, bs, bg) = q[0]._ptrs(), q[1]._ptrs()
+        C = torch.empty(M * N + 8, dtype=DT[out], device="cuda")
+        good = dict(ac=ac, as_=as_, ag=ag, bc=bc, bs=bs, bg=bg, C=C.data_ptr(), bias=f, res=f)
+        off = dict(ac=8, as_=8, ag=2, bc=8, bs=4, bg=1, C=size // 2, bias=2, res=1)
+        for k, d in off.items():
+            a = dict(good, **{k: good[k] + d})
+            assert lib.gemm_fp4_run(pl.handle, *a.values(), 1.0, None) == -3, k
