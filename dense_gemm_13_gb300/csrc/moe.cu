@@ -35,10 +35,10 @@
 // that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Measured (bytes of the chosen experts over time): 16 tokens, 64 experts of 2048 x 1024:
-// 116 us, 5.5 TB/s (0.82 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 486 us,
+// 114 us, 5.6 TB/s (0.84 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 486 us,
 // 5.0 TB/s (the tokens' values take half of what the SMs read; where an expert has 32
 // tokens or more they take most of it, and 2.5 TB/s remain); one token, 2 of 8
-// experts of 768 x 3072: 16.8 us, of which 3 are bytes and the rest a chain of two
+// experts of 768 x 3072: 16 us, of which 3 are bytes and the rest a chain of two
 // kernels, the routing, the barrier and the join, each a trip or two to L2.  (Blocks of
 // 16 columns instead of 64 in the down product cut fewer of them between CTAs and
 // still took 17 us: sixteen teams' sums are slower to add than four's.)
@@ -500,11 +500,13 @@ __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1
 }
 
 // The same for rows that all lie on 16 bytes (ROWS_16) or 32 (ROWS_32) and are a multiple of
-// that long: two batches of U steps in flight in registers, 64 KB per SM and batch at U = 2.
+// that long: two batches of U steps in flight in registers, 64 KB per SM and batch at U = 2.  (Down, with
+// one group of tokens, U = 1: one token 15.7 us instead of 16.2, 16 tokens 114 instead of 116; up, or with
+// two groups, it is the slower one: 16 tokens 118, 64 tokens 498 instead of 486.)
 template <typename T, int ROWS, int NT, int NTMAX, int PARTS>
 __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x,
                                               int s0, int s1, int K, int KS, int t4, float (&acc)[NTMAX][4]) {
-    constexpr int U = NT <= 2 ? 2 : 1;
+    constexpr int U = NT == 2 || (NT == 1 && PARTS == 1) ? 2 : 1;
     Row16 wa[2][U], wb[2][U];
     const auto load = [&](int b, int s) {
 #pragma unroll
