@@ -19,7 +19,7 @@
 //            barrier between them:
 //     up     work units of 16 weight rows of a chosen expert (SwiGLU: 8 gate rows
 //            and their 8 up rows, so one thread holds both factors) x 64-element
-//            steps along H.  A CTA takes an equal share of the units; its warps take
+//            steps along H.  A CTA takes an equal share of the units' costs; its warps take
 //            whole units in turn, and equal shares of the steps of those left over,
 //            joined through shared memory in warp order.
 //     down   units (64 output columns, chosen expert), column block major; CTAs, and
@@ -35,8 +35,8 @@
 // that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Measured (bytes of the chosen experts over time): 16 tokens, 64 experts of 2048 x 1024:
-// 114 us, 5.6 TB/s (0.84 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 486 us,
-// 5.0 TB/s (the tokens' values take half of what the SMs read; where an expert has 32
+// 114 us, 5.6 TB/s (0.84 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 467 us,
+// 5.2 TB/s (the tokens' values take half of what the SMs read; where an expert has 32
 // tokens or more they take most of it, and 2.5 TB/s remain); one token, 2 of 8
 // experts of 768 x 3072: 16 us, of which 3 are bytes and the rest a chain of two
 // kernels, the routing, the barrier and the join, each a trip or two to L2.  (Blocks of
@@ -72,7 +72,7 @@ constexpr int kMaxDevices = 64;
 
 // A 16-byte piece of a row.  (Two loads meet in most 32-byte sectors: without room in L1 the second
 // would fetch it again; 132 us instead of 144 with 16 tokens and unaligned rows, 525 instead of 659
-// with 64, h still in one part; 136 and 550 now.)
+// with 64, h still in one part.)
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.L1::evict_first.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -308,9 +308,11 @@ struct MoeShared {
     unsigned long long mask[kMoeMaxExperts];  // tokens of each expert
     short off[kMoeMaxExperts];                // first slot of each expert
     short active[kMoeMaxExperts];             // experts that have tokens
+    short cost[kMoeMaxExperts];               // of each of them: the unit costs of those before it
     float slot_weight[kMoeMaxTokens * kMoeMaxTopK];
     uint8_t slot_token[kMoeMaxTokens * kMoeMaxTopK];
-    int n_active;
+    int n_active, all_cost;
+    int u_lo, u_hi;  // this CTA's units of the up product
     int team_first[kMoeTeams], team_last[kMoeTeams];  // output blocks that each team adds to
     int last[2];                              // this CTA joins its first / last output block
     int gave_up;
@@ -320,6 +322,15 @@ struct MoePicks {
     float weight[kMoeMaxTokens * kMoeMaxTopK];
     short expert[kMoeMaxTokens * kMoeMaxTopK];
 };
+
+// Time of a unit of the up product by its expert's tokens (the more columns, the more of its time goes to
+// the tokens' values; ratios as measured with every expert alike): the CTAs' shares are equal in this.
+// Shares of equally many units gave all units of a busy expert to two or three CTAs, and every other one
+// waited for them at the barrier: 64 tokens, 8 of 64 experts of 4096 x 1536, one of which has 17: 630 us
+// instead of 482; none of which has more than 16: 486 instead of 467.
+__device__ __forceinline__ int unit_cost(int n) {
+    return n <= 8 ? 5 : n <= 16 ? 6 : n <= 32 ? 10 : 15;
+}
 
 // Order-preserving key of a logit; NaN below every number, 0 is free for "not there".
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -409,7 +420,7 @@ __device__ __forceinline__ void route_tokens(const MoeArgs& a, MoeShared& s, Moe
 // 16 columns as pointers, read in 16-byte pieces; more as 32-bit offsets in steps, read in
 // 32-byte pieces, which leaves registers (64 tokens on 8 of 16 experts each, 4096 x 1536: 237 us
 // instead of 266; with few columns the address arithmetic stands before every load: 489 us
-// instead of 452 with 64 tokens on 8 of 64 experts; h still in one part, 241 and 486 now).
+// instead of 452 with 64 tokens on 8 of 64 experts; h still in one part and shares of equally many units).
 template <int NT>
 struct Columns {
     static constexpr bool FEW = NT <= 2;
@@ -502,7 +513,7 @@ __device__ __forceinline__ void steps_any(const uint16_t* w0, const uint16_t* w1
 // The same for rows that all lie on 16 bytes (ROWS_16) or 32 (ROWS_32) and are a multiple of
 // that long: two batches of U steps in flight in registers, 64 KB per SM and batch at U = 2.  (Down, with
 // one group of tokens, U = 1: one token 15.7 us instead of 16.2, 16 tokens 114 instead of 116; up, or with
-// two groups, it is the slower one: 16 tokens 118, 64 tokens 498 instead of 486.)
+// two groups, it is the slower one: 16 tokens 118 instead of 116, 64 tokens 498 instead of 486, at the time.)
 template <typename T, int ROWS, int NT, int NTMAX, int PARTS>
 __device__ __forceinline__ void steps_aligned(const uint16_t* w0, const uint16_t* w1, const Columns<NT>& x,
                                               int s0, int s1, int K, int KS, int t4, float (&acc)[NTMAX][4]) {
@@ -595,23 +606,29 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     }
     __syncthreads();
     if (warp == 0) {
-        int n = 0, slots = 0;
+        int n = 0, slots = 0;  // (with the costs in the high 16 bits, as in the sums below)
         for (int e0 = 0; e0 < E; e0 += 32) {
             const int e = e0 + lane;
             const int c = e < E ? __popcll(s.mask[e]) : 0;
             const unsigned has = __ballot_sync(0xFFFFFFFFu, c > 0);
-            int pre = c;  // inclusive prefix sum of the counts
+            const int both = c + (c > 0 ? unit_cost(c) << 16 : 0);
+            int pre = both;  // inclusive prefix sums of the counts and the costs
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xFFFFFFFFu, pre, o);
                 if (lane >= o) pre += up;
             }
-            if (e < E) s.off[e] = static_cast<short>(slots + pre - c);
-            if (c > 0) s.active[n + __popc(has & ((1u << lane) - 1u))] = static_cast<short>(e);
+            const int before = slots + pre - both;
+            if (e < E) s.off[e] = static_cast<short>(before & 0xFFFF);
+            if (c > 0) {
+                const int i = n + __popc(has & ((1u << lane) - 1u));
+                s.active[i] = static_cast<short>(e);
+                s.cost[i] = static_cast<short>(before >> 16);
+            }
             n += __popc(has);
             slots += __shfl_sync(0xFFFFFFFFu, pre, 31);
         }
-        if (lane == 0) s.n_active = n;
+        if (lane == 0) s.n_active = n, s.all_cost = slots >> 16;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < tok * top_k; i += MT) {
@@ -624,8 +641,29 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
             if (a.weights) a.weights[i] = picks.weight[i];
         }
     }
-    __syncthreads();
     const int A = s.n_active;
+    const bool gated = d.act == GEMM_MOE_SWIGLU;
+    const int per = gated ? 8 : 16;  // values of h per unit
+    // (the host keeps units times steps below 2^30, and E and I keep units below 2^26)
+    const int UB = static_cast<int>((d.I + per - 1) / per);
+    if constexpr (NTMAX > 2) {
+        // equal shares of the costs: a share's bounds are units, found in the expert that holds them
+        const Share ctas(s.all_cost * UB, G);
+        const int bound[2] = {ctas.lo(cta), ctas.lo(cta + 1)};
+        for (int i = threadIdx.x; i < A; i += MT) {
+            const int w = unit_cost(__popcll(s.mask[s.active[i]]));
+            const int first = s.cost[i] * UB, next = first + w * UB;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                if (bound[k] >= first && (bound[k] < next || i == A - 1))
+                    (k == 0 ? s.u_lo : s.u_hi) = i * UB + (bound[k] - first + w - 1) / w;
+        }
+    } else if (threadIdx.x == 0) {  // (one cost)
+        const Share ctas(UB * A, G);
+        s.u_lo = ctas.lo(cta);
+        s.u_hi = ctas.lo(cta + 1);
+    }
+    __syncthreads();
 
     // ---------------------------------------------------------------- up
     const uint16_t* xp = reinterpret_cast<const uint16_t*>(a.ws + a.w.x);
@@ -633,13 +671,8 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     const int g = lane >> 2, t4 = lane & 3;
     float* my_tile = tiles + warp * 2 * TILE;
     {
-        const bool gated = d.act == GEMM_MOE_SWIGLU;
-        const int per = gated ? 8 : 16;  // values of h per unit
-        // (the host keeps these counts below 2^31)
-        const int UB = static_cast<int>((d.I + per - 1) / per), U = UB * A;
         const int KS = static_cast<int>(a.w.hp / 64);
-        const Share ctas(U, G);
-        const int u_lo = ctas.lo(cta), n_u = ctas.lo(cta + 1) - u_lo;
+        const int u_lo = s.u_lo, n_u = s.u_hi - u_lo;
         // Whole units go to the warps in turn: all warps walk H together and find the tokens'
         // values in L1 (each x row comes from L2 once per 16 units).  The units left over are cut.
         const int whole = n_u / kMoeWarps, u_cut = u_lo + whole * kMoeWarps;

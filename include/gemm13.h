@@ -375,7 +375,8 @@ int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  * infinity; an infinite weight in W2 may give NaN where h alone gives an
  * infinity).  Every weight of a chosen expert is read once.  A token with a
  * logit that is NaN or +infinity, or with none above -infinity, gets a row of
- * NaN, and no other token's row changes.
+ * NaN, and nothing of it enters another token's row.  (What the tokens choose decides
+ * where sums are cut: a row's last bits may depend on the other tokens of its call.)
  */
 typedef enum {
     GEMM_MOE_GELU = 0,  /* GELU (erf form) of W1[e] . x, W1[e] [I][H] */

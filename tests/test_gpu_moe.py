@@ -75,6 +75,25 @@ def test_layer(case, act):
             assert torch.equal(y, g13.moe_layer(*ts, k, act=act, normalize=normalize))
 
 
+@pytest.mark.parametrize("case", [(17, 9, 2, 160, 72), (40, 70, 3, 96, 33), (64, 5, 1, 264, 200), (64, 300, 2, 64, 8)],
+                         ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("act", ["relu", "swiglu"])
+def test_busy_experts(case, act):
+    # one expert that many tokens choose, one that no token chooses, few tokens for the others
+    T, E, k, H, I = case
+    for n in range(20):
+        x, router, w1, w2 = inputs(("busy", case, act, n), T, E, H, I, act, "bf16", top_k=k)
+        x[:, 0], router[:, 0] = 4, 0
+        router[E // 2, 0], router[E - 1, 0] = 1.5, -8
+        if moe_ref.routing(x.double().numpy(), router.double().numpy(), k)[3] > 0:
+            break
+    ts = on_gpu((x, router, w1, w2))
+    y, ids, wts = g13.moe_layer(*ts, k, act=act, return_routing=True)
+    per = torch.bincount(ids.flatten().long().cpu(), minlength=E)
+    assert per.max() >= T // 4 and per.min() == 0  # (of 300 experts others are liked as much)
+    check(*ts, k, act, True, y, ids, wts)
+
+
 @pytest.mark.parametrize("pad", [(8, 8), (1, 0), (3, 2), (0, 8), (6, 1)])
 @pytest.mark.parametrize("T", [2, 20, 50])
 def test_strides(T, pad):
