@@ -471,9 +471,12 @@ class _Torch:
         """Context in which `stream` (a torch stream or a handle) is the current one: what a call allocates then
         belongs to the stream that uses it."""
         cuda = self.torch.cuda
-        if not isinstance(stream, int) and stream.device.index != index:
+        if isinstance(stream, int):
+            # 0 and 1 (cudaStreamLegacy) are the default stream; ExternalStream(0) would be a new one of torch's pool
+            stream = cuda.ExternalStream(stream, device=index) if stream > 1 else cuda.default_stream(index)
+        elif stream.device.index != index:
             _refuse("stream", "it belongs to another device than the tensors")
-        return cuda.stream(cuda.ExternalStream(stream, device=index) if isinstance(stream, int) else stream)
+        return cuda.stream(stream)
 
     def device(self, index: int):
         d = self._devices.get(index)
