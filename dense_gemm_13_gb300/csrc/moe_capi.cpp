@@ -34,7 +34,7 @@ int check_desc(gemm_moe_desc_t& d) {
     if (d.dtype != GEMM_F32 && d.dtype != GEMM_F16 && d.dtype != GEMM_BF16) return GEMM_ERR_INVALID_ARG;
     if (d.act != GEMM_MOE_GELU && d.act != GEMM_MOE_RELU && d.act != GEMM_MOE_SWIGLU)
         return GEMM_ERR_INVALID_ARG;
-    if (d.normalize != 0 && d.normalize != 1) return GEMM_ERR_INVALID_ARG;
+    if ((d.normalize != 0 && d.normalize != 1) || (d.flags & ~GEMM_FLAG_TEST_STALL)) return GEMM_ERR_INVALID_ARG;
     if (d.T < 0 || d.E < 1 || d.H < 1 || d.I < 1 || d.top_k < 1 || d.top_k > d.E) return GEMM_ERR_INVALID_ARG;
     if (d.dtype == GEMM_F32 || d.T > kMoeMaxTokens || d.E > kMoeMaxExperts || d.top_k > kMoeMaxTopK ||
         d.H > kMoeMaxH || d.I > (int64_t(1) << 20))

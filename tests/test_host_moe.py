@@ -99,3 +99,9 @@ def test_reference(act):
             want += p[e] * (w2[e] @ np.array(h))
         assert np.allclose(y[t], want, rtol=1e-12, atol=1e-13)
     assert (bound > 0).all() and gap > 0
+
+
+@pytest.mark.parametrize("flags", [0x1, 0x2, g13.FLAG_TEST_STALL_PEER, g13.FLAG_TEST_STALL | 0x10, 0x7FFFFFFF])
+def test_flags_that_mean_nothing_are_refused(lib, flags):
+    assert plan(lib, flags=flags) == -1
+    assert plan(lib, flags=g13.FLAG_TEST_STALL) in (0, -7)
