@@ -20,7 +20,7 @@ __all__ = ["Epilogue", "Config", "Plan", "GemmError", "gemm_plan", "gemm_run", "
            "gemm_strerror", "gemm_version", "gemm_run_noalloc", "lib", "load", "matmul", "DTYPES", "ACTS", "LAYOUTS",
            "KERNELS", "LIB_PATH", "FP4_FORMATS", "Fp4Tensor", "Fp4Plan", "fp4_quantize", "fp4_dequantize",
            "gemm_fp4_plan", "gemm_fp4_run", "gemm_fp4_status", "gemm_fp4_select_config", "fp4_matmul",
-           "MOE_ACTS", "MoePlan", "gemm_moe_plan", "gemm_moe_run", "gemm_moe_status", "moe_layer"]
+           "MOE_ACTS", "MoePlan", "gemm_moe_plan", "gemm_moe_run", "gemm_moe_status", "moe_layer", "gemm_kept_status"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm13.so")
 
@@ -371,7 +371,8 @@ def matmul(A, B, *, b_layout="kn", alpha=1.0, bias=None, act="none", residual=No
            out_dtype="f32", out=None):
     """C = cast(act(alpha*A@B + bias) + beta*residual) for 2-D or 3-D (batched) CUDA tensors.
 
-    Plans are created once per (shape, dtype, strides, epilogue) and kept.
+    Plans are created once per (shape, dtype, strides, epilogue) and kept; gemm_kept_status tells
+    whether a kernel of one of them gave up on a wait.
     """
     import torch
     tdt = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
@@ -682,7 +683,8 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     bias: FP32 [N]; residual: FP32 [M, N]; out overlaps none of the inputs.  Plans are created once per (shape, format, strides,
     epilogue, device) and kept; they hold no workspace, so calls may overlap on any streams.  (The
     first call of a shape makes its plan, and is refused while a graph is being captured.)  With
-    `stream`, the call runs, and allocates, as if that were the current stream.
+    `stream`, the call runs, and allocates, as if that were the current stream.  gemm_kept_status tells
+    whether a kernel gave up on a wait: what it returned is then undefined.
     """
     what, t = "fp4_matmul", _t()
     index, format, M, K, N = A._index, A._format, A._rows, A._cols, B._rows
@@ -784,7 +786,8 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     return_routing (y, expert ids int32 [T, top_k], their weights FP32 [T, top_k]).  Plans are kept per
     shape, strides and device (the first call makes its plan, and is refused while a graph is being
     captured); every call has a workspace of its own from torch's allocator.  out overlaps no input.  With
-    `stream`, the call runs, and allocates, as if that were the current stream.
+    `stream`, the call runs, and allocates, as if that were the current stream.  gemm_kept_status tells
+    whether a kernel gave up on a wait: what it returned is then undefined.
     """
     what, t = "moe_layer", _t()
     dt = t.name.get(x.dtype)
@@ -839,3 +842,18 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     if rc != 0:
         raise GemmError(rc, what)
     return (out, ids, wts) if return_routing else out
+
+
+def gemm_kept_status() -> int:
+    """Synchronise and return the sticky device status of the plans that matmul, fp4_matmul and moe_layer keep.
+
+    0, or the code of one whose kernel gave up on a wait (-5): what the calls of its shape have returned
+    is not to be used.
+    """
+    for plans, status in ((_plans, gemm_plan_status), (_fp4_plans, gemm_fp4_status), (_moe_plans, gemm_moe_status)):
+        for key, plan in list(plans.items()):
+            with _t().torch.cuda.device(key[-1]):
+                rc = status(plan)
+            if rc != 0:
+                return rc
+    return 0
