@@ -365,6 +365,17 @@ def gemm_run_noalloc(dtype: str, M: int, N: int, K: int, A, lda: int, B, ldb: in
 
 
 _plans: dict = {}
+_keep_lock = threading.Lock()
+
+
+def _keep(plans: dict, key, make):
+    """plans[key], made by the first call that wants it: two threads never make it twice, which would
+    destroy one of the two while its kernel may still run."""
+    with _keep_lock:
+        pl = plans.get(key)
+        if pl is None:
+            pl = plans[key] = make()
+    return pl
 
 
 def matmul(A, B, *, b_layout="kn", alpha=1.0, bias=None, act="none", residual=None, beta=1.0,
@@ -395,8 +406,7 @@ def matmul(A, B, *, b_layout="kn", alpha=1.0, bias=None, act="none", residual=No
     key = (dt, M, N, K, lda, ldb, ldc, tuple(sorted(vars(ep).items())), A.device.index)
     pl = _plans.get(key)
     if pl is None:
-        pl = gemm_plan(dt, M, N, K, lda, ldb, ldc, ep)
-        _plans[key] = pl
+        pl = _keep(_plans, key, lambda: gemm_plan(dt, M, N, K, lda, ldb, ldc, ep))
     gemm_run(pl, A, B, out, bias, residual, alpha)
     return out
 
@@ -716,7 +726,7 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
         _no_capture(t, what)
         ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
                       residual=residual is not None, beta=beta, ldr=ldr)
-        pl = _fp4_plans[key] = gemm_fp4_plan(format, M, N, K, ldc, ep)
+        pl = _keep(_fp4_plans, key, lambda: gemm_fp4_plan(format, M, N, K, ldc, ep))
     rc = (_lib or load()).gemm_fp4_run(pl.handle, *A._ptrs(), *B._ptrs(), out.data_ptr(), _ptr(bias), _ptr(residual),
                                        alpha, t.raw_stream(index))
     if rc != 0:
@@ -830,8 +840,9 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
     pl = _moe_plans.get(key)
     if pl is None:
         _no_capture(t, what)
-        pl = _moe_plans[key] = gemm_moe_plan(dt, T, E, top_k, H, I, act, normalize, ldx=ldx, ld_router=ldr,
-                                             ld_w1=ld1, stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=ldy)
+        pl = _keep(_moe_plans, key, lambda: gemm_moe_plan(
+            dt, T, E, top_k, H, I, act, normalize, ldx=ldx, ld_router=ldr, ld_w1=ld1, stride_w1=st1, ld_w2=ld2,
+            stride_w2=st2, ldy=ldy))
     ids = wts = None
     if return_routing:
         ids = t.empty((T, top_k), dtype=t.i32, device=dev)

@@ -1,4 +1,7 @@
 """The plans that fp4_matmul and moe_layer keep: a wait that runs out is told."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -51,3 +54,33 @@ def test_fp4_matmul_that_timed_out(monkeypatch):
     assert g13.gemm_kept_status() == -5
     monkeypatch.undo()
     assert torch.equal(g13.fp4_matmul(A, B), want)
+
+
+@pytest.mark.parametrize("call", ["matmul", "fp4_matmul", "moe_layer"])
+def test_first_calls_of_two_threads_make_one_plan(monkeypatch, call):
+    A, B = (torch.randn(n, 88, device="cuda").bfloat16() for n in (5, 48))
+    run, kept, maker = {
+        "matmul": (lambda: g13.matmul(A, B, b_layout="nk"), "_plans", "gemm_plan"),
+        "fp4_matmul": (lambda: g13.fp4_matmul(g13.fp4_quantize(A), g13.fp4_quantize(B)), "_fp4_plans", "gemm_fp4_plan"),
+        "moe_layer": (lambda m=moe_inputs(): g13.moe_layer(*m, 2), "_moe_plans", "gemm_moe_plan")}[call]
+    want = run()
+    torch.cuda.synchronize()
+    make, made, got = getattr(g13, maker), [], []
+
+    def slowly(*a, **k):
+        made.append(1)
+        time.sleep(0.2)
+        return make(*a, **k)
+
+    def work():
+        got.append(run())
+        torch.cuda.synchronize()
+
+    monkeypatch.setattr(g13, kept, {})
+    monkeypatch.setattr(g13, maker, slowly)
+    both = [threading.Thread(target=work) for _ in range(2)]
+    for t in both:
+        t.start()
+    for t in both:
+        t.join()
+    assert len(made) == 1 and len(got) == 2 and all(torch.equal(y, want) for y in got)
