@@ -517,6 +517,13 @@ def _no_capture(t: _Torch, what: str):
         _refuse(what, "no plan for this shape yet: call it once before capturing a graph")
 
 
+def _on_device(what: str, index: int, *tensors):
+    """Refuses tensors that the kernels of the current device cannot read (None and addresses pass)."""
+    for x in tensors:
+        if x is not None and not isinstance(x, int) and x.get_device() != index:
+            _refuse(what, "tensors on the current device are wanted")
+
+
 def _rows_ok(x) -> bool:
     """Row-major, rows not overlapping: what a C entry point takes as [rows][ld]."""
     rows, cols = x.shape
@@ -661,8 +668,12 @@ def gemm_fp4_run(plan: Fp4Plan, A: Fp4Tensor, B: Fp4Tensor, C, bias=None, residu
             or B._format != plan.format:
         _refuse("gemm_fp4_run", "the operands do not fit the plan")
     t = _t()
+    index = t.device_index()
+    if A._index != index or B._index != index:
+        _refuse("gemm_fp4_run", "the operands are not on the current device")
+    _on_device("gemm_fp4_run", index, C, bias, residual)
     rc = (_lib or load()).gemm_fp4_run(plan.handle, *A._ptrs(), *B._ptrs(), _ptr(C), _ptr(bias), _ptr(residual), alpha,
-                                       _stream(t, t.device_index(), stream))
+                                       _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, "gemm_fp4_run")
     return rc
@@ -772,8 +783,12 @@ def gemm_moe_run(plan: MoePlan, X, router, W1, W2, Y, workspace, expert_ids=None
                  stream=None) -> int:
     """Enqueue one layer on `stream` (default: torch's current stream); raises on error."""
     t = _t()
+    index = t.device_index()
+    _on_device("gemm_moe_run", index, X, router, W1, W2, Y, workspace, expert_ids, expert_weights)
+    if hasattr(workspace, "data_ptr") and workspace.numel() * workspace.element_size() < plan.workspace_bytes:
+        _refuse("gemm_moe_run", f"workspace: {plan.workspace_bytes} bytes are wanted")
     rc = lib().gemm_moe_run(plan.handle, _ptr(X), _ptr(router), _ptr(W1), _ptr(W2), _ptr(Y), _ptr(expert_ids),
-                            _ptr(expert_weights), _ptr(workspace), _stream(t, t.device_index(), stream))
+                            _ptr(expert_weights), _ptr(workspace), _stream(t, index, stream))
     if rc != 0:
         raise GemmError(rc, "gemm_moe_run")
     return rc
