@@ -172,35 +172,38 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) 
     tmem_ld_32x32b_x32(taddr, r);
     tmem_ld_wait_regs(r);
 }
-// GELU of two values, 0.5 y (1 + erf(y / sqrt 2)), with erf from Abramowitz & Stegun, Handbook
-// of Mathematical Functions, formula 7.1.28 (|error| <= 3e-7): for x >= 0
-//     1 - erf(x) = (1 + a1 x + ... + a6 x^6)^-16,
-//     a1..a6 = 0.0705230784, 0.0422820123, 0.0092705272, 0.0001520143, 0.0002765672, 0.0000430638
-// (here with x = |y| / sqrt 2 and the powers of 1 / sqrt 2 in the constants).  One special-function
-// operation a value, the reciprocal; formula 7.1.26 takes two, which alone took a third of a
-// 256 x 256 tile's epilogue.  |y| is kept at 30, where the result is max(y, 0) to the last bit, so that
-// an infinity gives one; NaN stays NaN.
-__device__ __forceinline__ void gelu2_as7128(float& y0, float& y1) {
-    const float c0 = fminf(fabsf(y0), 30.0f), c1 = fminf(fabsf(y1), 30.0f);
-    const uint64_t x = f2_pack(c0, c1);
+// GELU of two values, y Phi(y) = max(y, 0) - z Q(z) with z = |y| and Q(z) = erfc(z / sqrt 2) / 2, the
+// normal distribution's tail.  Q(z) = exp(-z^2 / 2) R(z), and R falls smoothly like 1 / z: in t = 1 / (1 + 0.301 z)
+// (the substitution of Hastings' formulas, Abramowitz & Stegun 7.1.26) it is t times a polynomial, of
+// degree 7 here, fitted by weighted least squares with Lawson's weights to the least relative error over
+// 0 <= z <= 13.5: 1.5e-7 with rounded coefficients.  With the FP32 steps the result is within half a unit
+// in its last place + (20 + 1.5 z^2) 2^-24 z Q(z), so it keeps its leading digits in all of the left tail, where formulas for erf
+// lose them.  (7.1.28, with one special-function operation a value instead of two, takes 4096 x 3072 x 768
+// 18.3 us instead of 20.3, but errs by up to 7e-7, and by 5 % at y = -5.  One reciprocal for both values: 21.0.)
+// z is kept at 30, where Q is zero, so that an infinity gives max(y, 0); NaN stays NaN.
+__device__ __forceinline__ void gelu2(float& y0, float& y1) {
+    const uint64_t z = f2_pack(fminf(fabsf(y0), 30.0f), fminf(fabsf(y1), 30.0f));
     const auto two = [](float v) { return f2_pack(v, v); };
-    uint64_t p = f2_fma(two(5.3829750e-06f), x, two(4.8890639e-05f));
-    p = f2_fma(p, x, two(3.8003575e-05f));
-    p = f2_fma(p, x, two(3.2776264e-03f));
-    p = f2_fma(p, x, two(2.1141006e-02f));
-    p = f2_fma(p, x, two(4.9867347e-02f));
-    p = f2_fma(p, x, two(1.0f));
-    p = f2_mul(p, p);
-    p = f2_mul(p, p);
-    p = f2_mul(p, p);
-    p = f2_mul(p, p);
-    float p0, p1, h0, h1, m0, m1;
-    f2_unpack(p, p0, p1);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(h0) : "f"(p0));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(h1) : "f"(p1));
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m0) : "f"(y0));
-    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(m1) : "f"(y1));
-    f2_unpack(f2_fma(f2_mul(x, f2_pack(h0, h1)), two(-0.5f), f2_pack(m0, m1)), y0, y1);
+    float a, b, c, d;
+    f2_unpack(f2_fma(z, two(0.301f), two(1.0f)), a, b);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(a));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(b));
+    const uint64_t t = f2_pack(c, d);
+    // -R(z) / t
+    uint64_t p = f2_fma(two(-0.036172338f), t, two(0.15756063f));
+    p = f2_fma(p, t, two(-0.20416015f));
+    p = f2_fma(p, t, two(0.05221945f));
+    p = f2_fma(p, t, two(-0.1279228f));
+    p = f2_fma(p, t, two(-0.10035842f));
+    p = f2_fma(p, t, two(-0.12113759f));
+    p = f2_fma(p, t, two(-0.12002871f));
+    p = f2_mul(p, t);
+    // exp(-z^2 / 2) = 2^(-z^2 log2(e) / 2)
+    f2_unpack(f2_mul(f2_mul(z, two(-0.72134752f)), z), a, b);
+    p = f2_mul(p, f2_pack(ex2_approx(a), ex2_approx(b)));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(c) : "f"(y0));
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(d) : "f"(y1));
+    f2_unpack(f2_fma(z, p, f2_pack(c, d)), y0, y1);
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
@@ -233,7 +236,7 @@ __device__ __forceinline__ void f4_store(const EpiParams& e, float alpha, float 
     for (int j = 0; j < CN; j += 2) f2_unpack(f2_fma(f2_pack(v[j], v[j + 1]), a2, b2), v[j], v[j + 1]);
     if (e.act == GEMM_ACT_GELU_ERF) {
 #pragma unroll
-        for (int j = 0; j < CN; j += 2) gelu2_as7128(v[j], v[j + 1]);
+        for (int j = 0; j < CN; j += 2) gelu2(v[j], v[j + 1]);
     } else if (e.act == GEMM_ACT_RELU) {
 #pragma unroll
         for (int j = 0; j < CN; ++j) v[j] = v[j] < 0.0f ? 0.0f : v[j];

@@ -339,7 +339,9 @@ int gemm_fp4_dequantize(gemm_fp4_format_t format, gemm_dtype_t dtype, int64_t ro
  * UNSUPPORTED); strides a, b, c, r are ignored.
  * gemm_fp4_run enqueues on `stream`: arrays as described above, tensor scales
  * for GEMM_NVFP4 only (NULL: 1); bias, residual and C as for gemm_run; C must
- * not overlap any input.  Runs of one plan may overlap on the GPU.
+ * not overlap any input.  Runs of one plan may overlap on the GPU.  GELU is
+ * max(y, 0) - z Q(z), z = |y|, Q the normal distribution's tail: off by at most
+ * (20 + 1.5 z^2) 2^-24 z Q(z) (2.2e-7, near z = 0.8) and the casts' rounding.
  * Errors: as gemm_plan and gemm_run; MISALIGNED where codes or scales are not
  * 16-byte aligned, or another array not to its element type.
  */
