@@ -49,7 +49,7 @@ typedef enum { GEMM_MXFP4 = 0, GEMM_NVFP4 = 1 } gemm_fp4_format_t;
 typedef enum {
     GEMM_ACT_NONE = 0,
     GEMM_ACT_GELU_ERF = 1, /* 0.5*y*(1+erf(y/sqrt(2))) */
-    GEMM_ACT_RELU = 2,     /* max(y, 0) */
+    GEMM_ACT_RELU = 2,     /* max(y, 0); of a NaN: 0 in gemm_run, NaN in gemm_fp4_run */
     GEMM_ACT_SOFTMAX = 3   /* softmax over each output row: exp(y_ij - max_j y_ij) divided by
                               sum_j exp(y_ij - max_j y_ij), with y = alpha*A.B + bias over all N
                               columns -- the attention step Softmax(QK^T) of "CUDA Tile ...
@@ -382,7 +382,7 @@ int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  */
 typedef enum {
     GEMM_MOE_GELU = 0,  /* GELU (erf form) of W1[e] . x, W1[e] [I][H] */
-    GEMM_MOE_RELU = 1,  /* max(W1[e] . x, 0) */
+    GEMM_MOE_RELU = 1,  /* max(W1[e] . x, 0); of a NaN: NaN */
     GEMM_MOE_SWIGLU = 2 /* silu(gate) * up, W1[e] [2I][H]: gate rows, then up rows */
 } gemm_moe_act_t;
 

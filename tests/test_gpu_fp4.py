@@ -420,3 +420,11 @@ def test_misaligned_arrays_are_refused():
         for k, d in off.items():
             a = dict(good, **{k: good[k] + d})
             assert lib.gemm_fp4_run(pl.handle, *a.values(), 1.0, None) == -3, k
+
+
+@pytest.mark.parametrize("M", [1, 200])
+def test_relu_of_nan_is_nan(M):
+    A, B = (g13.fp4_quantize(torch.zeros(n, 64, device="cuda"), "nvfp4") for n in (M, 5))
+    bias = torch.tensor([float("nan"), -1.0, 2.0, float("inf"), float("-inf")], device="cuda")
+    want = torch.tensor([float("nan"), 0.0, 2.0, float("inf"), 0.0], device="cuda").expand(M, 5)
+    assert torch.equal(g13.fp4_matmul(A, B, bias=bias, act="relu").nan_to_num(-7), want.nan_to_num(-7))

@@ -261,3 +261,16 @@ def test_stream_argument():
         ys = [g13.moe_layer(*s, k, stream=st) for _ in range(4)]
         side.synchronize()
         assert all(torch.equal(y, want) for y in ys)
+
+
+@pytest.mark.parametrize("T", [5, 30])
+def test_relu_of_nan_is_nan(T):
+    # a NaN among an expert's weights reaches every output of its tokens, and no other
+    E, k, H, I = 6, 2, 96, 48
+    x, router, w1, w2 = on_gpu(inputs(("relu nan", T), T, E, H, I, "relu", "bf16"))
+    y, ids, _ = g13.moe_layer(x, router, w1, w2, k, act="relu", return_routing=True)
+    e = int(ids[0, 0])
+    w1[e, 7, 11] = float("nan")
+    got = g13.moe_layer(x, router, w1, w2, k, act="relu")
+    hit = (ids == e).any(1)
+    assert bool(got[hit].isnan().all()) and torch.equal(got[~hit], y[~hit])
