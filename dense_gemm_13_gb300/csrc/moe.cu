@@ -70,6 +70,12 @@ constexpr int kMoeTeams = kMoeWarps / 4;  // down product: teams of four warps
 constexpr int RT = 256;              // threads per router CTA
 constexpr int kMaxDevices = 64;
 
+// h is held in two parts, its rounding and the rest.  FP16 has a second such array, in units of 2^16, for the
+// values beyond its range (the router clears it; the second product reads it only where one exists).
+constexpr float kMoeBigUnit = 65536.0f, kMoeBigFrom = 65520.0f;  // (less rounds to 65504)
+template <typename T>
+constexpr bool kMoeBig = std::is_same<T, __half>::value;
+
 // A 16-byte piece of a row.  (Two loads meet in most 32-byte sectors: without room in L1 the second
 // would fetch it again; 132 us instead of 144 with 16 tokens and unaligned rows, 525 instead of 659
 // with 64, h still in one part.)
@@ -228,6 +234,16 @@ __device__ __forceinline__ float moe_act(int act, float y) {
     if (act == GEMM_MOE_GELU) return epi_act(GEMM_ACT_GELU_ERF, y);
     return y < 0.0f ? 0.0f : y;
 }
+__device__ __forceinline__ float swiglu(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
+// A number in two parts (an infinity, or NaN, in the first alone), the second `step` elements on.
+template <typename T>
+__device__ __forceinline__ void two_parts(T* p, int64_t step, float v) {
+    const T hi = cast16<T>(v);
+    const float f = as_float(hi);
+    p[0] = hi;
+    p[step] = cast16<T>(fabsf(f) < INFINITY ? v - f : 0.0f);
+}
 
 // ------------------------------------------------------------------ router
 // A CTA takes two experts and four tokens; its threads take 8 elements of H each, so that
@@ -298,9 +314,14 @@ __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
         reinterpret_cast<uint4*>(xp)[i] = ld_row8<VEC>(x + row * d.ldx + k, H - k);
     }
     uint16_t* h = reinterpret_cast<uint16_t*>(a.ws + a.w.h);
-    const int pad = static_cast<int>(a.w.ip - d.I);
-    for (int i = tid; i < static_cast<int>(d.T * d.top_k) * 2 * pad; i += nthreads)  // both parts of each h
+    const int pad = static_cast<int>(a.w.ip - d.I), parts = static_cast<int>(d.T * d.top_k) * 2;
+    for (int i = tid; i < parts * pad; i += nthreads)  // both parts of each h
         h[static_cast<int64_t>(i / pad) * a.w.ip + d.I + i % pad] = 0;
+    if constexpr (kMoeBig<T>) {
+        uint4* big = reinterpret_cast<uint4*>(h + parts * a.w.ip);
+        const int64_t n = parts * (a.w.ip / 8);
+        for (int64_t i = tid; i < n; i += nthreads) big[i] = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // ------------------------------------------------------------------ experts
@@ -316,6 +337,7 @@ struct MoeShared {
     int team_first[kMoeTeams], team_last[kMoeTeams];  // output blocks that each team adds to
     int last[2];                              // this CTA joins its first / last output block
     int gave_up;
+    int big;  // a value of h lies beyond FP16: one that this CTA wrote, after the barrier one that any wrote
 };
 // While the routing is worked out, each token's choice lies where the tiles of sums are later.
 struct MoePicks {
@@ -576,8 +598,75 @@ constexpr int kMoeSmem = (static_cast<int>(sizeof(MoeShared)) + 127) / 128 * 128
                               ? kMoeTileBytes<NTMAX>
                               : static_cast<int>(sizeof(MoePicks)));
 
+// Moves this thread's values of h that lie beyond FP16, of a unit's sums, to their own array.  Out of line, as
+// below: in the unit's own code it cost one token 0.9 us of 16.6 (instructions to fetch) and 16 tokens on
+// unaligned rows 5 %; so it is 0.5 us and 3 %, the clearing of the array included.
+template <typename T, int NTMAX>
+__device__ __noinline__ void put_big(const MoeArgs& a, const float (&acc)[NTMAX][4], int e, int i0) {
+    extern __shared__ __align__(128) uint8_t moe_smem[];
+    MoeShared& s = *reinterpret_cast<MoeShared*>(moe_smem);
+    const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3, n = __popcll(s.mask[e]);
+    const bool gated = a.d.act == GEMM_MOE_SWIGLU;
+    T* h = reinterpret_cast<T*>(a.ws + a.w.h);
+    for (int col = t4 * 2; col < n; col += col & 1 ? 7 : 1)
+        for (int r = 0; r < (gated ? 1 : 2); ++r) {
+            const float* v = &acc[col >> 3][col & 1];
+            const float y = gated ? swiglu(v[0], v[2]) : moe_act(a.d.act, v[2 * r]);
+            if (i0 + g + 8 * r >= a.d.I || !(fabsf(y) >= kMoeBigFrom && fabsf(y) < INFINITY)) continue;
+            T* p = h + (s.off[e] + col) * 2 * a.w.ip + i0 + g + 8 * r;
+            two_parts(p, a.w.ip, 0.0f);
+            two_parts(p + a.d.T * a.d.top_k * 2 * a.w.ip, a.w.ip, y * (1.0f / kMoeBigUnit));
+            s.big = 1;
+        }
+}
+
+// What the values of h beyond FP16 give to a warp's sums of the down product: elementwise, for the columns that
+// have any.  Out of line, and with nothing handed over that the kernel would have to keep in registers, since few layers
+// ever come here.  (The products with this array by the loop that takes the others cost every FP16 layer of 64
+// tokens 8 %, this function with the loop's variables as arguments 4 %.  Where most of h lies beyond FP16 a layer
+// takes 2 to 8 times as long: 16 tokens, 64 experts of 2048 x 1024, 400 us instead of 111.)
+template <typename T, int NTMAX>
+__device__ __noinline__ void add_big(const MoeArgs& a) {
+    extern __shared__ __align__(128) uint8_t moe_smem[];
+    const MoeShared& s = *reinterpret_cast<const MoeShared*>(moe_smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp & 3, team = warp >> 2;
+    const int cta = static_cast<int>(blockIdx.x), tok = static_cast<int>(a.d.T), A = s.n_active;
+    const int H = static_cast<int>(a.d.H), I = static_cast<int>(a.d.I), KS = static_cast<int>(a.w.ip / 64);
+    const Share ctas((H + kMoeBlock - 1) / kMoeBlock * A * KS, static_cast<int>(gridDim.x));
+    const int c_lo = ctas.lo(cta);
+    const Share teams(ctas.lo(cta + 1) - c_lo, kMoeTeams);
+    const int lo = c_lo + teams.lo(team), hi = c_lo + teams.lo(team + 1);
+    float* yt = reinterpret_cast<float*>(moe_smem + (sizeof(MoeShared) + 127) / 128 * 128) + warp * 2 * 16 * 8 * NTMAX;
+    float* flushed = reinterpret_cast<float*>(a.ws + a.w.flushed) + ((cta * kMoeTeams + team) * kMoeBlock + sub * 16) * tok;
+    const T* h = reinterpret_cast<const T*>(a.ws + a.w.h) + a.d.T * a.d.top_k * 2 * a.w.ip;
+    for (int cur = lo; cur < hi;) {
+        const int v = cur / KS, s0 = cur % KS, s1 = min(KS, s0 + hi - cur);
+        const int ob = v / A, e = s.active[v - ob * A], n = __popcll(s.mask[e]);
+        float* sums = ob == (hi - 1) / KS / A ? yt : flushed;
+        const int k0 = s0 * 64 + lane, k1 = min(s1 * 64, I);
+        for (int c = 0; c < n; ++c) {
+            const int slot = s.off[e] + c;
+            const T* b = h + slot * 2 * a.w.ip;
+            bool any = false;
+            for (int k = k0; k < k1; k += 32) any = any || as_float(b[k]) != 0.0f;
+            if (!__any_sync(0xFFFFFFFFu, any)) continue;
+            for (int r = 0; r < 16; ++r) {
+                const T* row = static_cast<const T*>(a.w2) + e * a.d.stride_w2 +
+                               min(ob * kMoeBlock + sub * 16 + r, H - 1) * a.d.ld_w2;
+                float sum = 0.0f;
+                for (int k = k0; k < k1; k += 32) sum = fmaf(as_float(row[k]), as_float(b[k]) + as_float(b[a.w.ip + k]), sum);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                if (lane == 0) sums[r * tok + s.slot_token[slot]] += s.slot_weight[slot] * kMoeBigUnit * sum;
+            }
+        }
+        __syncwarp();
+        cur += s1 - s0;
+    }
+}
+
 template <typename T, int ROWS, int NTMAX>
-__global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
+__global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constant__ MoeArgs a) {
     constexpr int TILE = 16 * 8 * NTMAX;  // a warp's tile of sums
     extern __shared__ __align__(128) uint8_t moe_smem[];
     MoeShared& s = *reinterpret_cast<MoeShared*>(moe_smem);
@@ -590,7 +679,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
 
     // ---------------------------------------------------------------- routing
     for (int e = threadIdx.x; e < E; e += MT) s.mask[e] = 0ull;
-    if (threadIdx.x == 0) s.gave_up = 0;
+    if (threadIdx.x == 0) s.gave_up = s.big = 0;
     griddep_wait();  // the router's results
     __syncthreads();
     static_assert(kMoeMaxTopK <= 32, "a lane for each pick");
@@ -679,17 +768,11 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         const Share warps(n_u % kMoeWarps * KS, kMoeWarps);
         const int lo = warps.lo(warp), hi = warps.lo(warp + 1);
         const uint16_t* w1 = static_cast<const uint16_t*>(a.w1);
-        // An h in two parts (an infinity, or NaN, in the first alone).
-        const auto put = [&](T* p, float v) {
-            const T hi = cast16<T>(v);
-            const float f = as_float(hi);
-            p[0] = hi;
-            p[a.w.ip] = cast16<T>(fabsf(f) < INFINITY ? v - f : 0.0f);
-        };
         const auto finish = [&](int u, const float (&acc)[NTMAX][4]) {
             const int e = s.active[u / UB];
             const int i0 = u % UB * per;
             const int n = __popcll(s.mask[e]), off = s.off[e];
+            float top = 0.0f;  // the largest magnitude
 #pragma unroll
             for (int j = 0; j < NTMAX; ++j) {
 #pragma unroll
@@ -698,12 +781,24 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
                     if (col >= n) continue;
                     T* row = h + (off + col) * 2 * a.w.ip;
                     const float v0 = acc[j][c], v1 = acc[j][2 + c];
+                    const auto put = [&](int i, float v) {
+                        two_parts(row + i, a.w.ip, v);
+                        top = fmaxf(top, fabsf(v));
+                    };
                     if (gated) {
-                        if (i0 + g < d.I) put(row + i0 + g, v0 / (1.0f + expf(-v0)) * v1);
+                        if (i0 + g < d.I) put(i0 + g, swiglu(v0, v1));
                     } else {
-                        if (i0 + g < d.I) put(row + i0 + g, moe_act(d.act, v0));
-                        if (i0 + g + 8 < d.I) put(row + i0 + g + 8, moe_act(d.act, v1));
+                        if (i0 + g < d.I) put(i0 + g, moe_act(d.act, v0));
+                        if (i0 + g + 8 < d.I) put(i0 + g + 8, moe_act(d.act, v1));
                     }
+                }
+            }
+            if constexpr (kMoeBig<T>) {
+                if (top >= kMoeBigFrom) {
+                    float copy[NTMAX][4];
+#pragma unroll
+                    for (int j = 0; j < NTMAX * 4; ++j) copy[j / 4][j % 4] = acc[j / 4][j % 4];
+                    put_big<T, NTMAX>(a, copy, e, i0);
                 }
             }
         };
@@ -801,15 +896,19 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
     if (threadIdx.x == 0) {
         unsigned* bar = reinterpret_cast<unsigned*>(a.ws + a.w.bar);
         if (!((d.flags & GEMM_FLAG_TEST_STALL) && cta == 0))
-            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
+            // (the low 16 bits count the CTAs, the high ones those that wrote a value beyond FP16)
+            asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(bar), "r"(1u + (static_cast<unsigned>(s.big) << 16))
+                         : "memory");
         const uint64_t t0 = globaltimer_ns();
-        while (ld_acquire_gpu(bar) < static_cast<unsigned>(G)) {
+        unsigned all;
+        while (((all = ld_acquire_gpu(bar)) & 0xFFFFu) < static_cast<unsigned>(G)) {
             if (globaltimer_ns() - t0 > a.timeout_ns) {
                 atomicOr(a.status, DEVERR_TIMEOUT);
                 s.gave_up = 1;
                 break;
             }
         }
+        s.big = static_cast<int>(all >> 16);
     }
     __syncthreads();
     if (s.gave_up) return;
@@ -863,6 +962,9 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const MoeArgs a) {
         }
         __syncwarp();
         cur += s1 - s0;
+    }
+    if constexpr (kMoeBig<T>) {
+        if (s.big) add_big<T, NTMAX>(a);
     }
     __syncthreads();
 
@@ -1009,7 +1111,7 @@ MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid) {
     w.logits = w.counters + round_up((d.H + kMoeBlock - 1) / kMoeBlock * 4, 256);
     w.x = w.logits + round_up(d.T * d.E * 4, 256);
     w.h = w.x + round_up(d.T * w.hp * 2, 256);
-    w.partial = w.h + round_up(d.T * d.top_k * 2 * w.ip * 2, 256);
+    w.partial = w.h + round_up(d.T * d.top_k * (d.dtype == GEMM_F16 ? 4 : 2) * w.ip * 2, 256);
     w.flushed = w.partial + static_cast<int64_t>(grid) * 2 * kMoeBlock * d.T * 4;
     w.bytes = w.flushed + static_cast<int64_t>(grid) * kMoeTeams * kMoeBlock * d.T * 4;
     return w;

@@ -373,8 +373,9 @@ int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  *
  * in FP32 accumulation; cast rounds to nearest even to `dtype`, that of X, Wr,
  * W1, W2 and Y (GEMM_F16 or GEMM_BF16).  Between the products h is held as two
- * numbers of that type, its rounding and the rest (beyond FP16's range: an
- * infinity; an infinite weight in W2 may give NaN where h alone gives an
+ * numbers of that type, its rounding and the rest (GEMM_F16: values beyond its
+ * range, up to 2^32, in units of 2^16, which takes longer, and further on as
+ * infinities; an infinite weight in W2 may give NaN where h alone gives an
  * infinity).  Every weight of a chosen expert is read once.  A token with a
  * logit that is NaN or +infinity, or with none above -infinity, gets a row of
  * NaN, and nothing of it enters another token's row.  (What the tokens choose decides

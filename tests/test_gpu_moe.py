@@ -274,3 +274,33 @@ def test_relu_of_nan_is_nan(T):
     got = g13.moe_layer(x, router, w1, w2, k, act="relu")
     hit = (ids == e).any(1)
     assert bool(got[hit].isnan().all()) and torch.equal(got[~hit], y[~hit])
+
+
+def check_beyond_fp16(key, act, T, E, k, H, I, pad=(0, 0)):
+    # one expert's h lies beyond 65504, its output does not
+    x, router, w1, w2 = inputs(key, T, E, H, I, act, "f16", pad, k)
+    e = int(moe_ref.routing(x.double().numpy(), router.double().numpy(), k)[2][0, 0])
+    w1[e] *= 300 if act == "swiglu" else 40000
+    w2[e] *= 2.0 ** -10
+    ts = on_gpu((x, router, w1, w2))
+    a = torch.einsum("th,ih->ti", x.double(), w1[e].double())
+    h = a[:, :I] * torch.sigmoid(a[:, :I]) * a[:, I:] if act == "swiglu" else a.clamp(min=0)
+    assert h.abs().max() > 65504 and h.abs().max() < 2 ** 32
+    y = g13.moe_layer(*ts, k, act=act)
+    assert bool(y.isfinite().all())
+    check(*ts, k, act, True, y)
+    assert torch.equal(y, g13.moe_layer(*ts, k, act=act))
+
+
+@pytest.mark.parametrize("pad", [(0, 0), (1, 0)])
+@pytest.mark.parametrize("T", [3, 12, 30, 60])
+@pytest.mark.parametrize("act", list(g13.MOE_ACTS))
+def test_values_between_the_products_beyond_fp16(act, T, pad):
+    check_beyond_fp16(("big", act, T, pad), act, T, 5, 2, 200, 72, pad)
+
+
+@pytest.mark.parametrize("case", [(12, 8, 3, 4096, 200), (40, 8, 3, 4096, 333), (2, 2, 2, 16384, 520)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_values_beyond_fp16_in_blocks_cut_between_teams(case):
+    # several steps a team, output blocks that begin and end inside its share
+    check_beyond_fp16(("big cut", case), "swiglu", *case)
