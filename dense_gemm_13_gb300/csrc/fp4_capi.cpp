@@ -41,6 +41,13 @@ bool sizes_ok(int64_t rows, int64_t cols) {
     return rows == 0 || cols == 0 || ((rows + 127) / 128 * 4) * ((cols + 255) / 256) < (int64_t(1) << 30);
 }
 
+bool product_sizes_ok(int64_t M, int64_t N, int64_t K) {
+    if (!sizes_ok(M, K) || !sizes_ok(N, K)) return false;
+    // tile counts, and byte offsets along a row of C, are 32-bit in the kernel
+    return N < (int64_t(1) << 30) &&
+           (M == 0 || N == 0 || ((M + 127) / 128) * ((N + 127) / 128) < (int64_t(1) << 27));
+}
+
 int check_convert(int format, int dtype, int64_t rows, int64_t cols, int64_t ld, const void* matrix,
                   const float* tensor_scale, const void* codes, const void* scales) {
     if (!format_ok(format) || dtype_size(dtype) == 0) return GEMM_ERR_INVALID_ARG;
@@ -89,6 +96,7 @@ int gemm_fp4_dequantize(gemm_fp4_format_t format, gemm_dtype_t dtype, int64_t ro
 
 int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gemm_config_t* out) {
     if (!out || M < 0 || N < 0 || K < 0 || num_sms < 1) return GEMM_ERR_INVALID_ARG;
+    if (!product_sizes_ok(M, N, K)) return GEMM_ERR_UNSUPPORTED;
     const Fp4Config c = fp4_choose(M, N, K, num_sms);
     std::memset(out, 0, sizeof(*out));
     out->kernel = GEMM_KERNEL_TC;
@@ -118,11 +126,7 @@ int gemm_fp4_plan(gemm_fp4_format_t format, int64_t M, int64_t N, int64_t K, int
                                 std::max<int64_t>(e.b_layout == GEMM_B_KN ? N : K, 1), ldc, &e, &p);
     if (rc != GEMM_OK) return rc;
     if (p.epi.b_layout != GEMM_B_NK || p.epi.act == GEMM_ACT_SOFTMAX) return GEMM_ERR_UNSUPPORTED;
-    if (!sizes_ok(M, K) || !sizes_ok(N, K)) return GEMM_ERR_UNSUPPORTED;
-    // tile counts, and byte offsets along a row of C, are 32-bit in the kernel
-    if (N >= (int64_t(1) << 30)) return GEMM_ERR_UNSUPPORTED;
-    if (M > 0 && N > 0 && ((M + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 27))
-        return GEMM_ERR_UNSUPPORTED;
+    if (!product_sizes_ok(M, N, K)) return GEMM_ERR_UNSUPPORTED;
 
     int dev = 0, major = 0, minor = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||

@@ -357,7 +357,7 @@ int gemm_fp4_status(gemm_fp4_plan_t plan);
 void gemm_fp4_destroy(gemm_fp4_plan_t plan);
 /* Host-only: the tile that gemm_fp4_plan would choose on a device with num_sms
  * SMs: rows of A per tile (bn; 128 rows of B), and the CTAs that share a tile's
- * K (split_k).  Errors: INVALID_ARG. */
+ * K (split_k).  Errors: INVALID_ARG, UNSUPPORTED (sizes that gemm_fp4_plan refuses). */
 int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gemm_config_t* out);
 
 /*

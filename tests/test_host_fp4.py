@@ -146,3 +146,12 @@ def test_reference_layout():
     assert t[0] == byte[0, 0] and t[1] == byte[0, 1] and t[16] == byte[1, 0] and t[4] == byte[32, 0]
     assert t[512] == byte[0, 4] and t[1024 + 16] == byte[129, 0] and t[513] == 0
     assert ref.pack(np.array([[1, 2, 3]], np.uint8)).tolist() == [[0x21, 3] + [0] * 14]
+
+
+@pytest.mark.parametrize("M,N,K", [(1 << 31, 40, 64), (4, 1 << 30, 64), (4, 40, 1 << 31), (1 << 29, 1 << 29, 64),
+                                   (1 << 62, 1 << 62, 1 << 62), ((1 << 63) - 1, 1, 1)])
+def test_tile_choice_of_sizes_that_no_plan_takes(lib, M, N, K):
+    # refused with the plan's code, before any of them is multiplied
+    c, h = g13._Config(), ctypes.c_void_p()
+    assert lib.gemm_fp4_select_config(M, N, K, 152, ctypes.byref(c)) == UNSUPPORTED
+    assert lib.gemm_fp4_plan(1, M, N, K, N, None, ctypes.byref(h)) == UNSUPPORTED
