@@ -35,7 +35,7 @@
 // that are not 16-byte aligned are loaded as the granules that hold them and shifted.
 //
 // Measured (bytes of the chosen experts over time): 16 tokens, 64 experts of 2048 x 1024:
-// 114 us, 5.6 TB/s (0.84 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 467 us,
+// 110 us, 5.7 TB/s (0.85 of a copy's rate); 64 tokens, 64 experts of 4096 x 1536: 467 us,
 // 5.2 TB/s (the tokens' values take half of what the SMs read; where an expert has 32
 // tokens or more they take most of it, and 2.5 TB/s remain); one token, 2 of 8
 // experts of 768 x 3072: 16 us, of which 3 are bytes and the rest a chain of two
