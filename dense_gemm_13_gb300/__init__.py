@@ -518,9 +518,11 @@ def _no_capture(t: _Torch, what: str):
 
 
 def _on_device(what: str, index: int, *tensors):
-    """Refuses tensors that the kernels of the current device cannot read (None and addresses pass)."""
+    """Refuses tensors that the kernels of the current device cannot read (None, addresses and objects that only
+    have one pass)."""
     for x in tensors:
-        if x is not None and not isinstance(x, int) and x.get_device() != index:
+        device = getattr(x, "get_device", None)
+        if device is not None and device() != index:
             _refuse(what, "tensors on the current device are wanted")
 
 
@@ -785,7 +787,7 @@ def gemm_moe_run(plan: MoePlan, X, router, W1, W2, Y, workspace, expert_ids=None
     t = _t()
     index = t.device_index()
     _on_device("gemm_moe_run", index, X, router, W1, W2, Y, workspace, expert_ids, expert_weights)
-    if hasattr(workspace, "data_ptr") and workspace.numel() * workspace.element_size() < plan.workspace_bytes:
+    if hasattr(workspace, "numel") and workspace.numel() * workspace.element_size() < plan.workspace_bytes:
         _refuse("gemm_moe_run", f"workspace: {plan.workspace_bytes} bytes are wanted")
     rc = lib().gemm_moe_run(plan.handle, _ptr(X), _ptr(router), _ptr(W1), _ptr(W2), _ptr(Y), _ptr(expert_ids),
                             _ptr(expert_weights), _ptr(workspace), _stream(t, index, stream))

@@ -81,3 +81,14 @@ def test_moe_run_short_workspace(current):
     with pytest.raises(g13.GemmError) as e:  # an address is taken as it is
         g13.gemm_moe_run(plan, **dict(args, workspace=1 << 20))
     assert e.value.status == BAD_PLAN
+
+
+def test_objects_that_only_have_an_address(current):
+    # taken as they are, like an address
+    thing = SimpleNamespace(data_ptr=lambda: 1 << 20)
+    with pytest.raises(g13.GemmError) as e:
+        g13.gemm_fp4_run(SimpleNamespace(handle=None, M=2, N=3, K=64, format="nvfp4"), fp4(1, 2), fp4(1, 3), thing, thing)
+    assert e.value.status == BAD_PLAN
+    with pytest.raises(g13.GemmError) as e:
+        g13.gemm_moe_run(SimpleNamespace(handle=None, workspace_bytes=4096), **{n: thing for n in NAMES})
+    assert e.value.status == BAD_PLAN
