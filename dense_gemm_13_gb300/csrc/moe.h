@@ -11,7 +11,7 @@ constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 512, kMoeMaxTopK = 32, kMoeMa
 constexpr int kMoeWarps = 16;
 constexpr int kMoeBlock = 64;  // output columns that the down product's CTAs share or cut
 
-// Byte offsets of the parts of a run's workspace.
+// Byte offsets of the parts of a run's workspace (FP16: behind h, as large, its values beyond FP16's range).
 struct MoeWorkspace {
     int64_t bar, counters, logits, x, h, partial, flushed, bytes;
     int64_t hp, ip;  // row lengths of the padded copies of x and of h (multiples of 64)
