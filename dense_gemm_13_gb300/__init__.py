@@ -157,6 +157,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
         L.gemm_moe_status.restype = i32
         L.gemm_moe_destroy.argtypes = [vp]
         L.gemm_moe_destroy.restype = None
+        from . import blocks
+        blocks.prototypes(L)
         if path is None:
             _lib = L
         return L
@@ -873,15 +875,23 @@ def moe_layer(x, router, w1, w2, top_k: int, *, act: str = "swiglu", normalize: 
 
 
 def gemm_kept_status() -> int:
-    """Synchronise and return the sticky device status of the plans that matmul, fp4_matmul and moe_layer keep.
+    """Synchronise and return the sticky device status of the plans that matmul, fp4_matmul, fp8_matmul and
+    moe_layer keep.
 
     0, or the code of one whose kernel gave up on a wait (-5): what the calls of its shape have returned
     is not to be used.
     """
-    for plans, status in ((_plans, gemm_plan_status), (_fp4_plans, gemm_fp4_status), (_moe_plans, gemm_moe_status)):
+    for plans, status in ((_plans, gemm_plan_status), (_fp4_plans, gemm_fp4_status), (_moe_plans, gemm_moe_status),
+                          (blocks._fp8_plans, gemm_fp8_status)):
         for key, plan in list(plans.items()):
             with _t().torch.cuda.device(key[-1]):
                 rc = status(plan)
             if rc != 0:
                 return rc
     return 0
+
+
+from . import blocks  # noqa: E402  (it builds on what stands above)
+from .blocks import *  # noqa: E402,F401,F403
+
+__all__ += blocks.__all__

@@ -52,7 +52,6 @@ namespace g13 {
 namespace {
 
 constexpr int FW = 128;            // weight rows (TMEM lanes) of a tile
-constexpr int F_KB = 256;          // K elements per stage: 128 bytes of codes
 constexpr int F_W_TILE = FW * 128;
 enum F4Mode { F4_ONE = 0, F4_SPLIT = 1, F4_PAIR = 2 };
 
@@ -63,7 +62,7 @@ struct F4Layout {
     static constexpr int THREADS = 64 + 32 * EW;
     static constexpr int TILE_W = PAIR ? 2 * FW : FW;       // weight rows of a tile
     static constexpr int X_ROWS = PAIR ? BN / 2 : BN;       // tokens that this CTA loads
-    static constexpr int CT = F_KB / (4 * fp4_block(FMT));  // scale tiles per stage along K
+    static constexpr int CT = fp4_stage_k(FMT) / (4 * fp4_block(FMT));  // scale tiles per stage along K
     static constexpr int XT = (BN + 127) / 128;             // row tiles of the token side
     static constexpr int X_TILE = X_ROWS * 128;
     static constexpr int SFW_BYTES = CT * kFp4TileBytes;
@@ -127,7 +126,12 @@ __device__ __forceinline__ void sf_copy(uint32_t taddr, uint64_t sdesc) {
 template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t acc) {
-    if (FMT == GEMM_MXFP4) {
+    if (FMT == kMxfp8) {
+        if (PAIR)
+            G13_MMA_F4("2", "mxf8f6f4", "1X");
+        else
+            G13_MMA_F4("1", "mxf8f6f4", "1X");
+    } else if (FMT == GEMM_MXFP4) {
         if (PAIR)
             G13_MMA_F4("2", "mxf4", "2X");
         else
@@ -477,7 +481,8 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
         const uint64_t w_desc = smem_desc_sw128(ring, 16, 1024);
         const uint64_t x_desc = smem_desc_sw128(ring + F_W_TILE, 16, 1024);
         const uint64_t s_desc = sf_desc(ring + F_W_TILE + L::X_TILE);
-        const int k_steps = static_cast<int>((args.K + 63) / 64);
+        constexpr int STEP_K = fp4_stage_k(FMT) / 4;  // K elements of an MMA: 32 bytes
+        const int k_steps = static_cast<int>((args.K + STEP_K - 1) / STEP_K);
         const auto commit = [&](uint64_t* bar) {
             if (PAIR)
                 tc_commit_pair(smem_u32(bar), 0x3);
@@ -521,7 +526,7 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
                 if (one) {
                     // TMEM columns of scale tile c: weights at 4c, tokens' row tile x at
                     // 4 (CT + c XT + x).  nvfp4: a tile per step; mxfp4: two steps share
-                    // a tile, bytes 0-1 and 2-3
+                    // a tile, bytes 0-1 and 2-3; mxfp8: four, a byte each
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
                         if (kk > 0 && steps <= kk) break;
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(F4Layout<BN, FMT, MODE>::THREADS, 1)
                                 sf_copy<PAIR>(sf_t + 4 * (L::CT + c * L::XT + x),
                                               s_desc + off + ((L::SFW_BYTES * (1 + x) + c * kFp4TileBytes) >> 4));
                         }
-                        const uint32_t id = PER == 2 ? (kk & 1) * 2u : 0u;
+                        const uint32_t id = PER == 4 ? kk : PER == 2 ? (kk & 1) * 2u : 0u;
                         mma_f4<FMT, PAIR>(d, w_desc + off + kk * 2, x_desc + off + kk * 2,
                                           args.idesc | (id << 29) | (id << 4), sf_t + 4 * c,
                                           sf_t + 4 * (L::CT + c * L::XT), (kb > kb_lo || kk > 0) ? 1u : 0u);
@@ -711,6 +716,7 @@ cudaError_t launch_f4(const F4Maps& m, const F4Args& a, int splits, int num_sms,
 
 template <int BN, int STAGES, int MODE>
 cudaError_t launch_fmt(int fmt, const F4Maps& m, const F4Args& a, int splits, int num_sms, cudaStream_t st) {
+    if (fmt == kMxfp8) return launch_f4<BN, STAGES, kMxfp8, MODE>(m, a, splits, num_sms, st);
     return fmt == GEMM_MXFP4 ? launch_f4<BN, STAGES, GEMM_MXFP4, MODE>(m, a, splits, num_sms, st)
                              : launch_f4<BN, STAGES, GEMM_NVFP4, MODE>(m, a, splits, num_sms, st);
 }
@@ -734,20 +740,22 @@ int launch_fp4_gemm(const Fp4Config& c, int fmt, const Fp4Operand& A, const Fp4O
     a.gx = A.tensor_scale;
     a.n_tiles = (e.N + tile_w - 1) / tile_w;
     a.m_tiles = (e.M + c.bn - 1) / c.bn;
-    a.k_blocks = static_cast<int>((K + F_KB - 1) / F_KB);
+    const int stage_k = fp4_stage_k(fmt);
+    a.k_blocks = static_cast<int>((K + stage_k - 1) / stage_k);
     a.raster = 8;
     a.e = e;
     a.status = lc.status;
     a.timeout_ns = lc.timeout_ns;
     a.flags = lc.flags;
-    // instruction descriptor: E2M1 operands (1), scale type (1: UE8M0), N, M
-    a.idesc = (1u << 7) | (1u << 10) | (static_cast<uint32_t>(c.bn >> 3) << 17) |
-              ((fmt == GEMM_MXFP4 ? 1u : 0u) << 23) | (static_cast<uint32_t>(tile_w >> 7) << 27);
+    // instruction descriptor: operands (1: E2M1, in kind::mxf8f6f4 0: E4M3), scale type (1: UE8M0), N, M
+    const uint32_t type = fmt == kMxfp8 ? 0u : 1u;
+    a.idesc = (type << 7) | (type << 10) | (static_cast<uint32_t>(c.bn >> 3) << 17) |
+              ((fmt == GEMM_NVFP4 ? 0u : 1u) << 23) | (static_cast<uint32_t>(tile_w >> 7) << 27);
     F4Maps m{};
     if (K > 0) {
-        const int64_t rb = fp4_row_bytes(K);
+        const int64_t rb = fp4_row_bytes(fmt, K);
         const int64_t ct = fp4_col_tiles(fmt, K);
-        const uint32_t box_ct = static_cast<uint32_t>(F_KB / (4 * fp4_block(fmt)));
+        const uint32_t box_ct = static_cast<uint32_t>(stage_k / (4 * fp4_block(fmt)));
         int rc = tmap_encode_rows_u8(&m.w, B.codes, rb, e.N, FW);
         if (rc == GEMM_OK)
             rc = tmap_encode_rows_u8(&m.x, A.codes, rb, e.M, static_cast<uint32_t>(pair ? c.bn / 2 : c.bn));
@@ -765,6 +773,10 @@ int launch_fp4_gemm(const Fp4Config& c, int fmt, const Fp4Operand& A, const Fp4O
         case 64: ce = launch_bn<64, 7>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
         case 128: ce = launch_bn<128, 6>(fmt, m, a, c.splits, lc.num_sms, lc.stream); break;
         case 256:  // as many stages as shared memory holds (mxfp4's 35 KB: 6, 184 us at 8192^3 instead of 187)
+            if (fmt == kMxfp8) {
+                ce = launch_f4<256, 6, kMxfp8, F4_PAIR>(m, a, 1, lc.num_sms, lc.stream);
+                break;
+            }
             ce = fmt == GEMM_MXFP4 ? launch_f4<256, 6, GEMM_MXFP4, F4_PAIR>(m, a, 1, lc.num_sms, lc.stream)
                                    : launch_f4<256, 5, GEMM_NVFP4, F4_PAIR>(m, a, 1, lc.num_sms, lc.stream);
             break;
@@ -782,14 +794,14 @@ int64_t clusters_at_once(int splits, int num_sms) {
 // Up to 64 tokens: the narrowest of 16, 32, 64 that holds them all (a stage streams the same
 // weights with any of them), K split over a cluster of 2, 4 or 8 while all tiles run at once.
 // Above: the cheapest of 128 x 128 tiles, those with K split, and CTA pairs on 256 x 256, by a
-// model in ns: a stage of 256 K elements takes 300 on 128 x 128 (the bytes from L2 bound it: 36 KB
+// model in ns: a stage (128 bytes of each row) takes 300 on 128 x 128 (the bytes from L2 bound it: 36 KB
 // per SM) and 360 on a pair for four times the area (38 KB per SM); a tile's stages hide the one
 // before's epilogue, or wait for it (1500, 3000); launch, fill and last epilogue as measured.
-Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
+Fp4Config fp4_choose(int fmt, int64_t M, int64_t N, int64_t K, int num_sms) {
     Fp4Config best{};
     best.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     best.splits = 1;
-    const int64_t n_tiles = (N + FW - 1) / FW, kbs = (K + F_KB - 1) / F_KB;
+    const int64_t n_tiles = (N + FW - 1) / FW, kbs = (K + fp4_stage_k(fmt) - 1) / fp4_stage_k(fmt);
     const int64_t tiles = n_tiles * ((M + best.bn - 1) / best.bn);
     if (tiles == 0) return best;
     const auto waves = [](int64_t t, int64_t at_once) { return (t + at_once - 1) / at_once; };

@@ -11,7 +11,7 @@ struct Fp4Config {
     int bn;      // tokens per tile: 16, 32, 64, 128, or 256 on CTA pairs
     int splits;  // CTAs of a cluster that share a tile's K (1 to 8)
 };
-Fp4Config fp4_choose(int64_t M, int64_t N, int64_t K, int num_sms);
+Fp4Config fp4_choose(int fmt, int64_t M, int64_t N, int64_t K, int num_sms);
 
 // A matrix in 4 bits (device pointers).
 struct Fp4Operand {

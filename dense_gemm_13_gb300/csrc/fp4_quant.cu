@@ -1,10 +1,12 @@
-// fp4_quant.cu -- matrices to microscaled 4-bit floats and back.
+// fp4_quant.cu -- matrices to microscaled 4-bit (and 8-bit) floats and back.
 //
 //   mxfp4  d = 2^E, E = floor(log2 max|x|) - 2 over blocks of 32, kept in
 //          [-127, 127] (the exponent rule of the OCP microscaling formats)
 //   nvfp4  s = E4M3(max|x| / (6 g)) over blocks of 16, d = fl32(s g), with a
 //          scale g of the whole tensor
 //   code   = nearest E2M1 value to fl32(x / d), ties to even, saturating at 6
+//   mxfp8  blocks of 32 as mxfp4's, E the least with max|x| <= 448 2^E (mxfp4's rule would
+//          saturate the largest eighth of a binade); code = nearest E4M3 value to x / d
 //
 // Both directions move every byte once, so memory bounds them.  A thread takes
 // 16 elements at a time (an nvfp4 block; half an mxfp4 block, joined by one
@@ -21,7 +23,9 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "fp4.cuh"
+#include <type_traits>
+
+#include "fp8.cuh"
 #include "internal.h"
 
 namespace g13 {
@@ -83,23 +87,6 @@ __device__ __forceinline__ void e2m1x8_values(uint32_t codes, float* y) {
     }
 }
 
-// E4M3 byte of a value in [0, 448] (round to nearest even), and its value.
-__device__ __forceinline__ uint32_t e4m3_byte(float v) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
-    return r & 0xFFu;
-}
-__device__ __forceinline__ float e4m3_value(uint32_t byte) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-}
-// The value of a UE8M0 byte, 2^(byte - 127); 255 is NaN.
-__device__ __forceinline__ float ue8m0_value(uint32_t byte) {
-    if (byte == 0xFFu) return __uint_as_float(0x7FFFFFFFu);
-    return __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
-}
-
 // 16 consecutive elements of a row.
 template <typename T>
 struct __align__(16) Sixteen {
@@ -159,7 +146,7 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 
 // VEC: rows are 16-byte aligned.
 template <int FMT, typename T, bool VEC>
-__global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
+__global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : FMT == kMxfp8 ? 6 : 8)
     fp4_quantize_kernel(const T* __restrict__ src, int64_t rows, int64_t cols, int64_t ld,
                         const float* __restrict__ gscale, uint8_t* __restrict__ codes,
                         uint8_t* __restrict__ scales, int64_t col_blocks) {
@@ -171,7 +158,7 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
     const int64_t rb = blockIdx.x / col_blocks, cb = blockIdx.x - rb * col_blocks;
     const int64_t rt = rb >> 2;          // row tile of 128
     const int sub = static_cast<int>(rb & 3);
-    const int64_t row_bytes = fp4_row_bytes(cols);
+    const int64_t row_bytes = fp4_row_bytes(FMT, cols);
     const int64_t ctiles = fp4_col_tiles(FMT, cols);
     const float g = FMT == GEMM_NVFP4 && gscale ? __ldg(gscale) : 1.0f;
     const int tc = threadIdx.x & 15, tr = threadIdx.x >> 4;
@@ -202,7 +189,7 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
         const int slot = p * 16 + tr;
         const int64_t row = row_of(slot), c0 = cb * QCOLS + tc * 16;
         uint32_t top = top16(x[p]);
-        if (FMT == GEMM_MXFP4) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        if (BLK == 32) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         uint32_t byte;
         float d = 1.0f, inv;
         bool near = true;  // the block's quotients x / d stay far inside FP32
@@ -212,6 +199,9 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
             const int e = static_cast<int>(top >> 23) - 127 - 2;
             byte = top >= 0x7F800000u ? 0xFFu : static_cast<uint32_t>(max(e, -127) + 127);
             inv = ue8m0_value(254u - min(byte, 254u));  // 2^-E
+        } else if (FMT == kMxfp8) {
+            byte = mxfp8_scale(top);
+            inv = ue8m0_value(254u - min(byte, 254u));
         } else {
             const float r = __fdiv_rn(__uint_as_float(top), 6.0f * g);
             near = r < 0x1p60f;
@@ -219,13 +209,13 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
             d = e4m3_value(byte) * g;
             inv = __frcp_rn(d);
         }
-        uint32_t code[2];
+        uint32_t code[FMT == kMxfp8 ? 4 : 2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float v[8], y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(x[p].v[8 * h + i]);
-            if (FMT == GEMM_MXFP4) {
+            if (BLK == 32) {
                 // exact products, apart from results far below the least code
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
@@ -248,10 +238,20 @@ __global__ void __launch_bounds__(QT, sizeof(T) == 4 ? 5 : 8)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] = d > 0.0f ? __fdiv_rn(v[i], d) : 0.0f * v[i];
             }
-            code[h] = e2m1x8(y);
+            if constexpr (FMT == kMxfp8) {
+                code[2 * h] = e4m3x4(y);
+                code[2 * h + 1] = e4m3x4(y + 4);
+            } else {
+                code[h] = e2m1x8(y);
+            }
         }
-        if (row < rows && c0 / 2 < row_bytes)
-            *reinterpret_cast<uint2*>(codes + row * row_bytes + c0 / 2) = make_uint2(code[0], code[1]);
+        if constexpr (FMT == kMxfp8) {
+            if (row < rows && c0 < row_bytes)
+                *reinterpret_cast<uint4*>(codes + row * row_bytes + c0) = make_uint4(code[0], code[1], code[2], code[3]);
+        } else {
+            if (row < rows && c0 / 2 < row_bytes)
+                *reinterpret_cast<uint2*>(codes + row * row_bytes + c0 / 2) = make_uint2(code[0], code[1]);
+        }
         // blocks past the row's end and rows past the matrix: zeros
         if (row >= rows || c0 / BLK >= (cols + BLK - 1) / BLK) byte = 0;
         const int blk = tc * 16 / BLK;  // block within the CTA
@@ -279,18 +279,26 @@ __global__ void __launch_bounds__(QT)
     const int64_t c0 = (i - row * groups) * 16;
     __align__(32) T out[16];
     if (row < rows) {
-        const int64_t row_bytes = fp4_row_bytes(cols);
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + row * row_bytes + c0 / 2));
+        const int64_t row_bytes = fp4_row_bytes(FMT, cols);
         const int64_t blk = c0 / fp4_block(FMT);
         const int r = static_cast<int>(row & 127);
         const uint32_t byte =
             __ldg(scales + ((row >> 7) * fp4_col_tiles(FMT, cols) + (blk >> 2)) * kFp4TileBytes +
                   (r & 31) * 16 + (r >> 5) * 4 + (blk & 3));
-        const float d = FMT == GEMM_MXFP4 ? ue8m0_value(byte)
-                                          : e4m3_value(byte) * (gscale ? __ldg(gscale) : 1.0f);
+        const float d = fp4_block(FMT) == 32 ? ue8m0_value(byte)
+                                             : e4m3_value(byte) * (gscale ? __ldg(gscale) : 1.0f);
         float y[16];
-        e2m1x8_values(w.x, y);
-        e2m1x8_values(w.y, y + 8);
+        if constexpr (FMT == kMxfp8) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(codes + row * row_bytes + c0));
+            e4m3x4_values(w.x, y);
+            e4m3x4_values(w.y, y + 4);
+            e4m3x4_values(w.z, y + 8);
+            e4m3x4_values(w.w, y + 12);
+        } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes + row * row_bytes + c0 / 2));
+            e2m1x8_values(w.x, y);
+            e2m1x8_values(w.y, y + 8);
+        }
 #pragma unroll
         for (int j = 0; j < 16; ++j) out[j] = from_f32<T>(y[j] * d);
     }
@@ -367,35 +375,29 @@ cudaError_t dequantize_t(const uint8_t* codes, const uint8_t* scales, const floa
 cudaError_t launch_fp4_quantize(int fmt, int dtype, const void* src, int64_t rows, int64_t cols,
                                 int64_t ld, const float* g, uint8_t* codes, uint8_t* scales,
                                 cudaStream_t st) {
-    if (fmt == GEMM_MXFP4) {
-        if (dtype == GEMM_F32)
-            return quantize_t<GEMM_MXFP4, float>(src, rows, cols, ld, g, codes, scales, st);
-        if (dtype == GEMM_F16)
-            return quantize_t<GEMM_MXFP4, __half>(src, rows, cols, ld, g, codes, scales, st);
-        return quantize_t<GEMM_MXFP4, __nv_bfloat16>(src, rows, cols, ld, g, codes, scales, st);
-    }
-    if (dtype == GEMM_F32)
-        return quantize_t<GEMM_NVFP4, float>(src, rows, cols, ld, g, codes, scales, st);
-    if (dtype == GEMM_F16)
-        return quantize_t<GEMM_NVFP4, __half>(src, rows, cols, ld, g, codes, scales, st);
-    return quantize_t<GEMM_NVFP4, __nv_bfloat16>(src, rows, cols, ld, g, codes, scales, st);
+    const auto run = [&](auto f) {
+        constexpr int F = decltype(f)::value;
+        if (dtype == GEMM_F32) return quantize_t<F, float>(src, rows, cols, ld, g, codes, scales, st);
+        if (dtype == GEMM_F16) return quantize_t<F, __half>(src, rows, cols, ld, g, codes, scales, st);
+        return quantize_t<F, __nv_bfloat16>(src, rows, cols, ld, g, codes, scales, st);
+    };
+    if (fmt == kMxfp8) return run(std::integral_constant<int, kMxfp8>{});
+    if (fmt == GEMM_MXFP4) return run(std::integral_constant<int, GEMM_MXFP4>{});
+    return run(std::integral_constant<int, GEMM_NVFP4>{});
 }
 
 cudaError_t launch_fp4_dequantize(int fmt, int dtype, const uint8_t* codes, const uint8_t* scales,
                                   const float* g, void* dst, int64_t rows, int64_t cols, int64_t ld,
                                   cudaStream_t st) {
-    if (fmt == GEMM_MXFP4) {
-        if (dtype == GEMM_F32)
-            return dequantize_t<GEMM_MXFP4, float>(codes, scales, g, dst, rows, cols, ld, st);
-        if (dtype == GEMM_F16)
-            return dequantize_t<GEMM_MXFP4, __half>(codes, scales, g, dst, rows, cols, ld, st);
-        return dequantize_t<GEMM_MXFP4, __nv_bfloat16>(codes, scales, g, dst, rows, cols, ld, st);
-    }
-    if (dtype == GEMM_F32)
-        return dequantize_t<GEMM_NVFP4, float>(codes, scales, g, dst, rows, cols, ld, st);
-    if (dtype == GEMM_F16)
-        return dequantize_t<GEMM_NVFP4, __half>(codes, scales, g, dst, rows, cols, ld, st);
-    return dequantize_t<GEMM_NVFP4, __nv_bfloat16>(codes, scales, g, dst, rows, cols, ld, st);
+    const auto run = [&](auto f) {
+        constexpr int F = decltype(f)::value;
+        if (dtype == GEMM_F32) return dequantize_t<F, float>(codes, scales, g, dst, rows, cols, ld, st);
+        if (dtype == GEMM_F16) return dequantize_t<F, __half>(codes, scales, g, dst, rows, cols, ld, st);
+        return dequantize_t<F, __nv_bfloat16>(codes, scales, g, dst, rows, cols, ld, st);
+    };
+    if (fmt == kMxfp8) return run(std::integral_constant<int, kMxfp8>{});
+    if (fmt == GEMM_MXFP4) return run(std::integral_constant<int, GEMM_MXFP4>{});
+    return run(std::integral_constant<int, GEMM_NVFP4>{});
 }
 
 }  // namespace g13

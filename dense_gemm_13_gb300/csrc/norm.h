@@ -1,0 +1,24 @@
+// norm.h -- root-mean-square norm: arguments and launcher.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gemm13.h"
+
+namespace g13 {
+
+constexpr int64_t kNormMaxCols = int64_t(1) << 22;
+
+struct NormArgs {
+    gemm_norm_desc_t d;
+    const void* x;
+    const void* r;  // residual, or null
+    const void* w;  // or null
+    void* h;        // or null
+    void* y;        // values, or codes
+    uint8_t* scales;
+};
+
+cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);
+
+}  // namespace g13

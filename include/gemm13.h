@@ -361,6 +361,184 @@ void gemm_fp4_destroy(gemm_fp4_plan_t plan);
 int gemm_fp4_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gemm_config_t* out);
 
 /*
+ * 8-bit floats (mxfp8).  A matrix [rows][cols] is two device arrays, both
+ * 16-byte aligned:
+ *   codes   E4M3 values (sign, 4 exponent bits, 3 mantissa bits; up to 448), a
+ *           byte each, in rows of gemm_fp8_row_bytes(cols) bytes (cols padded to
+ *           32 elements).
+ *   scales  as for GEMM_MXFP4: blocks of 32 along a row, byte b the scale
+ *           2^(b - 127) (255: NaN), in the same tiles of 128 rows x 4 blocks,
+ *           gemm_fp8_scales_bytes() bytes in all.  element = code * scale.
+ * Padding in both arrays is zero; gemm_fp8_quantize and gemm_rms_norm write all of it.
+ *
+ * gemm_fp8_quantize: scale 2^E, E the least with max|x| <= 448 * 2^E over the
+ * block, kept in [-127, 127] (a block of zeros: -127); code the nearest E4M3 value
+ * to x / scale, ties to the even code.  A block that holds an infinity or a NaN
+ * gets a NaN scale (its codes mean nothing).
+ * The calls are as the gemm_fp4_ calls of the same names, without the format and
+ * the tensor scales; the product's K elements of a stage are 128 instead of 256.
+ */
+int64_t gemm_fp8_row_bytes(int64_t cols);
+int64_t gemm_fp8_scales_bytes(int64_t rows, int64_t cols);
+int gemm_fp8_quantize(gemm_dtype_t dtype, int64_t rows, int64_t cols, const void* src, int64_t ld, void* codes,
+                      void* scales, void* stream);
+int gemm_fp8_dequantize(gemm_dtype_t dtype, int64_t rows, int64_t cols, const void* codes, const void* scales,
+                        void* dst, int64_t ld, void* stream);
+typedef struct gemm_fp8_plan_s* gemm_fp8_plan_t;
+int gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int64_t ldc, const gemm_epilogue_t* epilogue,
+                  gemm_fp8_plan_t* out_plan);
+int gemm_fp8_run(gemm_fp8_plan_t plan, const void* a_codes, const void* a_scales, const void* b_codes,
+                 const void* b_scales, void* C, const void* bias, const void* residual, float alpha, void* stream);
+int gemm_fp8_status(gemm_fp8_plan_t plan);
+void gemm_fp8_destroy(gemm_fp8_plan_t plan);
+int gemm_fp8_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gemm_config_t* out);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it:
+ *
+ *     H = cast(X + R)                 to R's type, round to nearest even (has_residual; else H is X)
+ *     Y = cast( H / sqrt(mean_k H^2 + eps) * (weight + weight_offset) )
+ *
+ * sums and all steps in FP32.  Y is computed from the rounded H, so that a later call on H
+ * alone gives the same.  With mxfp8, Y is written as 8-bit floats (above): codes and scales of
+ * the FP32 values, as gemm_fp8_quantize would of them (sums added in 64 bits, the factor and its product
+ * with H and the weight to 2^-23 of their values before the one rounding).
+ * A row's sum of squares must stay within FP32.  NaN and infinities: as the formula has them.
+ */
+typedef struct {
+    gemm_dtype_t dtype;          /* X; default GEMM_BF16 */
+    int has_residual;            /* 1: R is added */
+    gemm_dtype_t residual_dtype; /* R and H: GEMM_F32 or `dtype`; default GEMM_BF16 */
+    gemm_dtype_t weight_dtype;   /* default GEMM_BF16 */
+    gemm_dtype_t out_dtype;      /* Y, unless mxfp8; default GEMM_BF16 */
+    int mxfp8;                   /* 1: Y holds codes, `scales` the scales */
+    int64_t rows, cols;          /* cols: 1 to 2^22 */
+    int64_t ldx, ldr, ldh, ldy;  /* in elements; 0 means cols (ldy: not used with mxfp8) */
+    float eps;                   /* default 1e-6; finite, >= 0 */
+    float weight_offset;         /* default 0; finite */
+} gemm_norm_desc_t;
+
+/* Fills *d with the defaults listed above (0 elsewhere). */
+void gemm_norm_desc_init(gemm_norm_desc_t* d);
+
+/*
+ * Enqueues the norm (one kernel) on `stream`.  All pointers are device pointers aligned to
+ * their element type (codes and scales to 16 bytes); rows that all start on 16 bytes go
+ * fastest.  residual: R, NULL iff !has_residual.  weight: [cols], or NULL for ones.  H: NULL
+ * (not wanted), and without a residual always.  scales: NULL iff !mxfp8.  H, and Y unless mxfp8, may be
+ * X or R itself (same type and stride; not both the same one); they overlap nothing else.
+ * Allocates nothing and needs no workspace; calls may overlap.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED (sizes), NO_DEVICE, CUDA.
+ */
+int gemm_rms_norm(const gemm_norm_desc_t* desc, const void* X, const void* residual, const void* weight, void* H,
+                  void* Y, void* scales, void* stream);
+
+/*
+ * 4-bit weights with group scales.  W [N][K] (rows: output columns, as a weight
+ * lies for X.W^T) in integers 0..15:  w = (q - z) * s  with a 16-bit scale s
+ * (GEMM_F16 or GEMM_BF16) and an integer zero z in 0..15 for each `group` (a multiple of 32) columns of
+ * a row; without an array of zeros z = 8.  Device arrays, 16-byte aligned:
+ *   codes   gemm_w4_codes_bytes() bytes in blocks of 16 rows x 64 columns, 512
+ *           bytes each, the blocks of 16 rows one after another along K.  Row r,
+ *           column k of a block are in its 32-bit word
+ *           ((r % 8) * 4 + k % 32 / 8) * 4 + k / 32 * 2 + r / 8  (little endian),
+ *           at bits 4 * (k % 2 * 4 + k % 8 / 2).
+ *   scales, zeros (a byte each)   gemm_w4_scales_count() entries; row r, group c
+ *           at ((r / 16) * groups + c) * 16 + r % 8 * 2 + r % 16 / 8,
+ *           groups = ceil(K / group).
+ * Padding is zero; the two calls that write them write all of it.  N up to 2^28,
+ * K and group up to 65536, codes below 2^31 blocks; the size calls return 0 for others.
+ */
+int64_t gemm_w4_codes_bytes(int64_t N, int64_t K);
+int64_t gemm_w4_scales_count(int64_t N, int64_t K, int64_t group);
+
+/*
+ * Quantises src (dtype, [N][ld]) to the nearest codes.  With zeros: lo = min(w, 0)
+ * and hi = max(w, 0) of the group, s = (hi - lo) / 15 rounded to scale_dtype,
+ * z = -lo / s rounded, in 0..15; zeros NULL: s = max|w| / 7.5.  q = w / s rounded + z, kept in
+ * 0..15 (FP32; halves to even).  A group that holds an infinity or a NaN gets a NaN scale.
+ * src overlaps no output.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA.
+ */
+int gemm_w4_quantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, int64_t K, int64_t group,
+                     const void* src, int64_t ld, void* codes, void* scales, void* zeros, void* stream);
+/* Codes of a checkpoint, a byte each (q [N][ldq], its low four bits), scales (16 bits, [N][lds]) and
+ * zeros (a byte each, [N][ldz]; NULL with `zeros` NULL) of its groups, into the arrays above.  Errors: as above. */
+int gemm_w4_pack(int64_t N, int64_t K, int64_t group, const void* q, int64_t ldq, const void* s, int64_t lds,
+                 const void* z, int64_t ldz, void* codes, void* scales, void* zeros, void* stream);
+/* (q - z) * s in FP32, rounded to nearest even to dtype, into dst ([N][ld]).  Errors: as above. */
+int gemm_w4_dequantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, int64_t K, int64_t group,
+                       const void* codes, const void* scales, const void* zeros, void* dst, int64_t ld, void* stream);
+
+/*
+ * Y = cast( act( alpha * X.W^T + bias ) + beta * R ) for 1 to 64 tokens.  X [M][K] in the scales'
+ * type; products of X with q - z are exact, their sums over a group and the sums of
+ * scale * group in FP32: no weight is rounded.  (More tokens: gemm_w4_dequantize, then gemm_run.)
+ */
+typedef struct {
+    gemm_dtype_t dtype;     /* X and the scales: GEMM_BF16 (default) or GEMM_F16 */
+    gemm_dtype_t out_dtype; /* default GEMM_BF16 */
+    int64_t M;              /* tokens, 0 to 64 */
+    int64_t N, K, group;    /* group: default 128 */
+    int has_zeros;
+    int has_bias;           /* FP32 [N] */
+    gemm_act_t act;         /* none, GELU or ReLU (as in gemm_run) */
+    int has_residual;       /* FP32 [M][ldr] */
+    float beta;             /* default 1 */
+    int64_t ldx, ldy, ldr;  /* in elements; 0 means K, N and ldy */
+} gemm_w4_desc_t;
+
+/* Fills *d with the defaults listed above (0 elsewhere). */
+void gemm_w4_desc_init(gemm_w4_desc_t* d);
+
+/* Enqueues the product (one kernel) on `stream`.  Pointers aligned to their element type
+ * (codes, scales, zeros: 16 bytes); Y overlaps no input.  Allocates nothing and needs no
+ * workspace; calls may overlap.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA. */
+int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, const void* scales, const void* zeros,
+                void* Y, const void* bias, const void* residual, float alpha, void* stream);
+
+/*
+ * Routing to experts: the choice of each token's experts, and their weights, from
+ * its logits z [T][E] (any number of tokens):
+ *
+ *     s = softmax(z) over all E experts, or sigmoid(z)
+ *     c = s + bias                     (bias FP32 [E], NULL: none)
+ *     groups > top_groups: the experts lie in `groups` equal groups, one after
+ *       another; the top_groups groups with the largest score stay, the score
+ *       being their largest c, or the sum of their two largest c
+ *     the top_k experts of a token are those with the largest c among the groups that stay
+ *     weight = s, with normalize divided by the sum of the chosen s; times scale
+ *
+ * Experts come in falling order of c, groups and experts that are equal by the lowest index.
+ * The order is that of c as a real number: without a bias the logits themselves are compared,
+ * and where c in FP32 leaves two in doubt it is computed in 64 bits.  NaN comes
+ * last.  Weights are FP32 throughout; a token whose logits hold a NaN or +infinity, or
+ * none above -infinity, gets NaN weights with softmax (with sigmoid only a chosen NaN does so).
+ */
+typedef enum { GEMM_ROUTE_SOFTMAX = 0, GEMM_ROUTE_SIGMOID = 1 } gemm_route_scores_t;
+typedef enum { GEMM_ROUTE_GROUP_MAX = 0, GEMM_ROUTE_GROUP_TOP2 = 1 } gemm_route_group_t;
+typedef struct {
+    gemm_dtype_t dtype;             /* logits; default GEMM_F32 */
+    int64_t T;                      /* tokens, >= 0 */
+    int64_t E;                      /* experts, 1 to 512 */
+    int64_t top_k;                  /* 1 to min(E / groups * top_groups, 32) */
+    gemm_route_scores_t scores;     /* default GEMM_ROUTE_SOFTMAX */
+    int64_t groups, top_groups;     /* default 1, 1; groups divides E, at most 32 */
+    gemm_route_group_t group_score; /* default GEMM_ROUTE_GROUP_MAX */
+    int normalize;                  /* default 1 */
+    float scale;                    /* default 1; finite */
+    int64_t ld;                     /* logits' row stride in elements; 0 means E */
+} gemm_route_desc_t;
+
+/* Fills *d with the defaults listed above (0 elsewhere). */
+void gemm_route_desc_init(gemm_route_desc_t* d);
+
+/* Enqueues the routing (one kernel) on `stream`: expert_ids int32 [T][top_k], expert_weights FP32
+ * [T][top_k].  Pointers aligned to their element type; outputs overlap no input.  Allocates nothing; calls may
+ * overlap.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA. */
+int gemm_route(const gemm_route_desc_t* desc, const void* logits, const float* bias, int32_t* expert_ids,
+               float* expert_weights, void* stream);
+
+/*
  * A mixture-of-experts layer for a few tokens, all of it: router, choice of
  * experts, both products of each chosen expert, and their weighted sum.
  *
