@@ -615,6 +615,8 @@ def fp4_dequantize(q: Fp4Tensor, dtype: str = "f32", out=None, stream=None):
     if code is None:
         _refuse(what, f"unknown dtype {dtype!r}")
     index, rows, cols = q._index, q._rows, q._cols
+    if q._format not in FP4_FORMATS:
+        _refuse(what, "an Fp4Tensor is wanted")
     if stream is not None:
         with t.on(stream, index):
             return fp4_dequantize(q, dtype, out)
@@ -738,6 +740,8 @@ def fp4_matmul(A: Fp4Tensor, B: Fp4Tensor, *, alpha=1.0, bias=None, act="none", 
     key = (format, M, N, K, ldc, ldr, out_dtype, bias is not None, act, beta, index)
     pl = _fp4_plans.get(key)
     if pl is None:
+        if format not in FP4_FORMATS:
+            _refuse(what, "Fp4Tensors are wanted")
         _no_capture(t, what)
         ep = Epilogue(b_layout="nk", out_dtype=out_dtype, bias=bias is not None, act=act,
                       residual=residual is not None, beta=beta, ldr=ldr)

@@ -7,12 +7,13 @@ from __future__ import annotations
 
 import ctypes
 
-from . import (ACTS, DTYPES, Config, Epilogue, GemmError, _Config, _keep, _ld, _no_capture, _on_device,
-               _ptr, _refuse, _rows_ok, _stream, _t, lib)
+from . import (ACTS, DTYPES, MOE_ACTS, Config, Epilogue, GemmError, MoePlan, _Config, _keep, _ld, _moe_plans,
+               _no_capture, _on_device, _ptr, _refuse, _rows_ok, _stream, _t, gemm_moe_plan, lib)
 
 __all__ = ["rms_norm", "Fp8Tensor", "Fp8Plan", "fp8_quantize", "fp8_dequantize", "gemm_fp8_plan", "gemm_fp8_run",
            "gemm_fp8_status", "gemm_fp8_select_config", "fp8_matmul", "W4Tensor", "w4_quantize", "w4_pack",
-           "w4_dequantize", "w4_matmul", "ROUTE_SCORES", "ROUTE_GROUP_SCORES", "route"]
+           "w4_dequantize", "w4_matmul", "ROUTE_SCORES", "ROUTE_GROUP_SCORES", "route", "gemm_moe_run_routed",
+           "moe_experts"]
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 ROUTE_GROUP_SCORES = {"max": 0, "top2": 1}
@@ -61,7 +62,8 @@ def prototypes(L) -> None:
             ("gemm_w4_desc_init", None, [P(_W4Desc)]),
             ("gemm_w4_run", i32, [P(_W4Desc)] + [vp] * 7 + [f32, vp]),
             ("gemm_route_desc_init", None, [P(_RouteDesc)]),
-            ("gemm_route", i32, [P(_RouteDesc)] + [vp] * 5)):
+            ("gemm_route", i32, [P(_RouteDesc)] + [vp] * 5),
+            ("gemm_moe_run_routed", i32, [vp] * 9)):
         f = getattr(L, name)
         f.restype, f.argtypes = res, args
 
@@ -217,7 +219,7 @@ class Fp8Tensor:
 
     rows = property(lambda self: self._rows)
     cols = property(lambda self: self._cols)
-    format = property(lambda self: "mxfp8")
+    format = _format = property(lambda self: "mxfp8")
 
     def _ptrs(self):
         """Addresses of codes and scales (and None, the tensor scale that this format lacks)."""
@@ -644,3 +646,73 @@ def route(logits, top_k: int, *, scores: str = "softmax", bias=None, groups: int
     if rc != 0:
         raise GemmError(rc, what)
     return ids, weights
+
+
+def gemm_moe_run_routed(plan: MoePlan, X, expert_ids, expert_weights, W1, W2, Y, workspace, stream=None) -> int:
+    """Enqueue one layer whose experts are chosen already on `stream` (default: torch's current stream)."""
+    what, t = "gemm_moe_run_routed", _t()
+    index = t.device_index()
+    _on_device(what, index, X, expert_ids, expert_weights, W1, W2, Y, workspace)
+    if hasattr(workspace, "numel") and workspace.numel() * workspace.element_size() < plan.workspace_bytes:
+        _refuse(what, f"workspace: {plan.workspace_bytes} bytes are wanted")
+    rc = lib().gemm_moe_run_routed(plan.handle, _ptr(X), _ptr(expert_ids), _ptr(expert_weights), _ptr(W1), _ptr(W2),
+                                   _ptr(Y), _ptr(workspace), _stream(t, index, stream))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return rc
+
+
+def moe_experts(x, w1, w2, expert_ids, expert_weights, *, act: str = "swiglu", out=None, stream=None):
+    """The experts' part of a mixture-of-experts layer for 1 to 64 tokens (gemm_moe_run_routed).
+
+    x [T, H], w1 and w2 as for moe_layer; expert_ids int32 [T, top_k] and expert_weights FP32 [T, top_k], contiguous, as
+    route gives them (an id outside 0 .. E - 1 takes no part).  Returns y [T, H].  Plans, workspaces, `stream` and
+    gemm_kept_status as for moe_layer.  out overlaps no input.
+    """
+    what, t = "moe_experts", _t()
+    dt, dtype, index = t.name.get(x.dtype), x.dtype, x.get_device()
+    if dt not in ("f16", "bf16") or act not in MOE_ACTS:
+        _refuse(what, "FP16 or BF16 tensors and act gelu, relu or swiglu are wanted")
+    if x.dim() != 2 or w1.dim() != 3 or w2.dim() != 3 or expert_ids.dim() != 2:
+        _refuse(what, "x [T, H], w1 [E, I or 2I, H], w2 [E, H, I], expert_ids [T, top_k] are wanted")
+    (T, H), (E, rows, H1), (E2, H2, I), (Tk, top_k) = x.shape, w1.shape, w2.shape, expert_ids.shape
+    if not (H1 == H2 == H and E2 == E and Tk == T and rows == (2 * I if act == "swiglu" else I)) \
+            or expert_weights.shape != expert_ids.shape or (out is not None and tuple(out.shape) != (T, H)):
+        _refuse(what, "the shapes of x, w1, w2, expert_ids, expert_weights and out do not fit one another")
+    if expert_ids.dtype is not t.i32 or expert_weights.dtype is not t.f32 or not expert_ids.is_contiguous() \
+            or not expert_weights.is_contiguous():
+        _refuse(what, "contiguous expert_ids (int32) and expert_weights (FP32) are wanted")
+    if index < 0 or any(a.get_device() != index for a in (w1, w2, expert_ids, expert_weights)) \
+            or w1.dtype is not dtype or w2.dtype is not dtype \
+            or (out is not None and (out.get_device() != index or out.dtype is not dtype)):
+        _refuse(what, "tensors of x's dtype on x's device, a GPU, are wanted")
+    if stream is not None or index != t.device_index():
+        with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
+            return moe_experts(x, w1, w2, expert_ids, expert_weights, act=act, out=out)
+    if out is None:
+        out = t.empty((T, H), dtype=dtype, device=x.device)
+    (ldx, cx), (ldy, cy), (st1, ld1, c1), (st2, ld2, c2) = x.stride(), out.stride(), w1.stride(), w2.stride()
+    if (H > 1 and not cx == cy == c1 == 1) or (I > 1 and c2 != 1) or (T > 1 and (ldx < H or ldy < H)) \
+            or (E > 1 and (st1 == 0 or st2 == 0)) or (rows > 1 and ld1 < H) or (H > 1 and ld2 < I):
+        _refuse(what, "rows that are contiguous and not shared are wanted")
+    # strides that no element uses may be anything
+    if T <= 1:
+        ldx = ldy = H
+    if rows <= 1:
+        ld1 = H
+    if H <= 1:
+        ld2 = I
+    if E <= 1:
+        st1, st2 = rows * ld1, H * ld2
+    key = ("routed", dt, T, E, top_k, H, I, act, ldx, ld1, st1, ld2, st2, ldy, index)
+    pl = _moe_plans.get(key)
+    if pl is None:
+        _no_capture(t, what)
+        pl = _keep(_moe_plans, key, lambda: gemm_moe_plan(dt, T, E, top_k, H, I, act, ldx=ldx, ld_w1=ld1,
+                                                          stride_w1=st1, ld_w2=ld2, stride_w2=st2, ldy=ldy))
+    ws = t.empty(pl.workspace_bytes, dtype=t.u8, device=x.device)
+    rc = lib().gemm_moe_run_routed(pl.handle, x.data_ptr(), expert_ids.data_ptr(), expert_weights.data_ptr(),
+                                   w1.data_ptr(), w2.data_ptr(), out.data_ptr(), ws.data_ptr(), t.raw_stream(index))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return out

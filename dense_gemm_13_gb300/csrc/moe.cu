@@ -6,6 +6,8 @@
 //   act: GELU or ReLU of I rows, or SwiGLU: silu(gate) * up, gate = rows 0..I-1 of
 //   W1[e], up = rows I..2I-1
 //
+// or with experts and weights of each token that were chosen beforehand, instead of the first two lines.
+//
 // A few tokens leave two products per weight byte and token: reading the chosen
 // experts' weights once is the cost, so everything is laid out to keep those
 // loads in flight.  Two kernels:
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     const uint16_t* r = static_cast<const uint16_t*>(a.router);
     float acc[RE][RTOK] = {};
-    for (int k = threadIdx.x * 8; k < H; k += RT * 8) {
+    for (int k = a.given_ids ? H : threadIdx.x * 8; k < H; k += RT * 8) {
         uint4 w[RE], v[RTOK];
 #pragma unroll
         for (int e = 0; e < RE; ++e) w[e] = ld_row8<VEC>(r + (e0 + e) * d.ld_router + k, e0 + e < E ? H - k : 0);
@@ -293,7 +295,7 @@ __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
         for (int i = 0; i < RE * RTOK; ++i) sums[warp][i] = acc[i / RTOK][i % RTOK];
     __syncthreads();
     const int e = e0 + static_cast<int>(threadIdx.x) / RTOK, t = t0 + static_cast<int>(threadIdx.x) % RTOK;
-    if (threadIdx.x < RE * RTOK && e < E && t < tok) {
+    if (threadIdx.x < RE * RTOK && e < E && t < tok && !a.given_ids) {
         float z = 0.0f;
 #pragma unroll
         for (int w = 0; w < RT / 32; ++w) z += sums[w][threadIdx.x];
@@ -434,6 +436,33 @@ __device__ __forceinline__ void route_tokens(const MoeArgs& a, MoeShared& s, Moe
             picks.expert[t * k + lane] = static_cast<short>(my_e[n]);
             picks.weight[t * k + lane] = p;
             atomicOr(&s.mask[my_e[n]], 1ull << t);
+        }
+    }
+}
+
+// The choice made beforehand, a warp's tokens t0, t0 + step, ...: ids outside 0 .. E - 1 take no part (expert -1),
+// and an expert that a token names twice is one pick with the sum of the weights.
+__device__ __forceinline__ void take_given(const MoeArgs& a, MoeShared& s, MoePicks& picks, int t0, int step, int tok, int lane) {
+    const int E = static_cast<int>(a.d.E), k = static_cast<int>(a.d.top_k);
+    for (int t = t0; t < tok; t += step) {
+        int e = lane < k ? __ldg(a.given_ids + t * k + lane) : -1;
+        const float w = lane < k ? __ldg(a.given_weights + t * k + lane) : 0.0f;
+        if (e < 0 || e >= E) e = -1;
+        float sum = 0.0f;
+        bool first = true;
+        for (int j = 0; j < k; ++j) {
+            const int o = __shfl_sync(0xFFFFFFFFu, e, j);
+            const float ow = __shfl_sync(0xFFFFFFFFu, w, j);
+            if (o == e) {
+                sum += ow;
+                first = first && j >= lane;
+            }
+        }
+        if (!first) e = -1;
+        if (lane < k) {
+            picks.expert[t * k + lane] = static_cast<short>(e);
+            picks.weight[t * k + lane] = sum;
+            if (e >= 0) atomicOr(&s.mask[e], 1ull << t);
         }
     }
 }
@@ -683,7 +712,9 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
     griddep_wait();  // the router's results
     __syncthreads();
     static_assert(kMoeMaxTopK <= 32, "a lane for each pick");
-    if (E > 64) {
+    if (a.given_ids) {
+        take_given(a, s, picks, warp, kMoeWarps, tok, lane);
+    } else if (E > 64) {
         for (int t = warp; t < tok; t += kMoeWarps)
             route_tokens<kMoeMaxExperts / 32, 1>(a, s, picks, t, kMoeWarps, tok, lane);
     } else if (tok > 2 * kMoeWarps) {
@@ -722,6 +753,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
     __syncthreads();
     for (int i = threadIdx.x; i < tok * top_k; i += MT) {
         const int t = i / top_k, e = picks.expert[i];
+        if (e < 0) continue;
         const int slot = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1ull));
         s.slot_token[slot] = static_cast<uint8_t>(t);
         s.slot_weight[slot] = picks.weight[i];
@@ -731,6 +763,11 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
         }
     }
     const int A = s.n_active;
+    if (A == 0) {  // (of choices made beforehand) no token has an expert
+        for (int64_t i = cta * MT + static_cast<int>(threadIdx.x); i < tok * d.H; i += static_cast<int64_t>(G) * MT)
+            static_cast<T*>(a.y)[i / d.H * d.ldy + i % d.H] = cast16<T>(0.0f);
+        return;
+    }
     const bool gated = d.act == GEMM_MOE_SWIGLU;
     const int per = gated ? 8 : 16;  // values of h per unit
     // (the host keeps units times steps below 2^30, and E and I keep units below 2^26)
@@ -1078,9 +1115,11 @@ cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
 
 template <typename T, int ROWS>
 cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
-    const unsigned blocks = static_cast<unsigned>((a.d.E + RE - 1) / RE * ((a.d.T + RTOK - 1) / RTOK));
+    const unsigned blocks = a.given_ids
+                                ? static_cast<unsigned>(std::min<int64_t>((a.d.T * a.w.hp / 8 + RT - 1) / RT, grid))
+                                : static_cast<unsigned>((a.d.E + RE - 1) / RE * ((a.d.T + RTOK - 1) / RTOK));
     // the router's rows and x take vector loads on their own terms
-    const bool rvec = reinterpret_cast<uintptr_t>(a.router) % 16 == 0 && a.d.ld_router % 8 == 0 &&
+    const bool rvec = (a.given_ids || (reinterpret_cast<uintptr_t>(a.router) % 16 == 0 && a.d.ld_router % 8 == 0)) &&
                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.d.ldx % 8 == 0 && a.d.H % 8 == 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);

@@ -28,6 +28,8 @@ struct MoeArgs {
     void* y;
     int32_t* ids;
     float* weights;
+    const int32_t* given_ids;    // a choice made beforehand, or null: the router's
+    const float* given_weights;
     char* ws;
     unsigned* status;
     uint64_t timeout_ns;

@@ -63,6 +63,35 @@ int check_desc(gemm_moe_desc_t& d) {
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+// A layer with a router (Wr), or with a choice made beforehand (given_ids, given_weights).
+int run_layer(const gemm_moe_plan_s* plan, const void* X, const void* Wr, const int32_t* given_ids,
+              const float* given_weights, const void* W1, const void* W2, void* Y, int32_t* expert_ids,
+              float* expert_weights, void* workspace, void* stream) {
+    if (!X || !W1 || !W2 || !Y || !workspace) return GEMM_ERR_INVALID_ARG;
+    if (!aligned(X, 2) || !aligned(Wr, 2) || !aligned(W1, 2) || !aligned(W2, 2) || !aligned(Y, 2) ||
+        !aligned(expert_ids, 4) || !aligned(expert_weights, 4) || !aligned(given_ids, 4) ||
+        !aligned(given_weights, 4) || !aligned(workspace, 256))
+        return GEMM_ERR_MISALIGNED;
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess || cur != plan->device) return GEMM_ERR_INVALID_ARG;
+    MoeArgs a{};
+    a.d = plan->d;
+    a.w = plan->w;
+    a.x = X;
+    a.router = Wr;
+    a.w1 = W1;
+    a.w2 = W2;
+    a.y = Y;
+    a.ids = expert_ids;
+    a.weights = expert_weights;
+    a.given_ids = given_ids;
+    a.given_weights = given_weights;
+    a.ws = static_cast<char*>(workspace);
+    a.status = plan->d_status;
+    a.timeout_ns = static_cast<uint64_t>(plan->d.timeout_ms) * 1000000ull;
+    return cuda_status(launch_moe(a, plan->grid, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -123,26 +152,16 @@ int gemm_moe_run(gemm_moe_plan_t plan, const void* X, const void* Wr, const void
                  void* Y, int32_t* expert_ids, float* expert_weights, void* workspace, void* stream) {
     if (!alive(plan)) return GEMM_ERR_BAD_PLAN;
     if (plan->d.T == 0) return GEMM_OK;
-    if (!X || !Wr || !W1 || !W2 || !Y || !workspace) return GEMM_ERR_INVALID_ARG;
-    if (!aligned(X, 2) || !aligned(Wr, 2) || !aligned(W1, 2) || !aligned(W2, 2) || !aligned(Y, 2) ||
-        !aligned(expert_ids, 4) || !aligned(expert_weights, 4) || !aligned(workspace, 256))
-        return GEMM_ERR_MISALIGNED;
-    int cur = -1;
-    if (cudaGetDevice(&cur) != cudaSuccess || cur != plan->device) return GEMM_ERR_INVALID_ARG;
-    MoeArgs a{};
-    a.d = plan->d;
-    a.w = plan->w;
-    a.x = X;
-    a.router = Wr;
-    a.w1 = W1;
-    a.w2 = W2;
-    a.y = Y;
-    a.ids = expert_ids;
-    a.weights = expert_weights;
-    a.ws = static_cast<char*>(workspace);
-    a.status = plan->d_status;
-    a.timeout_ns = static_cast<uint64_t>(plan->d.timeout_ms) * 1000000ull;
-    return cuda_status(launch_moe(a, plan->grid, static_cast<cudaStream_t>(stream)));
+    if (!Wr) return GEMM_ERR_INVALID_ARG;
+    return run_layer(plan, X, Wr, nullptr, nullptr, W1, W2, Y, expert_ids, expert_weights, workspace, stream);
+}
+
+int gemm_moe_run_routed(gemm_moe_plan_t plan, const void* X, const int32_t* expert_ids, const float* expert_weights,
+                        const void* W1, const void* W2, void* Y, void* workspace, void* stream) {
+    if (!alive(plan)) return GEMM_ERR_BAD_PLAN;
+    if (plan->d.T == 0) return GEMM_OK;
+    if (!expert_ids || !expert_weights) return GEMM_ERR_INVALID_ARG;
+    return run_layer(plan, X, nullptr, expert_ids, expert_weights, W1, W2, Y, nullptr, nullptr, workspace, stream);
 }
 
 int gemm_moe_status(gemm_moe_plan_t plan) {

@@ -611,6 +611,14 @@ int64_t gemm_moe_workspace_bytes(gemm_moe_plan_t plan);
  */
 int gemm_moe_run(gemm_moe_plan_t plan, const void* X, const void* Wr, const void* W1, const void* W2,
                  void* Y, int32_t* expert_ids, float* expert_weights, void* workspace, void* stream);
+/*
+ * The same layer with a choice made beforehand (gemm_route, say) instead of the router:
+ * expert_ids int32 [T][top_k] and expert_weights FP32 [T][top_k], read as they are
+ * (normalize does not count).  An id outside 0 .. E - 1 takes no part, an expert that a token names twice
+ * counts with the sum of its weights, and a token without experts gets zeros.
+ */
+int gemm_moe_run_routed(gemm_moe_plan_t plan, const void* X, const int32_t* expert_ids, const float* expert_weights,
+                        const void* W1, const void* W2, void* Y, void* workspace, void* stream);
 /* As gemm_plan_status and gemm_plan_destroy. */
 int gemm_moe_status(gemm_moe_plan_t plan);
 void gemm_moe_destroy(gemm_moe_plan_t plan);
