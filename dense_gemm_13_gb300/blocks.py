@@ -6,6 +6,7 @@ Argument checks and marshalling only, as in the package itself, which exports ev
 from __future__ import annotations
 
 import ctypes
+import sys
 
 from . import (ACTS, DTYPES, MOE_ACTS, Config, Epilogue, GemmError, MoePlan, _Config, _keep, _ld, _moe_plans,
                _no_capture, _on_device, _ptr, _refuse, _rows_ok, _stream, _t, gemm_moe_plan, lib)
@@ -14,6 +15,8 @@ __all__ = ["rms_norm", "Fp8Tensor", "Fp8Plan", "fp8_quantize", "fp8_dequantize",
            "gemm_fp8_status", "gemm_fp8_select_config", "fp8_matmul", "W4Tensor", "w4_quantize", "w4_pack",
            "w4_dequantize", "w4_matmul", "ROUTE_SCORES", "ROUTE_GROUP_SCORES", "route", "gemm_moe_run_routed",
            "moe_experts"]
+
+_package = sys.modules[__package__]
 
 ROUTE_SCORES = {"softmax": 0, "sigmoid": 1}
 ROUTE_GROUP_SCORES = {"max": 0, "top2": 1}
@@ -39,6 +42,11 @@ class _RouteDesc(ctypes.Structure):
                 ("scores", ctypes.c_int), ("groups", ctypes.c_int64), ("top_groups", ctypes.c_int64),
                 ("group_score", ctypes.c_int), ("normalize", ctypes.c_int), ("scale", ctypes.c_float),
                 ("ld", ctypes.c_int64)]
+
+
+def _lib_of():
+    """The library, where it is loaded already."""
+    return _package._lib
 
 
 def prototypes(L) -> None:
@@ -98,13 +106,49 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
     allocates, as if that were the current stream.
     """
     what, t = "rms_norm", _t()
-    dt, index = t.name.get(x.dtype), x.get_device()
-    if dt is None or x.dim() != 2 or index < 0:
-        _refuse(what, "x: a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
-    if stream is not None or index != t.device_index():
+    index = x.get_device()
+    if stream is not None or (index != t.device_index() and index >= 0):
         with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
             return rms_norm(x, weight, residual=residual, eps=eps, weight_offset=weight_offset, out_dtype=out_dtype,
                             out=out, residual_out=residual_out)
+    # what the checks below look at, apart from the addresses: arguments that passed them once pass them again
+    key = (x.shape, x.stride(), x.dtype, index, eps, weight_offset, out_dtype,
+           None if weight is None else (weight.shape, weight.stride(), weight.dtype, weight.get_device()),
+           None if residual is None else (residual.shape, residual.stride(), residual.dtype, residual.get_device()),
+           None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()),
+           None if residual_out is None else (residual_out.shape, residual_out.stride(), residual_out.dtype,
+                                              residual_out.get_device()))
+    known = _norm_descs.get(key)
+    if known is None:
+        known = _check_norm(t, what, x, weight, residual, eps, weight_offset, out_dtype, out, residual_out, index)
+        if len(_norm_descs) > 4096:
+            _norm_descs.clear()
+        _norm_descs[key] = known
+    d, T, H, odt = known
+    if out is not None or residual_out is not None:
+        _check_norm_overlap(what, x, weight, residual, residual_out, out)
+    h = residual_out
+    if residual is not None and h is None:
+        h = t.empty((T, H), dtype=residual.dtype, device=x.device)
+    if odt is None:
+        y = _new_fp8(t, T, H, x.device, index)
+        p, ps, _ = y._ptrs()
+    else:
+        y = t.empty((T, H), dtype=odt, device=x.device) if out is None else out
+        p, ps = y.data_ptr(), None
+    rc = (_lib_of() or lib()).gemm_rms_norm(d, x.data_ptr(), None if residual is None else residual.data_ptr(),
+                                            None if weight is None else weight.data_ptr(),
+                                            None if h is None else h.data_ptr(), p, ps, t.raw_stream(index))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return y if residual is None else (y, h)
+
+
+def _check_norm(t, what, x, weight, residual, eps, weight_offset, out_dtype, out, residual_out, index):
+    """(gemm_norm_desc_t, T, H, the output's torch dtype or None for mxfp8), or a refusal."""
+    dt = t.name.get(x.dtype)
+    if dt is None or x.dim() != 2 or index < 0:
+        _refuse(what, "x: a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
     T, H = x.shape
     ldx, step = x.stride()
     if T <= 1:
@@ -117,56 +161,34 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
         if wdt is None or weight.dim() != 1 or weight.shape[0] != H or weight.get_device() != index \
                 or (H > 1 and weight.stride(0) != 1):
             _refuse(what, "weight: contiguous [H] in f32, f16 or bf16 on x's device is wanted")
-    rdt, ldr, ldh, h = dt, 0, 0, None
+    rdt, ldr, ldh, ldy = dt, 0, 0, 0
     if residual is not None:
         rdt = t.name.get(residual.dtype)
         if rdt not in ("f32", dt) or not _out_ok(t, residual, (T, H), rdt, index):
             _refuse(what, "residual: a row-major [T, H] in f32 or x's dtype on x's device is wanted")
-        ldr = ldh = _ld(residual) if T > 1 else H
-        if residual_out is None:
-            h, ldh = t.empty((T, H), dtype=residual.dtype, device=x.device), H
-        else:
-            h = residual_out
-            if not _out_ok(t, h, (T, H), rdt, index):
+        ldr = _ld(residual) if T > 1 else H
+        ldh = H
+        if residual_out is not None:
+            if not _out_ok(t, residual_out, (T, H), rdt, index):
                 _refuse(what, "residual_out: a row-major [T, H] of the residual's dtype on x's device is wanted")
-            ldh = _ld(h) if T > 1 else H
+            ldh = _ld(residual_out) if T > 1 else H
     elif residual_out is not None:
         _refuse(what, "residual_out without a residual")
     f8 = out_dtype == "mxfp8"
-    odt = dt if out_dtype is None else out_dtype
-    if f8:
+    odt = dt if out_dtype is None or f8 else out_dtype
+    if f8 and out is not None:
+        _refuse(what, "out: mxfp8 makes its own arrays")
+    if odt not in DTYPES:
+        _refuse(what, f"unknown out_dtype {out_dtype!r}")
+    if not f8:
+        ldy = H
         if out is not None:
-            _refuse(what, "out: mxfp8 makes its own arrays")
-        odt, ldy = dt, 0
-    else:
-        if odt not in DTYPES:
-            _refuse(what, f"unknown out_dtype {out_dtype!r}")
-        if out is None:
-            out, ldy = t.empty((T, H), dtype=t.dtype[odt], device=x.device), H
-        else:
             if not _out_ok(t, out, (T, H), odt, index):
                 _refuse(what, f"out: a row-major {odt} [T, H] on x's device is wanted")
             ldy = _ld(out) if T > 1 else H
-    if residual_out is not None or (out is not None and out_dtype != "mxfp8"):
-        _check_norm_overlap(what, x, weight, residual, h if residual_out is not None else None, out)
-    key = (T, H, dt, rdt, wdt, odt, f8, residual is None, ldx, ldr, ldh, ldy, eps, weight_offset)
-    d = _norm_descs.get(key)
-    if d is None:
-        d = _NormDesc(DTYPES[dt], residual is not None, DTYPES[rdt], DTYPES[wdt], DTYPES[odt], f8, T, H, ldx, ldr, ldh,
-                      ldy, eps, weight_offset)
-        if len(_norm_descs) > 4096:
-            _norm_descs.clear()
-        _norm_descs[key] = d = ctypes.byref(d)
-    L = lib()
-    if f8:
-        y = _new_fp8(t, T, H, x.device, index)
-        p, ps, _ = y._ptrs()
-    else:
-        y, p, ps = out, out.data_ptr(), None
-    rc = L.gemm_rms_norm(d, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(h), p, ps, t.raw_stream(index))
-    if rc != 0:
-        raise GemmError(rc, what)
-    return y if residual is None else (y, h)
+    d = _NormDesc(DTYPES[dt], residual is not None, DTYPES[rdt], DTYPES[wdt], DTYPES[odt], f8, T, H, ldx, ldr, ldh, ldy,
+                  eps, weight_offset)
+    return ctypes.byref(d), T, H, None if f8 else t.dtype[odt]
 
 
 def _check_norm_overlap(what, x, weight, residual, h, out):
@@ -394,7 +416,7 @@ def fp8_matmul(A: Fp8Tensor, B: Fp8Tensor, *, alpha=1.0, bias=None, act="none", 
                       residual=residual is not None, beta=beta, ldr=ldr)
         pl = _keep(_fp8_plans, key, lambda: gemm_fp8_plan(M, N, K, ldc, ep))
     (ac, as_, _), (bc, bs, _) = A._ptrs(), B._ptrs()
-    rc = lib().gemm_fp8_run(pl.handle, ac, as_, bc, bs, out.data_ptr(), _ptr(bias), _ptr(residual), alpha,
+    rc = (_lib_of() or lib()).gemm_fp8_run(pl.handle, ac, as_, bc, bs, out.data_ptr(), _ptr(bias), _ptr(residual), alpha,
                             t.raw_stream(index))
     if rc != 0:
         raise GemmError(rc, what)
@@ -552,13 +574,42 @@ def w4_matmul(x, w: W4Tensor, *, alpha=1.0, bias=None, act="none", residual=None
     what, t = "w4_matmul", _t()
     if type(w) is not W4Tensor:
         _refuse(what, "w: a W4Tensor is wanted")
-    dt, index, N, K = w._dtype, w._index, w._rows, w._cols
-    if x.dim() != 2 or t.name.get(x.dtype) != dt or x.get_device() != index or x.shape[1] != K:
-        _refuse(what, f"x: [M, {K}] in {dt} on the weight's device is wanted")
+    index = w._index
     if stream is not None or index != t.device_index():
         with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
             return w4_matmul(x, w, alpha=alpha, bias=bias, act=act, residual=residual, beta=beta,
                              out_dtype=out_dtype, out=out)
+    if bias is not None or residual is not None:
+        _check_epilogue(t, what, bias, residual, x.shape[0], w._rows, index)
+    # what the checks look at: arguments that passed them once pass them again
+    key = (x.shape, x.stride(), x.dtype, x.get_device(), out_dtype, act, bias is None, beta,
+           None if residual is None else residual.stride(),
+           None if out is None else (out.shape, out.stride(), out.dtype, out.get_device()))
+    known = w._descs.get(key)
+    if known is None:
+        known = _check_w4(t, what, x, w, bias, act, residual, beta, out_dtype, out)
+        if len(w._descs) > 256:
+            w._descs.clear()
+        w._descs[key] = known
+    d, M, odt = known
+    if out is None:
+        out = t.empty((M, w._rows), dtype=odt, device=x.device)
+    z = w._zeros
+    rc = (_lib_of() or lib()).gemm_w4_run(d, x.data_ptr(), w._codes.data_ptr(), w._scales.data_ptr(),
+                                          None if z is None else z.data_ptr(), out.data_ptr(),
+                                          None if bias is None else bias.data_ptr(),
+                                          None if residual is None else residual.data_ptr(), alpha,
+                                          t.raw_stream(index))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return out
+
+
+def _check_w4(t, what, x, w, bias, act, residual, beta, out_dtype, out):
+    """(gemm_w4_desc_t, M, the output's torch dtype), or a refusal."""
+    dt, index, N, K = w._dtype, w._index, w._rows, w._cols
+    if x.dim() != 2 or t.name.get(x.dtype) != dt or x.get_device() != index or x.shape[1] != K:
+        _refuse(what, f"x: [M, {K}] in {dt} on the weight's device is wanted")
     M = x.shape[0]
     if M > 64:
         _refuse(what, "at most 64 tokens (more: w4_dequantize, then matmul)")
@@ -570,30 +621,13 @@ def w4_matmul(x, w: W4Tensor, *, alpha=1.0, bias=None, act="none", residual=None
     odt = dt if out_dtype is None else out_dtype
     if odt not in DTYPES or act not in ("none", "gelu", "relu"):
         _refuse(what, "out_dtype: f32, f16 or bf16; act: none, gelu or relu")
-    if bias is not None or residual is not None:
-        _check_epilogue(t, what, bias, residual, M, N, index)
-    if out is None:
-        out, ldy = t.empty((M, N), dtype=t.dtype[odt], device=t.device(index)), N
-    else:
-        if not _out_ok(t, out, (M, N), odt, index):
-            _refuse(what, f"out: a row-major {odt} [M, N] on the weight's device is wanted")
-        ldy = _ld(out)
+    if out is not None and not _out_ok(t, out, (M, N), odt, index):
+        _refuse(what, f"out: a row-major {odt} [M, N] on the weight's device is wanted")
+    ldy = N if out is None else _ld(out)
     ldr = 0 if residual is None else _ld(residual)
-    key = (M, ldx, ldy, ldr, odt, act, bias is None, residual is None, beta)
-    d = w._descs.get(key)
-    if d is None:
-        d = ctypes.byref(_W4Desc(DTYPES[dt], DTYPES[odt], M, N, K, w._group, w._zeros is not None, bias is not None,
-                                 ACTS[act], residual is not None, beta, ldx, ldy, ldr))
-        if len(w._descs) > 256:
-            w._descs.clear()
-        w._descs[key] = d
-    z = w._zeros
-    rc = lib().gemm_w4_run(d, x.data_ptr(), w._codes.data_ptr(), w._scales.data_ptr(),
-                           None if z is None else z.data_ptr(), out.data_ptr(), _ptr(bias), _ptr(residual), alpha,
-                           t.raw_stream(index))
-    if rc != 0:
-        raise GemmError(rc, what)
-    return out
+    d = _W4Desc(DTYPES[dt], DTYPES[odt], M, N, K, w._group, w._zeros is not None, bias is not None, ACTS[act],
+                residual is not None, beta, ldx, ldy, ldr)
+    return ctypes.byref(d), M, t.dtype[odt]
 
 
 # ------------------------------------------------------------------ routing to experts
@@ -611,41 +645,52 @@ def route(logits, top_k: int, *, scores: str = "softmax", bias=None, groups: int
     takes them.  With `stream`, the call runs, and allocates, as if that were the current stream.
     """
     what, t = "route", _t()
-    dt, index = t.name.get(logits.dtype), logits.get_device()
-    if dt is None or logits.dim() != 2 or index < 0:
-        _refuse(what, "logits: a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
-    if stream is not None or index != t.device_index():
+    index = logits.get_device()
+    if stream is not None or (index != t.device_index() and index >= 0):
         with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
             return route(logits, top_k, scores=scores, bias=bias, groups=groups, top_groups=top_groups,
                          group_score=group_score, normalize=normalize, scale=scale)
+    # what the checks look at: arguments that passed them once pass them again
+    key = (logits.shape, logits.stride(), logits.dtype, index, top_k, scores, groups, top_groups, group_score, normalize,
+           scale, None if bias is None else (bias.shape, bias.stride(), bias.dtype, bias.get_device()))
+    known = _route_descs.get(key)
+    if known is None:
+        known = _check_route(t, what, logits, top_k, scores, bias, groups, top_groups, group_score, normalize, scale,
+                             index)
+        if len(_route_descs) > 4096:
+            _route_descs.clear()
+        _route_descs[key] = known
+    d, T = known
+    ids = t.empty((T, top_k), dtype=t.i32, device=logits.device)
+    weights = t.empty((T, top_k), dtype=t.f32, device=logits.device)
+    rc = (_lib_of() or lib()).gemm_route(d, logits.data_ptr(), None if bias is None else bias.data_ptr(),
+                                         ids.data_ptr(), weights.data_ptr(), t.raw_stream(index))
+    if rc != 0:
+        raise GemmError(rc, what)
+    return ids, weights
+
+
+def _check_route(t, what, logits, top_k, scores, bias, groups, top_groups, group_score, normalize, scale, index):
+    """(gemm_route_desc_t, T), or a refusal."""
+    dt = t.name.get(logits.dtype)
+    if dt is None or logits.dim() != 2 or index < 0:
+        _refuse(what, "logits: a 2-D CUDA tensor in f32, f16 or bf16 is wanted")
     T, E = logits.shape
     ld, step = logits.stride()
     if T <= 1:
         ld = E
-    key = (T, E, top_k, dt, scores, groups, top_groups, group_score, normalize, scale, ld)
-    d = _route_descs.get(key)
-    if d is None:
-        if scores not in ROUTE_SCORES or group_score not in ROUTE_GROUP_SCORES:
-            _refuse(what, "scores: softmax or sigmoid; group_score: max or top2")
-        d = ctypes.byref(_RouteDesc(DTYPES[dt], T, E, top_k, ROUTE_SCORES[scores], groups,
-                                    groups if top_groups is None else top_groups, ROUTE_GROUP_SCORES[group_score],
-                                    bool(normalize), scale, ld))
-        if len(_route_descs) > 4096:
-            _route_descs.clear()
-        _route_descs[key] = d
     if (E > 1 and step != 1) or ld < E:
         _refuse(what, "logits: rows contiguous and not overlapping are wanted")
+    if scores not in ROUTE_SCORES or group_score not in ROUTE_GROUP_SCORES:
+        _refuse(what, "scores: softmax or sigmoid; group_score: max or top2")
     if bias is not None and (bias.dtype is not t.f32 or bias.dim() != 1 or bias.shape[0] != E
                              or bias.get_device() != index or not bias.is_contiguous()):
         _refuse(what, "bias: contiguous FP32 [E] on the logits' device is wanted")
     if top_k < 1:
         _refuse(what, "top_k: at least 1 is wanted")
-    ids = t.empty((T, top_k), dtype=t.i32, device=logits.device)
-    weights = t.empty((T, top_k), dtype=t.f32, device=logits.device)
-    rc = lib().gemm_route(d, logits.data_ptr(), _ptr(bias), ids.data_ptr(), weights.data_ptr(), t.raw_stream(index))
-    if rc != 0:
-        raise GemmError(rc, what)
-    return ids, weights
+    d = _RouteDesc(DTYPES[dt], T, E, top_k, ROUTE_SCORES[scores], groups, groups if top_groups is None else top_groups,
+                   ROUTE_GROUP_SCORES[group_score], bool(normalize), scale, ld)
+    return ctypes.byref(d), T
 
 
 def gemm_moe_run_routed(plan: MoePlan, X, expert_ids, expert_weights, W1, W2, Y, workspace, stream=None) -> int:

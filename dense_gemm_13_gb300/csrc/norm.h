@@ -19,6 +19,18 @@ struct NormArgs {
     uint8_t* scales;
 };
 
+// A number as the sum of two, the second of them what the first leaves.
+struct Two {
+    float hi, lo;
+};
+
+struct NormShape {
+    int cols;
+    Two inv;                 // 1 / cols
+    int64_t rows, rows_all;  // rows_all: with the padding of the scales' last tile
+    int64_t row_bytes, col_tiles;
+};
+
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);
 
 }  // namespace g13

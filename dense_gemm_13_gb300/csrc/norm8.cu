@@ -1,0 +1,10 @@
+// norm8.cu -- the norm's kernels with an output in mxfp8.
+#include "norm_kernel.cuh"
+
+namespace g13 {
+
+cudaError_t launch_norm8(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
+    return launch_norm_kind<true>(a, s, num_sms, st);
+}
+
+}  // namespace g13

@@ -2,19 +2,24 @@
 //
 //   Y = cast( act( alpha sum_k X[m,k] (q[n,k] - z[n,k/g]) s[n,k/g] + bias[n] ) + beta R[m,n] )
 //
-// The weights' bytes are the cost (half a byte a weight); every one is read once, by 16-byte loads
-// of whole 512-byte blocks, several blocks ahead in registers.  A warp multiplies a block of 16 rows
-// x 64 columns with 8 tokens by four mma.sync m16n8k16: the weights are the 16 rows, the tokens the columns.
-// A code becomes a 16-bit float by its bits alone: 128 + q in BF16 (1024 + q in FP16) has q as its lowest
-// bits; taking off 128 + z leaves q - z exactly.  The group's scale multiplies the FP32 sum of its products
-// (32 or 64 columns at a time), so no weight is rounded.
+// The weights' bytes are the cost (half a byte a weight); every one is read once, by 16-byte loads of whole 512-byte
+// blocks, several ahead in registers.  A warp multiplies a step of 16 rows x 128 columns with 8 tokens by eight mma.sync
+// m16n8k16: the weights are the 16 rows, the tokens the columns.  What is left to save is instructions, so the codes go into
+// the product as they lie: a nibble in the lowest or second lowest place of 16 bits, the others masked off, is the FP16
+// number q 2^-24 or 16 q 2^-24, exactly (its subnormal range is linear).  Five instructions make eight weights (as
+// 1024 + q or 128 + q, minus 1024 + z: nine and eleven).  The zero comes off afterwards:
 //
-// A CTA of eight warps takes 16 (or 32) rows at a time; the warps take the blocks of a row in turn, so that
-// the CTA reads whole kilobytes that follow one another, and their sums are joined through shared memory in warp
-// order.  CTAs are persistent; a warp's loads run on into the CTA's next rows while these are joined.  The
-// tokens' values lie in shared memory, all of the CTA's part of K.  Where there are few rows, or more of K than
-// shared memory holds, a cluster of CTAs shares K and its first CTA adds the others' sums through
-// distributed shared memory, in rank order.  Nothing depends on timing, and nothing needs a workspace.
+//   sum_k (q - z) x = sum_k q x - z sum_k x      over a group, FP32; the sums of x are worked out once per CTA
+//
+// and the group's scale multiplies the difference, so no weight is rounded.  The activations are brought into the upper
+// part of FP16's range by a power of two for every 128 of a token's, and those that meet 16 q by 1 / 16 more: exact, but for
+// values below 2^-27 of the largest of them (FP16 ones: 2^-24), which are off by 2^-35 of it at most.
+//
+// A CTA has eight warps.  `wk` of them share its part of K, the others have 16 rows each of their own; the sums of those
+// that share K are joined through shared memory in warp order.  CTAs are persistent; a warp's loads run on into
+// its next rows while these are joined.  The tokens' values lie in shared memory, all of the CTA's part of K.  Where there
+// are few rows, or more of K than shared memory holds, a cluster of CTAs shares K and each adds its share of the
+// sums through distributed shared memory, in rank order.  Nothing depends on timing, and nothing needs a workspace.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -33,255 +38,361 @@ constexpr int WW = 8;            // warps of a CTA
 constexpr int WT = WW * 32;
 constexpr int kMaxDevices = 64;
 constexpr int kW4Smem = 200 * 1024;  // at most, of the 227 KB that a CTA can have
+// CTAs per SM that the registers are kept for.
+#ifndef C1
+#define C1 3
+#define D1 3
+#define C2 2
+#define D2 3
+#define C4 2
+#define D4 3
+#define C8 1
+#define D8 3
+#endif
+constexpr int w4_ctas(int nt) { return nt == 1 ? C1 : nt == 2 ? C2 : nt == 4 ? C4 : C8; }
+// Steps ahead of each warp.
+constexpr int w4_depth(int nt) { return nt == 1 ? D1 : nt == 2 ? D2 : nt == 4 ? D4 : D8; }
 
-template <typename T>
-struct Half;
-template <>
-struct Half<__half> {
-    static constexpr uint32_t magic = 0x64006400u;  // 1024, twice
-    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    static __device__ __forceinline__ float2 two(uint32_t v) {
-        return __half22float2(*reinterpret_cast<const __half2*>(&v));
-    }
-    static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
+// Two 16-bit numbers to FP32.
+__device__ __forceinline__ float2 two(uint32_t v, bool bf16) {
+    if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+// c = (or c +=) a 16 x 16 tile of weights times 16 values of 8 tokens.
+template <bool FRESH>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if (FRESH)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+            " {%10, %10, %10, %10};"
+            : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
             " {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    }
-};
-template <>
-struct Half<__nv_bfloat16> {
-    static constexpr uint32_t magic = 0x43004300u;  // 128, twice
-    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        const __nv_bfloat162 r =
-            __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-        return *reinterpret_cast<const uint32_t*>(&r);
-    }
-    static __device__ __forceinline__ float2 two(uint32_t v) {
-        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
-    }
-    static __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
-            " {%0, %1, %2, %3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    }
-};
-
-__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 
-// A block as it is loaded: the codes, and of each group that it holds the scales of rows g and g + 8 (two 16-bit
-// numbers) and their zeros (two bytes).
-template <int R, int GROUPS>
-struct Block {
-    uint4 w[R];
-    uint32_t s[R][GROUPS];
-    uint32_t z[R][GROUPS];
+// Loads that are made only if `on`, else v keeps what it holds.  (The predicate sits inside the assembly: behind a
+// branch the loaded values were copied where the branches meet, which waits for them there.)
+__device__ __forceinline__ void ld_codes(uint4& v, const uint8_t* p, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+                 : "l"(p), "r"(static_cast<int>(on)));
+}
+__device__ __forceinline__ void ld_nc32(uint32_t& v, const uint32_t* p, bool on) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "+r"(v)
+                 : "l"(p), "r"(static_cast<int>(on)));
+}
+__device__ __forceinline__ void ld_nc16(uint32_t& v, const uint16_t* p, bool on) {  // (into a 32-bit register's low half)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
+                 : "+r"(v)
+                 : "l"(p), "r"(static_cast<int>(on)));
+}
+__device__ const uint16_t kEights = 0x0808;
+
+// A step is 128 columns of 16 rows, two blocks.  As it is loaded: the codes, and of each of the NG groups that it
+// meets the scales of rows g and g + 8 (two 16-bit numbers) and their zeros (two bytes).
+template <int NG>
+struct Step {
+    uint4 lo, hi;
+    uint32_t s[NG], z[NG];
 };
 
-// Shared memory: the tokens' rows, then the warps' sums.  A row is 64 bytes longer than its values (a multiple of
-// 128), so that the eight rows of a fragment load meet all banks.
-__host__ __device__ constexpr int w4_row(int blocks) { return blocks * 128 + 64; }
-template <int NT, int R>
-constexpr int kSumRow = 16 * R + 4;  // (the four extra spread the lanes' writes over the banks)
-template <int NT, int R>
-constexpr int kSums = 8 * NT * kSumRow<NT, R>;
+// Shared memory: the tokens' rows (FP16); for each step, group and pair of tokens two sums and two powers of two; the
+// warps' sums.  A token's row is 64 bytes longer than its values (a multiple of 256), so that the eight rows of a
+// fragment load meet all banks.
+__host__ __device__ constexpr int w4_row(int steps) { return steps * 256 + 64; }
+// The sums of a token, from one to the next (the four extra spread the lanes' writes over the banks).
+__host__ __device__ constexpr int w4_sum_row(int rows) { return rows + 4; }
+// The groups that a step meets: one, two, or four (of which some may be the same one).
+constexpr int w4_per_step(int64_t group) { return group % 128 == 0 ? 1 : group % 64 == 0 ? 2 : 4; }
 
-// HALVES: groups of 32 columns, two to a block; else a block lies in one group.
-template <typename T, int NT, int R, bool HALVES, int DEPTH>
-__global__ void __launch_bounds__(WT) w4_kernel(const __grid_constant__ W4Args a, int kb_rank, bool xvec, uint32_t inv_group) {
-    constexpr int GROUPS = HALVES ? 2 : 1, TOK = 8 * NT;
+struct W4Plan {
+    int steps_rank;      // steps of K that a CTA has
+    uint32_t inv_steps;  // its reciprocal (exact below 2^16; 0: one step)
+    int windows;         // windows of a unit: DEPTH steps of each warp (some may not exist)
+    uint32_t inv;        // reciprocal of group / 32 (exact below 2^16; 0: a group of 32)
+    int blocks, tiles, groups, units;  // a unit: 16 rows to each of the 8 / WK warps that share no K
+    int xvec;            // X takes 16-byte loads
+    int bf16;
+};
+// i / n by n's reciprocal.
+__device__ __forceinline__ int over(uint32_t i, uint32_t inv) { return static_cast<int>(inv ? __umulhi(i, inv) : i); }
+uint32_t reciprocal(int64_t n) {
+    return n == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + static_cast<uint64_t>(n) - 1) / static_cast<uint64_t>(n));
+}
+
+// WK warps share a CTA's part of K.  DENSE: a group is 128 / NG columns, so that groups follow one another as the
+// steps do; else each step looks up its own.
+template <int NT, int WK, int NG, bool DENSE, int DEPTH>
+__global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_constant__ W4Args a, const __grid_constant__ W4Plan plan) {
+    constexpr int TOK = 8 * NT, WR = WW / WK, ROWS = WR * 16;
     extern __shared__ __align__(128) uint8_t w4_raw[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     uint32_t ranks, rank;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const int blocks = static_cast<int>(w4_blocks(a.K)), tiles = static_cast<int>(w4_tiles(a.N));
-    const int groups = static_cast<int>(w4_groups(a.K, a.group));
-    const int kb0 = min(static_cast<int>(rank) * kb_rank, blocks), kb1 = min(kb0 + kb_rank, blocks);
+    const int my_k = warp % WK, my_row = warp / WK;
+    const int blocks = plan.blocks, tiles = plan.tiles, groups = plan.groups, steps_rank = plan.steps_rank;
+    const bool bf16 = plan.bf16 != 0;  // of X and the scales
+    const int first_block = min(static_cast<int>(rank) * steps_rank * 2, blocks);
+    const int my_blocks = min(blocks - first_block, steps_rank * 2);
+    const int my_steps = (my_blocks + 1) / 2;
     const int tok0 = static_cast<int>(blockIdx.y) * TOK, tok = min(TOK, static_cast<int>(a.M) - tok0);
-    const int units = (tiles + R - 1) / R;
-    const int first = static_cast<int>(blockIdx.x / ranks), step = static_cast<int>(gridDim.x / ranks);
-    const int n_units = first < units ? (units - first + step - 1) / step : 0;
-    const int turns = (kb_rank + WW - 1) / WW;  // blocks of a row tile that a warp takes (some may not exist)
-    const int row_bytes = w4_row(kb_rank);
-    float* sums = reinterpret_cast<float*>(w4_raw + tok * row_bytes);  // [warp][token][row]
+    const int first = static_cast<int>(ranks == 1 ? blockIdx.x : blockIdx.x / ranks);
+    const int stride = static_cast<int>(ranks == 1 ? gridDim.x : gridDim.x / ranks);
+    const int row_bytes = w4_row(steps_rank);
 
-    // ---- this warp's stream of blocks, DEPTH ahead
-    Block<R, GROUPS> ring[DEPTH];
-    int lu = first, lt = 0;  // unit and turn of the next load
-    const auto load = [&](Block<R, GROUPS>& b) {
-        const int kb = kb0 + lt * WW + warp;
+    // ---- this warp's stream of steps, a window of DEPTH ahead
+    Step<NG> ring[DEPTH] = {};
+    int lj = my_k, ltile = first * WR + my_row;  // first step and tile of the next window that is loaded
+    const int64_t tile_bytes = static_cast<int64_t>(blocks) * 512;
+    const uint8_t* codes = a.codes + ltile * tile_bytes + static_cast<int64_t>(first_block + my_k * 2) * 512 + lane * 16;
+    const int64_t entry = static_cast<int64_t>(ltile) * groups * 8 + g + (DENSE ? (first_block / 2 + my_k) * NG * 8 : 0);
+    const uint32_t* scales = static_cast<const uint32_t*>(a.scales) + entry;
+    // (without zeros: two eights, always the same ones)
+    const uint16_t* zeros = a.zeros ? reinterpret_cast<const uint16_t*>(a.zeros) + entry : &kEights;
+    const int zero_step = a.zeros ? 8 : 0;
+    const auto load = [&](Step<NG>& b, int d) {
+        const int j = lj + d * WK;
+        const bool on = j < my_steps && ltile < tiles;
+        const uint8_t* p = codes + d * (WK * 1024);
+        ld_codes(b.lo, p, on);
+        // (past the row's end any codes will do: the tokens' values there are zeros)
+        ld_codes(b.hi, p + 512, on && 2 * j + 1 < my_blocks);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int tile = lu * R + r;
-            const bool on = kb < kb1 && tile < tiles && lu < units;
-            if (!on) continue;
-            b.w[r] = ld_codes(a.codes + (static_cast<int64_t>(tile) * blocks + kb) * 512 + lane * 16);
-#pragma unroll
-            for (int h = 0; h < GROUPS; ++h) {
-                // the group of these 32 columns: their index over group / 32, by the reciprocal (exact
-                // below 2^16; 0: group 32)
-                const uint32_t i = static_cast<uint32_t>(kb * 2 + h);
-                const int c = HALVES && inv_group == 0 ? min(static_cast<int>(i), groups - 1)
-                                                       : min(static_cast<int>(__umulhi(i, inv_group)), groups - 1);
-                const int64_t at = (static_cast<int64_t>(tile) * groups + c) * 8 + g;
-                b.s[r][h] = __ldg(static_cast<const uint32_t*>(a.scales) + at);
-                b.z[r][h] = a.zeros ? __ldg(reinterpret_cast<const uint16_t*>(a.zeros) + at) : 0x0808u;
+        for (int h = 0; h < NG; ++h) {
+            int c = d * WK * NG + h;
+            if (DENSE) {
+                // (past the last group the last one again)
+                if (NG > 1 && h > 0) c = d * WK * NG + min(h, groups - 1 - (first_block / 2 + j) * NG);
+            } else {
+                // the group of these columns: their place in units of 32 columns over group / 32
+                c = min(over(static_cast<uint32_t>(first_block * 2 + j * 4 + h * (4 / NG)), plan.inv), groups - 1);
             }
+            ld_nc32(b.s[h], scales + c * 8, on);
+            ld_nc16(b.z[h], zeros + c * zero_step, on);
         }
-        if (++lt == turns) {
-            lt = 0;
-            lu += step;
+    };
+    const auto advance = [&] {
+        lj += DEPTH * WK;
+        codes += DEPTH * WK * 1024;
+        if (DENSE) {
+            scales += DEPTH * WK * NG * 8;
+            zeros += DEPTH * WK * NG * zero_step;
+        }
+        if (lj >= plan.windows * DEPTH * WK) {  // the next unit
+            const int back = plan.windows * DEPTH * WK;
+            lj -= back;
+            ltile += stride * WR;
+            codes += stride * WR * tile_bytes - static_cast<int64_t>(back) * 1024;
+            const int64_t on = static_cast<int64_t>(stride * WR) * groups - (DENSE ? back * NG : 0);
+            scales += on * 8;
+            zeros += on * zero_step;
         }
     };
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i) load(ring[i]);
+    for (int i = 0; i < DEPTH; ++i) load(ring[i], i);
+    advance();
 
-    // ---- the tokens' values of this CTA's part of K (zeros past the end)
+    // ---- the tokens' values of this CTA's part of K (zeros past the end).  Sixteen lanes take a step of a token, each
+    // the 16 bytes that it asked for itself.
+    float* pairs = reinterpret_cast<float*>(w4_raw + tok * row_bytes);  // [step][group][pair of tokens][4]
+    float* sums = pairs + steps_rank * NG * TOK * 2;                    // [warp of K][token][row]
     {
+        const int items = tok * steps_rank, piece = threadIdx.x & 15;
         const uint16_t* x = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(tok0) * a.ldx;
-        const int per = kb_rank * 8, k0 = kb0 * 64;  // 16-byte pieces of a row
-        for (int i = threadIdx.x; i < tok * per; i += WT) {
-            const int t = i / per, c = i - t * per, k = k0 + c * 8;
+        const int k0 = first_block * 64 + piece * 8;
+#pragma unroll 4
+        for (int i = threadIdx.x >> 4; i < items; i += WT / 16) {
+            const int t = over(i, plan.inv_steps), j = i - t * steps_rank, k = k0 + j * 128;
             const uint16_t* p = x + t * a.ldx + k;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (xvec && k + 8 <= a.K) {
-                v = __ldg(reinterpret_cast<const uint4*>(p));
+            uint8_t* to = w4_raw + t * row_bytes + j * 256 + piece * 16;
+            const int left = static_cast<int>(a.K) - k;
+            if (plan.xvec) {  // (zeros behind the bytes that exist)
+                cp_async_16z(smem_u32(to), left > 0 ? p : x, left >= 8 ? 16u : left > 0 ? static_cast<uint32_t>(left) * 2u : 0u);
             } else {
-                uint16_t e[8];
+                uint32_t e[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) e[j] = k + j < a.K ? __ldg(p + j) : uint16_t(0);
-                v = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+                for (int l = 0; l < 8; ++l) e[l] = l < left ? __ldg(p + l) : uint16_t(0);
+                *reinterpret_cast<uint4*>(to) = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
             }
-            *reinterpret_cast<uint4*>(w4_raw + t * row_bytes + c * 16) = v;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        const unsigned lanes = 0xFFFFu << (lane & 16);
+        for (int i = threadIdx.x >> 4; i < items; i += WT / 16) {
+            const int t = over(i, plan.inv_steps), j = i - t * steps_rank;
+            uint4* p = reinterpret_cast<uint4*>(w4_raw + t * row_bytes + j * 256 + piece * 16);
+            const uint4 v = *p;
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            float f[8];
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+                const float2 h = two(w[l], bf16);
+                f[2 * l] = h.x;
+                f[2 * l + 1] = h.y;
+            }
+            // the largest finite magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^E
+            uint32_t top = 0;
+#pragma unroll
+            for (int l = 0; l < 8; ++l) {
+                const uint32_t m = __float_as_uint(f[l]) & 0x7FFFFFFFu;
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o *= 2) top = max(top, __shfl_xor_sync(lanes, top, o));
+            const uint32_t biased = max(top >> 23, 28u);  // (2^(14 - E) stays a normal number)
+            const float up = __uint_as_float((127u + 14u + 127u - biased) << 23), down = __uint_as_float(biased << 23);
+            float sum = 0.0f;
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {  // the pairs 1 and 3 meet nibbles that count 16 times
+                const float m = l % 2 ? up * 0.0625f : up;
+                const __half2 h = __floats2half2_rn(f[2 * l] * m, f[2 * l + 1] * m);
+                w[l] = *reinterpret_cast<const uint32_t*>(&h);
+                const float2 r = __half22float2(h);
+                sum = fmaf(r.x + r.y, l % 2 ? 16.0f : 1.0f, sum);
+            }
+            *p = make_uint4(w[0], w[2], w[1], w[3]);  // (two pairs for each of the two products)
+#pragma unroll
+            for (int o = 1; o < 16 / NG; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
+            if (piece % (16 / NG) == 0) {  // (times 2^-24, like the products)
+                float* q = pairs + ((j * NG + piece / (16 / NG)) * (TOK / 2) + t / 2) * 4 + t % 2;
+                q[0] = sum * 0x1p-24f;
+                q[2] = down;
+            }
         }
     }
     __syncthreads();
 
-    float acc[R][NT][4];
+    float acc[NT][4];
     const auto clear = [&] {
 #pragma unroll
-        for (int i = 0; i < R * NT * 4; ++i) acc[i / (NT * 4)][i / 4 % NT][i % 4] = 0.0f;
+        for (int i = 0; i < NT * 4; ++i) acc[i / 4][i % 4] = 0.0f;
     };
     clear();
-    int u = first, turn = 0;
-    const auto compute = [&](const Block<R, GROUPS>& b) {
-        const int j = turn * WW + warp;  // block within the CTA's part of K
-        if (kb0 + j >= kb1) return;
+    // (columns past the last token read its values, and any sums: what comes of them is not used)
+    const uint8_t* xrow[NT];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // sixteen bytes of each token: columns 32 h + 8 t4 .. + 7 of the block
-            uint4 xv[NT];
+    for (int n = 0; n < NT; ++n) xrow[n] = w4_raw + min(n * 8 + g, tok - 1) * row_bytes + my_k * 256 + t4 * 16;
+    const float* xs = pairs + (my_k * NG * (TOK / 2) + t4) * 4;
+    int j0 = 0;  // the window's first step, of the first warp of K
+    const auto compute = [&](const Step<NG>& b, int d) {
+        if (j0 + d * WK + my_k >= my_steps) return;
+        float d0[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                xv[n] = n * 8 + g < tok ? *reinterpret_cast<const uint4*>(w4_raw + (n * 8 + g) * row_bytes + j * 128 +
-                                                                          h * 64 + t4 * 16)
-                                        : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 4; ++h) {
+            // 32 columns: sixteen bytes of each token, columns 32 h + 8 t4 .. + 7 of the step
+            const uint4 v = h < 2 ? b.lo : b.hi;
+            const uint32_t w0 = h & 1 ? v.z : v.x, w1 = h & 1 ? v.w : v.y, u0 = w0 >> 8, u1 = w1 >> 8;
+            constexpr uint32_t LOW = 0x000F000Fu, HIGH = 0x00F000F0u;
+            constexpr int LEN = 4 / NG;  // such pieces of a group
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                constexpr uint32_t magic = Half<T>::magic;
-                const int gr = HALVES ? h : 0;
-                // magic + z, twice, of rows g and g + 8
-                const uint32_t z0 = __byte_perm(b.z[r][gr], magic, 0x5050), z1 = __byte_perm(b.z[r][gr], magic, 0x5151);
-                const uint32_t w0 = h == 0 ? b.w[r].x : b.w[r].z, w1 = h == 0 ? b.w[r].y : b.w[r].w;
-                uint32_t p[4], q[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    p[i] = Half<T>::sub(((w0 >> (4 * i)) & 0x000F000Fu) | magic, z0);
-                    q[i] = Half<T>::sub(((w1 >> (4 * i)) & 0x000F000Fu) | magic, z1);
-                }
-                const float2 sc = Half<T>::two(b.s[r][gr]);
+            for (int n = 0; n < NT; ++n) {
+                const uint4 x = *reinterpret_cast<const uint4*>(xrow[n] + j0 * 256 + d * (WK * 256) + h * 64);
+                if (h % LEN == 0)
+                    mma<true>(d0[n], w0 & LOW, w1 & LOW, u0 & LOW, u1 & LOW, x.x, x.y);
+                else
+                    mma<false>(d0[n], w0 & LOW, w1 & LOW, u0 & LOW, u1 & LOW, x.x, x.y);
+                mma<false>(d0[n], w0 & HIGH, w1 & HIGH, u0 & HIGH, u1 & HIGH, x.z, x.w);
+            }
+            if ((h + 1) % LEN == 0) {
+                const int gr = h / LEN;
+                const float2 s = two(b.s[gr], bf16);
+                // a zero as the lowest bits of 2^23
+                const float z0 = __uint_as_float(__byte_perm(b.z[gr], 0x4B000000u, 0x7440)) - 0x1p23f;
+                const float z1 = __uint_as_float(__byte_perm(b.z[gr], 0x4B000000u, 0x7441)) - 0x1p23f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    Half<T>::mma(d, p[0], q[0], p[1], q[1], xv[n].x, xv[n].y);
-                    Half<T>::mma(d, p[2], q[2], p[3], q[3], xv[n].z, xv[n].w);
-                    acc[r][n][0] = fmaf(sc.x, d[0], acc[r][n][0]);
-                    acc[r][n][1] = fmaf(sc.x, d[1], acc[r][n][1]);
-                    acc[r][n][2] = fmaf(sc.y, d[2], acc[r][n][2]);
-                    acc[r][n][3] = fmaf(sc.y, d[3], acc[r][n][3]);
+                    const float4 m = *reinterpret_cast<const float4*>(xs + j0 * (NG * TOK * 2) +
+                                                                      (d * WK * NG + gr) * (TOK * 2) + n * 16);
+                    const float e[4] = {fmaf(-z0, m.x, d0[n][0]), fmaf(-z0, m.y, d0[n][1]), fmaf(-z1, m.x, d0[n][2]),
+                                        fmaf(-z1, m.y, d0[n][3])};
+                    const float f[4] = {s.x * m.z, s.x * m.w, s.y * m.z, s.y * m.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(f[i], e[i], acc[n][i]);
                 }
             }
         }
     };
-    // The sums of a unit's rows: warps in order, then the cluster's CTAs in order.
-    const auto join = [&] {
-        float* mine = sums + warp * kSums<NT, R>;
+    // The sums of a unit's rows: each CTA of the cluster adds its share of them, warps and CTAs in order.
+    constexpr int SUM_ROW = w4_sum_row(ROWS);
+    const int part = tok * SUM_ROW;
+    const auto join = [&](int u) {
+        float* mine = sums + my_k * part + my_row * 16 + g;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mine[(n * 8 + t4 * 2 + (i & 1)) * kSumRow<NT, R> + r * 16 + g + (i >> 1) * 8] = acc[r][n][i];
-        __syncthreads();
-        clear();
-        const int count = tok * 16 * R;
-        for (int i = threadIdx.x; i < count; i += WT) {
-            const int t = i / (16 * R), row = i % (16 * R);
-            float* p = sums + t * kSumRow<NT, R> + row;
-            float v = p[0];
-#pragma unroll
-            for (int w = 1; w < WW; ++w) v += p[w * kSums<NT, R>];
-            if (ranks == 1)
-                epi_store1(a.e, 0, tok0 + t, static_cast<int64_t>(u) * 16 * R + row, v);
-            else
-                p[0] = v;
-        }
-        if (ranks > 1) {
+            for (int c = 0; c < 2; ++c) {
+                const int t = n * 8 + t4 * 2 + c;
+                if (t >= tok) continue;
+                // (2^24, of which the powers of two hold 2^14)
+                mine[t * SUM_ROW] = acc[n][c] * 0x1p10f;
+                mine[t * SUM_ROW + 8] = acc[n][2 + c] * 0x1p10f;
+            }
+        if (ranks > 1)
             cluster_sync();
-            if (rank == 0) {
-                for (int i = threadIdx.x; i < count; i += WT) {
-                    const int t = i / (16 * R), row = i % (16 * R);
-                    const float* p = sums + t * kSumRow<NT, R> + row;
-                    float v = p[0];
-                    for (uint32_t k = 1; k < ranks; ++k) {
+        else
+            __syncthreads();
+        clear();
+        const int count = tok * ROWS, step = WT * static_cast<int>(ranks);
+        for (int i = static_cast<int>(rank) * WT + threadIdx.x; i < count; i += step) {
+            const int t = i / ROWS, row = i % ROWS;
+            const float* p = sums + t * SUM_ROW + row;
+            float v = 0.0f;
+            if (ranks == 1) {
+#pragma unroll
+                for (int w = 0; w < WK; ++w) v += p[w * part];
+            } else {
+                for (uint32_t k = 0; k < ranks; ++k) {
+                    const uint32_t at = mapa_shared(smem_u32(p), k);
+#pragma unroll
+                    for (int w = 0; w < WK; ++w) {
                         float o;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(mapa_shared(smem_u32(p), k)) : "memory");
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(at + w * part * 4) : "memory");
                         v += o;
                     }
-                    epi_store1(a.e, 0, tok0 + t, static_cast<int64_t>(u) * 16 * R + row, v);
                 }
             }
-            cluster_sync();  // (the sums are read before they are written again, or the CTA leaves)
-        } else {
+            epi_store1(a.e, 0, tok0 + t, static_cast<int64_t>(u) * ROWS + row, v);
+        }
+        // (the sums are read before they are written again, or the CTA leaves)
+        if (ranks > 1)
+            cluster_sync();
+        else
             __syncthreads();
-        }
     };
-    const int total = n_units * turns;
-    for (int i = 0; i < total; i += DEPTH) {
+    for (int u = first; u < plan.units; u += stride) {
+        for (int w = 0; w < plan.windows; ++w) {
+            j0 = w * (DEPTH * WK);
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-            if (i + d >= total) break;
-            compute(ring[d]);
-            load(ring[d]);
-            if (++turn == turns) {
-                join();
-                turn = 0;
-                u += step;
+            for (int d = 0; d < DEPTH; ++d) {
+                compute(ring[d], d);
+                load(ring[d], d);
             }
+            advance();
         }
+        join(u);
     }
 }
 
-template <typename T, int NT, int R, bool HALVES, int DEPTH>
-cudaError_t launch(const W4Args& a, int splits, int num_sms, cudaStream_t st) {
-    auto k = w4_kernel<T, NT, R, HALVES, DEPTH>;
+int64_t w4_smem(int nt, int ng, int64_t tokens, int64_t steps_rank, int wk) {
+    const int64_t tok = std::min<int64_t>(tokens, 8 * nt);
+    return tok * w4_row(static_cast<int>(steps_rank)) + steps_rank * ng * 8 * nt * 8 +
+           wk * tok * w4_sum_row(WW / wk * 16) * 4;
+}
+// CTAs that an SM holds: by the registers that the kernel is compiled for, and its 228 KB (1 KB to each CTA itself).
+int w4_per_sm(int nt, int64_t smem) { return static_cast<int>(std::min<int64_t>(w4_ctas(nt), 228 * 1024 / (smem + 1024))); }
+
+template <int NT, int WK, int NG, bool DENSE>
+cudaError_t launch(const W4Args& a, const W4Config& c, int num_sms, cudaStream_t st) {
+    constexpr int DEPTH = w4_depth(NT);
+    auto k = w4_kernel<NT, WK, NG, DENSE, DEPTH>;
     static std::atomic<unsigned char> ready[kMaxDevices];
     int dev = 0;
     cudaError_t ce = cudaGetDevice(&dev);
@@ -291,54 +402,45 @@ cudaError_t launch(const W4Args& a, int splits, int num_sms, cudaStream_t st) {
         if (ce != cudaSuccess) return ce;
         if (dev < kMaxDevices) ready[dev].store(1, std::memory_order_release);
     }
-    const int kb_rank = static_cast<int>((w4_blocks(a.K) + splits - 1) / splits);
-    const int tok = static_cast<int>(std::min<int64_t>(a.M, 8 * NT));
-    const int smem = tok * w4_row(kb_rank) + WW * kSums<NT, R> * 4;
-    const int64_t units = (w4_tiles(a.N) + R - 1) / R;
-    int per_sm = 0;
-    ce = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k, WT, smem);
-    if (ce != cudaSuccess) return ce;
-    const int64_t at_once = std::max<int64_t>(1, static_cast<int64_t>(per_sm) * num_sms / splits);
+    const int64_t steps = (a.K + 127) / 128;
+    W4Plan p{};
+    p.steps_rank = static_cast<int>((steps + c.splits - 1) / c.splits);
+    p.inv_steps = reciprocal(p.steps_rank);
+    p.windows = (p.steps_rank + DEPTH * WK - 1) / (DEPTH * WK);
+    p.inv = reciprocal(a.group / 32);
+    p.blocks = static_cast<int>(w4_blocks(a.K));
+    p.tiles = static_cast<int>(w4_tiles(a.N));
+    p.groups = static_cast<int>(w4_groups(a.K, a.group));
+    p.xvec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.M <= 1 || a.ldx % 8 == 0);
+    p.bf16 = a.dtype == GEMM_BF16;
+    const int64_t smem = w4_smem(NT, NG, a.M, p.steps_rank, WK);
+    const int64_t unit_rows = WW / WK * 16, units = (a.N + unit_rows - 1) / unit_rows;
+    p.units = static_cast<int>(units);
+    const int64_t at_once = std::max<int64_t>(1, static_cast<int64_t>(std::max(1, w4_per_sm(NT, smem))) * num_sms / c.splits);
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min(units, at_once) * splits),
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min(units, at_once) * c.splits),
                        static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)));
     cfg.blockDim = dim3(WT);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
-    if (splits > 1) {
+    if (c.splits > 1) {
         at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = static_cast<unsigned>(splits);
+        at[0].val.clusterDim.x = static_cast<unsigned>(c.splits);
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    const bool xvec = reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && (a.M <= 1 || a.ldx % 8 == 0);
-    const uint32_t per = static_cast<uint32_t>(a.group / 32);
-    const uint32_t inv = per == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + per - 1) / per);
-    return cudaLaunchKernelEx(&cfg, k, a, kb_rank, xvec, inv);
+    return cudaLaunchKernelEx(&cfg, k, a, p);
 }
 
-// Row tiles of a unit: two where a token's values would be read from shared memory faster than the weights come.
-constexpr int w4_r(int nt) { return nt == 1 ? 1 : 2; }
-template <int NT>
-int64_t w4_smem(int64_t tokens, int64_t kb_rank) {
-    return std::min<int64_t>(tokens, 8 * NT) * w4_row(static_cast<int>(kb_rank)) + WW * kSums<NT, w4_r(NT)> * 4;
-}
-int64_t w4_smem(int nt, int64_t tokens, int64_t kb_rank) {
-    return nt == 1   ? w4_smem<1>(tokens, kb_rank)
-           : nt == 2 ? w4_smem<2>(tokens, kb_rank)
-           : nt == 4 ? w4_smem<4>(tokens, kb_rank)
-                     : w4_smem<8>(tokens, kb_rank);
-}
-
-template <typename T, bool HALVES>
+template <int NG, bool DENSE>
 cudaError_t launch_nt(const W4Config& c, const W4Args& a, int num_sms, cudaStream_t st) {
     switch (c.nt) {
-        case 1: return launch<T, 1, w4_r(1), HALVES, 4>(a, c.splits, num_sms, st);
-        case 2: return launch<T, 2, w4_r(2), HALVES, 2>(a, c.splits, num_sms, st);
-        case 4: return launch<T, 4, w4_r(4), HALVES, 2>(a, c.splits, num_sms, st);
-        default: return launch<T, 8, w4_r(8), HALVES, 2>(a, c.splits, num_sms, st);
+        case 1: return c.wk == 8 ? launch<1, 8, NG, DENSE>(a, c, num_sms, st) : launch<1, 2, NG, DENSE>(a, c, num_sms, st);
+        case 2: return launch<2, 2, NG, DENSE>(a, c, num_sms, st);
+        case 4: return launch<4, 2, NG, DENSE>(a, c, num_sms, st);
+        default: return launch<8, 2, NG, DENSE>(a, c, num_sms, st);
     }
 }
 
@@ -460,27 +562,51 @@ cudaError_t with_types(int dtype, int scale_dtype, const F& f) {
 
 }  // namespace
 
-// The fewest passes over the weights that shared memory allows, then CTAs of a cluster to a row tile's K: as many
-// as it takes for the tokens' values to fit, and more (up to 8, eight blocks of K each at least) while all row
-// tiles leave SMs without work.
-W4Config w4_choose(int64_t M, int64_t N, int64_t K, int num_sms) {
-    const int64_t blocks = w4_blocks(K);
+// The fewest passes over the weights that shared memory allows, then the cheapest cut by a model in ns: a CTA's
+// steps take their bytes at its share of 45 bytes per ns and SM, or half a microsecond a turn where that is more; a
+// unit's join 300, or 1800 where a cluster shares K.
+W4Config w4_choose(int64_t M, int64_t N, int64_t K, int64_t group, int num_sms) {
+    const int64_t steps = (K + 127) / 128;
+    const int ng = w4_per_step(group);
     for (int nt = M <= 8 ? 1 : M <= 16 ? 2 : M <= 32 ? 4 : 8;; nt /= 2) {
-        const int64_t units = (w4_tiles(N) + w4_r(nt) - 1) / w4_r(nt) * ((M + 8 * nt - 1) / (8 * nt));
-        for (int s = 1; s <= 8; s *= 2) {
-            if (w4_smem(nt, M, (blocks + s - 1) / s) > kW4Smem) continue;
-            while (s < 8 && units * s * 2 <= num_sms * 2 && blocks >= 16 * s) s *= 2;
-            return W4Config{nt, s};
-        }
-        if (nt == 1) return W4Config{1, 8};  // (not reached: K is at most 65536)
+        W4Config best{nt, 0, 0};
+        double least = 0;
+        for (int s = 1; s <= 8; s *= 2)
+            for (int wk = nt == 1 ? 8 : 2; wk >= 2; wk /= 4) {
+                const int64_t rank_steps = (steps + s - 1) / s, turns = (rank_steps + wk - 1) / wk;
+                const int64_t smem = w4_smem(nt, ng, M, rank_steps, wk);
+                if (smem > kW4Smem || (s > 1 && (s - 1) * rank_steps >= steps)) continue;
+                const int64_t rows = WW / wk * 16, passes = (M + 8 * nt - 1) / (8 * nt);
+                const int64_t units = (N + rows - 1) / rows * passes;
+                const int per_sm = w4_per_sm(nt, smem);
+                const int64_t at_once = std::max<int64_t>(1, int64_t(per_sm) * num_sms / s);
+                const int64_t rounds = (units + at_once - 1) / at_once;
+                const int64_t ctas_sm = std::min<int64_t>(per_sm, (units * s + num_sms - 1) / num_sms);
+                const double bytes = double(turns) * WW * 1024 * ctas_sm / 45.0;
+                const double t = rounds * (std::max(bytes, turns * 500.0) + (s > 1 ? 1800 : 300)) +
+                                 std::min<int64_t>(M, 8 * nt) * rank_steps * 256 * ctas_sm / 60.0;
+                if (best.splits == 0 || t < least) {
+                    least = t;
+                    best.splits = s;
+                    best.wk = wk;
+                }
+            }
+        if (best.splits > 0) return best;
+        if (nt == 1) return W4Config{1, 8, 8};  // (not reached: K is at most 65536)
     }
 }
 
 cudaError_t launch_w4(const W4Config& c, const W4Args& a, int num_sms, cudaStream_t st) {
-    const bool f16 = a.dtype == GEMM_F16, halves = a.group % 64 != 0;
-    if (halves)
-        return f16 ? launch_nt<__half, true>(c, a, num_sms, st) : launch_nt<__nv_bfloat16, true>(c, a, num_sms, st);
-    return f16 ? launch_nt<__half, false>(c, a, num_sms, st) : launch_nt<__nv_bfloat16, false>(c, a, num_sms, st);
+    switch (a.group) {
+        case 32: return launch_nt<4, true>(c, a, num_sms, st);
+        case 64: return launch_nt<2, true>(c, a, num_sms, st);
+        case 128: return launch_nt<1, true>(c, a, num_sms, st);
+    }
+    switch (w4_per_step(a.group)) {
+        case 1: return launch_nt<1, false>(c, a, num_sms, st);
+        case 2: return launch_nt<2, false>(c, a, num_sms, st);
+        default: return launch_nt<4, false>(c, a, num_sms, st);
+    }
 }
 
 cudaError_t launch_w4_quantize(int dtype, int scale_dtype, int64_t N, int64_t K, int64_t group, const void* src,

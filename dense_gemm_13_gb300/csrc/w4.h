@@ -42,11 +42,11 @@ struct W4Args {
     EpiParams e;
 };
 
-// How a product is cut: 8 * nt tokens a pass, `splits` CTAs of a cluster to a row tile's K.
+// How a product is cut: 8 * nt tokens a pass, `splits` CTAs of a cluster to K, `wk` of a CTA's warps to its part of K.
 struct W4Config {
-    int nt, splits;
+    int nt, splits, wk;
 };
-W4Config w4_choose(int64_t M, int64_t N, int64_t K, int num_sms);
+W4Config w4_choose(int64_t M, int64_t N, int64_t K, int64_t group, int num_sms);
 
 cudaError_t launch_w4(const W4Config& c, const W4Args& a, int num_sms, cudaStream_t st);
 // src: [N][ld] of `dtype`; scales of `scale_dtype`; zeros null: symmetric.

@@ -135,7 +135,7 @@ int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, co
     a.e.beta = d.beta;
     a.e.out_dtype = d.out_dtype;
     a.e.act = d.act;
-    return cuda_status(launch_w4(w4_choose(d.M, d.N, d.K, sms), a, sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_w4(w4_choose(d.M, d.N, d.K, d.group, sms), a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 void gemm_w4_desc_init(gemm_w4_desc_t* d) {

@@ -471,8 +471,10 @@ int gemm_w4_dequantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, 
 
 /*
  * Y = cast( act( alpha * X.W^T + bias ) + beta * R ) for 1 to 64 tokens.  X [M][K] in the scales'
- * type; products of X with q - z are exact, their sums over a group and the sums of
- * scale * group in FP32: no weight is rounded.  (More tokens: gemm_w4_dequantize, then gemm_run.)
+ * type.  A group's sum of x (q - z) is that of x q less z times that of x, in FP32, and so is the sum of
+ * scale * group: no weight is rounded, and a result is off by some 2^-20 of sum |x| (q + z) s at most.
+ * (BF16 values below 2^-31 of their token's largest count to 2^-40 of it.  A token that holds an infinity
+ * or a NaN gives values that are not finite.)  More tokens: gemm_w4_dequantize, then gemm_run.
  */
 typedef struct {
     gemm_dtype_t dtype;     /* X and the scales: GEMM_BF16 (default) or GEMM_F16 */

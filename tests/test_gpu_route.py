@@ -99,6 +99,33 @@ def test_near_ties_are_told_apart():
             check(torch.from_numpy(z).cuda(), 8, bias, scores=scores, **kw)
 
 
+def test_groups_in_doubt():
+    # group scores that agree to FP32's accuracy, and scores within a group that do: the exact ones decide
+    T, G, per = 400, 8, 32
+    for scores, group_score in (("sigmoid", "top2"), ("sigmoid", "max"), ("softmax", "top2"), ("softmax", "max")):
+        r = rng("groups", scores, group_score)
+        z = r.standard_normal((T, G, per)).astype(np.float32)
+        z = np.sort(z, 2)
+        z[:, :, -3:] = np.array([0.5, 1.0, 2.0], np.float32) + (r.standard_normal((T, G, 3)) * 2e-7).astype(np.float32)
+        z[:, 5, -1], z[:, 6, -3:] = 3.0, 1.0
+        z = np.take_along_axis(z, r.permuted(np.tile(np.arange(per), (T, G, 1)), axis=2), 2).reshape(T, G * per)
+        bias = (r.standard_normal(G * per) * 1e-7).astype(np.float32)
+        for b in (None, bias):
+            for top in (2, 4, 7):
+                check(torch.from_numpy(z).cuda(), 6, b, scores=scores, groups=G, top_groups=top, group_score=group_score)
+
+
+def test_many_in_doubt():
+    # more experts than a warp has lanes within FP32's accuracy of one another
+    r = rng("many")
+    z = (1.0 + r.standard_normal((50, 300)) * 1e-7).astype(np.float32)
+    bias = (r.standard_normal(300) * 1e-8).astype(np.float32)
+    for scores in ("sigmoid", "softmax"):
+        check(torch.from_numpy(z).cuda(), 20, bias, scores=scores)
+        check(torch.from_numpy(z).cuda(), 20, None, scores=scores)
+        check(torch.from_numpy(z).cuda(), 32, bias, scores=scores, groups=10, top_groups=4, group_score="top2")
+
+
 def test_not_finite_logits():
     nan, inf = float("nan"), float("inf")
     z = torch.tensor([[1.0, nan, 3.0, 2.0], [1.0, inf, 3.0, 2.0], [-inf, -inf, 5.0, -inf], [-inf] * 4, [nan] * 4,

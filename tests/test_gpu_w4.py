@@ -1,10 +1,11 @@
 """4-bit weights with group scales on the GPU: layout and quantisation element for element, products against 64-bit sums.
 
-Tolerance of a product, with S = sum |x (q - z) s| of an element and u = 2^-24: a tensor-core step adds 16 exact products
-to a running value (off by at most 2^-22 of the magnitudes so far if it truncates), two or four steps to a sum that a
-scale multiplies: 4 * 2^-22 S; a warp adds one such sum for every 32 columns of its eighth of K, then eight warps' and up
-to eight CTAs' sums are added: (K / 256 + 16) u S; alpha rounds once:
-    |Y - ref| <= (2^-20 + (K / 256 + 17) 2^-24) S      before the epilogue.
+Tolerance of a product, with S = sum |x| (q + z) s of an element and u = 2^-24: a group's products q x come in two chains of
+at most four tensor-core steps (each adds 16 exact products, off by at most 2^-22 of the magnitudes so far if it
+truncates); its sum of x has at most eight additions; taking off z times it, joining the chains and multiplying by
+the scale into a running sum round once each; a warp adds one such sum for every 32 columns of its share of K, then at most
+eight warps' and eight CTAs' sums are added; alpha rounds once. BF16 activations below 2^-31 of their token's largest are off by 2^-40 of it:
+    |Y - ref| <= (2^-20 + (K / 32 + 28) u) S + 2^-40 max|x| sum (q + z) s      before the epilogue.
 GELU (erff) is off by at most 4 units of |y|; each FP32 step of the epilogue rounds its result; the cast adds half a
 step of its type.
 """
@@ -33,14 +34,16 @@ def rng(*key):
 
 
 def weight(r, N, K, group, dtype, zeros=True, ints=False):
-    """(W4Tensor made by w4_pack, codes, scales, zeros, 64-bit values)."""
+    """(W4Tensor made by w4_pack, codes, scales, zeros, (64-bit values, (q + z) s))."""
     G = -(-K // group)
     q = r.integers(0, 16, (N, K)).astype(np.uint8)
     s = torch.from_numpy((2.0 ** r.integers(-1, 2, (N, G)) if ints else r.random((N, G)) * 0.1 + 0.01).astype(np.float32))
     s = s.to(DT[dtype])
     z = r.integers(0, 16, (N, G)).astype(np.uint8) if zeros else None
     W = g13.w4_pack(torch.from_numpy(q).cuda(), s.cuda(), None if z is None else torch.from_numpy(z).cuda(), group)
-    return W, q, s, z, ref.w4_values(q, s.double().numpy(), z, group)
+    s64 = s.double().numpy()
+    z64 = np.full(s64.shape, 8.0) if z is None else z
+    return W, q, s, z, (ref.w4_values(q, s64, z, group), ref.w4_values(q, s64, -z64.astype(float), group))
 
 
 LAYOUTS = [(1, 1, 32), (16, 64, 64), (17, 65, 32), (40, 130, 128), (100, 1000, 96), (33, 300, 256), (5, 64, 65536)]
@@ -52,6 +55,7 @@ LAYOUTS = [(1, 1, 32), (16, 64, 64), (17, 65, 32), (40, 130, 128), (100, 1000, 9
 def test_pack_and_read_back(shape, dtype, zeros):
     N, K, group = shape
     W, q, s, z, values = weight(rng("pack", shape, zeros), N, K, group, dtype, zeros)
+    values = values[0]
     assert np.array_equal(W.codes.cpu().numpy(), ref.w4_words(q))
     bits = s.view(torch.int16).numpy()
     assert np.array_equal(W.scales.view(torch.int16).cpu().numpy(), ref.w4_entries(bits))
@@ -128,8 +132,10 @@ def test_quantise_not_finite():
 
 def check_product(got, x, w, out, bias=None, act="none", R=None, alpha=1.0, beta=1.0):
     x, K = x.double().cpu().numpy(), x.shape[1]
-    S, y = np.abs(x) @ np.abs(w).T * abs(alpha), alpha * (x @ w.T)
-    tol = (2.0 ** -20 + (K / 256 + 17) * 2.0 ** -24) * S
+    w, both = w  # values, (q + z) s
+    S, y = np.abs(x) @ both.T * abs(alpha), alpha * (x @ w.T)
+    tol = (2.0 ** -20 + (K / 32 + 28) * 2.0 ** -24) * S
+    tol = tol + 2.0 ** -40 * abs(alpha) * np.abs(x).max(1)[:, None] * both.sum(1)
     if bias is not None:
         y = y + bias.double().cpu().numpy()
         tol = tol + 2.0 ** -24 * np.abs(y)
@@ -160,7 +166,7 @@ def test_product_exact_integers(shape, dtype):
     M, N, K, group = shape
     for zeros in (True, False):
         r = rng("int", shape, zeros)
-        W, _, _, _, w = weight(r, N, K, group, dtype, zeros, ints=True)
+        W, _, _, _, (w, _) = weight(r, N, K, group, dtype, zeros, ints=True)
         assert 30 * K < 2 ** 22
         x = torch.from_numpy(r.integers(-1, 2, (M, K)).astype(np.float32)).to(DT[dtype]).cuda()
         big = torch.full((M + 2, N + 3), 7.0, device="cuda")
@@ -209,10 +215,31 @@ def test_not_finite_values_stay_in_their_row():
     W, _, _, _, w = weight(r, 40, 300, 64, "bf16")
     x = torch.randn(5, 300, device="cuda").bfloat16()
     x[1, 7], x[3, 299] = float("nan"), float("inf")
+    for t in (torch.bfloat16, torch.float16):
+        V = W if t is torch.bfloat16 else g13.W4Tensor(W.codes, W.scales.half(), W.zeros, 40, 300, 64)
+        y = g13.w4_matmul(x.to(t), V, out_dtype="f32")
+        assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[3]).any())
     y = g13.w4_matmul(x, W, out_dtype="f32")
-    assert bool(torch.isnan(y[1]).all()) and not bool(torch.isfinite(y[3]).any())
     rest = [0, 2, 4]
     check_product(y[rest], x[rest], w, "f32")
+
+
+def test_magnitudes_far_apart():
+    # BF16's whole range, between tokens and within one; tokens of zeros
+    r = rng("range")
+    W, _, _, _, w = weight(r, 60, 1000, 128, "bf16")
+    x = r.standard_normal((8, 1000)).astype(np.float32)
+    x *= np.exp2(np.array([0, 100, -100, -120, 60, -60, 0, 0]))[:, None].astype(np.float32)
+    x[4] *= np.exp2(r.integers(-28, 1, 1000)).astype(np.float32)
+    x[5, ::7] = 0
+    x[6] = 0
+    x[7], x[7, 500:] = 1e-38, 0
+    x = torch.from_numpy(x).bfloat16().cuda()
+    y = g13.w4_matmul(x, W, out_dtype="f32")
+    check_product(y, x, w, "f32")
+    assert bool((y[6] == 0).all())
+    for i in range(8):  # (a token's neighbours do not count)
+        check_product(g13.w4_matmul(x[i: i + 1], W, out_dtype="f32"), x[i: i + 1], w, "f32")
 
 
 def test_large_codes():
