@@ -14,10 +14,10 @@
 // elements.
 //
 // In mxfp8 four threads' chunks (a warp's 32 elements, where rows are not aligned) are a
-// block: its largest magnitude by shuffles, eight codes as one store.  y is rounded to four
-// bits, and the closer it is to its value before that, the fewer codes lie on the wrong side of
-// a border: so there the threads' sums, 1 / sqrt and the product h w are kept in two FP32 numbers
-// each (FP64, which a few of its operations a row would take 5 us of, is far too slow).
+// block: its largest magnitude by shuffles, eight codes as one store.  Codes and scales are those of
+// the exact y but for what the sum of squares is off by: the threads' sums and 1 / sqrt are kept in two
+// FP32 numbers each (a few FP64 operations a row would take 5 us), and values next to a border are
+// worked out again with theirs.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -151,44 +151,55 @@ struct Part {
         }
     }
 
+    // The weight of chunk u, its offset added.
+    __device__ __forceinline__ void weight(int u, float (&w)[8]) const {
+        const gemm_norm_desc_t& d = a.d;
+        if (!a.w) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+        } else if (whole(u)) {
+            Raw8<8> rw;
+            const char* p = static_cast<const char*>(a.w) + col(u, 0) * size(d.weight_dtype);
+            const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p));
+            rw.v[0] = lo.x, rw.v[1] = lo.y, rw.v[2] = lo.z, rw.v[3] = lo.w;
+            if (d.weight_dtype == GEMM_F32) {
+                const uint4 hi = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+                rw.v[4] = hi.x, rw.v[5] = hi.y, rw.v[6] = hi.z, rw.v[7] = hi.w;
+            }
+            to_floats(d.weight_dtype, rw, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = col(u, i) < s.cols ? one(a.w, d.weight_dtype, col(u, i)) : 0.0f;
+        }
+        if (d.weight_offset != 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] += d.weight_offset;
+        }
+    }
+    // v w (rs + rs_lo) to 2^-46 of itself, rounded to odd (the last bit set where something was cut off), so that the
+    // rounding to four bits that follows does not see a tie that is none.
+    static __device__ __forceinline__ float to_odd(float v, float w, float rs, float rs_lo) {
+        const float p = v * w, e = fmaf(v, w, -p), c = fmaf(p, rs_lo, e * rs), hi = fmaf(p, rs, c);  // v w = p + e
+        const float lo = fmaf(p, rs, -hi) + c;
+        int bits = __float_as_int(hi);
+        if (lo != 0.0f && fabsf(hi) < INFINITY && (bits & 1) == 0) bits += (lo < 0.0f) == (hi < 0.0f) ? 1 : -1;
+        return hi == 0.0f ? hi : __int_as_float(bits);
+    }
+    // Whether a number may round otherwise to three mantissa bits (or, of a block's largest, fall on the other side of
+    // 1.75) if it is off by four units in its last place.
+    static __device__ __forceinline__ bool near_tie(float y) {
+        return ((__float_as_uint(y) + 4u - 0x80000u) & 0xFFFFFu) < 8u;
+    }
+    static __device__ __forceinline__ bool near_border(uint32_t top) { return ((top + 4u - 0x600000u) & 0x7FFFFFu) < 9u; }
+
     // y of chunk u from its h: rs (+ rs_lo) is the row's factor.
     __device__ __forceinline__ void finish(int64_t row, int u, const float (&v)[8], float rs, float rs_lo) const {
         const gemm_norm_desc_t& d = a.d;
-        float y[8];
-        if (a.w) {
-            if (whole(u)) {
-                Raw8<8> rw;
-                const char* p = static_cast<const char*>(a.w) + col(u, 0) * size(d.weight_dtype);
-                const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p));
-                rw.v[0] = lo.x, rw.v[1] = lo.y, rw.v[2] = lo.z, rw.v[3] = lo.w;
-                if (d.weight_dtype == GEMM_F32) {
-                    const uint4 hi = __ldg(reinterpret_cast<const uint4*>(p) + 1);
-                    rw.v[4] = hi.x, rw.v[5] = hi.y, rw.v[6] = hi.z, rw.v[7] = hi.w;
-                }
-                to_floats(d.weight_dtype, rw, y);
-            } else {
+        float w[8], y[8];
+        weight(u, w);
+        const float r1 = rs + rs_lo;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = col(u, i) < s.cols ? one(a.w, d.weight_dtype, col(u, i)) : 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = 1.0f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float w = y[i] + d.weight_offset;
-            if constexpr (F8) {
-                // h w = p + e, times rs + rs_lo: hi + lo.  Rounded to odd (the last bit set where something
-                // was cut off), so that the rounding to four bits does not see a tie that is none.
-                const float p = v[i] * w, e = fmaf(v[i], w, -p), c = fmaf(p, rs_lo, e * rs), hi = fmaf(p, rs, c);
-                const float lo = fmaf(p, rs, -hi) + c;
-                int bits = __float_as_int(hi);
-                if (lo != 0.0f && fabsf(hi) < INFINITY && (bits & 1) == 0) bits += (lo < 0.0f) == (hi < 0.0f) ? 1 : -1;
-                y[i] = hi == 0.0f ? hi : __int_as_float(bits);
-            } else {
-                y[i] = v[i] * rs * w;
-            }
-        }
+        for (int i = 0; i < 8; ++i) y[i] = v[i] * r1 * w[i];
         if constexpr (!F8) {
             if (whole(u)) {
                 char* p = static_cast<char*>(a.y) + (row * d.ldy + col(u, 0)) * size(d.out_dtype);
@@ -211,19 +222,31 @@ struct Part {
             uint8_t* codes = static_cast<uint8_t*>(a.y) + row * s.row_bytes;
             uint8_t* tile = a.scales + (row >> 7) * s.col_tiles * kFp4TileBytes + (row & 31) * 16 + (row >> 5 & 3) * 4;
             const bool live = row < s.rows;
+            // Three roundings put y off by less than four units in its last place.  Where that may matter to a value of
+            // the warp (one warp in a few hundred), all of its values are worked out again, exactly.
             if constexpr (VEC) {
-                uint32_t top = 0;
+                uint32_t byte = 0;
+                for (bool again = false;; again = true) {
+                    uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (col(u, i) >= s.cols) y[i] = 0.0f;  // (a factor of NaN leaves the padding zero)
-                    top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                    for (int i = 0; i < 8; ++i) {
+                        if (col(u, i) >= s.cols) y[i] = 0.0f;  // (a factor of NaN leaves the padding zero)
+                        top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                    }
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    byte = mxfp8_scale(top);
+                    const float inv = ue8m0_value(254u - min(byte, 254u));
+                    bool near = near_border(top);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        y[i] *= inv;
+                        near = near || near_tie(y[i]);
+                    }
+                    if (again || !__any_sync(0xFFFFFFFFu, near)) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = to_odd(v[i], w[i], rs, rs_lo);
                 }
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                uint32_t byte = mxfp8_scale(top);
-                const float inv = ue8m0_value(254u - min(byte, 254u));
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= inv;
                 if (live && col(u, 0) < s.row_bytes)
                     *reinterpret_cast<uint2*>(codes + col(u, 0)) = make_uint2(e4m3x4(y), e4m3x4(y + 4));
                 // (a row in the padding, and a block past the row's end: zero.)  Eight lanes have two of a
@@ -242,10 +265,17 @@ struct Part {
                 for (int i = 0; i < 8; ++i) {
                     const int c = col(u, i), c0 = c & ~31;  // the warp's 32 elements are a block
                     if (c0 >= static_cast<int64_t>(s.col_tiles) * 128) break;
-                    if (c >= s.cols) y[i] = 0.0f;
-                    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-                    uint32_t byte = mxfp8_scale(top);
-                    const float v4[4] = {y[i] * ue8m0_value(254u - min(byte, 254u)), 0.0f, 0.0f, 0.0f};
+                    uint32_t byte = 0;
+                    float scaled = 0.0f;
+                    for (bool again = false;; again = true) {
+                        if (c >= s.cols) y[i] = 0.0f;
+                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                        byte = mxfp8_scale(top);
+                        scaled = y[i] * ue8m0_value(254u - min(byte, 254u));
+                        if (again || !__any_sync(0xFFFFFFFFu, near_tie(scaled) || near_border(top))) break;
+                        y[i] = to_odd(v[i], w[i], rs, rs_lo);
+                    }
+                    const float v4[4] = {scaled, 0.0f, 0.0f, 0.0f};
                     if (live && c < s.row_bytes) codes[c] = static_cast<uint8_t>(e4m3x4(v4));
                     if (!live || c0 >= s.cols) byte = 0;
                     if (lane == 0) tile[static_cast<int64_t>(c0 / 128) * kFp4TileBytes + (c0 >> 5 & 3)] = static_cast<uint8_t>(byte);
@@ -291,9 +321,9 @@ __device__ __forceinline__ S shuffle_sum(S v, int lanes) {
     return v;
 }
 
-// CTAs per SM that the registers are kept for: a thousand threads, a half where a chunk takes twice the words.
+// CTAs per SM that the registers are kept for: a thousand threads, fewer where a thread holds more.
 __host__ __device__ constexpr int norm_ctas(bool vec, int w, int tpr, int u) {
-    return (u == 4 || (vec && w == 8 && u > 1) ? 512 : 1024) / (tpr < 128 ? 128 : tpr);
+    return (u == 4 || (vec && w == 8 && u > 1) ? 512 : u == 3 ? 768 : 1024) / (tpr < 128 ? 128 : tpr);
 }
 
 // U = 0: the row is read twice instead of kept.
@@ -401,14 +431,20 @@ cudaError_t launch_shape(const NormArgs& a, const NormShape& s, int num_sms, cud
     if (VEC && chunks <= 16) return launch<F8, VEC, W, VEC ? 16 : 32, 1>(a, s, num_sms, st);
     if (chunks <= 32) return launch<F8, VEC, W, 32, 1>(a, s, num_sms, st);
     if (chunks > 2048) return launch<F8, VEC, W, 512, 0>(a, s, num_sms, st);
-    // one chunk a thread where there are few rows (latency counts) or the loads are single elements (eight a chunk)
-    if (!VEC || s.rows <= 2 * num_sms) {
+    // one chunk a thread where there are few rows: latency counts
+    if (s.rows <= 2 * num_sms) {
         if (chunks <= 64) return launch<F8, VEC, W, 64, 1>(a, s, num_sms, st);
         if (chunks <= 128) return launch<F8, VEC, W, 128, 1>(a, s, num_sms, st);
         if (chunks <= 256) return launch<F8, VEC, W, 256, 1>(a, s, num_sms, st);
         if (chunks <= 512) return launch<F8, VEC, W, 512, 1>(a, s, num_sms, st);
         if (chunks <= 768) return launch<F8, VEC, W, 768, 1>(a, s, num_sms, st);
         if (chunks <= 1024) return launch<F8, VEC, W, 1024, 1>(a, s, num_sms, st);
+    }
+    if constexpr (!VEC) {  // single elements, eight a chunk: threads without any would cost as much
+        if (chunks > 128 && chunks <= 192) return launch<F8, VEC, W, 64, 3>(a, s, num_sms, st);
+        if (chunks > 256 && chunks <= 384) return launch<F8, VEC, W, 128, 3>(a, s, num_sms, st);
+        if (chunks > 512 && chunks <= 768) return launch<F8, VEC, W, 256, 3>(a, s, num_sms, st);
+        if (chunks > 1024 && chunks <= 1536) return launch<F8, VEC, W, 512, 3>(a, s, num_sms, st);
     }
     if (chunks <= 64) return launch<F8, VEC, W, 32, 2>(a, s, num_sms, st);
     if (chunks <= 128) return launch<F8, VEC, W, 64, 2>(a, s, num_sms, st);
