@@ -37,21 +37,11 @@ namespace {
 constexpr int WW = 8;            // warps of a CTA
 constexpr int WT = WW * 32;
 constexpr int kMaxDevices = 64;
-constexpr int kW4Smem = 200 * 1024;  // at most, of the 227 KB that a CTA can have
-// CTAs per SM that the registers are kept for.
-#ifndef C1
-#define C1 3
-#define D1 3
-#define C2 2
-#define D2 3
-#define C4 2
-#define D4 3
-#define C8 1
-#define D8 3
-#endif
-constexpr int w4_ctas(int nt) { return nt == 1 ? C1 : nt == 2 ? C2 : nt == 4 ? C4 : C8; }
-// Steps ahead of each warp.
-constexpr int w4_depth(int nt) { return nt == 1 ? D1 : nt == 2 ? D2 : nt == 4 ? D4 : D8; }
+constexpr int kW4Smem = 226 * 1024;  // at most, of the 227 KB that a CTA can have
+// CTAs per SM that the registers are kept for, and steps ahead of each warp.  (Of one to four CTAs and two to six steps,
+// these were the fastest, or within 3 % of it, from 1 x 6144 x 6144 to 64 x 16384 x 8192.)
+constexpr int w4_ctas(int nt) { return nt == 1 ? 3 : nt <= 4 ? 2 : 1; }
+constexpr int w4_depth(int nt, int ng) { return nt == 1 && ng == 4 ? 2 : nt <= 2 ? 3 : 4; }
 
 // Two 16-bit numbers to FP32.
 __device__ __forceinline__ float2 two(uint32_t v, bool bf16) {
@@ -93,6 +83,14 @@ __device__ __forceinline__ void ld_nc16(uint32_t& v, const uint16_t* p, bool on)
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
                  : "+r"(v)
                  : "l"(p), "r"(static_cast<int>(on)));
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 __device__ const uint16_t kEights = 0x0808;
 
@@ -201,69 +199,84 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
     for (int i = 0; i < DEPTH; ++i) load(ring[i], i);
     advance();
 
-    // ---- the tokens' values of this CTA's part of K (zeros past the end).  Sixteen lanes take a step of a token, each
-    // the 16 bytes that it asked for itself.
+    // ---- the tokens' values of this CTA's part of K (zeros past the end).  Eight lanes take a step of a token, each
+    // the 32 bytes that it asked for itself.
     float* pairs = reinterpret_cast<float*>(w4_raw + tok * row_bytes);  // [step][group][pair of tokens][4]
-    float* sums = pairs + steps_rank * NG * TOK * 2;                    // [warp of K][token][row]
+    float* sums = pairs + steps_rank * NG * TOK * 2;                    // [set][warp of K][token][row]
     {
-        const int items = tok * steps_rank, piece = threadIdx.x & 15;
+        const int items = tok * steps_rank, piece = threadIdx.x & 7;
         const uint16_t* x = static_cast<const uint16_t*>(a.x) + static_cast<int64_t>(tok0) * a.ldx;
-        const int k0 = first_block * 64 + piece * 8;
+        const int k0 = first_block * 64 + piece * 16;
 #pragma unroll 4
-        for (int i = threadIdx.x >> 4; i < items; i += WT / 16) {
+        for (int i = threadIdx.x >> 3; i < items; i += WT / 8) {
             const int t = over(i, plan.inv_steps), j = i - t * steps_rank, k = k0 + j * 128;
             const uint16_t* p = x + t * a.ldx + k;
-            uint8_t* to = w4_raw + t * row_bytes + j * 256 + piece * 16;
-            const int left = static_cast<int>(a.K) - k;
-            if (plan.xvec) {  // (zeros behind the bytes that exist)
-                cp_async_16z(smem_u32(to), left > 0 ? p : x, left >= 8 ? 16u : left > 0 ? static_cast<uint32_t>(left) * 2u : 0u);
-            } else {
-                uint32_t e[8];
+            uint8_t* to = w4_raw + t * row_bytes + j * 256 + piece * 32;
+            const int left = static_cast<int>(a.K) - k;  // (zeros behind the values that exist)
+            if (plan.xvec) {
 #pragma unroll
-                for (int l = 0; l < 8; ++l) e[l] = l < left ? __ldg(p + l) : uint16_t(0);
-                *reinterpret_cast<uint4*>(to) = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+                for (int h = 0; h < 2; ++h) {
+                    const int n = left - 8 * h;
+                    cp_async_16z(smem_u32(to + 16 * h), n > 0 ? p + 8 * h : x, n >= 8 ? 16u : n > 0 ? static_cast<uint32_t>(n) * 2u : 0u);
+                }
+            } else {
+                // aligned words, each of which holds at least one of the values, shifted
+                const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1 & 1);
+                const uint32_t* q = reinterpret_cast<const uint32_t*>(p - odd);
+                uint32_t e[9], v[8];
+#pragma unroll
+                for (int l = 0; l < 9; ++l) e[l] = 2 * l - odd < left && (l < 8 || odd) ? __ldg(q + l) : 0u;
+#pragma unroll
+                for (int l = 0; l < 8; ++l) {
+                    v[l] = __funnelshift_r(e[l], e[l + 1], odd * 16);
+                    if (2 * l + 1 >= left) v[l] = 2 * l >= left ? 0u : v[l] & 0xFFFFu;
+                }
+                reinterpret_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
             }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        const unsigned lanes = 0xFFFFu << (lane & 16);
-        for (int i = threadIdx.x >> 4; i < items; i += WT / 16) {
+        const unsigned lanes = 0xFFu << (lane & 24);
+        for (int i = threadIdx.x >> 3; i < items; i += WT / 8) {
             const int t = over(i, plan.inv_steps), j = i - t * steps_rank;
-            uint4* p = reinterpret_cast<uint4*>(w4_raw + t * row_bytes + j * 256 + piece * 16);
-            const uint4 v = *p;
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            float f[8];
+            uint4* p = reinterpret_cast<uint4*>(w4_raw + t * row_bytes + j * 256 + piece * 32);
+            const uint4 lo = p[0], hi = p[1];
+            uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            float f[16], top = 0.0f, sum = 0.0f;
 #pragma unroll
-            for (int l = 0; l < 4; ++l) {
+            for (int l = 0; l < 8; ++l) {
                 const float2 h = two(w[l], bf16);
                 f[2 * l] = h.x;
                 f[2 * l + 1] = h.y;
             }
-            // the largest finite magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^E
-            uint32_t top = 0;
 #pragma unroll
-            for (int l = 0; l < 8; ++l) {
-                const uint32_t m = __float_as_uint(f[l]) & 0x7FFFFFFFu;
-                top = max(top, m < 0x7F800000u ? m : 0u);
+            for (int l = 0; l < 16; ++l) {
+                top = fmaxf(top, fabsf(f[l]));  // (a NaN does not count)
+                sum += f[l];
             }
+            if (top == INFINITY) {  // nor does an infinity
+                top = 0.0f;
 #pragma unroll
-            for (int o = 1; o < 16; o *= 2) top = max(top, __shfl_xor_sync(lanes, top, o));
-            const uint32_t biased = max(top >> 23, 28u);  // (2^(14 - E) stays a normal number)
+                for (int l = 0; l < 16; ++l) top = fabsf(f[l]) < INFINITY ? fmaxf(top, fabsf(f[l])) : top;
+            }
+            // the largest magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^E
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
+            const uint32_t biased = max(__float_as_uint(top) >> 23, 28u);  // (2^(14 - E) stays a normal number)
             const float up = __uint_as_float((127u + 14u + 127u - biased) << 23), down = __uint_as_float(biased << 23);
-            float sum = 0.0f;
 #pragma unroll
-            for (int l = 0; l < 4; ++l) {  // the pairs 1 and 3 meet nibbles that count 16 times
+            for (int l = 0; l < 8; ++l) {  // the pairs 1 and 3 of eight columns meet nibbles that count 16 times
                 const float m = l % 2 ? up * 0.0625f : up;
                 const __half2 h = __floats2half2_rn(f[2 * l] * m, f[2 * l + 1] * m);
                 w[l] = *reinterpret_cast<const uint32_t*>(&h);
-                const float2 r = __half22float2(h);
-                sum = fmaf(r.x + r.y, l % 2 ? 16.0f : 1.0f, sum);
             }
-            *p = make_uint4(w[0], w[2], w[1], w[3]);  // (two pairs for each of the two products)
+            p[0] = make_uint4(w[0], w[2], w[1], w[3]);  // (two pairs for each of the two products)
+            p[1] = make_uint4(w[4], w[6], w[5], w[7]);
 #pragma unroll
-            for (int o = 1; o < 16 / NG; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
-            if (piece % (16 / NG) == 0) {  // (times 2^-24, like the products)
-                float* q = pairs + ((j * NG + piece / (16 / NG)) * (TOK / 2) + t / 2) * 4 + t % 2;
-                q[0] = sum * 0x1p-24f;
+            for (int o = 1; o < 8 / NG; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
+            if (piece % (8 / NG) == 0) {  // (times 2^-24, like the products)
+                float* q = pairs + ((j * NG + piece / (8 / NG)) * (TOK / 2) + t / 2) * 4 + t % 2;
+                q[0] = sum * (up * 0x1p-24f);
                 q[2] = down;
             }
         }
@@ -320,11 +333,16 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
             }
         }
     };
-    // The sums of a unit's rows: each CTA of the cluster adds its share of them, warps and CTAs in order.
+    // The sums of a unit's rows: each CTA of the cluster adds its share of them, four rows of a token at a time, warps
+    // and CTAs in order.  There are two sets of them in turn: one that is written is no longer read, since whoever
+    // reads it has to arrive at the barrier of the unit in between.
     constexpr int SUM_ROW = w4_sum_row(ROWS);
     const int part = tok * SUM_ROW;
+    int set = 0;
     const auto join = [&](int u) {
-        float* mine = sums + my_k * part + my_row * 16 + g;
+        float* base = sums + set * (WK * part);
+        set ^= 1;
+        float* mine = base + my_k * part + my_row * 16 + g;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -340,32 +358,34 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
         else
             __syncthreads();
         clear();
-        const int count = tok * ROWS, step = WT * static_cast<int>(ranks);
+        const int count = tok * (ROWS / 4), step = WT * static_cast<int>(ranks);
         for (int i = static_cast<int>(rank) * WT + threadIdx.x; i < count; i += step) {
-            const int t = i / ROWS, row = i % ROWS;
-            const float* p = sums + t * SUM_ROW + row;
-            float v = 0.0f;
+            const int t = i / (ROWS / 4), row = i % (ROWS / 4) * 4;
+            const float* p = base + t * SUM_ROW + row;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const auto add = [&](const float4& o) {
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            };
             if (ranks == 1) {
 #pragma unroll
-                for (int w = 0; w < WK; ++w) v += p[w * part];
+                for (int w = 0; w < WK; ++w) add(*reinterpret_cast<const float4*>(p + w * part));
             } else {
-                for (uint32_t k = 0; k < ranks; ++k) {
-                    const uint32_t at = mapa_shared(smem_u32(p), k);
+                // (all loads of a warp of K are asked for before the first is used)
+#pragma unroll 1
+                for (int w = 0; w < WK; ++w) {
+                    float4 o[8];
 #pragma unroll
-                    for (int w = 0; w < WK; ++w) {
-                        float o;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(o) : "r"(at + w * part * 4) : "memory");
-                        v += o;
-                    }
+                    for (uint32_t k = 0; k < 8; ++k)
+                        o[k] = k < ranks ? ld_cluster_f4(mapa_shared(smem_u32(p + w * part), k)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) add(o[k]);
                 }
             }
-            epi_store1(a.e, 0, tok0 + t, static_cast<int64_t>(u) * ROWS + row, v);
+            epi_store4(a.e, 0, tok0 + t, static_cast<int64_t>(u) * ROWS + row, v.x, v.y, v.z, v.w);
         }
-        // (the sums are read before they are written again, or the CTA leaves)
-        if (ranks > 1)
-            cluster_sync();
-        else
-            __syncthreads();
     };
     for (int u = first; u < plan.units; u += stride) {
         for (int w = 0; w < plan.windows; ++w) {
@@ -379,19 +399,25 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
         }
         join(u);
     }
+    if (ranks > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
 int64_t w4_smem(int nt, int ng, int64_t tokens, int64_t steps_rank, int wk) {
     const int64_t tok = std::min<int64_t>(tokens, 8 * nt);
     return tok * w4_row(static_cast<int>(steps_rank)) + steps_rank * ng * 8 * nt * 8 +
-           wk * tok * w4_sum_row(WW / wk * 16) * 4;
+           2 * wk * tok * w4_sum_row(WW / wk * 16) * 4;
+}
+// Clusters of `splits` CTAs that run at a time, with one CTA to an SM: a cluster stays within a part of the GPU, so
+// the larger ones leave SMs over (152 SMs hold 76, 36 and 15 of 2, 4 and 8).
+int64_t clusters_at_once(int splits, int num_sms) {
+    return splits == 1 ? num_sms : splits == 2 ? num_sms / 2 : splits == 4 ? num_sms / 4 - num_sms / 76 : num_sms / 10;
 }
 // CTAs that an SM holds: by the registers that the kernel is compiled for, and its 228 KB (1 KB to each CTA itself).
 int w4_per_sm(int nt, int64_t smem) { return static_cast<int>(std::min<int64_t>(w4_ctas(nt), 228 * 1024 / (smem + 1024))); }
 
 template <int NT, int WK, int NG, bool DENSE>
 cudaError_t launch(const W4Args& a, const W4Config& c, int num_sms, cudaStream_t st) {
-    constexpr int DEPTH = w4_depth(NT);
+    constexpr int DEPTH = w4_depth(NT, NG);
     auto k = w4_kernel<NT, WK, NG, DENSE, DEPTH>;
     static std::atomic<unsigned char> ready[kMaxDevices];
     int dev = 0;
@@ -416,7 +442,7 @@ cudaError_t launch(const W4Args& a, const W4Config& c, int num_sms, cudaStream_t
     const int64_t smem = w4_smem(NT, NG, a.M, p.steps_rank, WK);
     const int64_t unit_rows = WW / WK * 16, units = (a.N + unit_rows - 1) / unit_rows;
     p.units = static_cast<int>(units);
-    const int64_t at_once = std::max<int64_t>(1, static_cast<int64_t>(std::max(1, w4_per_sm(NT, smem))) * num_sms / c.splits);
+    const int64_t at_once = std::max<int64_t>(1, std::max(1, w4_per_sm(NT, smem)) * clusters_at_once(c.splits, num_sms));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(std::min(units, at_once) * c.splits),
                        static_cast<unsigned>((a.M + 8 * NT - 1) / (8 * NT)));
@@ -579,7 +605,7 @@ W4Config w4_choose(int64_t M, int64_t N, int64_t K, int64_t group, int num_sms) 
                 const int64_t rows = WW / wk * 16, passes = (M + 8 * nt - 1) / (8 * nt);
                 const int64_t units = (N + rows - 1) / rows * passes;
                 const int per_sm = w4_per_sm(nt, smem);
-                const int64_t at_once = std::max<int64_t>(1, int64_t(per_sm) * num_sms / s);
+                const int64_t at_once = std::max<int64_t>(1, per_sm * clusters_at_once(s, num_sms));
                 const int64_t rounds = (units + at_once - 1) / at_once;
                 const int64_t ctas_sm = std::min<int64_t>(per_sm, (units * s + num_sms - 1) / num_sms);
                 const double bytes = double(turns) * WW * 1024 * ctas_sm / 45.0;
