@@ -111,6 +111,27 @@ struct Part {
         if (W == 8 && type == GEMM_F32) ld16(c + 16, r.v + 4 % W);
     }
     __device__ __forceinline__ bool whole(int u) const { return VEC && col(u, 0) + 8 <= s.cols; }
+    // The elements of a chunk one by one, as FP32 (zeros past the row's end).  The types are asked once a chunk, and
+    // nothing is stored between the loads, which would wait for one another (1000 x 4097: 28.5 us).
+    template <typename T>
+    __device__ __forceinline__ void singles(const void* p, int64_t at, int u, Raw8<8>& o) const {
+        const T* q = static_cast<const T*>(p) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o.v[i] = col(u, i) < s.cols ? __float_as_uint(static_cast<float>(q[col(u, i)])) : 0u;
+    }
+    __device__ __forceinline__ void singles(const void* p, int type, int64_t at, int u, Raw8<8>& o) const {
+        if (type == GEMM_F32)
+            singles<float>(p, at, u, o);
+        else if (type == GEMM_BF16)
+            singles<__nv_bfloat16>(p, at, u, o);
+        else
+            singles<__half>(p, at, u, o);
+    }
+    __device__ __forceinline__ void singles(int64_t row, int u, Raw8<8>& rx, Raw8<8>& rr) const {
+        singles(a.x, a.d.dtype, row * a.d.ldx, u, rx);
+        if (a.r) singles(a.r, a.d.residual_dtype, row * a.d.ldr, u, rr);
+    }
 
     // v = h of chunk u (zeros past the row's end), from raw elements where the chunk is whole; writes h.
     __device__ __forceinline__ void sum_up(int64_t row, int u, const Raw8<W>& rx, const Raw8<W>& rr, float (&v)[8],
@@ -138,15 +159,17 @@ struct Part {
             }
             return;
         }
+        Raw8<8> x8, r8;
+        if constexpr (VEC)
+            singles(row, u, x8, r8);
+        else
+            x8 = rx, r8 = rr;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int c = col(u, i);
-            v[i] = 0.0f;
-            if (c >= s.cols) continue;
-            v[i] = one(a.x, d.dtype, row * d.ldx + c);
+            v[i] = __uint_as_float(x8.v[i]);
             if (a.r) {
-                v[i] = round_to(d.residual_dtype, v[i] + one(a.r, d.residual_dtype, row * d.ldr + c));
-                if (store) put(a.h, d.residual_dtype, row * d.ldh + c, v[i]);
+                v[i] = round_to(d.residual_dtype, v[i] + __uint_as_float(r8.v[i]));
+                if (store && col(u, i) < s.cols) put(a.h, d.residual_dtype, row * d.ldh + col(u, i), v[i]);
             }
         }
     }
@@ -261,24 +284,36 @@ struct Part {
                     if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(tile) = byte & 0xFFFFu;
                 }
             } else {
+                // (element i of the chunk is in the warp's i-th block of 32 neighbours)
+                uint32_t byte[8];
+                float scaled[8];
+                for (bool again = false;; again = true) {
+                    uint32_t top[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (col(u, i) >= s.cols) y[i] = 0.0f;
+                        top[i] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                    }
+                    bool near = false;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        byte[i] = mxfp8_scale(top[i]);
+                        scaled[i] = y[i] * ue8m0_value(254u - min(byte[i], 254u));
+                        near = near || near_tie(scaled[i]) || near_border(top[i]);
+                    }
+                    if (again || !__any_sync(0xFFFFFFFFu, near)) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] = to_odd(v[i], w[i], rs, rs_lo);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int c = col(u, i), c0 = c & ~31;  // the warp's 32 elements are a block
-                    if (c0 >= static_cast<int64_t>(s.col_tiles) * 128) break;
-                    uint32_t byte = 0;
-                    float scaled = 0.0f;
-                    for (bool again = false;; again = true) {
-                        if (c >= s.cols) y[i] = 0.0f;
-                        const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-                        byte = mxfp8_scale(top);
-                        scaled = y[i] * ue8m0_value(254u - min(byte, 254u));
-                        if (again || !__any_sync(0xFFFFFFFFu, near_tie(scaled) || near_border(top))) break;
-                        y[i] = to_odd(v[i], w[i], rs, rs_lo);
-                    }
-                    const float v4[4] = {scaled, 0.0f, 0.0f, 0.0f};
+                    const int c = col(u, i), c0 = c & ~31;
+                    if (c0 >= s.col_tiles * 128) continue;
+                    const float v4[4] = {scaled[i], 0.0f, 0.0f, 0.0f};
                     if (live && c < s.row_bytes) codes[c] = static_cast<uint8_t>(e4m3x4(v4));
-                    if (!live || c0 >= s.cols) byte = 0;
-                    if (lane == 0) tile[static_cast<int64_t>(c0 / 128) * kFp4TileBytes + (c0 >> 5 & 3)] = static_cast<uint8_t>(byte);
+                    if (lane == 0)
+                        tile[static_cast<int64_t>(c0 / 128) * kFp4TileBytes + (c0 >> 5 & 3)] =
+                            static_cast<uint8_t>(live && c0 < s.cols ? byte[i] : 0);
                 }
             }
         }
@@ -352,6 +387,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, 
             return q;
         };
         const auto load = [&](int u, Raw8<W>& rx, Raw8<W>& rr) {
+            if constexpr (!VEC) p.singles(row_in, u, rx, rr);
             if (!p.whole(u)) return;
             p.load(a.x, d.dtype, row_in * d.ldx + p.col(u, 0), rx);
             if (a.r) p.load(a.r, d.residual_dtype, row_in * d.ldr + p.col(u, 0), rr);
@@ -464,7 +500,7 @@ cudaError_t launch_norm_kind(const NormArgs& a, const NormShape& s, int num_sms,
     };
     const bool vec = on(a.x, d.dtype, d.ldx) && on(a.r, d.residual_dtype, d.ldr) && on(a.h, d.residual_dtype, d.ldh) &&
                      on(a.w, d.weight_dtype, 0) && (F8 || on(a.y, d.out_dtype, d.ldy));
-    if (!vec) return launch_shape<F8, false, 4>(a, s, num_sms, st);
+    if (!vec) return launch_shape<F8, false, 8>(a, s, num_sms, st);
     if (d.dtype == GEMM_F32 || d.residual_dtype == GEMM_F32) return launch_shape<F8, true, 8>(a, s, num_sms, st);
     return launch_shape<F8, true, 4>(a, s, num_sms, st);
 }

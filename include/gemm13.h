@@ -401,8 +401,9 @@ int gemm_fp8_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  *
  * sums and all steps in FP32.  Y is computed from the rounded H, so that a later call on H
  * alone gives the same.  With mxfp8, Y is written as 8-bit floats (above): codes and scales of
- * the FP32 values, as gemm_fp8_quantize would of them (sums added in 64 bits, the factor and its product
- * with H and the weight to 2^-23 of their values before the one rounding).
+ * the exact values of the formula, but for a sum of squares that is off by some 2^-40 of itself (it and
+ * the factor are held in two FP32 numbers each): values next to a border of the codes or the scales
+ * are worked out again with both.
  * A row's sum of squares must stay within FP32.  NaN and infinities: as the formula has them.
  */
 typedef struct {
@@ -473,8 +474,8 @@ int gemm_w4_dequantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, 
  * Y = cast( act( alpha * X.W^T + bias ) + beta * R ) for 1 to 64 tokens.  X [M][K] in the scales'
  * type.  A group's sum of x (q - z) is that of x q less z times that of x, in FP32, and so is the sum of
  * scale * group: no weight is rounded, and a result is off by some 2^-20 of sum |x| (q + z) s at most.
- * (BF16 values below 2^-31 of their token's largest count to 2^-40 of it.  A token that holds an infinity
- * or a NaN gives values that are not finite.)  More tokens: gemm_w4_dequantize, then gemm_run.
+ * (BF16 values below 2^-27, FP16 values below 2^-24 of the largest of their 128 columns, k / 128 alike,
+ * count to 2^-35 of it.  A token that holds an infinity or a NaN gives values that are not finite.)  More tokens: gemm_w4_dequantize, then gemm_run.
  */
 typedef struct {
     gemm_dtype_t dtype;     /* X and the scales: GEMM_BF16 (default) or GEMM_F16 */

@@ -4,8 +4,10 @@ Tolerance of a product, with S = sum |x| (q + z) s of an element and u = 2^-24: 
 at most four tensor-core steps (each adds 16 exact products, off by at most 2^-22 of the magnitudes so far if it
 truncates); its sum of x has at most eight additions; taking off z times it, joining the chains and multiplying by
 the scale into a running sum round once each; a warp adds one such sum for every 32 columns of its share of K, then at most
-eight warps' and eight CTAs' sums are added; alpha rounds once. BF16 activations below 2^-31 of their token's largest are off by 2^-40 of it:
-    |Y - ref| <= (2^-20 + (K / 32 + 28) u) S + 2^-40 max|x| sum (q + z) s      before the epilogue.
+eight warps' and eight CTAs' sums are added; alpha rounds once. Activations are brought
+to FP16 by a power of two per 128 columns that puts the largest of them into [2^14, 2^15), half of them by a 16th more, so
+[2^10, 2^11); half a step of FP16's lowest range, 2^-25, is 2^-35 of that at most:
+    |Y - ref| <= (2^-20 + (K / 32 + 28) u) S + 2^-35 sum_b max_b|x| sum_b (q + z) s      before the epilogue (b: 128 columns).
 GELU (erff) is off by at most 4 units of |y|; each FP32 step of the epilogue rounds its result; the cast adds half a
 step of its type.
 """
@@ -135,7 +137,8 @@ def check_product(got, x, w, out, bias=None, act="none", R=None, alpha=1.0, beta
     w, both = w  # values, (q + z) s
     S, y = np.abs(x) @ both.T * abs(alpha), alpha * (x @ w.T)
     tol = (2.0 ** -20 + (K / 32 + 28) * 2.0 ** -24) * S
-    tol = tol + 2.0 ** -40 * abs(alpha) * np.abs(x).max(1)[:, None] * both.sum(1)
+    for b in range(0, K, 128):
+        tol = tol + 2.0 ** -35 * abs(alpha) * np.abs(x[:, b:b + 128]).max(1)[:, None] * both[:, b:b + 128].sum(1)
     if bias is not None:
         y = y + bias.double().cpu().numpy()
         tol = tol + 2.0 ** -24 * np.abs(y)
