@@ -29,6 +29,8 @@ struct NormShape {
     Two inv;                 // 1 / cols
     int64_t rows, rows_all;  // rows_all: with the padding of the scales' last tile
     int64_t row_bytes, col_tiles;
+    int phase, phase_step;   // by how many elements row 0 is off 16 bytes, and each row more (of eight; FP32 alone: of four)
+    bool wide_weight;        // the weight takes loads of eight 16-bit numbers
 };
 
 cudaError_t launch_rms_norm(const NormArgs& a, int num_sms, cudaStream_t st);

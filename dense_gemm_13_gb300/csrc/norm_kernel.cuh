@@ -10,8 +10,10 @@
 // which each thread holds one to four chunks of eight neighbouring elements; the row's sum is
 // joined by shuffles, and between warps through shared memory with one barrier.  CTAs are
 // persistent, so that one row's loads overlap another's sums on the same SM.
-// Rows that are not 16-byte aligned go element by element, neighbouring lanes on neighbouring
-// elements.
+// Rows that do not start on 16 bytes: where those of all arrays are off by the same number of elements (as in
+// contiguous tensors with an odd number of columns), a row's chunks begin that much before its first
+// column, so that loads and stores stay whole ("phased"); other rows go element by element, neighbouring lanes on
+// neighbouring elements.
 //
 // In mxfp8 four threads' chunks (a warp's 32 elements, where rows are not aligned) are a
 // block: its largest magnitude by shuffles, eight codes as one store.  Codes and scales are those of
@@ -43,24 +45,11 @@ __device__ __forceinline__ void ld16(const void* p, uint32_t* v) {
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "l"(p));
 }
-__device__ __forceinline__ float one(const void* p, int type, int64_t i) {
-    if (type == GEMM_F32) return static_cast<const float*>(p)[i];
-    if (type == GEMM_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    return __half2float(static_cast<const __half*>(p)[i]);
-}
-__device__ __forceinline__ void put(void* p, int type, int64_t i, float v) {
-    if (type == GEMM_F32)
-        static_cast<float*>(p)[i] = v;
-    else if (type == GEMM_BF16)
-        static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-// v as a number of `type`.
-__device__ __forceinline__ float round_to(int type, float v) {
-    if (type == GEMM_F32) return v;
-    if (type == GEMM_BF16) return __bfloat162float(__float2bfloat16_rn(v));
-    return __half2float(__float2half_rn(v));
+__device__ __forceinline__ void ld16(const void* p, uint32_t* v, bool on) {  // (else v keeps what it holds)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+                 "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3])
+                 : "l"(p), "r"(static_cast<int>(on)));
 }
 template <int W>
 __device__ __forceinline__ void to_floats(int type, const Raw8<W>& r, float (&f)[8]) {
@@ -91,98 +80,154 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// One thread's part of a row: TPR threads a row, U chunks of 8 elements each.  With VEC a
-// chunk is eight neighbours, else elements TPR apart.
-template <bool F8, bool VEC, int W, int TPR>
+// How a row lies in its threads' chunks.
+enum Lay {
+    SINGLES = 0,  // element i of a chunk is i * TPR columns on
+    ALIGNED = 1,  // eight neighbours, the first chunk at column 0
+    PHASED = 2    // eight neighbours, the first chunk at column -o, 0 <= o < 8
+};
+
+// One thread's part of a row: TPR threads a row, U chunks of 8 elements each.
+template <bool F8, int LAY, int W, int TPR>
 struct Part {
+    static constexpr bool VEC = LAY != SINGLES;
     const NormArgs& a;
     const NormShape& s;
     int t;  // this thread within the row
+    int o;  // the row's phase
 
     __device__ __forceinline__ int col(int u, int i) const {
-        return VEC ? (u * TPR + t) * 8 + i : (u * 8 + i) * TPR + t;
+        return VEC ? (u * TPR + t) * 8 + i - (LAY == PHASED ? o : 0) : (u * 8 + i) * TPR + t;
     }
-    __device__ __forceinline__ int64_t size(int type) const { return type == GEMM_F32 ? 4 : 2; }
+    __device__ __forceinline__ bool in(int c) const { return static_cast<unsigned>(c) < static_cast<unsigned>(s.cols); }
+    __device__ __forceinline__ bool whole(int u) const {
+        return VEC && (LAY != PHASED || col(u, 0) >= 0) && col(u, 0) + 8 <= s.cols;
+    }
 
-    // The raw elements of chunk u of a row of p (whole chunks of VEC rows only).
-    __device__ __forceinline__ void load(const void* p, int type, int64_t at, Raw8<W>& r) const {
-        const char* c = static_cast<const char*>(p) + at * (W == 4 ? 2 : size(type));
-        ld16(c, r.v);
-        if (W == 8 && type == GEMM_F32) ld16(c + 16, r.v + 4 % W);
-    }
-    __device__ __forceinline__ bool whole(int u) const { return VEC && col(u, 0) + 8 <= s.cols; }
-    // The elements of a chunk one by one, as FP32 (zeros past the row's end).  The types are asked once a chunk, and
-    // nothing is stored between the loads, which would wait for one another (1000 x 4097: 28.5 us).
+    // Chunks past the row's end cost a branch only (one by one each took some 200 instructions: 4000 x 2049, 26 us).
+    __device__ __forceinline__ bool none(int u) const { return col(u, 0) >= s.cols; }
+
+    // The raw elements of chunk u of the row that begins at element `at` of p; zeros where the row has none.
     template <typename T>
-    __device__ __forceinline__ void singles(const void* p, int64_t at, int u, Raw8<8>& o) const {
-        const T* q = static_cast<const T*>(p) + at;
+    __device__ __forceinline__ void singles(const T* p, int u, Raw8<W>& r) const {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o.v[i] = col(u, i) < s.cols ? __float_as_uint(static_cast<float>(q[col(u, i)])) : 0u;
-    }
-    __device__ __forceinline__ void singles(const void* p, int type, int64_t at, int u, Raw8<8>& o) const {
-        if (type == GEMM_F32)
-            singles<float>(p, at, u, o);
-        else if (type == GEMM_BF16)
-            singles<__nv_bfloat16>(p, at, u, o);
-        else
-            singles<__half>(p, at, u, o);
-    }
-    __device__ __forceinline__ void singles(int64_t row, int u, Raw8<8>& rx, Raw8<8>& rr) const {
-        singles(a.x, a.d.dtype, row * a.d.ldx, u, rx);
-        if (a.r) singles(a.r, a.d.residual_dtype, row * a.d.ldr, u, rr);
-    }
-
-    // v = h of chunk u (zeros past the row's end), from raw elements where the chunk is whole; writes h.
-    __device__ __forceinline__ void sum_up(int64_t row, int u, const Raw8<W>& rx, const Raw8<W>& rr, float (&v)[8],
-                                           bool store) const {
-        const gemm_norm_desc_t& d = a.d;
-        if (whole(u)) {
-            to_floats(d.dtype, rx, v);
-            if (a.r) {
-                float w[8];
-                to_floats(d.residual_dtype, rr, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += w[i];
-                if (W == 4 || d.residual_dtype != GEMM_F32) {
-                    Raw8<W> o{};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o.v[i] = pack16(d.residual_dtype, v[2 * i], v[2 * i + 1]);
-                    to_floats(d.residual_dtype, o, v);
-                    if (store) *reinterpret_cast<uint4*>(static_cast<char*>(a.h) + (row * d.ldh + col(u, 0)) * 2) =
-                        make_uint4(o.v[0], o.v[1], o.v[2], o.v[3]);
-                } else if (store) {
-                    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.h) + row * d.ldh + col(u, 0));
-                    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    p[1] = make_float4(v[4], v[5], v[6], v[7]);
-                }
-            }
-            return;
-        }
-        Raw8<8> x8, r8;
-        if constexpr (VEC)
-            singles(row, u, x8, r8);
-        else
-            x8 = rx, r8 = rr;
+        for (int i = 0; i < W; ++i) r.v[i] = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[i] = __uint_as_float(x8.v[i]);
-            if (a.r) {
-                v[i] = round_to(d.residual_dtype, v[i] + __uint_as_float(r8.v[i]));
-                if (store && col(u, i) < s.cols) put(a.h, d.residual_dtype, row * d.ldh + col(u, i), v[i]);
+            const uint32_t v = in(col(u, i)) ? p[col(u, i)] : T(0);
+            if (sizeof(T) == 4)
+                r.v[i % W] = v;
+            else
+                r.v[i / 2] |= v << i % 2 * 16;
+        }
+    }
+    __device__ __forceinline__ void singles(const void* p, int type, int64_t at, int u, Raw8<W>& r) const {
+        if (W == 8 && type == GEMM_F32)
+            singles(static_cast<const uint32_t*>(p) + at, u, r);
+        else
+            singles(static_cast<const uint16_t*>(p) + at, u, r);
+    }
+    // Whether chunk u takes wide loads: in phased rows what is in it besides the row's elements then lies between the array's first and
+    // last element, in the gap between rows or in the next row, and is left out afterwards.
+    __device__ __forceinline__ bool wide(int64_t row, int64_t ld, int u) const {
+        const int c = col(u, 0);
+        if (LAY != PHASED) return whole(u);
+        return c < s.cols && (c >= 0 || row * ld >= 8) && (c + 8 <= s.cols || (s.rows - 1 - row) * ld >= 8);
+    }
+    // (A predicate instead of a branch, behind which the loaded values are copied, and waited for: FP16 with an FP32
+    // residual, 4000 x 2560, 23 -> 19 us.  Of 16-bit rows alone the branch is kept: 8192 x 8192, 87.5 us, else 90.)
+    __device__ __forceinline__ void load(const void* p, int type, int64_t row, int64_t ld, int u, Raw8<W>& r) const {
+        if constexpr (!VEC) {
+            singles(p, type, row * ld, u, r);
+        } else {
+            const bool four = W == 8 && type == GEMM_F32, on = wide(row, ld, u);
+            const char* c = static_cast<const char*>(p) + (row * ld + col(u, 0)) * (four ? 4 : 2);
+            if constexpr (LAY == ALIGNED && W == 4) {
+                if (on) ld16(c, r.v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < W; ++i) r.v[i] = 0;
+                ld16(c, r.v, on);
+                if (W == 8) ld16(c + 16, r.v + 4 % W, on && four);
             }
         }
+    }
+    // The numbers of a chunk that was loaded, those past the row's ends zero.
+    __device__ __forceinline__ void numbers(const void* p, int type, int64_t row, int64_t ld, int u, const Raw8<W>& r,
+                                            float (&v)[8]) const {
+        if (!VEC || whole(u) || wide(row, ld, u)) {
+            to_floats(type, r, v);
+        } else if (none(u)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        } else {
+            Raw8<W> q;
+            singles(p, type, row * ld, u, q);
+            to_floats(type, q, v);
+        }
+        if (LAY == PHASED && !whole(u)) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = in(col(u, i)) ? v[i] : 0.0f;
+        }
+    }
+    // Numbers to chunk u of the row that begins at element `at` of p, rounded to its type.
+    __device__ __forceinline__ void store(void* p, int type, int64_t at, int u, const float (&v)[8]) const {
+        if (none(u)) return;
+        if (!whole(u)) {
+            if (type == GEMM_F32) {
+                float* q = static_cast<float*>(p) + at;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (in(col(u, i))) q[col(u, i)] = v[i];
+            } else {
+                uint16_t* q = static_cast<uint16_t*>(p) + at;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const uint32_t two = pack16(type, v[i], v[i + 1]);
+                    if (in(col(u, i))) q[col(u, i)] = static_cast<uint16_t>(two);
+                    if (in(col(u, i + 1))) q[col(u, i + 1)] = static_cast<uint16_t>(two >> 16);
+                }
+            }
+        } else if (type == GEMM_F32) {
+            float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at + col(u, 0));
+            q[0] = make_float4(v[0], v[1], v[2], v[3]);
+            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at + col(u, 0)) =
+                make_uint4(pack16(type, v[0], v[1]), pack16(type, v[2], v[3]), pack16(type, v[4], v[5]),
+                           pack16(type, v[6], v[7]));
+        }
+    }
+
+    // v = h of chunk u (zeros where the row has none); writes h.
+    __device__ __forceinline__ void sum_up(int64_t row, int u, const Raw8<W>& rx, const Raw8<W>& rr, float (&v)[8],
+                                           bool write) const {
+        const gemm_norm_desc_t& d = a.d;
+        numbers(a.x, d.dtype, row, d.ldx, u, rx, v);
+        if (!a.r) return;
+        float w[8];
+        numbers(a.r, d.residual_dtype, row, d.ldr, u, rr, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += w[i];
+        if (W == 4 || d.residual_dtype != GEMM_F32) {
+            Raw8<W> h{};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h.v[i] = pack16(d.residual_dtype, v[2 * i], v[2 * i + 1]);
+            to_floats(d.residual_dtype, h, v);
+        }
+        if (write) store(a.h, d.residual_dtype, row * d.ldh, u, v);
     }
 
     // The weight of chunk u, its offset added.
     __device__ __forceinline__ void weight(int u, float (&w)[8]) const {
         const gemm_norm_desc_t& d = a.d;
-        if (!a.w) {
+        const int c = col(u, 0);
+        if (!a.w || none(u)) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-        } else if (whole(u)) {
+        } else if (LAY == ALIGNED && whole(u)) {
             Raw8<8> rw;
-            const char* p = static_cast<const char*>(a.w) + col(u, 0) * size(d.weight_dtype);
+            const char* p = static_cast<const char*>(a.w) + c * (d.weight_dtype == GEMM_F32 ? 4 : 2);
             const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p));
             rw.v[0] = lo.x, rw.v[1] = lo.y, rw.v[2] = lo.z, rw.v[3] = lo.w;
             if (d.weight_dtype == GEMM_F32) {
@@ -190,9 +235,34 @@ struct Part {
                 rw.v[4] = hi.x, rw.v[5] = hi.y, rw.v[6] = hi.z, rw.v[7] = hi.w;
             }
             to_floats(d.weight_dtype, rw, w);
-        } else {
+        } else if (LAY == PHASED && s.wide_weight && c + o + 8 <= s.cols) {
+            // two whole chunks, of which eight 16-bit numbers from the (8 - o)th are the ones
+            const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.w) + c + o);
+            const uint4 hi = __ldg(p), lo = o && c >= 0 ? __ldg(p - 1) : hi;  // (c <= 0: there is none before it, nor any need)
+            const uint32_t q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint32_t h[6], k[5];
+            Raw8<8> rw;
+            const int from = o ? 8 - o : 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = col(u, i) < s.cols ? one(a.w, d.weight_dtype, col(u, i)) : 0.0f;
+            for (int i = 0; i < 6; ++i) h[i] = from & 4 ? q[i + 2] : q[i];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) k[i] = from & 2 ? h[i + 1] : h[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rw.v[i] = __funnelshift_r(k[i], k[i + 1], from % 2 * 16);
+            to_floats(d.weight_dtype, rw, w);
+        } else if (d.weight_dtype == GEMM_F32) {
+            const float* p = static_cast<const float*>(a.w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = in(col(u, i)) ? __ldg(p + col(u, i)) : 0.0f;
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(a.w);
+            uint32_t e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = in(col(u, i)) ? __ldg(p + col(u, i)) : 0u;
+            Raw8<8> rw;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rw.v[i] = e[2 * i] | e[2 * i + 1] << 16;
+            to_floats(d.weight_dtype, rw, w);
         }
         if (d.weight_offset != 0.0f) {
 #pragma unroll
@@ -219,26 +289,13 @@ struct Part {
     __device__ __forceinline__ void finish(int64_t row, int u, const float (&v)[8], float rs, float rs_lo) const {
         const gemm_norm_desc_t& d = a.d;
         float w[8], y[8];
+        if (!F8 && none(u)) return;
         weight(u, w);
         const float r1 = rs + rs_lo;
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = v[i] * r1 * w[i];
         if constexpr (!F8) {
-            if (whole(u)) {
-                char* p = static_cast<char*>(a.y) + (row * d.ldy + col(u, 0)) * size(d.out_dtype);
-                if (d.out_dtype == GEMM_F32) {
-                    reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
-                } else {
-                    *reinterpret_cast<uint4*>(p) =
-                        make_uint4(pack16(d.out_dtype, y[0], y[1]), pack16(d.out_dtype, y[2], y[3]),
-                                   pack16(d.out_dtype, y[4], y[5]), pack16(d.out_dtype, y[6], y[7]));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (col(u, i) < s.cols) put(a.y, d.out_dtype, row * d.ldy + col(u, i), y[i]);
-            }
+            store(a.y, d.out_dtype, row * d.ldy, u, y);
         } else {
             // (every lane of the warp is here: rows of a warp end together, at rows_all)
             const int lane = threadIdx.x & 31;
@@ -357,21 +414,27 @@ __device__ __forceinline__ S shuffle_sum(S v, int lanes) {
 }
 
 // CTAs per SM that the registers are kept for: a thousand threads, fewer where a thread holds more.
-__host__ __device__ constexpr int norm_ctas(bool vec, int w, int tpr, int u) {
-    return (u == 4 || (vec && w == 8 && u > 1) ? 512 : u == 3 ? 768 : 1024) / (tpr < 128 ? 128 : tpr);
+__host__ __device__ constexpr int norm_ctas(int lay, int w, int tpr, int u) {
+    const int threads = u == 4 ? 512 : u == 3 || (lay != SINGLES && w == 8 && u == 2) ? 768 : 1024;
+    return threads / (tpr < 128 ? 128 : tpr);
 }
 
 // U = 0: the row is read twice instead of kept.
-template <bool F8, bool VEC, int W, int TPR, int U>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, U)) rms_norm_kernel(const NormArgs a, const NormShape s) {
+template <bool F8, int LAY, int W, int TPR, int U>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, U)) rms_norm_kernel(const NormArgs a, const NormShape s) {
     constexpr int THREADS = TPR < 128 ? 128 : TPR;
     constexpr int RPC = THREADS / TPR;  // rows of a CTA at a time
     constexpr int WARPS = TPR / 32;
     using S = typename std::conditional<F8, Two, float>::type;
     constexpr int LANES = WARPS <= 2 ? 2 : WARPS <= 4 ? 4 : WARPS <= 8 ? 8 : WARPS <= 16 ? 16 : 32;  // that hold their sums
+    // In mxfp8 blocks begin at column 0: a phased row's h goes through shared memory to threads that hold it as an
+    // aligned row (a word more after each 32, so that neither side's lanes, eight words apart, meet in a bank).
+    constexpr bool MOVE = F8 && LAY == PHASED;
+    constexpr int MOVE_ROW = TPR * U * 8 / 32 * 33;
+    __shared__ float moved[MOVE ? RPC * MOVE_ROW : 1];
     __shared__ S partial[2][THREADS / 32];
     const int slot = threadIdx.x / TPR;
-    const Part<F8, VEC, W, TPR> p{a, s, static_cast<int>(threadIdx.x) % TPR};
+    Part<F8, LAY, W, TPR> p{a, s, static_cast<int>(threadIdx.x) % TPR, 0};
     const gemm_norm_desc_t& d = a.d;
     int turn = 0;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * RPC; base < s.rows_all;
@@ -379,6 +442,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, 
         const int64_t row = base + slot;
         const int64_t row_in = min(row, s.rows - 1);  // rows of the padding read the last one again
         const bool live = row < s.rows;
+        if (LAY == PHASED) p.o = (s.phase + static_cast<int>(row_in & 7) * s.phase_step) & 7;
         float acc = 0.0f;
         const auto square = [&](const float (&v)[8]) {
             float q = 0.0f;
@@ -387,20 +451,26 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, 
             return q;
         };
         const auto load = [&](int u, Raw8<W>& rx, Raw8<W>& rr) {
-            if constexpr (!VEC) p.singles(row_in, u, rx, rr);
-            if (!p.whole(u)) return;
-            p.load(a.x, d.dtype, row_in * d.ldx + p.col(u, 0), rx);
-            if (a.r) p.load(a.r, d.residual_dtype, row_in * d.ldr + p.col(u, 0), rr);
+            p.load(a.x, d.dtype, row_in, d.ldx, u, rx);
+            if (a.r) p.load(a.r, d.residual_dtype, row_in, d.ldr, u, rr);
         };
         float v[U > 0 ? U : 1][8];
         if constexpr (U > 0) {
             Raw8<W> rx[U], rr[U];
+            // (all loads before the first store, which they would wait for: an output may be an input's own array)
 #pragma unroll
             for (int u = 0; u < U; ++u) load(u, rx[u], rr[u]);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 p.sum_up(row_in, u, rx[u], rr[u], v[u], a.h != nullptr && live);
                 acc += square(v[u]);
+                if constexpr (MOVE) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = (u * TPR + p.t) * 8 + i;
+                        moved[slot * MOVE_ROW + at + (at >> 5)] = v[u][i];
+                    }
+                }
             }
         } else {
             for (int u = 0; p.col(u, 0) < s.cols; ++u) {
@@ -416,10 +486,27 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, 
             if (lane == 0) partial[turn][threadIdx.x >> 5] = sum;
             __syncthreads();  // (the other buffer's readers have passed the barrier before)
             sum = broadcast(shuffle_sum(lane < WARPS ? partial[turn][slot * WARPS + lane] : S{}, LANES));
+        } else if (MOVE) {
+            __syncwarp();
         }
         float rs, rs_lo;
         factor(sum, s.inv, d.eps, rs, rs_lo);
-        if constexpr (U > 0) {
+        if constexpr (MOVE) {
+            const Part<F8, ALIGNED, W, TPR> q{a, s, p.t, 0};
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = q.col(u, i) + p.o;
+                    v[u][i] = q.in(q.col(u, i)) ? moved[slot * MOVE_ROW + at + (at >> 5)] : 0.0f;
+                }
+                q.finish(row, u, v[u], rs, rs_lo);
+            }
+            if (WARPS > 1)  // before the next row's h comes there
+                __syncthreads();
+            else
+                __syncwarp();
+        } else if constexpr (U > 0) {
             if (F8 || live) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) p.finish(row, u, v[u], rs, rs_lo);
@@ -428,18 +515,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, 
             // every lane of a warp takes as many turns, past the padding of the codes and the scales
             const int64_t end = F8 ? s.col_tiles * 128 : s.cols;
             for (int u = 0; static_cast<int64_t>(u) * TPR * 8 < end; ++u) {
+                Raw8<W> rx, rr;
                 if (a.h) {  // what this thread wrote in the first turn
-                    if (p.whole(u)) {
-                        Raw8<W> rh;
-                        p.load(a.h, d.residual_dtype, row_in * d.ldh + p.col(u, 0), rh);
-                        to_floats(d.residual_dtype, rh, v[0]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[0][i] = p.col(u, i) < s.cols ? one(a.h, d.residual_dtype, row_in * d.ldh + p.col(u, i)) : 0.0f;
-                    }
+                    p.load(a.h, d.residual_dtype, row_in, d.ldh, u, rx);
+                    p.numbers(a.h, d.residual_dtype, row_in, d.ldh, u, rx, v[0]);
                 } else {
-                    Raw8<W> rx, rr;
                     load(u, rx, rr);
                     p.sum_up(row_in, u, rx, rr, v[0], false);
                 }
@@ -449,60 +529,106 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(VEC, W, TPR, 
     }
 }
 
-template <bool F8, bool VEC, int W, int TPR, int U>
+template <bool F8, int LAY, int W, int TPR, int U>
 cudaError_t launch(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
     constexpr int THREADS = TPR < 128 ? 128 : TPR, RPC = THREADS / TPR;
     const int64_t blocks = (s.rows_all + RPC - 1) / RPC;
-    const int64_t grid = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * norm_ctas(VEC, W, TPR, U));
-    rms_norm_kernel<F8, VEC, W, TPR, U><<<static_cast<unsigned>(grid), THREADS, 0, st>>>(a, s);
+    const int64_t grid = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * norm_ctas(LAY, W, TPR, U));
+    rms_norm_kernel<F8, LAY, W, TPR, U><<<static_cast<unsigned>(grid), THREADS, 0, st>>>(a, s);
     return cudaGetLastError();
 }
 
-template <bool F8, bool VEC, int W>
-cudaError_t launch_shape(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
-    // what a row's threads hold: all of its codes' and scales' padding too
-    const int64_t cols = F8 ? (VEC ? (s.cols + 31) / 32 * 32 : s.col_tiles * 128) : s.cols;
-    const int64_t chunks = (cols + 7) / 8;
-    if (VEC && chunks <= 8) return launch<F8, VEC, W, VEC ? 8 : 32, 1>(a, s, num_sms, st);
-    if (VEC && chunks <= 16) return launch<F8, VEC, W, VEC ? 16 : 32, 1>(a, s, num_sms, st);
-    if (chunks <= 32) return launch<F8, VEC, W, 32, 1>(a, s, num_sms, st);
-    if (chunks > 2048) return launch<F8, VEC, W, 512, 0>(a, s, num_sms, st);
-    // one chunk a thread where there are few rows: latency counts
-    if (s.rows <= 2 * num_sms) {
-        if (chunks <= 64) return launch<F8, VEC, W, 64, 1>(a, s, num_sms, st);
-        if (chunks <= 128) return launch<F8, VEC, W, 128, 1>(a, s, num_sms, st);
-        if (chunks <= 256) return launch<F8, VEC, W, 256, 1>(a, s, num_sms, st);
-        if (chunks <= 512) return launch<F8, VEC, W, 512, 1>(a, s, num_sms, st);
-        if (chunks <= 768) return launch<F8, VEC, W, 768, 1>(a, s, num_sms, st);
-        if (chunks <= 1024) return launch<F8, VEC, W, 1024, 1>(a, s, num_sms, st);
-    }
-    if constexpr (!VEC) {  // single elements, eight a chunk: threads without any would cost as much
-        if (chunks > 128 && chunks <= 192) return launch<F8, VEC, W, 64, 3>(a, s, num_sms, st);
-        if (chunks > 256 && chunks <= 384) return launch<F8, VEC, W, 128, 3>(a, s, num_sms, st);
-        if (chunks > 512 && chunks <= 768) return launch<F8, VEC, W, 256, 3>(a, s, num_sms, st);
-        if (chunks > 1024 && chunks <= 1536) return launch<F8, VEC, W, 512, 3>(a, s, num_sms, st);
-    }
-    if (chunks <= 64) return launch<F8, VEC, W, 32, 2>(a, s, num_sms, st);
-    if (chunks <= 128) return launch<F8, VEC, W, 64, 2>(a, s, num_sms, st);
-    if (chunks <= 256) return launch<F8, VEC, W, 128, 2>(a, s, num_sms, st);
-    if (chunks <= 512) return launch<F8, VEC, W, 256, 2>(a, s, num_sms, st);
-    if (chunks <= 1024) return launch<F8, VEC, W, 512, 2>(a, s, num_sms, st);
-    return launch<F8, VEC, W, 512, 4>(a, s, num_sms, st);
-}
+// Phased rows go up to this many columns: what is moved fits the shared memory, or a row the registers.
+constexpr int norm_phased(bool f8) { return f8 ? 8192 - 7 : 16384 - 7; }
 
+template <bool F8, int LAY, int W>
+cudaError_t launch_shape(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
+    // what a row's threads hold: all of its codes' and scales' padding too, and the columns before a phased row's first
+    const int64_t codes = F8 ? (LAY == SINGLES ? s.col_tiles * 128 : (s.cols + 31) / 32 * 32) : 0;
+    const int64_t chunks = (std::max<int64_t>(s.cols + (LAY == PHASED ? 7 : 0), codes) + 7) / 8;
+    if constexpr (LAY == SINGLES) {
+        if (chunks <= 32) return launch<F8, LAY, W, 32, 1>(a, s, num_sms, st);
+        if (chunks <= 128) return launch<F8, LAY, W, 64, 2>(a, s, num_sms, st);
+        if (chunks <= 512) return launch<F8, LAY, W, 256, 2>(a, s, num_sms, st);
+        if (chunks <= 2048) return launch<F8, LAY, W, 512, 4>(a, s, num_sms, st);
+        return launch<F8, LAY, W, 512, 0>(a, s, num_sms, st);
+    } else {
+        if (chunks <= 8) return launch<F8, LAY, W, 8, 1>(a, s, num_sms, st);
+        if (chunks <= 16) return launch<F8, LAY, W, 16, 1>(a, s, num_sms, st);
+        if (chunks <= 32) return launch<F8, LAY, W, 32, 1>(a, s, num_sms, st);
+        if constexpr (LAY == ALIGNED) {
+            if (chunks > 2048) return launch<F8, LAY, W, 512, 0>(a, s, num_sms, st);
+            // one chunk a thread where there are few rows: latency counts
+            if (s.rows <= 2 * num_sms) {
+                if (chunks <= 64) return launch<F8, LAY, W, 64, 1>(a, s, num_sms, st);
+                if (chunks <= 128) return launch<F8, LAY, W, 128, 1>(a, s, num_sms, st);
+                if (chunks <= 256) return launch<F8, LAY, W, 256, 1>(a, s, num_sms, st);
+                if (chunks <= 512) return launch<F8, LAY, W, 512, 1>(a, s, num_sms, st);
+                if (chunks <= 768) return launch<F8, LAY, W, 768, 1>(a, s, num_sms, st);
+                if (chunks <= 1024) return launch<F8, LAY, W, 1024, 1>(a, s, num_sms, st);
+            }
+        }
+        if (chunks <= 64) return launch<F8, LAY, W, 32, 2>(a, s, num_sms, st);
+        if (chunks <= 96) return launch<F8, LAY, W, 32, 3>(a, s, num_sms, st);
+        if (chunks <= 128) return launch<F8, LAY, W, 64, 2>(a, s, num_sms, st);
+        if (chunks <= 192) return launch<F8, LAY, W, 64, 3>(a, s, num_sms, st);
+        if (chunks <= 256) return launch<F8, LAY, W, 128, 2>(a, s, num_sms, st);
+        if (chunks <= 384) return launch<F8, LAY, W, 128, 3>(a, s, num_sms, st);
+        if (chunks <= 512) return launch<F8, LAY, W, 256, 2>(a, s, num_sms, st);
+        if (chunks <= 768) return launch<F8, LAY, W, 256, 3>(a, s, num_sms, st);
+        if constexpr (F8 && LAY == PHASED)
+            return launch<F8, LAY, W, 512, 2>(a, s, num_sms, st);
+        else
+            return chunks <= 1024 ? launch<F8, LAY, W, 512, 2>(a, s, num_sms, st)
+                                  : launch<F8, LAY, W, 512, 4>(a, s, num_sms, st);
+    }
+}
 
 // norm.cu and norm8.cu
 template <bool F8>
-cudaError_t launch_norm_kind(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
+cudaError_t launch_norm_kind(const NormArgs& a, NormShape s, int num_sms, cudaStream_t st) {
     const gemm_norm_desc_t& d = a.d;
-    const auto on = [&](const void* p, int type, int64_t ld) {
-        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (d.rows <= 1 || ld * (type == GEMM_F32 ? 4 : 2) % 16 == 0);
+    const bool small = d.dtype != GEMM_F32 && d.residual_dtype != GEMM_F32;
+    // the phase: the first row's, and what a row adds, of a 16-bit array if there is one
+    int unit = 0;
+    const auto off = [](const void* p, int64_t ld, int type, int64_t& step) {
+        step = ld & 7;
+        return static_cast<int>(reinterpret_cast<uintptr_t>(p) / (type == GEMM_F32 ? 4 : 2) & 7);
     };
-    const bool vec = on(a.x, d.dtype, d.ldx) && on(a.r, d.residual_dtype, d.ldr) && on(a.h, d.residual_dtype, d.ldh) &&
-                     on(a.w, d.weight_dtype, 0) && (F8 || on(a.y, d.out_dtype, d.ldy));
-    if (!vec) return launch_shape<F8, false, 8>(a, s, num_sms, st);
-    if (d.dtype == GEMM_F32 || d.residual_dtype == GEMM_F32) return launch_shape<F8, true, 8>(a, s, num_sms, st);
-    return launch_shape<F8, true, 4>(a, s, num_sms, st);
+    struct Rows {
+        const void* p;
+        int type;
+        int64_t ld;
+    };
+    const Rows all[4] = {{a.x, d.dtype, d.ldx}, {a.r, d.residual_dtype, d.ldr}, {a.h, d.residual_dtype, d.ldh},
+                         {F8 ? nullptr : a.y, d.out_dtype, d.ldy}};
+    for (const Rows& r : all) {
+        const int n = r.type == GEMM_F32 ? 4 : 8;  // elements of 16 bytes
+        if (!r.p || n <= unit) continue;
+        unit = n;
+        int64_t step;
+        s.phase = off(r.p, r.ld, r.type, step) & (n - 1);
+        s.phase_step = d.rows > 1 ? static_cast<int>(step) & (n - 1) : 0;
+    }
+    bool phased = s.cols <= norm_phased(F8);
+    for (const Rows& r : all) {
+        if (!r.p) continue;
+        const int n = r.type == GEMM_F32 ? 4 : 8;
+        int64_t step;
+        const int first = off(r.p, r.ld, r.type, step);
+        phased = phased && ((first ^ s.phase) & (n - 1)) == 0 && (d.rows <= 1 || ((step ^ s.phase_step) & (n - 1)) == 0);
+    }
+    s.wide_weight = d.weight_dtype != GEMM_F32 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+    const bool weight = reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
+    bool aligned = weight;
+    for (const Rows& r : all)
+        aligned = aligned && reinterpret_cast<uintptr_t>(r.p) % 16 == 0 &&
+                  (!r.p || d.rows <= 1 || r.ld * (r.type == GEMM_F32 ? 4 : 2) % 16 == 0);
+    if (aligned)
+        return small ? launch_shape<F8, ALIGNED, 4>(a, s, num_sms, st) : launch_shape<F8, ALIGNED, 8>(a, s, num_sms, st);
+    if (phased && (!F8 || weight))
+        return small ? launch_shape<F8, PHASED, 4>(a, s, num_sms, st) : launch_shape<F8, PHASED, 8>(a, s, num_sms, st);
+    return small ? launch_shape<F8, SINGLES, 4>(a, s, num_sms, st) : launch_shape<F8, SINGLES, 8>(a, s, num_sms, st);
 }
 
 }  // namespace

@@ -135,6 +135,34 @@ def test_strides_and_offsets(H):
         assert bool((room_y == 7).all()) and bool((room_h == 7).all()), "store outside the rows"
 
 
+@pytest.mark.parametrize("H", [3, 9, 200, 1001, 4097, 8185, 8191, 16377, 16383])
+@pytest.mark.parametrize("lds", [(0, 0, 0, 0), (1, 9, 17, 1), (1, 2, 3, 4), (7, 3, 7, 7)])
+def test_rows_off_16_bytes(H, lds):
+    # row strides that agree modulo eight and some that do not, from an odd first element; every other row, and what
+    # lies between the rows, holds NaN, which stays where it is
+    T, r = 7, rng("off", H, lds)
+    for dtype, res, out, left in (("bf16", "bf16", "bf16", 0), ("f16", "f32", "f16", 5), ("f32", "f32", "f32", 3)):
+        def room(name, ld, fill=None):
+            flat = torch.full((left + T * (H + ld),), float("nan") if fill is None else fill, device="cuda").to(DT[name])
+            rows = torch.as_strided(flat, (T, H), (H + ld, 1), left)
+            if fill is None:
+                rows[::2] = tensor(r, name, 4, H)
+            return flat, rows
+        (_, x), (_, rs) = room(dtype, lds[0]), room(res, lds[1])
+        (fh, h), (fy, y) = room(res, lds[2], 7.0), room(out, lds[3], 7.0)
+        w = tensor(r, dtype, H)
+        g13.rms_norm(x, w, residual=rs, out=y, residual_out=h)
+        want, h64 = stream_of(x, rs)
+        assert torch.equal(h[::2], want[::2]) and bool(torch.isnan(h[1::2]).all()) and bool(torch.isnan(y[1::2]).all())
+        check_values(y[::2], h64[::2], w, 1e-6, 0.0, out)
+        q = g13.rms_norm(x, w, residual=rs, out_dtype="mxfp8")[0]
+        good = g13.rms_norm(x[::2], w, residual=rs[::2], out_dtype="mxfp8")[0]
+        assert torch.equal(q.codes[::2], good.codes)
+        check_fp8(good, h64[::2], w, 1e-6, 0.0)
+        h[:], y[:] = 7, 7
+        assert bool((fh == 7).all()) and bool((fy == 7).all()), "store outside the rows"
+
+
 @pytest.mark.parametrize("H", [96, 4096, 4097, 18000])
 def test_in_place(H):
     r = rng("place", H)
