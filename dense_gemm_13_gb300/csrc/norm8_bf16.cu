@@ -1,0 +1,10 @@
+// norm8_bf16.cu -- the norm's kernels with an output in mxfp8, rows and residual in BF16.
+#include "norm_kernel.cuh"
+
+namespace g13 {
+
+cudaError_t launch_norm8_bf16(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
+    return launch_norm_lay<true, GEMM_BF16>(a, s, num_sms, st);
+}
+
+}  // namespace g13

@@ -80,17 +80,13 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&t);
 }
 
-// How a row lies in its threads' chunks.
-enum Lay {
-    SINGLES = 0,  // element i of a chunk is i * TPR columns on
-    ALIGNED = 1,  // eight neighbours, the first chunk at column 0
-    PHASED = 2    // eight neighbours, the first chunk at column -o, 0 <= o < 8
-};
-
-// One thread's part of a row: TPR threads a row, U chunks of 8 elements each.
-template <bool F8, int LAY, int W, int TPR>
+// One thread's part of a row: TPR threads a row, U chunks of 8 elements each.  XT: the 16-bit type of x and the residual, or
+// ANY (chosen while the kernel runs, for each chunk, which the compiler turns into both conversions and a choice).
+constexpr int ANY = -1;
+template <bool F8, int LAY, int XT, int TPR>
 struct Part {
     static constexpr bool VEC = LAY != SINGLES;
+    static constexpr int W = XT == ANY ? 8 : 4;  // words that hold a chunk
     const NormArgs& a;
     const NormShape& s;
     int t;  // this thread within the row
@@ -99,6 +95,8 @@ struct Part {
     __device__ __forceinline__ int col(int u, int i) const {
         return VEC ? (u * TPR + t) * 8 + i - (LAY == PHASED ? o : 0) : (u * 8 + i) * TPR + t;
     }
+    __device__ __forceinline__ int x_type() const { return XT == ANY ? a.d.dtype : XT; }
+    __device__ __forceinline__ int r_type() const { return XT == ANY ? a.d.residual_dtype : XT; }
     __device__ __forceinline__ bool in(int c) const { return static_cast<unsigned>(c) < static_cast<unsigned>(s.cols); }
     __device__ __forceinline__ bool whole(int u) const {
         return VEC && (LAY != PHASED || col(u, 0) >= 0) && col(u, 0) + 8 <= s.cols;
@@ -203,19 +201,19 @@ struct Part {
     __device__ __forceinline__ void sum_up(int64_t row, int u, const Raw8<W>& rx, const Raw8<W>& rr, float (&v)[8],
                                            bool write) const {
         const gemm_norm_desc_t& d = a.d;
-        numbers(a.x, d.dtype, row, d.ldx, u, rx, v);
+        numbers(a.x, x_type(), row, d.ldx, u, rx, v);
         if (!a.r) return;
         float w[8];
-        numbers(a.r, d.residual_dtype, row, d.ldr, u, rr, w);
+        numbers(a.r, r_type(), row, d.ldr, u, rr, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += w[i];
-        if (W == 4 || d.residual_dtype != GEMM_F32) {
+        if (W == 4 || r_type() != GEMM_F32) {
             Raw8<W> h{};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h.v[i] = pack16(d.residual_dtype, v[2 * i], v[2 * i + 1]);
-            to_floats(d.residual_dtype, h, v);
+            for (int i = 0; i < 4; ++i) h.v[i] = pack16(r_type(), v[2 * i], v[2 * i + 1]);
+            to_floats(r_type(), h, v);
         }
-        if (write) store(a.h, d.residual_dtype, row * d.ldh, u, v);
+        if (write) store(a.h, r_type(), row * d.ldh, u, v);
     }
 
     // The weight of chunk u, its offset added.
@@ -278,11 +276,23 @@ struct Part {
         if (lo != 0.0f && fabsf(hi) < INFINITY && (bits & 1) == 0) bits += (lo < 0.0f) == (hi < 0.0f) ? 1 : -1;
         return hi == 0.0f ? hi : __int_as_float(bits);
     }
-    // Whether a number may round otherwise to three mantissa bits (or, of a block's largest, fall on the other side of
-    // 1.75) if it is off by four units in its last place.
-    static __device__ __forceinline__ bool near_tie(float y) {
-        return ((__float_as_uint(y) + 4u - 0x80000u) & 0xFFFFFu) < 8u;
+    // Whether numbers may round to another E4M3 value if they are off by four units in the last place: next to a tie of
+    // the third mantissa bit, or, below 2^-6, where E4M3's values are 2^-9 apart, of that after 2^-6 is added.
+    struct Doubt {
+        uint32_t tie = 0xFFFFFFFFu;
+        __device__ __forceinline__ void see(float y) {  // the lowest 20 bits, counted from four before a tie
+            tie = min(tie, __float_as_uint(y) * 4096u + ((4u - 0x80000u) << 12));
+        }
+        __device__ __forceinline__ void see_low(float y) {
+            if (fabsf(y) < 0.015625f) see(fabsf(y) + 0.015625f);
+        }
+        __device__ __forceinline__ bool any() const { return tie < (8u << 12); }
+    };
+    // Whether one of four E4M3 codes is below 2^-5.
+    static __device__ __forceinline__ bool low(uint32_t codes) {
+        return (((codes & 0x70707070u) + 0x7F7F7F7Fu) & 0x80808080u) != 0x80808080u;
     }
+    // Whether a block's largest may be on the other side of 1.75.
     static __device__ __forceinline__ bool near_border(uint32_t top) { return ((top + 4u - 0x600000u) & 0x7FFFFFu) < 9u; }
 
     // y of chunk u from its h: rs (+ rs_lo) is the row's factor.
@@ -305,30 +315,37 @@ struct Part {
             // Three roundings put y off by less than four units in its last place.  Where that may matter to a value of
             // the warp (one warp in a few hundred), all of its values are worked out again, exactly.
             if constexpr (VEC) {
-                uint32_t byte = 0;
+                uint32_t byte = 0, c0, c1;
                 for (bool again = false;; again = true) {
                     uint32_t top = 0;
+                    if (!whole(u)) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (col(u, i) >= s.cols) y[i] = 0.0f;  // (a factor of NaN leaves the padding zero)
-                        top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+                        for (int i = 0; i < 8; ++i) y[i] = in(col(u, i)) ? y[i] : 0.0f;  // (a factor of NaN leaves the padding zero)
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
                     byte = mxfp8_scale(top);
                     const float inv = ue8m0_value(254u - min(byte, 254u));
-                    bool near = near_border(top);
+                    Doubt doubt;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         y[i] *= inv;
-                        near = near || near_tie(y[i]);
+                        doubt.see(y[i]);
                     }
-                    if (again || !__any_sync(0xFFFFFFFFu, near)) break;
+                    c0 = e4m3x4(y), c1 = e4m3x4(y + 4);
+                    if (again) break;
+                    if (low(c0) || low(c1)) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) doubt.see_low(y[i]);
+                    }
+                    if (!__any_sync(0xFFFFFFFFu, doubt.any() || near_border(top))) break;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = to_odd(v[i], w[i], rs, rs_lo);
                 }
                 if (live && col(u, 0) < s.row_bytes)
-                    *reinterpret_cast<uint2*>(codes + col(u, 0)) = make_uint2(e4m3x4(y), e4m3x4(y + 4));
+                    *reinterpret_cast<uint2*>(codes + col(u, 0)) = make_uint2(c0, c1);
                 // (a row in the padding, and a block past the row's end: zero.)  Eight lanes have two of a
                 // tile's four scales of this row; the first lane of sixteen, or of eight, writes them
                 if (!live || col(u, 0) >= s.cols) byte = 0;
@@ -351,14 +368,17 @@ struct Part {
                         if (col(u, i) >= s.cols) y[i] = 0.0f;
                         top[i] = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(y[i]) & 0x7FFFFFFFu);
                     }
-                    bool near = false;
+                    Doubt doubt;
+                    bool border = false;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         byte[i] = mxfp8_scale(top[i]);
                         scaled[i] = y[i] * ue8m0_value(254u - min(byte[i], 254u));
-                        near = near || near_tie(scaled[i]) || near_border(top[i]);
+                        doubt.see(scaled[i]);
+                        doubt.see_low(scaled[i]);
+                        border = border || near_border(top[i]);
                     }
-                    if (again || !__any_sync(0xFFFFFFFFu, near)) break;
+                    if (again || !__any_sync(0xFFFFFFFFu, doubt.any() || border)) break;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[i] = to_odd(v[i], w[i], rs, rs_lo);
                 }
@@ -377,6 +397,60 @@ struct Part {
     }
 };
 
+// A thread's sum of squares in FP32: in one number, or (Two) in two with the roundings' errors beside it (D. E. Knuth's
+// two-sum), the even and the odd elements side by side in packed instructions: the sum is then exact but for some 2^-40 of it.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+template <bool TWO, bool EXACT>  // EXACT: the squares are (those of 16-bit numbers)
+struct Squares {
+    uint64_t hi = 0, lo = 0;
+    __device__ __forceinline__ void add(const float (&v)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint64_t x = pack2(v[i], v[i + 1]), p = fma2(x, x, 0);
+            const uint64_t s = add2(hi, p), t = sub2(s, hi), e = add2(sub2(hi, sub2(s, t)), sub2(p, t));
+            lo = add2(lo, e);
+            if (!EXACT) lo = add2(lo, fma2(x, x, p ^ 0x8000000080000000ull));
+            hi = s;
+        }
+    }
+    __device__ __forceinline__ Two sum() const;
+};
+template <bool EXACT>
+struct Squares<false, EXACT> {
+    float acc = 0.0f;
+    __device__ __forceinline__ void add(const float (&v)[8]) {
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q = fmaf(v[i], v[i], q);
+        acc += q;
+    }
+    __device__ __forceinline__ float sum() const { return acc; }
+};
+
 // A sum in two FP32 numbers (T. J. Dekker's double length addition, 1971), or in one.
 __device__ __forceinline__ Two add(Two a, Two b) {
     const float s = a.hi + b.hi, t = s - a.hi;
@@ -386,6 +460,12 @@ __device__ __forceinline__ Two add(Two a, Two b) {
     return Two{hi, fabsf(hi) < INFINITY ? e - (hi - s) : 0.0f};
 }
 __device__ __forceinline__ float add(float a, float b) { return a + b; }
+template <bool TWO, bool EXACT>
+__device__ __forceinline__ Two Squares<TWO, EXACT>::sum() const {
+    const float2 h = unpack2(hi), l = unpack2(lo);
+    // (an infinite or NaN sum has no error beside it)
+    return g13::add(Two{h.x, fabsf(h.x) < INFINITY ? l.x : 0.0f}, Two{h.y, fabsf(h.y) < INFINITY ? l.y : 0.0f});
+}
 __device__ __forceinline__ float broadcast(float v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ Two broadcast(Two v) { return Two{broadcast(v.hi), broadcast(v.lo)}; }
 __device__ __forceinline__ float from_lane(float v, int o) { return __shfl_xor_sync(0xFFFFFFFFu, v, o); }
@@ -407,6 +487,24 @@ __device__ __forceinline__ void factor(float sum, Two inv, float eps, float& rs,
     rs_lo = 0.0f;
 }
 
+// The sum over the warp of numbers >= 0 (none of them -0 or below): as integers in units of 2^-24 of the largest's binade
+// and 2^-25 of that, by integer reductions of the warp, exact but for 2^-49 of the largest (five steps of shuffles with
+// `add` are 70 instructions; these are 25).
+__device__ __forceinline__ Two warp_sum(Two v) {
+    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v.hi));
+    if (top >= 0x7F800000u) return Two{__uint_as_float(top), 0.0f};  // an infinity or a NaN
+    const uint32_t e = max(top >> 23, 25u);
+    const float scale = __uint_as_float((278u - e) << 23), unit = __uint_as_float((e - 24u) << 23);
+    const float h = v.hi * scale;  // below 2^25: 32 of them are below 2^30 (and the rests, one at most, in units of 2^-25)
+    const int i = __float2int_rn(h);
+    const int j = __float2int_rn(fmaf(v.lo, scale, h - __int2float_rn(i)) * 0x1p25f);
+    const int si = __reduce_add_sync(0xFFFFFFFFu, i), sj = __reduce_add_sync(0xFFFFFFFFu, j);
+    const float hi = __int2float_rn(si);
+    const float lo = fmaf(__int2float_rn(sj), 0x1p-25f, __int2float_rn(si - __float2int_rn(hi)));
+    const float all = hi + lo;
+    return Two{all * unit, (lo - (all - hi)) * unit};
+}
+
 template <typename S>
 __device__ __forceinline__ S shuffle_sum(S v, int lanes) {
     for (int o = lanes / 2; o > 0; o >>= 1) v = add(v, from_lane(v, o));
@@ -414,14 +512,14 @@ __device__ __forceinline__ S shuffle_sum(S v, int lanes) {
 }
 
 // CTAs per SM that the registers are kept for: a thousand threads, fewer where a thread holds more.
-__host__ __device__ constexpr int norm_ctas(int lay, int w, int tpr, int u) {
-    const int threads = u == 4 ? 512 : u == 3 || (lay != SINGLES && w == 8 && u == 2) ? 768 : 1024;
+__host__ __device__ constexpr int norm_ctas(int lay, int xt, int tpr, int u) {
+    const int threads = u == 4 ? 512 : u == 3 || (lay != SINGLES && xt == ANY && u == 2) ? 768 : 1024;
     return threads / (tpr < 128 ? 128 : tpr);
 }
 
 // U = 0: the row is read twice instead of kept.
-template <bool F8, int LAY, int W, int TPR, int U>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, U)) rms_norm_kernel(const NormArgs a, const NormShape s) {
+template <bool F8, int LAY, int XT, int TPR, int U>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, XT, TPR, U)) rms_norm_kernel(const NormArgs a, const NormShape s) {
     constexpr int THREADS = TPR < 128 ? 128 : TPR;
     constexpr int RPC = THREADS / TPR;  // rows of a CTA at a time
     constexpr int WARPS = TPR / 32;
@@ -434,7 +532,9 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, 
     __shared__ float moved[MOVE ? RPC * MOVE_ROW : 1];
     __shared__ S partial[2][THREADS / 32];
     const int slot = threadIdx.x / TPR;
-    Part<F8, LAY, W, TPR> p{a, s, static_cast<int>(threadIdx.x) % TPR, 0};
+    using P = Part<F8, LAY, XT, TPR>;
+    constexpr int W = P::W;
+    P p{a, s, static_cast<int>(threadIdx.x) % TPR, 0};
     const gemm_norm_desc_t& d = a.d;
     int turn = 0;
     for (int64_t base = static_cast<int64_t>(blockIdx.x) * RPC; base < s.rows_all;
@@ -443,16 +543,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, 
         const int64_t row_in = min(row, s.rows - 1);  // rows of the padding read the last one again
         const bool live = row < s.rows;
         if (LAY == PHASED) p.o = (s.phase + static_cast<int>(row_in & 7) * s.phase_step) & 7;
-        float acc = 0.0f;
-        const auto square = [&](const float (&v)[8]) {
-            float q = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q = fmaf(v[i], v[i], q);
-            return q;
-        };
+        Squares<F8, XT != ANY> squares;
         const auto load = [&](int u, Raw8<W>& rx, Raw8<W>& rr) {
-            p.load(a.x, d.dtype, row_in, d.ldx, u, rx);
-            if (a.r) p.load(a.r, d.residual_dtype, row_in, d.ldr, u, rr);
+            p.load(a.x, p.x_type(), row_in, d.ldx, u, rx);
+            if (a.r) p.load(a.r, p.r_type(), row_in, d.ldr, u, rr);
         };
         float v[U > 0 ? U : 1][8];
         if constexpr (U > 0) {
@@ -463,7 +557,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, 
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 p.sum_up(row_in, u, rx[u], rr[u], v[u], a.h != nullptr && live);
-                acc += square(v[u]);
+                squares.add(v[u]);
                 if constexpr (MOVE) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -477,22 +571,30 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, 
                 Raw8<W> rx, rr;
                 load(u, rx, rr);
                 p.sum_up(row_in, u, rx, rr, v[0], a.h != nullptr && live);
-                acc += square(v[0]);
+                squares.add(v[0]);
             }
         }
-        S sum = shuffle_sum(S{acc}, TPR < 32 ? TPR : 32);
+        S sum;
+        if constexpr (F8 && TPR >= 32)
+            sum = warp_sum(squares.sum());
+        else
+            sum = shuffle_sum(squares.sum(), TPR < 32 ? TPR : 32);
         if constexpr (WARPS > 1) {
             const int lane = threadIdx.x & 31;
             if (lane == 0) partial[turn][threadIdx.x >> 5] = sum;
             __syncthreads();  // (the other buffer's readers have passed the barrier before)
-            sum = broadcast(shuffle_sum(lane < WARPS ? partial[turn][slot * WARPS + lane] : S{}, LANES));
+            sum = lane < WARPS ? partial[turn][slot * WARPS + lane] : S{};
+            if constexpr (F8)
+                sum = warp_sum(sum);
+            else
+                sum = broadcast(shuffle_sum(sum, LANES));
         } else if (MOVE) {
             __syncwarp();
         }
         float rs, rs_lo;
         factor(sum, s.inv, d.eps, rs, rs_lo);
         if constexpr (MOVE) {
-            const Part<F8, ALIGNED, W, TPR> q{a, s, p.t, 0};
+            const Part<F8, ALIGNED, XT, TPR> q{a, s, p.t, 0};
 #pragma unroll
             for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -517,8 +619,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, 
             for (int u = 0; static_cast<int64_t>(u) * TPR * 8 < end; ++u) {
                 Raw8<W> rx, rr;
                 if (a.h) {  // what this thread wrote in the first turn
-                    p.load(a.h, d.residual_dtype, row_in, d.ldh, u, rx);
-                    p.numbers(a.h, d.residual_dtype, row_in, d.ldh, u, rx, v[0]);
+                    p.load(a.h, p.r_type(), row_in, d.ldh, u, rx);
+                    p.numbers(a.h, p.r_type(), row_in, d.ldh, u, rx, v[0]);
                 } else {
                     load(u, rx, rr);
                     p.sum_up(row_in, u, rx, rr, v[0], false);
@@ -529,106 +631,64 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, norm_ctas(LAY, W, TPR, 
     }
 }
 
-template <bool F8, int LAY, int W, int TPR, int U>
+template <bool F8, int LAY, int XT, int TPR, int U>
 cudaError_t launch(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
     constexpr int THREADS = TPR < 128 ? 128 : TPR, RPC = THREADS / TPR;
     const int64_t blocks = (s.rows_all + RPC - 1) / RPC;
-    const int64_t grid = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * norm_ctas(LAY, W, TPR, U));
-    rms_norm_kernel<F8, LAY, W, TPR, U><<<static_cast<unsigned>(grid), THREADS, 0, st>>>(a, s);
+    const int64_t grid = std::min<int64_t>(blocks, static_cast<int64_t>(num_sms) * norm_ctas(LAY, XT, TPR, U));
+    rms_norm_kernel<F8, LAY, XT, TPR, U><<<static_cast<unsigned>(grid), THREADS, 0, st>>>(a, s);
     return cudaGetLastError();
 }
 
-// Phased rows go up to this many columns: what is moved fits the shared memory, or a row the registers.
-constexpr int norm_phased(bool f8) { return f8 ? 8192 - 7 : 16384 - 7; }
-
-template <bool F8, int LAY, int W>
+template <bool F8, int LAY, int XT>
 cudaError_t launch_shape(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
     // what a row's threads hold: all of its codes' and scales' padding too, and the columns before a phased row's first
     const int64_t codes = F8 ? (LAY == SINGLES ? s.col_tiles * 128 : (s.cols + 31) / 32 * 32) : 0;
     const int64_t chunks = (std::max<int64_t>(s.cols + (LAY == PHASED ? 7 : 0), codes) + 7) / 8;
     if constexpr (LAY == SINGLES) {
-        if (chunks <= 32) return launch<F8, LAY, W, 32, 1>(a, s, num_sms, st);
-        if (chunks <= 128) return launch<F8, LAY, W, 64, 2>(a, s, num_sms, st);
-        if (chunks <= 512) return launch<F8, LAY, W, 256, 2>(a, s, num_sms, st);
-        if (chunks <= 2048) return launch<F8, LAY, W, 512, 4>(a, s, num_sms, st);
-        return launch<F8, LAY, W, 512, 0>(a, s, num_sms, st);
+        if (chunks <= 32) return launch<F8, LAY, XT, 32, 1>(a, s, num_sms, st);
+        if (chunks <= 128) return launch<F8, LAY, XT, 64, 2>(a, s, num_sms, st);
+        if (chunks <= 512) return launch<F8, LAY, XT, 256, 2>(a, s, num_sms, st);
+        if (chunks <= 2048) return launch<F8, LAY, XT, 512, 4>(a, s, num_sms, st);
+        return launch<F8, LAY, XT, 512, 0>(a, s, num_sms, st);
     } else {
-        if (chunks <= 8) return launch<F8, LAY, W, 8, 1>(a, s, num_sms, st);
-        if (chunks <= 16) return launch<F8, LAY, W, 16, 1>(a, s, num_sms, st);
-        if (chunks <= 32) return launch<F8, LAY, W, 32, 1>(a, s, num_sms, st);
+        if (chunks <= 8) return launch<F8, LAY, XT, 8, 1>(a, s, num_sms, st);
+        if (chunks <= 16) return launch<F8, LAY, XT, 16, 1>(a, s, num_sms, st);
+        if (chunks <= 32) return launch<F8, LAY, XT, 32, 1>(a, s, num_sms, st);
         if constexpr (LAY == ALIGNED) {
-            if (chunks > 2048) return launch<F8, LAY, W, 512, 0>(a, s, num_sms, st);
+            if (chunks > 2048) return launch<F8, LAY, XT, 512, 0>(a, s, num_sms, st);
             // one chunk a thread where there are few rows: latency counts
             if (s.rows <= 2 * num_sms) {
-                if (chunks <= 64) return launch<F8, LAY, W, 64, 1>(a, s, num_sms, st);
-                if (chunks <= 128) return launch<F8, LAY, W, 128, 1>(a, s, num_sms, st);
-                if (chunks <= 256) return launch<F8, LAY, W, 256, 1>(a, s, num_sms, st);
-                if (chunks <= 512) return launch<F8, LAY, W, 512, 1>(a, s, num_sms, st);
-                if (chunks <= 768) return launch<F8, LAY, W, 768, 1>(a, s, num_sms, st);
-                if (chunks <= 1024) return launch<F8, LAY, W, 1024, 1>(a, s, num_sms, st);
+                if (chunks <= 64) return launch<F8, LAY, XT, 64, 1>(a, s, num_sms, st);
+                if (chunks <= 128) return launch<F8, LAY, XT, 128, 1>(a, s, num_sms, st);
+                if (chunks <= 256) return launch<F8, LAY, XT, 256, 1>(a, s, num_sms, st);
+                if (chunks <= 512) return launch<F8, LAY, XT, 512, 1>(a, s, num_sms, st);
+                if (chunks <= 768) return launch<F8, LAY, XT, 768, 1>(a, s, num_sms, st);
+                if (chunks <= 1024) return launch<F8, LAY, XT, 1024, 1>(a, s, num_sms, st);
             }
         }
-        if (chunks <= 64) return launch<F8, LAY, W, 32, 2>(a, s, num_sms, st);
-        if (chunks <= 96) return launch<F8, LAY, W, 32, 3>(a, s, num_sms, st);
-        if (chunks <= 128) return launch<F8, LAY, W, 64, 2>(a, s, num_sms, st);
-        if (chunks <= 192) return launch<F8, LAY, W, 64, 3>(a, s, num_sms, st);
-        if (chunks <= 256) return launch<F8, LAY, W, 128, 2>(a, s, num_sms, st);
-        if (chunks <= 384) return launch<F8, LAY, W, 128, 3>(a, s, num_sms, st);
-        if (chunks <= 512) return launch<F8, LAY, W, 256, 2>(a, s, num_sms, st);
-        if (chunks <= 768) return launch<F8, LAY, W, 256, 3>(a, s, num_sms, st);
+        if (chunks <= 64) return launch<F8, LAY, XT, 32, 2>(a, s, num_sms, st);
+        if (chunks <= 96) return launch<F8, LAY, XT, 32, 3>(a, s, num_sms, st);
+        if (chunks <= 128) return launch<F8, LAY, XT, 64, 2>(a, s, num_sms, st);
+        if (chunks <= 192) return launch<F8, LAY, XT, 64, 3>(a, s, num_sms, st);
+        if (chunks <= 256) return launch<F8, LAY, XT, 128, 2>(a, s, num_sms, st);
+        if (chunks <= 384) return launch<F8, LAY, XT, 128, 3>(a, s, num_sms, st);
+        if (chunks <= 512) return launch<F8, LAY, XT, 256, 2>(a, s, num_sms, st);
+        if (chunks <= 768) return launch<F8, LAY, XT, 256, 3>(a, s, num_sms, st);
         if constexpr (F8 && LAY == PHASED)
-            return launch<F8, LAY, W, 512, 2>(a, s, num_sms, st);
+            return launch<F8, LAY, XT, 512, 2>(a, s, num_sms, st);
         else
-            return chunks <= 1024 ? launch<F8, LAY, W, 512, 2>(a, s, num_sms, st)
-                                  : launch<F8, LAY, W, 512, 4>(a, s, num_sms, st);
+            return chunks <= 1024 ? launch<F8, LAY, XT, 512, 2>(a, s, num_sms, st)
+                                  : launch<F8, LAY, XT, 512, 4>(a, s, num_sms, st);
     }
 }
 
-// norm.cu and norm8.cu
-template <bool F8>
-cudaError_t launch_norm_kind(const NormArgs& a, NormShape s, int num_sms, cudaStream_t st) {
-    const gemm_norm_desc_t& d = a.d;
-    const bool small = d.dtype != GEMM_F32 && d.residual_dtype != GEMM_F32;
-    // the phase: the first row's, and what a row adds, of a 16-bit array if there is one
-    int unit = 0;
-    const auto off = [](const void* p, int64_t ld, int type, int64_t& step) {
-        step = ld & 7;
-        return static_cast<int>(reinterpret_cast<uintptr_t>(p) / (type == GEMM_F32 ? 4 : 2) & 7);
-    };
-    struct Rows {
-        const void* p;
-        int type;
-        int64_t ld;
-    };
-    const Rows all[4] = {{a.x, d.dtype, d.ldx}, {a.r, d.residual_dtype, d.ldr}, {a.h, d.residual_dtype, d.ldh},
-                         {F8 ? nullptr : a.y, d.out_dtype, d.ldy}};
-    for (const Rows& r : all) {
-        const int n = r.type == GEMM_F32 ? 4 : 8;  // elements of 16 bytes
-        if (!r.p || n <= unit) continue;
-        unit = n;
-        int64_t step;
-        s.phase = off(r.p, r.ld, r.type, step) & (n - 1);
-        s.phase_step = d.rows > 1 ? static_cast<int>(step) & (n - 1) : 0;
-    }
-    bool phased = s.cols <= norm_phased(F8);
-    for (const Rows& r : all) {
-        if (!r.p) continue;
-        const int n = r.type == GEMM_F32 ? 4 : 8;
-        int64_t step;
-        const int first = off(r.p, r.ld, r.type, step);
-        phased = phased && ((first ^ s.phase) & (n - 1)) == 0 && (d.rows <= 1 || ((step ^ s.phase_step) & (n - 1)) == 0);
-    }
-    s.wide_weight = d.weight_dtype != GEMM_F32 && reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
-    const bool weight = reinterpret_cast<uintptr_t>(a.w) % 16 == 0;
-    bool aligned = weight;
-    for (const Rows& r : all)
-        aligned = aligned && reinterpret_cast<uintptr_t>(r.p) % 16 == 0 &&
-                  (!r.p || d.rows <= 1 || r.ld * (r.type == GEMM_F32 ? 4 : 2) % 16 == 0);
-    if (aligned)
-        return small ? launch_shape<F8, ALIGNED, 4>(a, s, num_sms, st) : launch_shape<F8, ALIGNED, 8>(a, s, num_sms, st);
-    if (phased && (!F8 || weight))
-        return small ? launch_shape<F8, PHASED, 4>(a, s, num_sms, st) : launch_shape<F8, PHASED, 8>(a, s, num_sms, st);
-    return small ? launch_shape<F8, SINGLES, 4>(a, s, num_sms, st) : launch_shape<F8, SINGLES, 8>(a, s, num_sms, st);
+// One of the files of kernels: rows of a 16-bit type's own, or of any types.
+template <bool F8, int XT>
+cudaError_t launch_norm_lay(const NormArgs& a, const NormShape& s, int num_sms, cudaStream_t st) {
+    if (s.lay == ALIGNED) return launch_shape<F8, ALIGNED, XT>(a, s, num_sms, st);
+    if (s.lay == PHASED) return launch_shape<F8, PHASED, XT>(a, s, num_sms, st);
+    return launch_shape<F8, SINGLES, XT>(a, s, num_sms, st);
 }
 
 }  // namespace
