@@ -22,7 +22,7 @@ SOURCES = ["capi.cpp", "dispatch.cpp", "tc_sm103.cu", "tc_any_kn.cu", "tc_any_nk
            "tc_spec_nk.cu", "tc_sk_kn.cu", "tc_sk_nk.cu", "sgemm_ffma.cu", "aux_kernels.cu",
            "skinny_tma.cu", "noalloc.cu", "fp4_quant.cu", "fp4_gemm.cu", "fp4_capi.cpp", "moe.cu",
            "moe_capi.cpp", "norm.cu", "norm_bf16.cu", "norm_f16.cu", "norm8.cu", "norm8_bf16.cu",
-           "norm8_f16.cu", "norm_capi.cpp", "w4.cu", "w4_capi.cpp", "route.cu", "route_capi.cpp"]
+           "norm8_f16.cu", "norm_capi.cpp", "w4.cu", "w4_tc.cu", "w4_capi.cpp", "route.cu", "route_capi.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -29,15 +29,13 @@
 
 #include "epilogue.cuh"
 #include "ptx.cuh"
-#include "w4.h"
+#include "w4.cuh"
 
 namespace g13 {
 namespace {
 
 constexpr int WW = 8;            // warps of a CTA
 constexpr int WT = WW * 32;
-constexpr int kMaxDevices = 64;
-constexpr int kW4Smem = 226 * 1024;  // at most, of the 227 KB that a CTA can have
 // CTAs per SM that the registers are kept for, and steps ahead of each warp.  (Of one to four CTAs and two to six steps,
 // these were the fastest, or within 3 % of it, from 1 x 6144 x 6144 to 64 x 16384 x 8192.)
 constexpr int w4_ctas(int nt) { return nt == 1 ? 3 : nt <= 4 ? 2 : 1; }
@@ -66,34 +64,6 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Loads that are made only if `on`, else v keeps what it holds.  (The predicate sits inside the assembly: behind a
-// branch the loaded values were copied where the branches meet, which waits for them there.)
-__device__ __forceinline__ void ld_codes(uint4& v, const uint8_t* p, bool on) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-                 "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-                 : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-                 : "l"(p), "r"(static_cast<int>(on)));
-}
-__device__ __forceinline__ void ld_nc32(uint32_t& v, const uint32_t* p, bool on) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
-                 : "+r"(v)
-                 : "l"(p), "r"(static_cast<int>(on)));
-}
-__device__ __forceinline__ void ld_nc16(uint32_t& v, const uint16_t* p, bool on) {  // (into a 32-bit register's low half)
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.u16 %0, [%1];\n\t}"
-                 : "+r"(v)
-                 : "l"(p), "r"(static_cast<int>(on)));
-}
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-__device__ const uint16_t kEights = 0x0808;
-
 // A step is 128 columns of 16 rows, two blocks.  As it is loaded: the codes, and of each of the NG groups that it
 // meets the scales of rows g and g + 8 (two 16-bit numbers) and their zeros (two bytes).
 template <int NG>
@@ -108,9 +78,6 @@ struct Step {
 __host__ __device__ constexpr int w4_row(int steps) { return steps * 256 + 64; }
 // The sums of a token, from one to the next (the four extra spread the lanes' writes over the banks).
 __host__ __device__ constexpr int w4_sum_row(int rows) { return rows + 4; }
-// The groups that a step meets: one, two, or four (of which some may be the same one).
-constexpr int w4_per_step(int64_t group) { return group % 128 == 0 ? 1 : group % 64 == 0 ? 2 : 4; }
-
 struct W4Plan {
     int steps_rank;      // steps of K that a CTA has
     uint32_t inv_steps;  // its reciprocal (exact below 2^16; 0: one step)
@@ -120,12 +87,6 @@ struct W4Plan {
     int xvec;            // X takes 16-byte loads
     int bf16;
 };
-// i / n by n's reciprocal.
-__device__ __forceinline__ int over(uint32_t i, uint32_t inv) { return static_cast<int>(inv ? __umulhi(i, inv) : i); }
-uint32_t reciprocal(int64_t n) {
-    return n == 1 ? 0u : static_cast<uint32_t>(((uint64_t(1) << 32) + static_cast<uint64_t>(n) - 1) / static_cast<uint64_t>(n));
-}
-
 // WK warps share a CTA's part of K.  DENSE: a group is 128 / NG columns, so that groups follow one another as the
 // steps do; else each step looks up its own.
 template <int NT, int WK, int NG, bool DENSE, int DEPTH>
@@ -406,11 +367,6 @@ int64_t w4_smem(int nt, int ng, int64_t tokens, int64_t steps_rank, int wk) {
     const int64_t tok = std::min<int64_t>(tokens, 8 * nt);
     return tok * w4_row(static_cast<int>(steps_rank)) + steps_rank * ng * 8 * nt * 8 +
            2 * wk * tok * w4_sum_row(WW / wk * 16) * 4;
-}
-// Clusters of `splits` CTAs that run at a time, with one CTA to an SM: a cluster stays within a part of the GPU, so
-// the larger ones leave SMs over (152 SMs hold 76, 36 and 15 of 2, 4 and 8).
-int64_t clusters_at_once(int splits, int num_sms) {
-    return splits == 1 ? num_sms : splits == 2 ? num_sms / 2 : splits == 4 ? num_sms / 4 - num_sms / 76 : num_sms / 10;
 }
 // CTAs that an SM holds: by the registers that the kernel is compiled for, and its 228 KB (1 KB to each CTA itself).
 int w4_per_sm(int nt, int64_t smem) { return static_cast<int>(std::min<int64_t>(w4_ctas(nt), 228 * 1024 / (smem + 1024))); }

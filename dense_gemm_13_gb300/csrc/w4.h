@@ -49,6 +49,9 @@ struct W4Config {
 W4Config w4_choose(int64_t M, int64_t N, int64_t K, int64_t group, int num_sms);
 
 cudaError_t launch_w4(const W4Config& c, const W4Args& a, int num_sms, cudaStream_t st);
+// On the tensor cores: into how many CTAs of a cluster K is divided, 0 where launch_w4 is better (or X is not aligned).
+int w4_tc_splits(const W4Args& a, int num_sms);
+cudaError_t launch_w4_tc(const W4Args& a, int splits, cudaStream_t st);
 // src: [N][ld] of `dtype`; scales of `scale_dtype`; zeros null: symmetric.
 cudaError_t launch_w4_quantize(int dtype, int scale_dtype, int64_t N, int64_t K, int64_t group, const void* src,
                                int64_t ld, uint8_t* codes, void* scales, uint8_t* zeros, cudaStream_t st);

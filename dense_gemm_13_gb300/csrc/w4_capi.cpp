@@ -139,6 +139,7 @@ int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, co
     const int64_t size = dtype_size(d.out_dtype);
     a.e.c_vec = on(Y, 4 * size) && (d.M <= 1 || d.ldy % 4 == 0);
     a.e.r_vec = on(residual, 16) && (d.M <= 1 || d.ldr % 4 == 0);
+    if (const int splits = w4_tc_splits(a, sms)) return cuda_status(launch_w4_tc(a, splits, static_cast<cudaStream_t>(stream)));
     return cuda_status(launch_w4(w4_choose(d.M, d.N, d.K, d.group, sms), a, sms, static_cast<cudaStream_t>(stream)));
 }
 
