@@ -145,16 +145,6 @@ __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 #undef G13_MMA_F4
 // One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-// A bounded wait of a whole warp: the same answer in every lane.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
-                                               unsigned* status, uint64_t timeout_ns) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, parity, abort_flag, status, timeout_ns));
-}
 // 16 or 32 consecutive columns of this thread's TMEM lane.
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(

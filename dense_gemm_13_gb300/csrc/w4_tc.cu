@@ -42,8 +42,9 @@ struct TcLayout {
     static constexpr int STAGES = TOK == 64 ? 4 : 5;
     static constexpr int STAGE_BYTES = TC_A_BYTES + TOK * 256;
     static constexpr int PITCH = TOK < 32 ? 32 : TOK;  // TMEM columns of a group's sums
-    static constexpr int COLS = 2 * NG * PITCH;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 5) * 8 + 16;
+    static constexpr int BUFS = 4 * NG * PITCH <= 512 ? 4 : 2;  // of steps' sums
+    static constexpr int COLS = BUFS * NG * PITCH;
+    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 2 * BUFS + 1) * 8 + 16;
     static_assert(COLS <= 512 && SMEM <= kW4Smem, "TMEM, shared memory");
     static_assert(TOK * TC_SUM_ROW * 4 <= STAGES * STAGE_BYTES, "the sums lie where the ring was");
 };
@@ -95,9 +96,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
     uint8_t* smem = tc_raw + ((1024 - (smem_u32(tc_raw) & 1023)) & 1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * L::STAGE_BYTES);
     uint64_t* empty = full + STAGES;
-    uint64_t* tfull = empty + STAGES;  // [2]
-    uint64_t* tempty = tfull + 2;      // [2]
-    uint64_t* drain = tempty + 2;
+    uint64_t* tfull = empty + STAGES;
+    uint64_t* tempty = tfull + L::BUFS;
+    uint64_t* drain = tempty + L::BUFS;
     uint32_t* slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* abort_flag = slot + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
             mbar_init(smem_u32(&full[s]), TC_PRODUCERS);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < L::BUFS; ++b) {
             mbar_init(smem_u32(&tfull[b]), 1);
             mbar_init(smem_u32(&tempty[b]), 4);
         }
@@ -220,26 +221,31 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
             }
         }
     } else if (warp == 12) {
-        if (lane == 0) {
-            bool ok = true;
-            int s = 0;
-            uint32_t parity = 0;
-            for (int j = 0; j < steps && ok; ++j) {
-                const int b = j & 1;
-                ok = wait(tempty[b], (j >> 1 & 1) ^ 1) && wait(full[s], parity);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sa = smem_u32(smem + s * L::STAGE_BYTES), sb = sa + TC_A_BYTES;
+        // The whole warp walks the steps, so that addresses and descriptors stay in uniform registers, and one lane issues
+        // (all of it in one lane's branch: 140 cycles to an MMA, 44 us at 16 x 16384 x 8192).
+        const bool one = elect_one();
+        const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), 16, 1024), bd0 = smem_desc_sw128(smem_u32(smem + TC_A_BYTES), 16, 1024);
+        bool ok = true;
+        int s = 0;
+        uint32_t parity = 0;
+        for (int j = 0; j < steps && ok; ++j) {
+            const int b = j % L::BUFS;
+            ok = mbar_wait_warp(smem_u32(&tempty[b]), (j / L::BUFS & 1) ^ 1, abort_flag, nullptr, TC_TIMEOUT_NS) &&
+                 mbar_wait_warp(smem_u32(&full[s]), parity, abort_flag, nullptr, TC_TIMEOUT_NS);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t ad = ad0 + static_cast<uint64_t>(s * (L::STAGE_BYTES >> 4)), bd = bd0 + static_cast<uint64_t>(s * (L::STAGE_BYTES >> 4));
+            if (one) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {  // 16 columns each
-                    const uint64_t ad = smem_desc_sw128(sa + (k >> 2) * (TC_A_BYTES / 2) + (k & 3) * 32, 16, 1024);
-                    const uint64_t bd = smem_desc_sw128(sb + (k >> 2) * (TOK * 128) + (k & 3) * 32, 16, 1024);
-                    tc_mma_f16(tmem + (b * NG + k * NG / 8) * L::PITCH, ad, bd, plan.idesc, k % (8 / NG) != 0);
-                }
+                for (int k = 0; k < 8; ++k)  // 16 columns each
+                    tc_mma_f16(tmem + (b * NG + k * NG / 8) * L::PITCH, ad + (((k >> 2) * (TC_A_BYTES / 2) + (k & 3) * 32) >> 4),
+                               bd + (((k >> 2) * (TOK * 128) + (k & 3) * 32) >> 4), plan.idesc, k % (8 / NG) != 0);
                 tc_commit(smem_u32(&empty[s]));
                 tc_commit(smem_u32(&tfull[b]));
-                if (++s == STAGES) s = 0, parity ^= 1;
             }
+            if (++s == STAGES) s = 0, parity ^= 1;
+        }
+        if (one) {
             tc_commit(smem_u32(drain));
             // (what was issued ends by itself; a bounded wait without the abort flag)
             volatile uint32_t none = 0;
@@ -267,8 +273,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
             for (int d = 0; d < TC_AHEAD; ++d) {
                 const int j = j0 + d;
                 if (!ok || j >= steps) continue;
-                const int b = d & 1;  // (TC_AHEAD is even)
-                ok = __all_sync(0xFFFFFFFFu, wait(tfull[b], j >> 1 & 1));
+                const int b = d % L::BUFS;
+                ok = __all_sync(0xFFFFFFFFu, wait(tfull[b], j / L::BUFS & 1));
                 if (!ok) continue;
                 tc_fence_after();
 #pragma unroll
@@ -380,7 +386,7 @@ cudaError_t launch_tokens(const W4Args& a, int splits, cudaStream_t st) {
 }  // namespace
 
 int w4_tc_splits(const W4Args& a, int num_sms) {
-    if (a.M <= 8 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || (a.M > 1 && a.ldx % 8 != 0)) return 0;
+    if (a.M <= 16 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || (a.M > 1 && a.ldx % 8 != 0)) return 0;
     const int64_t steps = (a.K + 127) / 128, tiles = (a.N + 127) / 128;
     if (tiles * 8 > (int64_t(1) << 31) - 1) return 0;
     int best = 1;
