@@ -472,10 +472,11 @@ int gemm_w4_dequantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, 
 
 /*
  * Y = cast( act( alpha * X.W^T + bias ) + beta * R ) for 1 to 64 tokens.  X [M][K] in the scales'
- * type.  A group's sum of x (q - z) is that of x q less z times that of x, in FP32, and so is the sum of
- * scale * group: no weight is rounded, and a result is off by some 2^-20 of sum |x| (q + z) s at most.
- * (BF16 values below 2^-27, FP16 values below 2^-24 of the largest of their 128 columns, k / 128 alike,
- * count to 2^-35 of it.  A token that holds an infinity or a NaN gives values that are not finite.)  More tokens: gemm_w4_dequantize, then gemm_run.
+ * type.  No weight is rounded: a group's sum of (q - z) x is added in FP32 and multiplied by its scale; a result
+ * is off by some 2^-19 of sum |x| (q + z) s at most before the epilogue.  Up to 16 tokens (and where rows of X do not
+ * start on 16 bytes) BF16 values below 2^-27, FP16 values below 2^-24 of the largest of their 128 columns, k / 128 alike,
+ * count to 2^-35 of it.  A token that holds an infinity or a NaN gives values that are not finite.  More tokens:
+ * gemm_w4_dequantize, then gemm_run.
  */
 typedef struct {
     gemm_dtype_t dtype;     /* X and the scales: GEMM_BF16 (default) or GEMM_F16 */
@@ -495,7 +496,8 @@ void gemm_w4_desc_init(gemm_w4_desc_t* d);
 
 /* Enqueues the product (one kernel) on `stream`.  Pointers aligned to their element type
  * (codes, scales, zeros: 16 bytes); Y overlaps no input.  Allocates nothing and needs no
- * workspace; calls may overlap.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA. */
+ * workspace; calls may overlap.  (Should a wait inside the kernel run out, after 2 s, the rows of W that were
+ * worked on give NaN.)  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA. */
 int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, const void* scales, const void* zeros,
                 void* Y, const void* bias, const void* residual, float alpha, void* stream);
 

@@ -1,12 +1,12 @@
 """4-bit weights with group scales on the GPU: layout and quantisation element for element, products against 64-bit sums.
 
-Tolerance of a product, with S = sum |x| (q + z) s of an element and u = 2^-24.  Up to eight tokens (or rows that are
+Tolerance of a product, with S = sum |x| (q + z) s of an element and u = 2^-24.  Up to sixteen tokens (or rows that are
 not aligned): a group's products q x come in two chains of at most four tensor-core steps (each adds 16 exact products, off by at
 most 2^-22 of the magnitudes so far if it truncates: 4 * 2^-22); its sum of x has at most eight additions; taking off z times
 it, joining the chains and multiplying by the scale into a running sum round once each.  More tokens: products (q - z) x, |q - z|
 <= q + z, in one chain of at most eight such steps (8 * 2^-22 = 2^-19), times the scale into the running sum.  A warp adds one such sum
 for every 32 columns of its share of K at most, then at most eight warps' and eight CTAs' sums are added; alpha rounds once.  Up
-to eight tokens activations are brought to FP16 by a power of two per 128 columns that puts the largest of them into [2^14, 2^15),
+to sixteen tokens activations are brought to FP16 by a power of two per 128 columns that puts the largest of them into [2^14, 2^15),
 half of them by a 16th more, so [2^10, 2^11); half a step of FP16's lowest range, 2^-25, is 2^-35 of that at most:
     |Y - ref| <= (2^-19 + (K / 32 + 28) u) S + 2^-35 sum_b max_b|x| sum_b (q + z) s      before the epilogue (b: 128 columns).
 GELU (erff) is off by at most 4 units of |y|; each FP32 step of the epilogue rounds its result; the cast adds half a
