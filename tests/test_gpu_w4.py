@@ -300,7 +300,8 @@ def test_empty_and_refusals():
                      ((torch.zeros(65, 100, device="cuda").bfloat16(), W), {}), ((x, W), dict(act="softmax")),
                      ((x, W), dict(out_dtype="e4m3")), ((x, W), dict(bias=f[0, :19])), ((x, W), dict(bias=f[0].bfloat16())),
                      ((x, W), dict(residual=f[:2])), ((x, W), dict(residual=f.bfloat16())), ((x, W), dict(out=f)),
-                     ((x, W), dict(out=f.bfloat16()[:2]))):
+                     ((x, W), dict(out=f.bfloat16()[:2])), ((torch.tensor(1.0, device="cuda"), W), dict(bias=f[0])),
+                     ((x, W), dict(residual=f, out=f, out_dtype="f32")), ((x, W), dict(out=x[:, :20]))):
         with pytest.raises(E):
             g13.w4_matmul(*args, **kw)
     for args in ((W.codes[:-1], W.scales, W.zeros, 20, 100, 32), (W.codes, W.scales.float(), W.zeros, 20, 100, 32),
