@@ -16,6 +16,7 @@
 #include <new>
 #include <unordered_set>
 
+#include "device.h"
 #include "dispatch.h"
 #include "gemm13.h"
 #include "internal.h"
@@ -702,8 +703,8 @@ void gemm_plan_destroy(gemm_plan_t plan) {
         std::lock_guard<std::mutex> lk(g_live_mu);
         if (!plan || !g_live.erase(plan)) return;
     }
-    if (plan->d_status) cudaFree(plan->d_status);
-    if (plan->d_ws) cudaFree(plan->d_ws);
+    free_plan_memory(plan->d_status);
+    free_plan_memory(plan->d_ws);
     plan->magic = 0;
     delete plan;
 }

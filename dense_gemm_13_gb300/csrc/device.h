@@ -1,4 +1,4 @@
-// device.h -- the current device, for calls without a plan.
+// device.h -- the current device, for calls without a plan; a plan's memory, when it goes.
 #pragma once
 #include <atomic>
 #include <cuda_runtime.h>
@@ -26,6 +26,16 @@ inline bool usable_device(int* sms, int* device = nullptr) {
     if (n < 0) return false;
     *sms = n - 1;
     return true;
+}
+
+// Frees a plan's memory.  A plan may be destroyed while this thread captures a graph (in Python, whenever the garbage
+// collector finds it), where a plain cudaFree would spoil the capture.
+inline void free_plan_memory(void* p) {
+    if (!p) return;
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    const bool changed = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
+    cudaFree(p);
+    if (changed) cudaThreadExchangeStreamCaptureMode(&mode);
 }
 
 }  // namespace g13

@@ -5,6 +5,7 @@
 #include <new>
 #include <unordered_set>
 
+#include "device.h"
 #include "dispatch.h"
 #include "fp4.cuh"
 #include "fp4_gemm.h"
@@ -218,7 +219,7 @@ void destroy(P* plan) {
         std::lock_guard<std::mutex> lk(g_live_mu);
         if (!plan || !live(plan).erase(plan)) return;
     }
-    if (plan->d_status) cudaFree(plan->d_status);
+    free_plan_memory(plan->d_status);
     delete plan;
 }
 

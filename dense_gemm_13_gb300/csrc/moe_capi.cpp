@@ -7,6 +7,7 @@
 #include <new>
 #include <unordered_set>
 
+#include "device.h"
 #include "internal.h"
 
 using namespace g13;
@@ -178,7 +179,7 @@ void gemm_moe_destroy(gemm_moe_plan_t plan) {
         std::lock_guard<std::mutex> lk(g_live_mu);
         if (!plan || !g_live.erase(plan)) return;
     }
-    if (plan->d_status) cudaFree(plan->d_status);
+    free_plan_memory(plan->d_status);
     delete plan;
 }
 

@@ -92,6 +92,23 @@ def test_tokens_through_4_bit_weights_and_experts(T):
     assert g13.gemm_kept_status() == 0
 
 
+def test_plans_that_go_during_a_capture():
+    # (as the garbage collector may have it)
+    x = randn(1, 8, 64).bfloat16()
+    y = g13.rms_norm(x)
+    plans = [g13.gemm_plan("bf16", 8, 8, 64, 64, 64, 8, g13.Epilogue(b_layout="nk")), g13.gemm_fp4_plan("mxfp4", 8, 8, 64, 8),
+             g13.gemm_fp8_plan(8, 8, 64, 8), g13.gemm_moe_plan("bf16", 8, 4, 2, 64, 64, "gelu")]
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        a = g13.rms_norm(x)
+        for p in plans:
+            p.destroy()
+        b = g13.rms_norm(a)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, y) and torch.equal(b, g13.rms_norm(y))
+
+
 def test_two_streams_at_once():
     # two requests at a time, on streams of their own
     H = 640
