@@ -18,11 +18,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgemm13.so")
-SOURCES = ["capi.cpp", "dispatch.cpp", "tc_sm103.cu", "tc_any_kn.cu", "tc_any_nk.cu", "tc_spec_kn.cu",
-           "tc_spec_nk.cu", "tc_sk_kn.cu", "tc_sk_nk.cu", "sgemm_ffma.cu", "aux_kernels.cu",
-           "skinny_tma.cu", "noalloc.cu", "fp4_quant.cu", "fp4_gemm.cu", "fp4_capi.cpp", "moe.cu",
-           "moe_capi.cpp", "norm.cu", "norm_bf16.cu", "norm_f16.cu", "norm8.cu", "norm8_bf16.cu",
-           "norm8_f16.cu", "norm_capi.cpp", "w4.cu", "w4_tc.cu", "w4_capi.cpp", "route.cu", "route_capi.cpp"]
+# (those that take longest first)
+SOURCES = ["moe.cu", "moe_given.cu", "norm8.cu", "norm8_bf16.cu", "norm8_f16.cu", "norm.cu", "norm_bf16.cu",
+           "norm_f16.cu", "w4.cu", "w4_tc.cu", "capi.cpp", "dispatch.cpp", "tc_sm103.cu", "tc_any_kn.cu",
+           "tc_any_nk.cu", "tc_spec_kn.cu", "tc_spec_nk.cu", "tc_sk_kn.cu", "tc_sk_nk.cu", "sgemm_ffma.cu",
+           "aux_kernels.cu", "skinny_tma.cu", "noalloc.cu", "fp4_quant.cu", "fp4_gemm.cu", "fp4_capi.cpp",
+           "moe_capi.cpp", "norm_capi.cpp", "w4_capi.cpp", "route.cu", "route_capi.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", INCLUDE, "-I", CSRC]
@@ -66,7 +67,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 8) as ex:
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)

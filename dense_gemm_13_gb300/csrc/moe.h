@@ -37,5 +37,6 @@ struct MoeArgs {
 
 // Routing kernel, then the experts' kernel on a cooperative grid of `grid` CTAs.
 cudaError_t launch_moe(const MoeArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_moe_given(const MoeArgs& a, int grid, cudaStream_t st);  // (of launch_moe, where given_ids is set)
 
 }  // namespace g13

@@ -1,4 +1,4 @@
-// moe.cu -- a mixture-of-experts layer for a few tokens (1 to 64):
+// moe_kernel.cuh -- a mixture-of-experts layer for a few tokens (1 to 64):
 //
 //   z = x Wr^T;  p = softmax(z) over all experts;  the top_k largest z (ties: the
 //   lowest index) with weights p, or p divided by their sum;
@@ -6,7 +6,8 @@
 //   act: GELU or ReLU of I rows, or SwiGLU: silu(gate) * up, gate = rows 0..I-1 of
 //   W1[e], up = rows I..2I-1
 //
-// or with experts and weights of each token that were chosen beforehand, instead of the first two lines.
+// or with experts and weights of each token that were chosen beforehand, instead of the first two lines (GIVEN: kernels of
+// their own; with both in one, asked for while it runs, the layer with a router took 116 us instead of 112 below).
 //
 // A few tokens leave two products per weight byte and token: reading the chosen
 // experts' weights once is the cost, so everything is laid out to keep those
@@ -53,6 +54,7 @@
 // second product, whose operands are 16-bit, as two numbers of that type, its rounding and
 // the rest.  (Rounded once, it made the output's error 1.4 times that of the output's own
 // rounding, and the layers took 112, 452 and 16 us.)
+#pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -252,7 +254,7 @@ __device__ __forceinline__ void two_parts(T* p, int64_t step, float v) {
 // everything a CTA reads is in flight at once.
 constexpr int RE = 2, RTOK = 4;
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool GIVEN>
 __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
     griddep_launch();  // the experts' kernel may take its place; it waits for this one's results
     griddep_wait();    // what came before has written its inputs, and is done with the workspace
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     const uint16_t* r = static_cast<const uint16_t*>(a.router);
     float acc[RE][RTOK] = {};
-    for (int k = a.given_ids ? H : threadIdx.x * 8; k < H; k += RT * 8) {
+    for (int k = GIVEN ? H : threadIdx.x * 8; k < H; k += RT * 8) {
         uint4 w[RE], v[RTOK];
 #pragma unroll
         for (int e = 0; e < RE; ++e) w[e] = ld_row8<VEC>(r + (e0 + e) * d.ld_router + k, e0 + e < E ? H - k : 0);
@@ -295,7 +297,7 @@ __global__ void __launch_bounds__(RT) moe_router_kernel(const MoeArgs a) {
         for (int i = 0; i < RE * RTOK; ++i) sums[warp][i] = acc[i / RTOK][i % RTOK];
     __syncthreads();
     const int e = e0 + static_cast<int>(threadIdx.x) / RTOK, t = t0 + static_cast<int>(threadIdx.x) % RTOK;
-    if (threadIdx.x < RE * RTOK && e < E && t < tok && !a.given_ids) {
+    if (threadIdx.x < RE * RTOK && e < E && t < tok && !GIVEN) {
         float z = 0.0f;
 #pragma unroll
         for (int w = 0; w < RT / 32; ++w) z += sums[w][threadIdx.x];
@@ -694,7 +696,7 @@ __device__ __noinline__ void add_big(const MoeArgs& a) {
     }
 }
 
-template <typename T, int ROWS, int NTMAX>
+template <typename T, int ROWS, int NTMAX, bool GIVEN>
 __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constant__ MoeArgs a) {
     constexpr int TILE = 16 * 8 * NTMAX;  // a warp's tile of sums
     extern __shared__ __align__(128) uint8_t moe_smem[];
@@ -712,7 +714,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
     griddep_wait();  // the router's results
     __syncthreads();
     static_assert(kMoeMaxTopK <= 32, "a lane for each pick");
-    if (a.given_ids) {
+    if constexpr (GIVEN) {
         take_given(a, s, picks, warp, kMoeWarps, tok, lane);
     } else if (E > 64) {
         for (int t = warp; t < tok; t += kMoeWarps)
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
     __syncthreads();
     for (int i = threadIdx.x; i < tok * top_k; i += MT) {
         const int t = i / top_k, e = picks.expert[i];
-        if (e < 0) continue;
+        if (GIVEN && e < 0) continue;
         const int slot = s.off[e] + __popcll(s.mask[e] & ((1ull << t) - 1ull));
         s.slot_token[slot] = static_cast<uint8_t>(t);
         s.slot_weight[slot] = picks.weight[i];
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
         }
     }
     const int A = s.n_active;
-    if (A == 0) {  // (of choices made beforehand) no token has an expert
+    if (GIVEN && A == 0) {  // (of choices made beforehand) no token has an expert
         for (int64_t i = cta * MT + static_cast<int>(threadIdx.x); i < tok * d.H; i += static_cast<int64_t>(G) * MT)
             static_cast<T*>(a.y)[i / d.H * d.ldy + i % d.H] = cast16<T>(0.0f);
         return;
@@ -1084,9 +1086,9 @@ __global__ void __launch_bounds__(MT, 1) moe_experts_kernel(const __grid_constan
 
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
-template <typename T, int ROWS, int NTMAX>
+template <typename T, int ROWS, int NTMAX, bool GIVEN>
 cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
-    auto k = moe_experts_kernel<T, ROWS, NTMAX>;
+    auto k = moe_experts_kernel<T, ROWS, NTMAX, GIVEN>;
     constexpr int smem = kMoeSmem<NTMAX>;
     static_assert(smem <= 232448, "shared memory");
     static std::atomic<unsigned char> ready[kMaxDevices];
@@ -1113,13 +1115,13 @@ cudaError_t launch_experts(const MoeArgs& a, int grid, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, k, a);
 }
 
-template <typename T, int ROWS>
+template <typename T, int ROWS, bool GIVEN>
 cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
-    const unsigned blocks = a.given_ids
+    const unsigned blocks = GIVEN
                                 ? static_cast<unsigned>(std::min<int64_t>((a.d.T * a.w.hp / 8 + RT - 1) / RT, grid))
                                 : static_cast<unsigned>((a.d.E + RE - 1) / RE * ((a.d.T + RTOK - 1) / RTOK));
     // the router's rows and x take vector loads on their own terms
-    const bool rvec = (a.given_ids || (reinterpret_cast<uintptr_t>(a.router) % 16 == 0 && a.d.ld_router % 8 == 0)) &&
+    const bool rvec = (GIVEN || (reinterpret_cast<uintptr_t>(a.router) % 16 == 0 && a.d.ld_router % 8 == 0)) &&
                       reinterpret_cast<uintptr_t>(a.x) % 16 == 0 && a.d.ldx % 8 == 0 && a.d.H % 8 == 0;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(blocks);
@@ -1130,42 +1132,27 @@ cudaError_t launch_t(const MoeArgs& a, int grid, cudaStream_t st) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t ce = cudaLaunchKernelEx(&cfg, rvec ? moe_router_kernel<T, true> : moe_router_kernel<T, false>, a);
+    cudaError_t ce = cudaLaunchKernelEx(&cfg, rvec ? moe_router_kernel<T, true, GIVEN> : moe_router_kernel<T, false, GIVEN>, a);
     if (ce != cudaSuccess) return ce;
     // groups of 8 tokens that one expert can be given: 1, 2, 4 or 8
-    if (a.d.T <= 8) return launch_experts<T, ROWS, 1>(a, grid, st);
-    if (a.d.T <= 16) return launch_experts<T, ROWS, 2>(a, grid, st);
-    if (a.d.T <= 32) return launch_experts<T, ROWS, 4>(a, grid, st);
-    return launch_experts<T, ROWS, 8>(a, grid, st);
+    if (a.d.T <= 8) return launch_experts<T, ROWS, 1, GIVEN>(a, grid, st);
+    if (a.d.T <= 16) return launch_experts<T, ROWS, 2, GIVEN>(a, grid, st);
+    if (a.d.T <= 32) return launch_experts<T, ROWS, 4, GIVEN>(a, grid, st);
+    return launch_experts<T, ROWS, 8, GIVEN>(a, grid, st);
 }
 
-}  // namespace
-
-MoeWorkspace moe_workspace(const gemm_moe_desc_t& d, int grid) {
-    MoeWorkspace w{};
-    w.hp = round_up(d.H, 64);
-    w.ip = round_up(d.I, 64);
-    w.bar = 0;
-    w.counters = 256;
-    w.logits = w.counters + round_up((d.H + kMoeBlock - 1) / kMoeBlock * 4, 256);
-    w.x = w.logits + round_up(d.T * d.E * 4, 256);
-    w.h = w.x + round_up(d.T * w.hp * 2, 256);
-    w.partial = w.h + round_up(d.T * d.top_k * (d.dtype == GEMM_F16 ? 4 : 2) * w.ip * 2, 256);
-    w.flushed = w.partial + static_cast<int64_t>(grid) * 2 * kMoeBlock * d.T * 4;
-    w.bytes = w.flushed + static_cast<int64_t>(grid) * kMoeTeams * kMoeBlock * d.T * 4;
-    return w;
-}
-
-cudaError_t launch_moe(const MoeArgs& a, int grid, cudaStream_t st) {
+template <bool GIVEN>
+cudaError_t launch_moe_kernels(const MoeArgs& a, int grid, cudaStream_t st) {
     const auto all = [&](int64_t n) {  // every row on n elements, rows a multiple of n long
         return reinterpret_cast<uintptr_t>(a.w1) % (2 * n) == 0 && reinterpret_cast<uintptr_t>(a.w2) % (2 * n) == 0 &&
                a.d.ld_w1 % n == 0 && a.d.ld_w2 % n == 0 && a.d.stride_w1 % n == 0 && a.d.stride_w2 % n == 0 &&
                a.d.H % n == 0 && a.d.I % n == 0;
     };
     const bool f16 = a.d.dtype == GEMM_F16;
-    if (all(16)) return f16 ? launch_t<__half, ROWS_32>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_32>(a, grid, st);
-    if (all(8)) return f16 ? launch_t<__half, ROWS_16>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_16>(a, grid, st);
-    return f16 ? launch_t<__half, ROWS_ANY>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_ANY>(a, grid, st);
+    if (all(16)) return f16 ? launch_t<__half, ROWS_32, GIVEN>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_32, GIVEN>(a, grid, st);
+    if (all(8)) return f16 ? launch_t<__half, ROWS_16, GIVEN>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_16, GIVEN>(a, grid, st);
+    return f16 ? launch_t<__half, ROWS_ANY, GIVEN>(a, grid, st) : launch_t<__nv_bfloat16, ROWS_ANY, GIVEN>(a, grid, st);
 }
 
+}  // namespace
 }  // namespace g13
