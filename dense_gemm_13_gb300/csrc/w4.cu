@@ -23,7 +23,7 @@
 //
 // Measured (BF16, groups of 128): 1 x 6144 x 6144 8.5 us, of which the bytes would take 2.9 and launch, staging and joins
 // take 4 to 5; 1 x 16384 x 8192 17.1 us (4.1 TB/s); 8 tokens 22.6 us, 16 tokens 31 us (groups of 64: 35), bound by the instructions that
-// stage the tokens and scale each group's sums; from 17 tokens on w4_tc.cu is faster (32 tokens: 45 us against 56 here).
+// stage the tokens and scale each group's sums; from 17 tokens on w4_tc.cu is faster (32 tokens: 34 us against 56 here).
 // Before: weights made into whole FP16 numbers first, 13.4 us at 1 x 6144 x 6144; loads behind a branch, 22 us at 1 x 16384 x
 // 8192; clusters counted as if all 76 of four CTAs fitted, 50 us at 16 tokens.
 #include <cuda_bf16.h>

@@ -4,18 +4,15 @@
 // codes into q - z, whole numbers of at most four bits and a sign and so exact in X's own type, and write them to shared memory
 // as the 128-byte-swizzled rows that tcgen05.mma reads; the tokens' values come beside them as they are (cp.async).  No
 // activation and no weight is rounded.  The scales stay out of the product: each group's sum (of a step at most) has
-// TMEM columns of its own, four warps read them, a thread to a row, and add scale * sum in FP32.
+// TMEM columns of its own, others read them, a thread to a row, and add scale * sum in FP32.
 //
-//   warps 0-3    sums: TMEM to registers, times the row's scale
-//   warps 4-11   codes and tokens to shared memory, in a ring: full[s] counts their arrivals
-//   warp 12      one lane issues the MMAs; commits free ring stages (empty[s]) and hand sums over (tfull[b])
+//   4 or 8 warps  sums: TMEM to registers, times the row's scale (32 tokens to a warp at most)
+//   16 warps      codes and tokens to shared memory, in a ring, eight to a step in turn: full[s] counts their arrivals
+//   the last      one lane issues the MMAs; commits free ring stages (empty[s]) and hand sums over (tfull[b])
 //
-// Measured (BF16, groups of 128): 64 x 16384 x 8192 46.5 us (mma.sync in w4.cu: 112), 32 tokens 44.6 (56), 16 tokens 41 (31,
-// so these stay there); 64 x 6144 x 6144 22 us (43).  The time hardly depends on the tokens: instructions bound it (2500 of a
-// warp to a step, half of them the codes'), then the tensor core's reads of the weights' rows from shared memory (some 64 bytes
-// a cycle, 75 cycles to an MMA whatever its columns).  Tried and not faster: 16 producer warps in two sets
-// (39 us at 32 tokens, but 58 at 64, where registers run out); weights in TMEM instead, tokens in the order that this wants by
-// copies of four bytes (39 us at 16 tokens, 84 at 64).
+// Measured (BF16, groups of 128): 64 x 16384 x 8192 45 us (mma.sync in w4.cu: 112), 32 tokens 34 (56), 16 tokens 30.8 (30.7, so
+// these stay there).  Instructions bound it (2500 of a warp to a step, half of them the codes'), then the tensor core's reads of
+// the rows from shared memory.  One set of producers: 45 us at 32 tokens; weights in TMEM, tokens by copies of four bytes: 84 at 64.
 //
 // A CTA has one tile, or a cluster of two to eight shares its K and adds the CTAs' sums in rank order through
 // distributed shared memory.  Every wait is bounded; after a timeout the tile's results are NaN.
@@ -32,8 +29,9 @@
 namespace g13 {
 namespace {
 
-constexpr int TC_PRODUCERS = 8, TC_THREADS = 32 * (4 + TC_PRODUCERS + 1);
-constexpr int TC_AHEAD = 4;            // steps of codes in registers
+constexpr int TC_WRITERS = 8;          // producer warps of a step, 16 rows each
+constexpr int TC_AHEAD = 4;            // steps whose codes are in registers, and tokens asked for
+constexpr int TC_SCALES = 4;           // steps of scales in registers
 constexpr int TC_A_BYTES = 128 * 256;  // 128 rows x 128 columns, two halves of 64 columns
 constexpr int TC_SUM_ROW = 128 + 4;
 constexpr uint64_t TC_TIMEOUT_NS = 2000000000ull;
@@ -46,14 +44,21 @@ struct W4TcPlan {
 
 template <int TOK, int NG>
 struct TcLayout {
-    static constexpr int STAGES = TOK == 64 ? 4 : 5;
-    static constexpr int STAGE_BYTES = TC_A_BYTES + TOK * 256;
+    static constexpr int TURNS = TOK == 64 ? 1 : 2;           // sets of producers, which take steps in turn
+    static constexpr int AHEAD = TC_AHEAD / TURNS;            // of a producer's own steps
+    static constexpr int STAGES = TOK == 64 ? 3 : 4;          // of codes
+    static constexpr int X_STAGES = STAGES + TC_AHEAD;        // of tokens: these are asked for that much earlier
+    static constexpr int X_BYTES = TOK * 256;
+    static constexpr int RING = STAGES * TC_A_BYTES + X_STAGES * X_BYTES;
+    static constexpr int WARP_TOK = TOK;  // tokens whose sums a warp has
+    static constexpr int EW = 4 * TOK / WARP_TOK;         // warps with sums
+    static constexpr int THREADS = 32 * (EW + TC_WRITERS * TURNS + 1);
     static constexpr int PITCH = TOK < 32 ? 32 : TOK;  // TMEM columns of a group's sums
     static constexpr int BUFS = 4 * NG * PITCH <= 512 ? 4 : 2;  // of steps' sums
     static constexpr int COLS = BUFS * NG * PITCH;
-    static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + (2 * STAGES + 2 * BUFS + 1) * 8 + 16;
+    static constexpr int SMEM = 1024 + RING + (2 * STAGES + 2 * BUFS + 1) * 8 + 16;
     static_assert(COLS <= 512 && SMEM <= kW4Smem, "TMEM, shared memory");
-    static_assert(TOK * TC_SUM_ROW * 4 <= STAGES * STAGE_BYTES, "the sums lie where the ring was");
+    static_assert(TOK * TC_SUM_ROW * 4 <= RING, "the sums lie where the ring was");
 };
 
 // Eight codes less their zero, columns in order, as 16-bit numbers.  FP16: 1024 + q less 1024 + z; in the second lowest
@@ -96,12 +101,13 @@ __device__ __forceinline__ uint4 numbers(uint32_t w, const Zero<BF16>& z) {
 }
 
 template <int TOK, int NG, bool BF16>
-__global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_constant__ W4Args a, const __grid_constant__ W4TcPlan plan) {
+__global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(const __grid_constant__ W4Args a, const __grid_constant__ W4TcPlan plan) {
     using L = TcLayout<TOK, NG>;
-    constexpr int STAGES = L::STAGES;
+    constexpr int TURNS = L::TURNS, AHEAD = L::AHEAD, STAGES = L::STAGES, EW = L::EW, MMA_WARP = EW + TC_WRITERS * TURNS;
     extern __shared__ uint8_t tc_raw[];
     uint8_t* smem = tc_raw + ((1024 - (smem_u32(tc_raw) & 1023)) & 1023);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * L::STAGE_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::RING);
+    uint8_t* tokens = smem + STAGES * TC_A_BYTES;
     uint64_t* empty = full + STAGES;
     uint64_t* tfull = empty + STAGES;
     uint64_t* tempty = tfull + L::BUFS;
@@ -115,18 +121,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(smem_u32(&full[s]), TC_PRODUCERS);
+            mbar_init(smem_u32(&full[s]), TC_WRITERS);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         for (int b = 0; b < L::BUFS; ++b) {
             mbar_init(smem_u32(&tfull[b]), 1);
-            mbar_init(smem_u32(&tempty[b]), 4);
+            mbar_init(smem_u32(&tempty[b]), EW);
         }
         mbar_init(smem_u32(drain), 1);
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    if (warp == 12) tmem_alloc(smem_u32(slot), L::COLS);
+    if (warp == MMA_WARP) tmem_alloc(smem_u32(slot), L::COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -142,11 +148,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
     const auto group = [&](int j, int h) {
         return min(over(static_cast<uint32_t>((first + j) * 4 + h * (4 / NG)), plan.inv), plan.groups - 1);
     };
-    float sums[TOK];  // (of warps 0-3)
+    float sums[L::WARP_TOK];  // (of the first warps)
 
-    if (warp >= 4 && warp < 12) {
+    if (warp >= EW && warp < MMA_WARP) {
         // ---- codes and tokens: a warp has 16 of the tile's rows
-        const int pw = warp - 4, tid = pw * 32 + lane, rb = tile * 8 + pw, r = lane >> 2, c = lane & 3;
+        const int pw = (warp - EW) % TC_WRITERS, turn = (warp - EW) / TC_WRITERS, tid = pw * 32 + lane, rb = tile * 8 + pw, r = lane >> 2, c = lane & 3;
         const bool live = rb < plan.tiles;
         const uint8_t* codes = a.codes + (static_cast<int64_t>(rb) * plan.blocks + first * 2) * 512 + lane * 16;
         const uint16_t* zeros = a.zeros ? reinterpret_cast<const uint16_t*>(a.zeros) + static_cast<int64_t>(rb) * plan.groups * 8 + r
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
         struct Ahead {
             uint4 lo, hi;
             uint32_t z[NG];
-        } ring[TC_AHEAD] = {};
+        } ring[AHEAD] = {};
         const auto load = [&](Ahead& b, int j) {
             const bool on = live && j < steps;
             const uint8_t* p = codes + static_cast<int64_t>(j) * 1024;
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
             for (int h = 0; h < NG; ++h) ld_nc16(b.z[h], zeros + static_cast<int64_t>(group(j, h)) * zero_step, on);
         };
 #pragma unroll
-        for (int d = 0; d < TC_AHEAD; ++d) load(ring[d], d);
+        for (int d = 0; d < AHEAD; ++d) load(ring[d], turn + d * TURNS);
         // of stage s: what this lane's words are in row r, and 8 rows on
         const uint32_t row = static_cast<uint32_t>(pw * 16 + r) * 128;
         // (lanes of odd rows write the other half first, so that eight lanes meet all banks)
@@ -178,27 +184,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&full[s]));
         };
-        bool ok = true;
-        int s = 0, done = 0;  // done: the stage that is reported next
-        uint32_t parity = 1;
-        for (int j0 = 0; ok && j0 < steps; j0 += TC_AHEAD) {
+        // the tokens of step j, into stage xs of theirs; a group of copies in any case
+        const auto fetch = [&](int j, int xs) {
+            uint8_t* stage = tokens + xs * L::X_BYTES;
+            const int64_t k = static_cast<int64_t>(first + j) * 128 + (tid & 15) * 8, left = a.K - k;
+            const int ch = tid & 15;
+            if (j < steps) {
 #pragma unroll
-            for (int d = 0; d < TC_AHEAD; ++d) {
-                const int j = j0 + d;
+                for (int i = 0; i < TOK / 16; ++i) {
+                    const int t = (tid >> 4) + i * 16;
+                    const bool on = t < a.M && left > 0;
+                    cp_async_16z(smem_u32(stage + (ch >> 3) * (TOK * 128) + t * 128 + (((ch & 7) ^ (t & 7)) * 16)),
+                                 on ? x + t * a.ldx + k : x, on ? static_cast<uint32_t>(min(left, static_cast<int64_t>(8))) * 2u : 0u);
+                }
+            }
+            cp_async_commit();
+        };
+        int xs = turn;  // the next stage of tokens to fill
+        const auto next_xs = [&] { xs = xs + TURNS >= L::X_STAGES ? xs + TURNS - L::X_STAGES : xs + TURNS; };
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            fetch(turn + d * TURNS, xs);
+            next_xs();
+        }
+        bool ok = true;
+        int s = turn;
+        uint32_t parity = 1;
+        for (int j0 = turn; ok && j0 < steps; j0 += TC_AHEAD) {
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) {
+                const int j = j0 + d * TURNS;
                 if (!ok || j >= steps) continue;
                 ok = wait(empty[s], parity);
                 if (!ok) continue;
-                uint8_t* stage = smem + s * L::STAGE_BYTES;
-                const int64_t k0 = static_cast<int64_t>(first + j) * 128;
-#pragma unroll
-                for (int i = 0; i < TOK / 16; ++i) {
-                    const int t = (tid >> 4) + i * 16, ch = tid & 15;
-                    const int64_t k = k0 + ch * 8, left = a.K - k;
-                    const bool on = t < a.M && left > 0;
-                    cp_async_16z(smem_u32(stage + TC_A_BYTES + (ch >> 3) * (TOK * 128) + t * 128 + (((ch & 7) ^ (t & 7)) * 16)),
-                                 on ? x + t * a.ldx + k : x, on ? static_cast<uint32_t>(min(left, static_cast<int64_t>(8))) * 2u : 0u);
-                }
-                cp_async_commit();
+                uint8_t* stage = smem + s * TC_A_BYTES;
                 const Ahead& b = ring[d];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {  // 64 columns each; word pairs: 32 columns, rows r and r + 8
@@ -212,28 +231,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
                     *reinterpret_cast<uint4*>(to + at1 + 1024) = numbers<BF16>(odd ? v.y : v.w, Zero<BF16>(zb >> 8 & 0xFFu));
                 }
                 load(ring[d], j + TC_AHEAD);
-                if (j >= 2) {  // the tokens of two steps ago are there
-                    cp_async_wait_group<2>();
-                    arrive(done);
-                    done = done + 1 == STAGES ? 0 : done + 1;
-                }
-                if (++s == STAGES) s = 0, parity ^= 1;
+                cp_async_wait_group<AHEAD - 1>();  // this step's tokens
+                arrive(s);
+                // (the stage of empty[s] was read by the products of step j - STAGES, and so were these tokens')
+                fetch(j + TC_AHEAD, xs);
+                next_xs();
+                s += TURNS;
+                if (s >= STAGES) s -= STAGES, parity ^= 1;
             }
         }
         cp_async_wait_all();
-        if (ok) {
-            for (int left = min(steps, 2); left > 0; --left) {
-                arrive(done);
-                done = done + 1 == STAGES ? 0 : done + 1;
-            }
-        }
-    } else if (warp == 12) {
+    } else if (warp == MMA_WARP) {
         // The whole warp walks the steps, so that addresses and descriptors stay in uniform registers, and one lane issues
         // (all of it in one lane's branch: 140 cycles to an MMA, 44 us at 16 x 16384 x 8192).
         const bool one = elect_one();
-        const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), 16, 1024), bd0 = smem_desc_sw128(smem_u32(smem + TC_A_BYTES), 16, 1024);
+        const uint64_t ad0 = smem_desc_sw128(smem_u32(smem), 16, 1024), bd0 = smem_desc_sw128(smem_u32(tokens), 16, 1024);
         bool ok = true;
-        int s = 0;
+        int s = 0, xs = 0;
         uint32_t parity = 0;
         for (int j = 0; j < steps && ok; ++j) {
             const int b = j % L::BUFS;
@@ -241,7 +255,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
                  mbar_wait_warp(smem_u32(&full[s]), parity, abort_flag, nullptr, TC_TIMEOUT_NS);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t ad = ad0 + static_cast<uint64_t>(s * (L::STAGE_BYTES >> 4)), bd = bd0 + static_cast<uint64_t>(s * (L::STAGE_BYTES >> 4));
+            const uint64_t ad = ad0 + static_cast<uint64_t>(s * (TC_A_BYTES >> 4)), bd = bd0 + static_cast<uint64_t>(xs * (L::X_BYTES >> 4));
             if (one) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // 16 columns each
@@ -251,6 +265,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
                 tc_commit(smem_u32(&tfull[b]));
             }
             if (++s == STAGES) s = 0, parity ^= 1;
+            if (++xs == L::X_STAGES) xs = 0;
         }
         if (one) {
             tc_commit(smem_u32(drain));
@@ -261,23 +276,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
         __syncwarp();
     } else {
         // ---- sums of row warp * 32 + lane
-        const int row = warp * 32 + lane, rb = tile * 8 + row / 16;
+        const int row = warp % 4 * 32 + lane, rb = tile * 8 + row / 16;
         const bool live = rb < plan.tiles;
         const uint16_t* scales = static_cast<const uint16_t*>(a.scales) + static_cast<int64_t>(rb) * plan.groups * 16 + row % 8 * 2 + row % 16 / 8;
-        uint32_t ring[TC_AHEAD][NG] = {};
+        uint32_t ring[TC_SCALES][NG] = {};
         const auto load = [&](uint32_t(&v)[NG], int j) {
 #pragma unroll
             for (int h = 0; h < NG; ++h) ld_nc16(v[h], scales + group(j, h) * 16, live && j < steps);
         };
 #pragma unroll
-        for (int i = 0; i < TOK; ++i) sums[i] = 0.0f;
+        for (int i = 0; i < L::WARP_TOK; ++i) sums[i] = 0.0f;
 #pragma unroll
-        for (int d = 0; d < TC_AHEAD; ++d) load(ring[d], d);
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        for (int d = 0; d < TC_SCALES; ++d) load(ring[d], d);
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + warp / 4 * 32;
         bool ok = true;
-        for (int j0 = 0; ok && j0 < steps; j0 += TC_AHEAD) {
+        for (int j0 = 0; ok && j0 < steps; j0 += TC_SCALES) {
 #pragma unroll
-            for (int d = 0; d < TC_AHEAD; ++d) {
+            for (int d = 0; d < TC_SCALES; ++d) {
                 const int j = j0 + d;
                 if (!ok || j >= steps) continue;
                 const int b = d % L::BUFS;
@@ -300,7 +315,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&tempty[b]));
-                load(ring[d], j + TC_AHEAD);
+                load(ring[d], j + TC_SCALES);
             }
         }
     }
@@ -311,17 +326,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
     // ---- the sums to shared memory, where the ring was, and the CTAs' shares of them added in rank order
     float* all = reinterpret_cast<float*>(smem);  // [token][row]
     const int tok = static_cast<int>(a.M);
-    if (warp < 4) {
+    if (warp < EW) {
         const bool failed = *abort_flag != 0;
+        const int t0 = warp / 4 * 32;
 #pragma unroll
-        for (int t = 0; t < TOK; ++t)
-            if (t < tok) all[t * TC_SUM_ROW + warp * 32 + lane] = failed ? __int_as_float(0x7FFFFFFF) : sums[t];
+        for (int t = 0; t < L::WARP_TOK; ++t)
+            if (t0 + t < tok) all[(t0 + t) * TC_SUM_ROW + warp % 4 * 32 + lane] = failed ? __int_as_float(0x7FFFFFFF) : sums[t];
     }
     if (ranks > 1)
         cluster_sync();
     else
         __syncthreads();
-    for (int i = static_cast<int>(rank) * TC_THREADS + threadIdx.x; i < tok * 32; i += TC_THREADS * static_cast<int>(ranks)) {
+    for (int i = static_cast<int>(rank) * L::THREADS + threadIdx.x; i < tok * 32; i += L::THREADS * static_cast<int>(ranks)) {
         const int t = i >> 5, row = (i & 31) * 4;
         const float* p = all + t * TC_SUM_ROW + row;
         float4 v = *reinterpret_cast<const float4*>(p);
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) w4_tc_kernel(const __grid_const
         epi_store4(a.e, 0, t, static_cast<int64_t>(tile) * 128 + row, v.x, v.y, v.z, v.w);
     }
     if (ranks > 1) cluster_sync();  // no CTA leaves while another reads its sums
-    if (warp == 12) tmem_dealloc(tmem, L::COLS);
+    if (warp == MMA_WARP) tmem_dealloc(tmem, L::COLS);
 }
 
 template <int TOK, int NG, bool BF16>
@@ -365,7 +381,7 @@ cudaError_t launch(const W4Args& a, int splits, cudaStream_t st) {
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(TOK >> 3) << 17) | (8u << 24);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128 * splits));
-    cfg.blockDim = dim3(TC_THREADS);
+    cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = L::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
