@@ -33,7 +33,6 @@
 #include <atomic>
 #include <type_traits>
 
-#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "w4.cuh"
 
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
                     for (int k = 0; k < 8; ++k) add(o[k]);
                 }
             }
-            epi_store4(a.e, 0, tok0 + t, static_cast<int64_t>(u) * ROWS + row, v.x, v.y, v.z, v.w);
+            w4_store4(a.e, tok0 + t, static_cast<int64_t>(u) * ROWS + row, v);
         }
     };
     for (int u = first; u < plan.units; u += stride) {

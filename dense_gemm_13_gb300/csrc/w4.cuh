@@ -2,6 +2,7 @@
 #pragma once
 #include <algorithm>
 
+#include "epilogue.cuh"
 #include "w4.h"
 
 namespace g13 {
@@ -37,6 +38,30 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 __device__ const uint16_t kEights = 0x0808;
+
+// Columns [col, col + 4) of a row's sums through the epilogue (epi_store4's, but that ReLU of a NaN is NaN: these kernels
+// have no status word, so a NaN is all that tells of a wait that ran out).
+__device__ __forceinline__ void w4_store4(const EpiParams& e, int64_t row, int64_t col, const float4& v) {
+    if (row >= e.M || col >= e.N) return;
+    float y[4] = {v.x * e.alpha, v.y * e.alpha, v.z * e.alpha, v.w * e.alpha};
+    if (e.bias) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (col + j < e.N) y[j] += __ldg(e.bias + col + j);
+    }
+    if (e.act == GEMM_ACT_RELU) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = y[j] < 0.0f ? 0.0f : y[j];
+    } else if (e.act == GEMM_ACT_GELU_ERF) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = epi_act(GEMM_ACT_GELU_ERF, y[j]);
+    }
+    EpiParams rest = e;  // the residual and the cast
+    rest.alpha = 1.0f;
+    rest.bias = nullptr;
+    rest.act = GEMM_ACT_NONE;
+    epi_store4(rest, 0, row, col, y[0], y[1], y[2], y[3]);
+}
 
 // The groups that a step meets: one, two, or four (of which some may be the same one).
 __host__ __device__ constexpr int w4_per_step(int64_t group) { return group % 128 == 0 ? 1 : group % 64 == 0 ? 2 : 4; }

@@ -22,7 +22,6 @@
 #include <algorithm>
 #include <atomic>
 
-#include "epilogue.cuh"
 #include "ptx.cuh"
 #include "w4.cuh"
 
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
                 v.w += o.w;
             }
         }
-        epi_store4(a.e, 0, t, static_cast<int64_t>(tile) * 128 + row, v.x, v.y, v.z, v.w);
+        w4_store4(a.e, t, static_cast<int64_t>(tile) * 128 + row, v);
     }
     if (ranks > 1) cluster_sync();  // no CTA leaves while another reads its sums
     if (warp == MMA_WARP) tmem_dealloc(tmem, L::COLS);

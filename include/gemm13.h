@@ -475,8 +475,8 @@ int gemm_w4_dequantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, 
  * type.  No weight is rounded: a group's sum of (q - z) x is added in FP32 and multiplied by its scale; a result
  * is off by some 2^-19 of sum |x| (q + z) s at most before the epilogue.  Up to 16 tokens (and where rows of X do not
  * start on 16 bytes) BF16 values below 2^-27, FP16 values below 2^-24 of the largest of their 128 columns, k / 128 alike,
- * count to 2^-35 of it.  A token that holds an infinity or a NaN gives values that are not finite.  More tokens:
- * gemm_w4_dequantize, then gemm_run.
+ * count to 2^-35 of it.  A token that holds an infinity or a NaN gives sums that are not finite; a NaN before the
+ * activation (any of them) is one after it.  More tokens: gemm_w4_dequantize, then gemm_run.
  */
 typedef struct {
     gemm_dtype_t dtype;     /* X and the scales: GEMM_BF16 (default) or GEMM_F16 */
@@ -485,7 +485,7 @@ typedef struct {
     int64_t N, K, group;    /* group: default 128 */
     int has_zeros;
     int has_bias;           /* FP32 [N] */
-    gemm_act_t act;         /* none, GELU or ReLU (as in gemm_run) */
+    gemm_act_t act;         /* none, GELU (as in gemm_run) or ReLU (of a NaN: NaN) */
     int has_residual;       /* FP32 [M][ldr] */
     float beta;             /* default 1 */
     int64_t ldx, ldy, ldr;  /* in elements; 0 means K, N and ldy */

@@ -1,0 +1,58 @@
+"""4-bit weights on the GPU where values leave the ordinary range: NaN and infinities behind an activation."""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_13_gb300 as g13
+from tests.test_gpu_w4 import DT, rng, weight
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from dense_gemm_13_gb300 import _build
+    _build.build()
+    g13.load()
+
+
+def rows_of(x, aligned):
+    """x with rows on 16 bytes, or off them."""
+    M, K = x.shape
+    big = torch.zeros((M, K // 8 * 8 + 24), dtype=x.dtype, device="cuda")
+    rows = big[:, :K] if aligned else big[:, 1: 1 + K]
+    rows.copy_(x)
+    return rows
+
+
+# one row, 2 to 16 (mma.sync), 17 to 64 (tcgen05, and mma.sync where rows are off 16 bytes)
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 32, 33, 64])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_activations_keep_a_nan(M, aligned, dtype):
+    N, K = 150, 600
+    r = rng("nan act", M, dtype)
+    W = weight(r, N, K, 64, dtype)[0]
+    x = torch.from_numpy(r.standard_normal((M, K)).astype(np.float32)).to(DT[dtype])
+    x[0, 7] = float("nan")
+    if M > 4:
+        x[2, 99], x[4, 599] = float("inf"), float("-inf")
+    x = rows_of(x, aligned)
+    bias = torch.zeros(N, device="cuda")
+    bias[3] = float("nan")
+    R = torch.zeros(M, N, device="cuda")
+    R[-1, 5] = float("nan")
+    for out in DT:
+        plain = g13.w4_matmul(x, W, bias=bias, out_dtype=out)
+        assert bool(plain[0].isnan().all()) and bool(plain[:, 3].isnan().all())
+        if M > 4:
+            assert not bool(torch.isfinite(plain[[2, 4]]).any())
+        relu = g13.w4_matmul(x, W, bias=bias, act="relu", out_dtype=out)
+        # (rounding keeps signs, so ReLU may come after it)
+        assert torch.equal(relu.nan_to_num(7, 8, 9), plain.clamp(min=0).nan_to_num(7, 8, 9))
+        gelu = g13.w4_matmul(x, W, bias=bias, act="gelu", out_dtype=out)
+        finite = torch.isfinite(plain)
+        assert bool(gelu[plain.isnan()].isnan().all()) and bool(torch.isfinite(gelu[finite]).all())
+        assert bool((gelu[plain == float("inf")] == float("inf")).all())
+        last = g13.w4_matmul(x, W, act="relu", residual=R, out_dtype=out)
+        assert bool(last[-1, 5].isnan()) and bool(last[0].isnan().all())
