@@ -57,27 +57,6 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-// Two FP32 values in one 64-bit register pair, for Blackwell's packed FP32
-// arithmetic (mul / fma .rn.f32x2: two IEEE operations per instruction).
-__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f2_unpack(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // GELU for the tensor-core epilogue, 0.5 y (1 + erf(y / sqrt 2)), two values
 // at a time, with erf from Abramowitz & Stegun, Handbook of Mathematical
 // Functions, formula 7.1.26 (|error| <= 1.5e-7 on erf): for x >= 0,

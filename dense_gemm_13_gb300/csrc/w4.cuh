@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "epilogue.cuh"
+#include "gelu.cuh"
 #include "w4.h"
 
 namespace g13 {
@@ -39,8 +40,9 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 }
 __device__ const uint16_t kEights = 0x0808;
 
-// Columns [col, col + 4) of a row's sums through the epilogue (epi_store4's, but that ReLU of a NaN is NaN: these kernels
-// have no status word, so a NaN is all that tells of a wait that ran out).
+// Columns [col, col + 4) of a row's sums through the epilogue (epi_store4's, but for the activations: GELU keeps its
+// digits in the left tail, and ReLU of a NaN is NaN, since these kernels have no status word and a NaN is all that tells
+// of a wait that ran out).
 __device__ __forceinline__ void w4_store4(const EpiParams& e, int64_t row, int64_t col, const float4& v) {
     if (row >= e.M || col >= e.N) return;
     float y[4] = {v.x * e.alpha, v.y * e.alpha, v.z * e.alpha, v.w * e.alpha};
@@ -53,8 +55,8 @@ __device__ __forceinline__ void w4_store4(const EpiParams& e, int64_t row, int64
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = y[j] < 0.0f ? 0.0f : y[j];
     } else if (e.act == GEMM_ACT_GELU_ERF) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = epi_act(GEMM_ACT_GELU_ERF, y[j]);
+        gelu2(y[0], y[1]);
+        gelu2(y[2], y[3]);
     }
     EpiParams rest = e;  // the residual and the cast
     rest.alpha = 1.0f;

@@ -485,7 +485,7 @@ typedef struct {
     int64_t N, K, group;    /* group: default 128 */
     int has_zeros;
     int has_bias;           /* FP32 [N] */
-    gemm_act_t act;         /* none, GELU (as in gemm_run) or ReLU (of a NaN: NaN) */
+    gemm_act_t act;         /* none, GELU (as in gemm_fp4_run) or ReLU (of a NaN: NaN) */
     int has_residual;       /* FP32 [M][ldr] */
     float beta;             /* default 1 */
     int64_t ldx, ldy, ldr;  /* in elements; 0 means K, N and ldy */

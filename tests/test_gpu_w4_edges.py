@@ -1,4 +1,5 @@
-"""4-bit weights on the GPU where values leave the ordinary range: NaN and infinities behind an activation."""
+"""4-bit weights on the GPU where values leave the ordinary range: NaN and infinities behind an activation, GELU's
+left tail."""
 import numpy as np
 import pytest
 import torch
@@ -56,3 +57,30 @@ def test_activations_keep_a_nan(M, aligned, dtype):
         assert bool((gelu[plain == float("inf")] == float("inf")).all())
         last = g13.w4_matmul(x, W, act="relu", residual=R, out_dtype=out)
         assert bool(last[-1, 5].isnan()) and bool(last[0].isnan().all())
+
+
+@pytest.mark.parametrize("M", [1, 16, 17, 64])
+@pytest.mark.parametrize("out", list(DT))
+def test_gelu_keeps_its_digits(M, out):
+    # a grid of values through the bias, the product zero; the bound is that of test_gpu_fp4_gelu.py, whose GELU this is
+    from scipy.special import erfc
+    N = 20001
+    y = np.linspace(-8, 8, N).astype(np.float32)
+    y[: N // 4] = -np.geomspace(1e-6, 12, N // 4)
+    W = weight(rng("gelu"), N, 64, 64, "bf16")[0]
+    x = torch.zeros(M, 64, dtype=torch.bfloat16, device="cuda")
+    got = g13.w4_matmul(x, W, bias=torch.from_numpy(y).cuda(), act="gelu", out_dtype=out)
+    assert torch.equal(got, got[:1].expand(M, N))
+    y = y.astype(np.float64)
+    z, u = np.abs(y), 2.0 ** -24
+    tail = z * erfc(z / np.sqrt(2)) / 2
+    want = np.maximum(y, 0) - tail
+    tol = u * np.abs(want) + (20 + 1.5 * z * z) * u * tail + 2.0 ** -120
+    f = torch.finfo(DT[out])
+    tol += f.eps / 2 * (np.abs(want) + tol) + (f.smallest_normal * f.eps / 2 if out == "f16" else 0)
+    err = np.abs(got[0].double().cpu().numpy() - want)
+    assert (err <= tol).all(), f"max err/tol {np.max(err / tol):.3g} at {y[np.argmax(err / tol)]}"
+    ends = torch.tensor([float("inf"), float("-inf"), float("nan"), 0.0, 3e38, -3e38, 40.0, -40.0])
+    got = g13.w4_matmul(x, weight(rng("ends"), 8, 64, 64, "bf16")[0], bias=ends.cuda(), act="gelu", out_dtype="f32").cpu()
+    want = torch.tensor([float("inf"), 0.0, float("nan"), 0.0, 3e38, 0.0, 40.0, 0.0])
+    assert torch.allclose(got, want.expand(M, 8), rtol=2.0 ** -22, atol=2.0 ** -126, equal_nan=True)
