@@ -502,12 +502,20 @@ __global__ void __launch_bounds__(RW * 32, PER == 16 ? 2 : 3) route_kernel(const
         }
         if (unsure) id = choose64(a, t, shared[warp], lane);
         // the weights
-        float w = 0.0f;
+        float v = 0.0f, w = 0.0f;
         if (lane < top_k) {
-            const float v = logit(a, t, id);
+            v = logit(a, t, id);
             w = softmax ? expf(v - top) / sum : 1.0f / (1.0f + expf(-v));
         }
         if (d.normalize) {
+            // Scores that FP32 holds badly or not at all (e^-87 is 2^-126) still have ratios: in units of e^most, most the
+            // largest chosen logit (with sigmoid scores, if that is below 0)
+            if (__any_sync(ALL, lane < top_k && (softmax ? v - top : v) < -80.0f)) {
+                float most = number(__reduce_max_sync(ALL, lane < top_k ? ordered(v) : NONE));
+                if (!softmax) most = fminf(most, 0.0f);  // (of a NaN: 0)
+                if (lane < top_k && (softmax || v < 0.0f))
+                    w = softmax ? (sum == sum ? expf(v - most) : sum) : expf(v - most) / (1.0f + expf(v));
+            }
             float all = w;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(ALL, all, o);
