@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
 #pragma unroll
             for (int l = 0; l < 16; ++l) {
                 top = fmaxf(top, fabsf(f[l]));  // (a NaN does not count)
-                sum += f[l];
+                sum = fmaf(f[l], 0x1p-8f, sum);  // (the plain sum of 128 columns may lie beyond FP32)
             }
             if (top == INFINITY) {  // nor does an infinity
                 top = 0.0f;
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
             for (int o = 1; o < 8 / NG; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
             if (piece % (8 / NG) == 0) {  // (times 2^-24, like the products)
                 float* q = pairs + ((j * NG + piece / (8 / NG)) * (TOK / 2) + t / 2) * 4 + t % 2;
-                q[0] = sum * (up * 0x1p-24f);
+                q[0] = sum * (up * 0x1p-16f);
                 q[2] = down;
             }
         }

@@ -1,11 +1,12 @@
 """4-bit weights on the GPU where values leave the ordinary range: NaN and infinities behind an activation, GELU's
-left tail."""
+left tail, activations near the top of BF16's range.  The bound of a product is that of test_gpu_w4.py."""
 import numpy as np
 import pytest
 import torch
 
 import dense_gemm_13_gb300 as g13
-from tests.test_gpu_w4 import DT, rng, weight
+from tests import blocks_ref as ref
+from tests.test_gpu_w4 import DT, check_product, rng, weight
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,31 @@ def test_gelu_keeps_its_digits(M, out):
     got = g13.w4_matmul(x, weight(rng("ends"), 8, 64, 64, "bf16")[0], bias=ends.cuda(), act="gelu", out_dtype="f32").cpu()
     want = torch.tensor([float("inf"), 0.0, float("nan"), 0.0, 3e38, 0.0, 40.0, 0.0])
     assert torch.allclose(got, want.expand(M, 8), rtol=2.0 ** -22, atol=2.0 ** -126, equal_nan=True)
+
+
+def given(q, s, z, group, dtype="bf16"):
+    """A weight of these codes, scales and zeros, as test_gpu_w4.weight gives it."""
+    s = torch.from_numpy(s.astype(np.float32)).to(DT[dtype])
+    W = g13.w4_pack(torch.from_numpy(q).cuda(), s.cuda(), None if z is None else torch.from_numpy(z).cuda(), group)
+    s64 = s.double().numpy()
+    z64 = np.full(s64.shape, 8.0) if z is None else z
+    return W, (ref.w4_values(q, s64, z, group), ref.w4_values(q, s64, -z64.astype(float), group))
+
+
+@pytest.mark.parametrize("M", [1, 7, 16])
+@pytest.mark.parametrize("group", [32, 64, 128, 192])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_activations_near_the_top_of_the_range(M, group, aligned):
+    # neighbours whose plain sum is beyond FP32, under scales that bring the products back
+    N, K = 100, 700
+    r = rng("top", M, group)
+    G = -(-K // group)
+    q = r.integers(0, 16, (N, K)).astype(np.uint8)
+    s = 2.0 ** -20 * (1 + r.random((N, G)))
+    x = r.standard_normal((M, K)).astype(np.float32) * 1e37
+    x[:, 5:9] = 3.0e38
+    x[-1] = -np.abs(x[-1])
+    x = rows_of(torch.from_numpy(x).bfloat16(), aligned)
+    for z in (None, np.zeros((N, G), np.uint8), r.integers(0, 16, (N, G)).astype(np.uint8)):
+        W, w = given(q, s, z, group)
+        check_product(g13.w4_matmul(x, W, out_dtype="f32"), x, w, "f32")
