@@ -225,11 +225,12 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
 #pragma unroll
                 for (int l = 0; l < 16; ++l) top = fabsf(f[l]) < INFINITY ? fmaxf(top, fabsf(f[l])) : top;
             }
-            // the largest magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^E
+            // the largest magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^(E - 2) (a group's
+            // sum of 128 values below 2^15 and codes up to 15, times 2^-24, is below 2^2)
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
             const uint32_t biased = max(__float_as_uint(top) >> 23, 28u);  // (2^(14 - E) stays a normal number)
-            const float up = __uint_as_float((127u + 14u + 127u - biased) << 23), down = __uint_as_float(biased << 23);
+            const float up = __uint_as_float((127u + 14u + 127u - biased) << 23), down = __uint_as_float((biased - 2u) << 23);
 #pragma unroll
             for (int l = 0; l < 8; ++l) {  // the pairs 1 and 3 of eight columns meet nibbles that count 16 times
                 const float m = l % 2 ? up * 0.0625f : up;
@@ -292,9 +293,12 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
                                                                       (d * WK * NG + gr) * (TOK * 2) + n * 16);
                     const float e[4] = {fmaf(-z0, m.x, d0[n][0]), fmaf(-z0, m.y, d0[n][1]), fmaf(-z1, m.x, d0[n][2]),
                                         fmaf(-z1, m.y, d0[n][3])};
-                    const float f[4] = {s.x * m.z, s.x * m.w, s.y * m.z, s.y * m.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(f[i], e[i], acc[n][i]);
+                    // (times the power first, which leaves the sum below FP32's largest; the power and a scale of
+                    // another group of the step may not have a product)
+                    acc[n][0] = fmaf(s.x, e[0] * m.z, acc[n][0]);
+                    acc[n][1] = fmaf(s.x, e[1] * m.w, acc[n][1]);
+                    acc[n][2] = fmaf(s.y, e[2] * m.z, acc[n][2]);
+                    acc[n][3] = fmaf(s.y, e[3] * m.w, acc[n][3]);
                 }
             }
         }
@@ -315,9 +319,9 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
             for (int c = 0; c < 2; ++c) {
                 const int t = n * 8 + t4 * 2 + c;
                 if (t >= tok) continue;
-                // (2^24, of which the powers of two hold 2^14)
-                mine[t * SUM_ROW] = acc[n][c] * 0x1p10f;
-                mine[t * SUM_ROW + 8] = acc[n][2 + c] * 0x1p10f;
+                // (2^24, of which the powers of two hold 2^12)
+                mine[t * SUM_ROW] = acc[n][c] * 0x1p12f;
+                mine[t * SUM_ROW + 8] = acc[n][2 + c] * 0x1p12f;
             }
         if (ranks > 1)
             cluster_sync();

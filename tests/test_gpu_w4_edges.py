@@ -113,3 +113,30 @@ def test_activations_near_the_top_of_the_range(M, group, aligned):
     for z in (None, np.zeros((N, G), np.uint8), r.integers(0, 16, (N, G)).astype(np.uint8)):
         W, w = given(q, s, z, group)
         check_product(g13.w4_matmul(x, W, out_dtype="f32"), x, w, "f32")
+
+
+@pytest.mark.parametrize("M", [1, 7, 16])
+@pytest.mark.parametrize("group", [32, 64, 96])
+def test_a_large_scale_beside_large_activations(M, group):
+    # 128 columns with a group of large activations and small scales, and one of small activations and scales
+    # above one: the product of the largest activation and the largest scale is beyond FP32, no result is
+    N, K = 50, 384
+    r = rng("beside", M, group)
+    G = -(-K // group)
+    q = r.integers(0, 16, (N, K)).astype(np.uint8)
+    z = r.integers(1, 16, (N, G)).astype(np.uint8)
+    s, x = np.full((N, G), 2.0 ** -40), np.full((M, K), 2.0 ** 126)
+    s[:, 1::2] = 2.0 ** r.integers(3, 20, (N, G // 2))
+    for c in range(1, G, 2):
+        x[:, c * group: (c + 1) * group] = r.standard_normal((M, len(range(c * group, min(K, (c + 1) * group)))))
+    x *= np.where(r.random((M, K)) < 0.5, -1, 1)
+    W, w = given(q, s, z, group)
+    x = torch.from_numpy(x.astype(np.float32)).bfloat16().cuda()
+    check_product(g13.w4_matmul(x, W, out_dtype="f32"), x, w, "f32")
+    # weights of zero under a large scale, on large activations
+    q[:] = np.repeat(z, group, 1)[:, :K]
+    W, w = given(q, np.full((N, G), 64.0), z, group)
+    x = torch.full((M, K), 3e38, device="cuda").bfloat16()
+    y = g13.w4_matmul(x, W, out_dtype="f32")
+    assert bool(torch.isfinite(y).all())
+    check_product(y, x, w, "f32")
