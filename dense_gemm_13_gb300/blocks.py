@@ -34,7 +34,8 @@ class _W4Desc(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("M", ctypes.c_int64), ("N", ctypes.c_int64),
                 ("K", ctypes.c_int64), ("group", ctypes.c_int64), ("has_zeros", ctypes.c_int),
                 ("has_bias", ctypes.c_int), ("act", ctypes.c_int), ("has_residual", ctypes.c_int),
-                ("beta", ctypes.c_float), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64)]
+                ("beta", ctypes.c_float), ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("flags", ctypes.c_uint32), ("timeout_ms", ctypes.c_uint32)]
 
 
 class _RouteDesc(ctypes.Structure):

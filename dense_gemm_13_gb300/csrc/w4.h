@@ -40,6 +40,8 @@ struct W4Args {
     const void* scales;
     const uint8_t* zeros;  // or null: 8
     EpiParams e;
+    uint64_t timeout_ns;  // of the waits inside a kernel
+    uint32_t flags;
 };
 
 // How a product is cut: 8 * nt tokens a pass, `splits` CTAs of a cluster to K, `wk` of a CTA's warps to its part of K.

@@ -93,7 +93,7 @@ int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, co
     if (d.act != GEMM_ACT_NONE && d.act != GEMM_ACT_GELU_ERF && d.act != GEMM_ACT_RELU)
         return d.act == GEMM_ACT_SOFTMAX ? GEMM_ERR_UNSUPPORTED : GEMM_ERR_INVALID_ARG;
     if ((d.has_zeros != 0 && d.has_zeros != 1) || (d.has_bias != 0 && d.has_bias != 1) ||
-        (d.has_residual != 0 && d.has_residual != 1) || d.M < 0)
+        (d.has_residual != 0 && d.has_residual != 1) || d.M < 0 || (d.flags & ~GEMM_FLAG_TEST_STALL))
         return GEMM_ERR_INVALID_ARG;
     const int rc = check_weight(d.N, d.K, d.group);
     if (rc != GEMM_OK) return rc;
@@ -135,6 +135,8 @@ int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, co
     a.e.beta = d.beta;
     a.e.out_dtype = d.out_dtype;
     a.e.act = d.act;
+    a.timeout_ns = (d.timeout_ms ? d.timeout_ms : 2000u) * uint64_t(1000000);
+    a.flags = d.flags;
     // four neighbouring columns as one access
     const int64_t size = dtype_size(d.out_dtype);
     a.e.c_vec = on(Y, 4 * size) && (d.M <= 1 || d.ldy % 4 == 0);

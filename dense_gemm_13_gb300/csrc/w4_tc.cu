@@ -33,12 +33,14 @@ constexpr int TC_AHEAD = 4;            // steps whose codes are in registers, an
 constexpr int TC_SCALES = 4;           // steps of scales in registers
 constexpr int TC_A_BYTES = 128 * 256;  // 128 rows x 128 columns, two halves of 64 columns
 constexpr int TC_SUM_ROW = 128 + 4;
-constexpr uint64_t TC_TIMEOUT_NS = 2000000000ull;
+constexpr uint64_t TC_DRAIN_NS = 2000000000ull;  // what was issued is waited for this long at most
 
 struct W4TcPlan {
     int steps, blocks, tiles, groups;  // tiles: blocks of 16 rows
     uint32_t inv;                      // reciprocal of group / 32
     uint32_t idesc;
+    uint64_t timeout_ns;               // of each wait
+    uint32_t flags;
 };
 
 template <int TOK, int NG>
@@ -140,8 +142,9 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
     const int tile = static_cast<int>(blockIdx.x / ranks);
     const int first = static_cast<int>(static_cast<uint32_t>(plan.steps) * rank / ranks);
     const int steps = static_cast<int>(static_cast<uint32_t>(plan.steps) * (rank + 1) / ranks) - first;
+    // A whole warp's wait: the same answer in every lane, so that none goes on alone.
     const auto wait = [&](uint64_t& bar, uint32_t parity) {
-        return mbar_wait_bounded(smem_u32(&bar), parity, abort_flag, nullptr, TC_TIMEOUT_NS);
+        return mbar_wait_warp(smem_u32(&bar), parity, abort_flag, nullptr, plan.timeout_ns);
     };
     // the group of piece h (of NG) of step j
     const auto group = [&](int j, int h) {
@@ -209,13 +212,18 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
         bool ok = true;
         int s = turn;
         uint32_t parity = 1;
-        for (int j0 = turn; ok && j0 < steps; j0 += TC_AHEAD) {
+        for (int j0 = turn; j0 < steps; j0 += TC_AHEAD) {
 #pragma unroll
             for (int d = 0; d < AHEAD; ++d) {
                 const int j = j0 + d * TURNS;
-                if (!ok || j >= steps) continue;
-                ok = wait(empty[s], parity);
-                if (!ok) continue;
+                if (j >= steps) continue;
+                // Lanes wait one by one (a vote on the answers costs up to 4 %, 64 x 16384 x 8192).  One whose wait ran out
+                // does no more, but meets the others, which may be in arrive, once a step to the end.
+                if (ok) ok = mbar_wait_bounded(smem_u32(&empty[s]), parity, abort_flag, nullptr, plan.timeout_ns);
+                if (!ok) {
+                    __syncwarp();
+                    continue;
+                }
                 uint8_t* stage = smem + s * TC_A_BYTES;
                 const Ahead& b = ring[d];
 #pragma unroll
@@ -248,10 +256,10 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
         bool ok = true;
         int s = 0, xs = 0;
         uint32_t parity = 0;
-        for (int j = 0; j < steps && ok; ++j) {
+        const int issued = (plan.flags & GEMM_FLAG_TEST_STALL) && blockIdx.x == 0 ? 0 : steps;
+        for (int j = 0; j < issued && ok; ++j) {
             const int b = j % L::BUFS;
-            ok = mbar_wait_warp(smem_u32(&tempty[b]), (j / L::BUFS & 1) ^ 1, abort_flag, nullptr, TC_TIMEOUT_NS) &&
-                 mbar_wait_warp(smem_u32(&full[s]), parity, abort_flag, nullptr, TC_TIMEOUT_NS);
+            ok = wait(tempty[b], (j / L::BUFS & 1) ^ 1) && wait(full[s], parity);
             if (!ok) break;
             tc_fence_after();
             const uint64_t ad = ad0 + static_cast<uint64_t>(s * (TC_A_BYTES >> 4)), bd = bd0 + static_cast<uint64_t>(xs * (L::X_BYTES >> 4));
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
             tc_commit(smem_u32(drain));
             // (what was issued ends by itself; a bounded wait without the abort flag)
             volatile uint32_t none = 0;
-            mbar_wait_bounded(smem_u32(drain), 0, &none, nullptr, TC_TIMEOUT_NS);
+            mbar_wait_bounded(smem_u32(drain), 0, &none, nullptr, TC_DRAIN_NS);
         }
         __syncwarp();
     } else {
@@ -295,7 +303,7 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
                 const int j = j0 + d;
                 if (!ok || j >= steps) continue;
                 const int b = d % L::BUFS;
-                ok = __all_sync(0xFFFFFFFFu, wait(tfull[b], j / L::BUFS & 1));
+                ok = wait(tfull[b], j / L::BUFS & 1);
                 if (!ok) continue;
                 tc_fence_after();
 #pragma unroll
@@ -375,6 +383,8 @@ cudaError_t launch(const W4Args& a, int splits, cudaStream_t st) {
     p.tiles = static_cast<int>(w4_tiles(a.N));
     p.groups = static_cast<int>(w4_groups(a.K, a.group));
     p.inv = reciprocal(a.group / 32);
+    p.timeout_ns = a.timeout_ns;
+    p.flags = a.flags;
     // kind::f16: FP32 sums, both operands of X's type and K-major, TOK columns, 128 rows
     const uint32_t type = BF16 ? 1u : 0u;
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | (static_cast<uint32_t>(TOK >> 3) << 17) | (8u << 24);

@@ -490,6 +490,8 @@ typedef struct {
     int has_residual;       /* FP32 [M][ldr] */
     float beta;             /* default 1 */
     int64_t ldx, ldy, ldr;  /* in elements; 0 means K, N and ldy */
+    uint32_t flags;         /* GEMM_FLAG_TEST_STALL, or 0 */
+    uint32_t timeout_ms;    /* bound on each wait inside the kernel; 0 means 2000 ms */
 } gemm_w4_desc_t;
 
 /* Fills *d with the defaults listed above (0 elsewhere). */
@@ -497,8 +499,8 @@ void gemm_w4_desc_init(gemm_w4_desc_t* d);
 
 /* Enqueues the product (one kernel) on `stream`.  Pointers aligned to their element type
  * (codes, scales, zeros: 16 bytes); Y overlaps no input.  Allocates nothing and needs no
- * workspace; calls may overlap.  (Should a wait inside the kernel run out, after 2 s, the rows of W that were
- * worked on give NaN.)  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA. */
+ * workspace; calls may overlap.  (Should a wait inside the kernel run out, the tile of 128 rows of W that was
+ * worked on gives NaN for all tokens, with any activation.)  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED, NO_DEVICE, CUDA. */
 int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, const void* scales, const void* zeros,
                 void* Y, const void* bias, const void* residual, float alpha, void* stream);
 

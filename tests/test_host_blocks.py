@@ -283,3 +283,13 @@ def test_ref_route():
     assert list(ids[0]) == [1, 0] and abs(w.sum() - 2) < 1e-12
     ids, _ = ref.route(z, 2, scores="sigmoid", groups=3, top_groups=1, group_score="top2")
     assert list(ids[0]) == [2, 3]
+
+
+def test_w4_run_flags(lib):
+    # the test flag only
+    for flags in (1, g13.FLAG_TEST_STALL_PEER, g13.FLAG_TEST_STALL | 2):
+        assert w4(lib, flags=flags) == INVALID
+    d = blocks._W4Desc(flags=7, timeout_ms=7)
+    lib.gemm_w4_desc_init(ctypes.byref(d))
+    assert (d.flags, d.timeout_ms) == (0, 0)
+    assert w4(lib, flags=g13.FLAG_TEST_STALL, timeout_ms=5, M=0) == OK
