@@ -91,6 +91,10 @@ def _bytes_overlap(a, b) -> bool:
     return p < qe and q < pe
 
 
+def _overlaps(out, *inputs) -> bool:
+    return any(a is not None and _bytes_overlap(out, a) for a in inputs)
+
+
 # ------------------------------------------------------------------ root-mean-square norm
 _norm_descs: dict = {}
 
@@ -582,7 +586,7 @@ def w4_matmul(x, w: W4Tensor, *, alpha=1.0, bias=None, act="none", residual=None
                              out_dtype=out_dtype, out=out)
     if bias is not None or residual is not None:
         _check_epilogue(t, what, bias, residual, x.shape[0] if x.dim() == 2 else -1, w._rows, index)
-    if out is not None and any(_bytes_overlap(out, a) for a in (x, bias, residual, w._codes, w._scales) if a is not None):
+    if out is not None and _overlaps(out, x, bias, residual, w._codes, w._scales, w._zeros):
         _refuse(what, "out overlaps an input")
     # what the checks look at: arguments that passed them once pass them again
     key = (x.shape, x.stride(), x.dtype, x.get_device(), out_dtype, act, bias is None, beta,
