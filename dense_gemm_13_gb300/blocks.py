@@ -82,13 +82,31 @@ def _out_ok(t, out, shape, dtype: str, index: int) -> bool:
             and _rows_ok(out))
 
 
+def _layout(x):
+    """(address, bytes of a row, bytes from a row to the next, rows) of a tensor's memory; without gaps it is one row."""
+    size = x.element_size()
+    if x.dim() == 2:
+        (rows, cols), (ld, step) = x.shape, x.stride()
+        if rows > 1 and ld > cols and (cols <= 1 or step == 1):
+            return x.data_ptr(), cols * size, ld * size, rows
+    n = sum((s - 1) * abs(st) for s, st in zip(x.shape, x.stride())) + 1
+    return x.data_ptr(), n * size, 0, 1
+
+
 def _bytes_overlap(a, b) -> bool:
-    """Whether the memory that two row-major tensors span overlaps."""
-    def span(x):
-        n = 0 if x.numel() == 0 else sum((s - 1) * abs(st) for s, st in zip(x.shape, x.stride())) + 1
-        return x.data_ptr(), x.data_ptr() + n * x.element_size()
-    (p, pe), (q, qe) = span(a), span(b)
-    return p < qe and q < pe
+    """Whether two tensors share memory.  (Column ranges of one buffer do not; of rows of different strides, whether the
+    memory that they span does.)"""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (p, la, sa, na), (q, lb, sb, nb) = _layout(a), _layout(b)
+    if p >= q + (nb - 1) * sb + lb or q >= p + (na - 1) * sa + la:
+        return False
+    s = sa or sb
+    if (sa and sb and sa != sb) or max(la, lb) > s:
+        return True
+    # row j of b begins r bytes into row k + j of a
+    k, r = divmod(q - p, s)
+    return (r < la and -nb < k < na) or (r + lb > s and -nb < k + 1 < na)
 
 
 def _overlaps(out, *inputs) -> bool:

@@ -2,7 +2,7 @@
 import pytest
 
 import dense_gemm_13_gb300 as g13
-from dense_gemm_13_gb300 import _build
+from dense_gemm_13_gb300 import _build, blocks
 
 torch = pytest.importorskip("torch")
 INVALID = -1
@@ -59,3 +59,59 @@ def test_w4_matmul_out_overlaps_no_input(called, which):
         if first >= 0:
             refused(lambda: call(pool[first: first + 2 * M * N].view(torch.bfloat16).view(M, N)))
     assert len(called) == 1
+
+
+def views(r, pool):
+    """Rows of a random stride, in one of a few types, somewhere in the pool."""
+    t = pool.view((torch.uint8, torch.bfloat16, torch.float32)[r.integers(3)])
+    rows, cols = int(r.integers(1, 5)), int(r.integers(1, 7))
+    ld = int(r.choice([cols, cols + 1, 8, 12])) if r.random() < 0.9 else cols + int(r.integers(0, 9))
+    ld = max(ld, cols)
+    left = t.numel() - (rows - 1) * ld - cols
+    return None if left < 0 else t.as_strided((rows, cols), (ld, 1), int(r.integers(0, left + 1)))
+
+
+def own_bytes(x, pool):
+    size, first = x.element_size(), x.data_ptr() - pool.data_ptr()
+    return {first + (i * x.stride(0) + j) * size + b for i in range(x.shape[0]) for j in range(x.shape[1]) for b in range(size)}
+
+
+def test_bytes_overlap_against_the_bytes_themselves():
+    np = pytest.importorskip("numpy")
+    r, pool = np.random.default_rng(5), torch.zeros(256, dtype=torch.uint8)
+    seen = {True: 0, False: 0}
+    for _ in range(4000):
+        a, b = views(r, pool), views(r, pool)
+        if a is None or b is None:
+            continue
+        want, got = bool(own_bytes(a, pool) & own_bytes(b, pool)), blocks._bytes_overlap(a, b)
+        assert got == blocks._bytes_overlap(b, a)
+        gaps = [x.stride(0) * x.element_size() for x in (a, b) if x.shape[0] > 1 and x.stride(0) > x.shape[1]]
+        if len(set(gaps)) <= 1:
+            assert got == want, (a.shape, a.stride(), a.dtype, b.shape, b.stride(), b.dtype, b.data_ptr() - a.data_ptr())
+            seen[want] += 1
+        else:
+            assert got or not want
+    assert min(seen.values()) > 300
+
+
+def test_columns_of_one_buffer_do_not_overlap():
+    buf = torch.zeros(4, 96, dtype=torch.bfloat16)
+    q, k, v = buf[:, :32], buf[:, 32:64], buf[:, 64:]
+    w = torch.ones(32, dtype=torch.bfloat16)
+    blocks._check_norm_overlap("rms_norm", q, w, k, k, v)
+    blocks._check_norm_overlap("rms_norm", q, buf[2, 40:72], None, None, v[:, 8:])
+    for out in (buf[:, 31:63], buf[:, 1:33], buf[1:, :32]):
+        with pytest.raises(g13.GemmError):
+            blocks._check_norm_overlap("rms_norm", q, w, None, None, out)
+    with pytest.raises(g13.GemmError):
+        blocks._check_norm_overlap("rms_norm", q, buf[2, 40:72], None, None, k)
+
+
+def test_w4_matmul_into_the_columns_beside_x(called):
+    buf = on0(torch.zeros(5, 64 + 32, dtype=torch.bfloat16))
+    W = g13.W4Tensor(*(on0(t) for t in (torch.zeros(1024, dtype=torch.uint8), torch.zeros(32, dtype=torch.bfloat16),
+                                        torch.zeros(32, dtype=torch.uint8))), 32, 64)
+    g13.w4_matmul(buf[:, :64], W, out=buf[:, 64:])
+    assert len(called) == 1
+    refused(lambda: g13.w4_matmul(buf[:, :64], W, out=buf[:, 63:95]))
