@@ -756,6 +756,8 @@ def moe_experts(x, w1, w2, expert_ids, expert_weights, *, act: str = "swiglu", o
             or w1.dtype is not dtype or w2.dtype is not dtype \
             or (out is not None and (out.get_device() != index or out.dtype is not dtype)):
         _refuse(what, "tensors of x's dtype on x's device, a GPU, are wanted")
+    if out is not None and _overlaps(out, x, w1, w2, expert_ids, expert_weights):
+        _refuse(what, "out overlaps an input")
     if stream is not None or index != t.device_index():
         with t.on(stream, index) if stream is not None else t.torch.cuda.device(index):
             return moe_experts(x, w1, w2, expert_ids, expert_weights, act=act, out=out)

@@ -24,7 +24,8 @@ def called(monkeypatch):
     L, calls = g13.load(), []
     monkeypatch.setattr(g13._t(), "device_index", lambda: 0)
     monkeypatch.setattr(g13._t(), "raw_stream", lambda i: 0)
-    monkeypatch.setattr(L, "gemm_w4_run", lambda *a: calls.append(a) or 0)
+    for name in ("gemm_w4_run", "gemm_moe_run_routed"):
+        monkeypatch.setattr(L, name, lambda *a: calls.append(a) or 0)
     return calls
 
 
@@ -58,6 +59,34 @@ def test_w4_matmul_out_overlaps_no_input(called, which):
     for first in (start - 2 * M * N + 2, end - 2):
         if first >= 0:
             refused(lambda: call(pool[first: first + 2 * M * N].view(torch.bfloat16).view(M, N)))
+    assert len(called) == 1
+
+
+@pytest.mark.parametrize("which", ["x", "w1", "w2", "ids", "weights"])
+def test_moe_experts_out_overlaps_no_input(called, monkeypatch, which):
+    T, E, k, H, I = 3, 4, 2, 32, 16
+    monkeypatch.setattr(blocks, "_no_capture", lambda *a: None)
+    monkeypatch.setattr(blocks, "_keep", lambda plans, key, make: type("P", (), dict(workspace_bytes=256, handle=0)))
+    pool = on0(torch.zeros(1 << 16, dtype=torch.uint8))
+    at = 0
+
+    def take(shape, dtype):
+        nonlocal at
+        n = torch.Size(shape).numel() * torch.empty(0, dtype=dtype).element_size()
+        t = pool[at: at + n].view(dtype).view(shape)
+        at += (n + 255) // 256 * 256
+        return t
+    bf = torch.bfloat16
+    a = dict(x=take((T, H), bf), w1=take((E, 2 * I, H), bf), w2=take((E, H, I), bf), ids=take((T, k), torch.int32),
+             weights=take((T, k), torch.float32))
+    call = lambda out: g13.moe_experts(a["x"], a["w1"], a["w2"], a["ids"], a["weights"], out=out)  # noqa: E731
+    free = take((T, H), bf)
+    assert call(free) is free and len(called) == 1
+    start = a[which].data_ptr() - pool.data_ptr()
+    end = start + a[which].numel() * a[which].element_size()
+    for first in (start - 2 * T * H + 2, end - 2):
+        if first >= 0:
+            refused(lambda: call(pool[first: first + 2 * T * H].view(bf).view(T, H)))
     assert len(called) == 1
 
 
@@ -115,3 +144,14 @@ def test_w4_matmul_into_the_columns_beside_x(called):
     g13.w4_matmul(buf[:, :64], W, out=buf[:, 64:])
     assert len(called) == 1
     refused(lambda: g13.w4_matmul(buf[:, :64], W, out=buf[:, 63:95]))
+
+
+def test_moe_experts_into_the_columns_beside_x(called, monkeypatch):
+    monkeypatch.setattr(blocks, "_no_capture", lambda *a: None)
+    monkeypatch.setattr(blocks, "_keep", lambda plans, key, make: type("P", (), dict(workspace_bytes=256, handle=0)))
+    buf, bf = on0(torch.zeros(3, 64, dtype=torch.bfloat16)), torch.bfloat16
+    w1, w2 = on0(torch.zeros(4, 32, 32, dtype=bf)), on0(torch.zeros(4, 32, 16, dtype=bf))
+    ids, weights = on0(torch.zeros(3, 2, dtype=torch.int32)), on0(torch.zeros(3, 2))
+    g13.moe_experts(buf[:, :32], w1, w2, ids, weights, out=buf[:, 32:])
+    assert len(called) == 1
+    refused(lambda: g13.moe_experts(buf[:, :32], w1, w2, ids, weights, out=buf[:, 31:63]))
