@@ -267,11 +267,12 @@ struct Part {
             for (int i = 0; i < 8; ++i) w[i] += d.weight_offset;
         }
     }
-    // v w (rs + rs_lo) to 2^-46 of itself, rounded to odd (the last bit set where something was cut off), so that the
-    // rounding to four bits that follows does not see a tie that is none.
+    // v (rs + rs_lo) w to 2^-46 of itself, rounded to odd (the last bit set where something was cut off), so that the
+    // rounding to four bits that follows does not see a tie that is none.  (v rs first: it is at most the root of the row's
+    // length, while v w may lie beyond FP32 where the result does not.)
     static __device__ __forceinline__ float to_odd(float v, float w, float rs, float rs_lo) {
-        const float p = v * w, e = fmaf(v, w, -p), c = fmaf(p, rs_lo, e * rs), hi = fmaf(p, rs, c);  // v w = p + e
-        const float lo = fmaf(p, rs, -hi) + c;
+        const float p = v * rs, p_lo = fmaf(v, rs_lo, fmaf(v, rs, -p)), c = p_lo * w, hi = fmaf(p, w, c);
+        const float lo = fmaf(p, w, -hi) + c;
         int bits = __float_as_int(hi);
         if (lo != 0.0f && fabsf(hi) < INFINITY && (bits & 1) == 0) bits += (lo < 0.0f) == (hi < 0.0f) ? 1 : -1;
         return hi == 0.0f ? hi : __int_as_float(bits);

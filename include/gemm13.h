@@ -400,11 +400,12 @@ int gemm_fp8_select_config(int64_t M, int64_t N, int64_t K, int32_t num_sms, gem
  *     Y = cast( H / sqrt(mean_k H^2 + eps) * (weight + weight_offset) )
  *
  * sums and all steps in FP32.  Y is computed from the rounded H, so that a later call on H
- * alone gives the same.  With mxfp8, Y is written as 8-bit floats (above): codes and scales of
- * the exact values of the formula, but for a sum of squares that is off by some 2^-40 of itself (it and
- * the factor are held in two FP32 numbers each): values next to a border of the codes or the scales
- * are worked out again with both.
- * A row's sum of squares must stay within FP32.  NaN and infinities: as the formula has them.
+ * alone gives the same.  With mxfp8, Y is written as 8-bit floats (above): codes and scales are those of
+ * the exact values of the formula, but that the sum of squares is off by some 2^-40 of itself, so a value that close to a border
+ * of the codes or the scales may fall on its other side (sum and factor are held in two FP32 numbers each; values next to a
+ * border are worked out again with both).
+ * A row's sum of squares must stay below 2^128; where it and eps are below 2^-90, or in mxfp8 results below 2^-100,
+ * digits are lost.  NaN and infinities: as the formula has them.
  */
 typedef struct {
     gemm_dtype_t dtype;          /* X; default GEMM_BF16 */
