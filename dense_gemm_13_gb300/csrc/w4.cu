@@ -21,9 +21,10 @@
 // are few rows, or more of K than shared memory holds, a cluster of CTAs shares K and each adds its share of the
 // sums through distributed shared memory, in rank order.  Nothing depends on timing, and nothing needs a workspace.
 //
-// Measured (BF16, groups of 128): 1 x 6144 x 6144 8.5 us, of which the bytes would take 2.9 and launch, staging and joins
-// take 4 to 5; 1 x 16384 x 8192 17.1 us (4.1 TB/s); 8 tokens 22.6 us, 16 tokens 31 us (groups of 64: 35), bound by the instructions that
-// stage the tokens and scale each group's sums; from 17 tokens on w4_tc.cu is faster (32 tokens: 34 us against 56 here).
+// Measured (BF16, groups of 128): 1 x 6144 x 6144 8.4 us, of which the bytes would take 2.9 and launch, staging and joins
+// take 4 to 5; 1 x 16384 x 8192 17.0 us (4.1 TB/s); 8 tokens 22.6 us, 16 tokens 30.7 us (groups of 64: 34.6).  At 16 tokens a step of
+// 16 rows is 200 warp instructions, which take 41 % of the issue slots; the rest is waiting, for the tokens to be staged before
+// the first product, for codes, and at the clusters' joins.  From 17 tokens on w4_tc.cu is faster (its figures are there).
 // Before: weights made into whole FP16 numbers first, 13.4 us at 1 x 6144 x 6144; loads behind a branch, 22 us at 1 x 16384 x
 // 8192; clusters counted as if all 76 of four CTAs fitted, 50 us at 16 tokens.
 #include <cuda_bf16.h>

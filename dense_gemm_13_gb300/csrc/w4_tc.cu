@@ -1,4 +1,4 @@
-// w4_tc.cu -- products of many tokens (up to 64) with 4-bit weights on the tensor cores (tcgen05).
+// w4_tc.cu -- products of 17 to 64 tokens with 4-bit weights on the tensor cores (tcgen05).
 //
 // The weights' rows are the 128 rows of a tile and the tokens its columns.  A step is 128 columns of K.  Eight warps turn its
 // codes into q - z, whole numbers of at most four bits and a sign and so exact in X's own type, and write them to shared memory
@@ -6,13 +6,16 @@
 // activation and no weight is rounded.  The scales stay out of the product: each group's sum (of a step at most) has
 // TMEM columns of its own, others read them, a thread to a row, and add scale * sum in FP32.
 //
-//   4 or 8 warps  sums: TMEM to registers, times the row's scale (32 tokens to a warp at most)
-//   16 warps      codes and tokens to shared memory, in a ring, eight to a step in turn: full[s] counts their arrivals
+//   4 warps       sums: TMEM to registers, times the row's scale
+//   8 or 16 warps codes and tokens to shared memory, in a ring, eight to a step: full[s] counts their arrivals.  Up to 32
+//                 tokens two sets of eight take steps in turn; with more the sums' registers leave room for one
 //   the last      one lane issues the MMAs; commits free ring stages (empty[s]) and hand sums over (tfull[b])
 //
-// Measured (BF16, groups of 128): 64 x 16384 x 8192 45 us (mma.sync in w4.cu: 112), 32 tokens 34 (56), 16 tokens 30.8 (30.7, so
-// these stay there).  Instructions bound it (2500 of a warp to a step, half of them the codes'), then the tensor core's reads of
-// the rows from shared memory.  One set of producers: 45 us at 32 tokens; weights in TMEM, tokens by copies of four bytes: 84 at 64.
+// Measured at 16384 x 8192, BF16, groups of 128 / 64 / 32: 17 tokens 33.6 / 40.1 / 68.1 us; 64 tokens 45.5 (128) and 68.2
+// (32); the bytes would take 10.8.  A step is 2660 warp instructions at 17 tokens and 3130 at 64, which take 77 % and 69 % of the
+// issue slots of the 128 SMs that have a tile (24 have none), and the tensor pipes 15 % and 22 %: the instructions bound the
+// first, and them together with the way of a step through a ring of three stages the second.  One set of
+// producers: 45 us at 32 tokens; weights in TMEM, tokens by copies of four bytes: 84 at 64.
 //
 // A CTA has one tile, or a cluster of two to eight shares its K and adds the CTAs' sums in rank order through
 // distributed shared memory.  Every wait is bounded; after a timeout the tile's results are NaN.
@@ -51,14 +54,12 @@ struct TcLayout {
     static constexpr int X_STAGES = STAGES + TC_AHEAD;        // of tokens: these are asked for that much earlier
     static constexpr int X_BYTES = TOK * 256;
     static constexpr int RING = STAGES * TC_A_BYTES + X_STAGES * X_BYTES;
-    static constexpr int WARP_TOK = TOK;  // tokens whose sums a warp has
-    static constexpr int EW = 4 * TOK / WARP_TOK;         // warps with sums
+    static constexpr int EW = 4;                              // warps with sums
     static constexpr int THREADS = 32 * (EW + TC_WRITERS * TURNS + 1);
-    static constexpr int PITCH = TOK < 32 ? 32 : TOK;  // TMEM columns of a group's sums
-    static constexpr int BUFS = 4 * NG * PITCH <= 512 ? 4 : 2;  // of steps' sums
-    static constexpr int COLS = BUFS * NG * PITCH;
+    static constexpr int BUFS = 4 * NG * TOK <= 512 ? 4 : 2;  // of steps' sums, TOK TMEM columns a group
+    static constexpr int COLS = BUFS * NG * TOK;
     static constexpr int SMEM = 1024 + RING + (2 * STAGES + 2 * BUFS + 1) * 8 + 16;
-    static_assert(COLS <= 512 && SMEM <= kW4Smem, "TMEM, shared memory");
+    static_assert(TOK % 32 == 0 && COLS <= 512 && SMEM <= kW4Smem, "TMEM, shared memory");
     static_assert(TOK * TC_SUM_ROW * 4 <= RING, "the sums lie where the ring was");
 };
 
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
     const auto group = [&](int j, int h) {
         return min(over(static_cast<uint32_t>((first + j) * 4 + h * (4 / NG)), plan.inv), plan.groups - 1);
     };
-    float sums[L::WARP_TOK];  // (of the first warps)
+    float sums[TOK];  // (of the first warps)
 
     if (warp >= EW && warp < MMA_WARP) {
         // ---- codes and tokens: a warp has 16 of the tile's rows
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
             if (one) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k)  // 16 columns each
-                    tc_mma_f16(tmem + (b * NG + k * NG / 8) * L::PITCH, ad + (((k >> 2) * (TC_A_BYTES / 2) + (k & 3) * 32) >> 4),
+                    tc_mma_f16(tmem + (b * NG + k * NG / 8) * TOK, ad + (((k >> 2) * (TC_A_BYTES / 2) + (k & 3) * 32) >> 4),
                                bd + (((k >> 2) * (TOK * 128) + (k & 3) * 32) >> 4), plan.idesc, k % (8 / NG) != 0);
                 tc_commit(smem_u32(&empty[s]));
                 tc_commit(smem_u32(&tfull[b]));
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
         __syncwarp();
     } else {
         // ---- sums of row warp * 32 + lane
-        const int row = warp % 4 * 32 + lane, rb = tile * 8 + row / 16;
+        const int row = warp * 32 + lane, rb = tile * 8 + row / 16;
         const bool live = rb < plan.tiles;
         const uint16_t* scales = static_cast<const uint16_t*>(a.scales) + static_cast<int64_t>(rb) * plan.groups * 16 + row % 8 * 2 + row % 16 / 8;
         uint32_t ring[TC_SCALES][NG] = {};
@@ -292,10 +293,10 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
             for (int h = 0; h < NG; ++h) ld_nc16(v[h], scales + group(j, h) * 16, live && j < steps);
         };
 #pragma unroll
-        for (int i = 0; i < L::WARP_TOK; ++i) sums[i] = 0.0f;
+        for (int i = 0; i < TOK; ++i) sums[i] = 0.0f;
 #pragma unroll
         for (int d = 0; d < TC_SCALES; ++d) load(ring[d], d);
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + warp / 4 * 32;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         bool ok = true;
         for (int j0 = 0; ok && j0 < steps; j0 += TC_SCALES) {
 #pragma unroll
@@ -313,10 +314,10 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
 #pragma unroll
                     for (int n = 0; n < TOK; n += 32) {
                         uint32_t v[32];
-                        tmem_ld_32x32b_x32(lanes + (b * NG + h) * L::PITCH + n, v);
+                        tmem_ld_32x32b_x32(lanes + (b * NG + h) * TOK + n, v);
                         tmem_ld_wait_regs(v);
 #pragma unroll
-                        for (int i = 0; i < 32 && n + i < TOK; ++i) sums[n + i] = fmaf(s, __uint_as_float(v[i]), sums[n + i]);
+                        for (int i = 0; i < 32; ++i) sums[n + i] = fmaf(s, __uint_as_float(v[i]), sums[n + i]);
                     }
                 }
                 tc_fence_before();
@@ -335,10 +336,9 @@ __global__ void __launch_bounds__(TcLayout<TOK, NG>::THREADS, 1) w4_tc_kernel(co
     const int tok = static_cast<int>(a.M);
     if (warp < EW) {
         const bool failed = *abort_flag != 0;
-        const int t0 = warp / 4 * 32;
 #pragma unroll
-        for (int t = 0; t < L::WARP_TOK; ++t)
-            if (t0 + t < tok) all[(t0 + t) * TC_SUM_ROW + warp % 4 * 32 + lane] = failed ? __int_as_float(0x7FFFFFFF) : sums[t];
+        for (int t = 0; t < TOK; ++t)
+            if (t < tok) all[t * TC_SUM_ROW + warp * 32 + lane] = failed ? __int_as_float(0x7FFFFFFF) : sums[t];
     }
     if (ranks > 1)
         cluster_sync();
@@ -410,13 +410,16 @@ cudaError_t launch_type(const W4Args& a, int splits, cudaStream_t st) {
 }
 template <int NG>
 cudaError_t launch_tokens(const W4Args& a, int splits, cudaStream_t st) {
-    return a.M <= 16   ? launch_type<16, NG>(a, splits, st)
-           : a.M <= 32 ? launch_type<32, NG>(a, splits, st)
-                       : launch_type<64, NG>(a, splits, st);
+    return a.M <= 32 ? launch_type<32, NG>(a, splits, st) : launch_type<64, NG>(a, splits, st);
 }
 
 }  // namespace
 
+// From 17 tokens on.  At 17, w4.cu takes 40.8 / 52.4 / 78.0 us instead of the 33.6 / 40.1 / 68.1 above; at 16 it takes
+// 30.7 / 34.7 / 43.0 where these kernels take 33.3 / 39.5 / 67.3.  (With few rows and a long K they win earlier:
+// 4096 x 14336, 16 tokens, groups of 128, 18.8 us against 22.7.)  Rows of X off 16 bytes go to w4.cu with any number of tokens.
+//
+// K is divided as a rough model in ns has it: a step 250, a tile's set-up and store 2500, a cluster's barriers and join 1500 more.
 int w4_tc_splits(const W4Args& a, int num_sms) {
     if (a.M <= 16 || reinterpret_cast<uintptr_t>(a.x) % 16 != 0 || (a.M > 1 && a.ldx % 8 != 0)) return 0;
     const int64_t steps = (a.K + 127) / 128, tiles = (a.N + 127) / 128;
