@@ -397,7 +397,12 @@ __global__ void __launch_bounds__(RW * 32, PER == 16 ? 2 : 3) route_kernel(const
                     b1 = max(b1, k);
                 }
             best_two(b1, b2, g.lanes);
-            if (sums && g.per > 1) b1 = ordered(number(b1) + number(b2) + 0.0f);
+            float size = 0.0f;  // what the roundings of a sum's terms go by (biases of both signs may cancel)
+            if (sums && g.per > 1) {
+                const float c1 = number(b1), c2 = number(b2), both = c1 + c2 + 0.0f;
+                if (has_group && fabsf(both) < INFINITY) size = fabsf(c1) + fabsf(c2);
+                b1 = ordered(both);
+            }
             if (!has_group || g.sub != 0) b1 = NONE;
             const int its_score = b1, second = sums && g.per > 1 ? b2 : b1;
             unsigned kept = 0;
@@ -413,7 +418,9 @@ __global__ void __launch_bounds__(RW * 32, PER == 16 ? 2 : 3) route_kernel(const
             }
             if (by_score || sums) {
                 const float lo = number(lowest), hi = number(most);
-                const float off = 4.0f * delta + 0x1.8p-23f * (fabsf(lo) + fabsf(hi));
+                // (of each group: 2^-24 of its terms' sizes, and of their sum)
+                size = __int_as_float(__reduce_max_sync(ALL, __float_as_int(size)));
+                const float off = 4.0f * delta + 0x1.8p-23f * (fabsf(lo) + fabsf(hi)) + 0x1.1p-23f * size;
                 if (!unsure && !(lo - hi > off)) {
                     // the groups that may go either way, and of each the experts that may be its best (two)
                     const float v = number(its_score);

@@ -87,3 +87,29 @@ def test_scores_of_zero():
         assert ids.tolist() == [[0, 1]] * 2 and bool(w[0].isnan().all()) and w[1].tolist() == [0.0, 1.0]
         ids, w = g13.route(z, 2, bias=bias, scores=scores, normalize=False)
         assert w[0].tolist() == [0.0, 0.0] and float(w[1, 0]) == 0 and float(w[1, 1]) > 0
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [1.0, 30.0, 1e3, 1e5])
+@pytest.mark.parametrize("groups,per", [(16, 2), (32, 2), (8, 8), (4, 60)])
+def test_group_scores_of_biases_that_cancel(scores, size, groups, per):
+    # the two best of a group have biases of opposite sign, whose sum FP32 rounds far more coarsely than its own size
+    # allows
+    r = rng("cancel", scores, size, groups)
+    z = torch.from_numpy(r.standard_normal((1500, groups * per)).astype(np.float32) * 2).cuda()
+    bias = np.full((groups, per), -3 * size, np.float32)
+    bias[:, 0] = size * (1 + r.random(groups))
+    bias[:, 1] = -bias[:, 0]
+    bias = np.take_along_axis(bias, r.permuted(np.tile(np.arange(per), (groups, 1)), axis=1), 1).reshape(-1)
+    for top in (1, 3):
+        check(z, 2, bias, scores=scores, groups=groups, top_groups=top, group_score="top2")
+
+
+def test_group_scores_with_experts_that_are_masked():
+    # a bias of -infinity takes experts out: some of a group, all but one, all
+    inf, r = float("inf"), rng("masked")
+    z = torch.from_numpy(r.standard_normal((400, 64)).astype(np.float32)).cuda()
+    bias = (r.standard_normal(64) * 0.1).astype(np.float32)
+    bias[:8], bias[9:16], bias[20:22] = -inf, -inf, -inf
+    for kw in (dict(), dict(groups=8, top_groups=3, group_score="top2"), dict(groups=8, top_groups=3)):
+        check(z, 6, bias, scores="sigmoid", **kw)
