@@ -364,10 +364,12 @@ __global__ void __launch_bounds__(RW * 32, PER == 16 ? 2 : 3) route_kernel(const
 #pragma unroll
             for (int i = 0; i < PER; ++i) c[i] = rcp(1.0f + ex2(z[i] * -LOG2E)) + bias[i];
         }
-        // How far c may be off, apart from its own rounding (2^-24 |c|): a sigmoid s by 1.1 * 2^-22 (ex2 by 2^-22 of its value,
-        // which counts s (1 - s) <= 1/4, its argument's rounding by 2^-24 of it, and s (1 - s) |z| <= 0.23; 1 + e and rcp
-        // by 3 * 2^-24); a softmax s by (|z - max| + 12) 2^-23 of itself, and s |z - max| stays below 0.37 of the largest:
-        // 2^-19 of that.
+        // How far c may be off, apart from its own rounding (2^-24 |c|).  A sigmoid s by 1.1 * 2^-22: ex2 by 2^-22 of its value,
+        // which counts s (1 - s) <= 1/4, its argument's roundings by 2^-24 and LOG2E's by 2^-26 of it, and s (1 - s) |z| <= 0.23;
+        // 1 + e and rcp by 3 * 2^-24.  Of two softmax scores the difference by 2 * 2^-19 of the largest, 1 / sum, with 1 = 2^-23:
+        // their common factor by 10 (a sum of 16 in a lane and five steps, half a unit each), 2 (ex2), 7 (the arguments' 1.12 |z - max|,
+        // whose mean over the scores is at most ln E - ln sum <= 6.3) and 1 (rcp), 20 times a difference of at most
+        // the largest; each by ex2 and its argument, (2 + 1.12 |z - max|) s, at most 2 of the largest: 24 <= 2 * 16.  Of two sums of two the same twice.
         const float delta = softmax ? 0x1p-19f * rcp(sum) : 0x1.2p-22f;
         bool unsure = softmax && sum != sum;
         int key[PER];

@@ -5,15 +5,17 @@
 // The weights' bytes are the cost (half a byte a weight); every one is read once, by 16-byte loads of whole 512-byte
 // blocks, several ahead in registers.  A warp multiplies a step of 16 rows x 128 columns with 8 tokens by eight mma.sync
 // m16n8k16: the weights are the 16 rows, the tokens the columns.  What is left to save is instructions, so the codes go into
-// the product as they lie: a nibble in the lowest or second lowest place of 16 bits, the others masked off, is the FP16
-// number q 2^-24 or 16 q 2^-24, exactly (its subnormal range is linear).  Five instructions make eight weights (as
-// 1024 + q or 128 + q, minus 1024 + z: nine and eleven).  The zero comes off afterwards:
+// the product nearly as they lie: a nibble in the second lowest place of 16 bits, the others masked off, is the FP16
+// number 16 q 2^-24, exactly (its subnormal range is linear).  Seven instructions make eight weights (as 1024 + q or 128 + q,
+// minus 1024 + z: nine and eleven).  In the lowest place two less would do, but the tensor cores line their sums up as if a
+// subnormal were 2^-14, and cut off what a small one has too far down: K = 8192, FP16, FP32 results 1.6e-6 of them off
+// instead of 1.8e-7 (16 tokens 30.8 us instead of 31.7, 1 x 16384 x 8192 16.9 instead of 17.6).  The zero comes off afterwards:
 //
 //   sum_k (q - z) x = sum_k q x - z sum_k x      over a group, FP32; the sums of x are worked out once per CTA
 //
 // and the group's scale multiplies the difference, so no weight is rounded.  The activations are brought into the upper
-// part of FP16's range by a power of two for every 128 of a token's, and those that meet 16 q by 1 / 16 more: exact, but for
-// values below 2^-27 of the largest of them (FP16 ones: 2^-24), which are off by 2^-35 of it at most.
+// part of FP16's range by a power of two for every 128 of a token's: exact, but for values below 2^-31 of the largest of them
+// (FP16 ones: 2^-28), which are off by 2^-39 of it at most.
 //
 // A CTA has eight warps.  `wk` of them share its part of K, the others have 16 rows each of their own; the sums of those
 // that share K are joined through shared memory in warp order.  CTAs are persistent; a warp's loads run on into
@@ -21,10 +23,11 @@
 // are few rows, or more of K than shared memory holds, a cluster of CTAs shares K and each adds its share of the
 // sums through distributed shared memory, in rank order.  Nothing depends on timing, and nothing needs a workspace.
 //
-// Measured (BF16, groups of 128): 1 x 6144 x 6144 8.4 us, of which the bytes would take 2.9 and launch, staging and joins
-// take 4 to 5; 1 x 16384 x 8192 17.0 us (4.1 TB/s); 8 tokens 22.6 us, 16 tokens 30.7 us (groups of 64: 34.6).  At 16 tokens a step of
-// 16 rows is 200 warp instructions, which take 41 % of the issue slots; the rest is waiting, for the tokens to be staged before
-// the first product, for codes, and at the clusters' joins.  From 17 tokens on w4_tc.cu is faster (its figures are there).
+// Measured (BF16, groups of 128): 1 x 6144 x 6144 8.7 us, of which the bytes would take 2.9 and launch, staging and joins
+// take 4 to 5; 1 x 16384 x 8192 17.6 us (4.0 TB/s); 8 tokens 23.5 us, 16 tokens 31.7 us (groups of 64: 35.4).  At 16 tokens a step of
+// 16 rows is some 220 warp instructions, which take less than half of the issue slots; the rest is waiting, for the tokens to be
+// staged before the first product, for codes, and at the clusters' joins.  From 17 tokens on w4_tc.cu is faster (its figures
+// are there).
 // Before: weights made into whole FP16 numbers first, 13.4 us at 1 x 6144 x 6144; loads behind a branch, 22 us at 1 x 16384 x
 // 8192; clusters counted as if all 76 of four CTAs fitted, 50 us at 16 tokens.
 #include <cuda_bf16.h>
@@ -68,6 +71,19 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
             " {%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A code from the lowest place to the second lowest, in both halves of a register: by an integer multiplication (the mask
+// comes after it), or of masked codes as FP16 numbers.  Either keeps off the pipe of the masks and shifts; one of
+// each is the fastest (1 x 16384 x 8192: 17.6 us, shifts 18.9, FP16 alone 17.9).
+__device__ __forceinline__ uint32_t up_int(uint32_t v) {
+    uint32_t r;
+    asm("mad.lo.u32 %0, %1, 16, 0;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t up_f16(uint32_t v) {
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v) : "r"(0x4C004C00u));
+    return v;
 }
 
 // A step is 128 columns of 16 rows, two blocks.  As it is loaded: the codes, and of each of the NG groups that it
@@ -226,25 +242,24 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
 #pragma unroll
                 for (int l = 0; l < 16; ++l) top = fabsf(f[l]) < INFINITY ? fmaxf(top, fabsf(f[l])) : top;
             }
-            // the largest magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^(E - 2) (a group's
-            // sum of 128 values below 2^15 and codes up to 15, times 2^-24, is below 2^2)
+            // the largest magnitude of the step, and from its exponent E the powers 2^(14 - E) and 2^(E - 6) (a group's
+            // sum of 128 values below 2^15 and codes up to 15, times 2^-20, is below 2^6)
 #pragma unroll
             for (int o = 1; o < 8; o *= 2) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
             const uint32_t biased = max(__float_as_uint(top) >> 23, 28u);  // (2^(14 - E) stays a normal number)
-            const float up = __uint_as_float((127u + 14u + 127u - biased) << 23), down = __uint_as_float((biased - 2u) << 23);
+            const float up = __uint_as_float((127u + 14u + 127u - biased) << 23), down = __uint_as_float((biased - 6u) << 23);
 #pragma unroll
-            for (int l = 0; l < 8; ++l) {  // the pairs 1 and 3 of eight columns meet nibbles that count 16 times
-                const float m = l % 2 ? up * 0.0625f : up;
-                const __half2 h = __floats2half2_rn(f[2 * l] * m, f[2 * l + 1] * m);
+            for (int l = 0; l < 8; ++l) {
+                const __half2 h = __floats2half2_rn(f[2 * l] * up, f[2 * l + 1] * up);
                 w[l] = *reinterpret_cast<const uint32_t*>(&h);
             }
             p[0] = make_uint4(w[0], w[2], w[1], w[3]);  // (two pairs for each of the two products)
             p[1] = make_uint4(w[4], w[6], w[5], w[7]);
 #pragma unroll
             for (int o = 1; o < 8 / NG; o *= 2) sum += __shfl_xor_sync(lanes, sum, o);
-            if (piece % (8 / NG) == 0) {  // (times 2^-24, like the products)
+            if (piece % (8 / NG) == 0) {  // (times 2^-20, like the products)
                 float* q = pairs + ((j * NG + piece / (8 / NG)) * (TOK / 2) + t / 2) * 4 + t % 2;
-                q[0] = sum * (up * 0x1p-16f);
+                q[0] = sum * (up * 0x1p-12f);
                 q[2] = down;
             }
         }
@@ -271,16 +286,17 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
             // 32 columns: sixteen bytes of each token, columns 32 h + 8 t4 .. + 7 of the step
             const uint4 v = h < 2 ? b.lo : b.hi;
             const uint32_t w0 = h & 1 ? v.z : v.x, w1 = h & 1 ? v.w : v.y, u0 = w0 >> 8, u1 = w1 >> 8;
-            constexpr uint32_t LOW = 0x000F000Fu, HIGH = 0x00F000F0u;
+            constexpr uint32_t LOW = 0x000F000Fu, AT = 0x00F000F0u;
+            const uint32_t p0 = up_int(w0) & AT, p1 = up_int(w1) & AT, p2 = up_f16(u0 & LOW), p3 = up_f16(u1 & LOW);
             constexpr int LEN = 4 / NG;  // such pieces of a group
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const uint4 x = *reinterpret_cast<const uint4*>(xrow[n] + j0 * 256 + d * (WK * 256) + h * 64);
                 if (h % LEN == 0)
-                    mma<true>(d0[n], w0 & LOW, w1 & LOW, u0 & LOW, u1 & LOW, x.x, x.y);
+                    mma<true>(d0[n], p0, p1, p2, p3, x.x, x.y);
                 else
-                    mma<false>(d0[n], w0 & LOW, w1 & LOW, u0 & LOW, u1 & LOW, x.x, x.y);
-                mma<false>(d0[n], w0 & HIGH, w1 & HIGH, u0 & HIGH, u1 & HIGH, x.z, x.w);
+                    mma<false>(d0[n], p0, p1, p2, p3, x.x, x.y);
+                mma<false>(d0[n], w0 & AT, w1 & AT, u0 & AT, u1 & AT, x.z, x.w);
             }
             if ((h + 1) % LEN == 0) {
                 const int gr = h / LEN;
@@ -320,7 +336,7 @@ __global__ void __launch_bounds__(WT, w4_ctas(NT)) w4_kernel(const __grid_consta
             for (int c = 0; c < 2; ++c) {
                 const int t = n * 8 + t4 * 2 + c;
                 if (t >= tok) continue;
-                // (2^24, of which the powers of two hold 2^12)
+                // (2^20, of which the powers of two hold 2^8)
                 mine[t * SUM_ROW] = acc[n][c] * 0x1p12f;
                 mine[t * SUM_ROW + 8] = acc[n][2 + c] * 0x1p12f;
             }

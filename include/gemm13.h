@@ -475,8 +475,8 @@ int gemm_w4_dequantize(gemm_dtype_t dtype, gemm_dtype_t scale_dtype, int64_t N, 
  * Y = cast( act( alpha * X.W^T + bias ) + beta * R ) for 1 to 64 tokens.  X [M][K] in the scales'
  * type.  No weight is rounded: a group's sum of (q - z) x is added in FP32 and multiplied by its scale (from 17
  * tokens on that sum has to stay within FP32, up to 16 the result); a result is off by some 2^-19 of sum |x| (q + z) s at most before the
- * epilogue.  Up to 16 tokens (and where rows of X do not start on 16 bytes) BF16 values below 2^-27, FP16 values below
- * 2^-24 of the largest of their 128 columns, k / 128 alike, count to 2^-35 of it.  A token that holds an infinity or a
+ * epilogue.  Up to 16 tokens (and where rows of X do not start on 16 bytes) BF16 values below 2^-31, FP16 values below
+ * 2^-28 of the largest of their 128 columns, k / 128 alike, count to 2^-39 of it.  A token that holds an infinity or a
  * NaN gives sums that are not finite; a NaN before the activation (any of them) is one after it.  More tokens:
  * gemm_w4_dequantize, then gemm_run.
  */

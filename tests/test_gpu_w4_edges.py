@@ -140,3 +140,22 @@ def test_a_large_scale_beside_large_activations(M, group):
     y = g13.w4_matmul(x, W, out_dtype="f32")
     assert bool(torch.isfinite(y).all())
     check_product(y, x, w, "f32")
+
+
+@pytest.mark.parametrize("M", [1, 5, 16, 17, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_fp32_results_are_as_exact_as_fp32_sums(M, dtype):
+    # With u = 2^-24: an FP32 sum over n = K / 128 groups of random signs, each addition off by u / sqrt(3) of a partial
+    # sum that grows like a random walk, is off by u sqrt(n / 6), 3.3 u at K = 8192; a group's own sum, the scale and the
+    # joins are allowed 1.2 u more.
+    N = 1024
+    for K in (512, 4096, 8192):
+        for group in (32, 64, 128, 256):
+            for zeros in (True, False):
+                r = rng("exact", M, K, group, zeros)
+                W, _, _, _, (w, _) = weight(r, N, K, group, dtype, zeros)
+                x = torch.from_numpy(r.standard_normal((M, K)).astype(np.float32)).to(DT[dtype])
+                want = x.double().numpy() @ w.T
+                got = g13.w4_matmul(x.cuda(), W, out_dtype="f32").double().cpu().numpy()
+                off = np.linalg.norm(got - want) / np.linalg.norm(want)
+                assert off <= ((K / 128 / 6) ** 0.5 + 1.2) * 2.0 ** -24, (K, group, zeros, off)
