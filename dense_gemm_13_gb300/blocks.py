@@ -125,8 +125,8 @@ def rms_norm(x, weight=None, *, residual=None, eps: float = 1e-6, weight_offset:
     x [T, H]: FP32, FP16 or BF16, rows contiguous; weight [H] of any of these (None: ones); residual [T, H]:
     FP32 or x's dtype.  out_dtype: "f32", "f16", "bf16" (default: x's), or "mxfp8", which gives an Fp8Tensor for
     fp8_matmul.  Returns y, or with a residual (y, h).  residual_out may be residual or x itself and out may be x
-    or residual (in place: same dtype and strides); they overlap nothing else.  With `stream`, the call runs, and
-    allocates, as if that were the current stream.
+    or residual (in place: same dtype and strides); they overlap nothing else.  A row's sum of squares must stay below
+    2^128 (beyond it y is 0).  With `stream`, the call runs, and allocates, as if that were the current stream.
     """
     what, t = "rms_norm", _t()
     index = x.get_device()
@@ -591,8 +591,9 @@ def w4_matmul(x, w: W4Tensor, *, alpha=1.0, bias=None, act="none", residual=None
     """y = cast(act(alpha * x @ W.T + bias) + beta * residual) for 1 to 64 tokens and a 4-bit weight (gemm_w4_run).
 
     x [M, K] in the dtype of W's scales, rows contiguous; bias: FP32 [N]; residual: FP32 [M, N]; out_dtype: "f32",
-    "f16" or "bf16" (default: x's).  out overlaps no input.  With `stream`, the call runs, and allocates, as if that
-    were the current stream.
+    "f16" or "bf16" (default: x's).  out overlaps no input.  A NaN stays one with any activation; should a wait inside the
+    kernel run out, after 2 s, 128 columns of y are NaN.  With `stream`, the call runs, and allocates, as if that were the
+    current stream.
     """
     what, t = "w4_matmul", _t()
     if type(w) is not W4Tensor:

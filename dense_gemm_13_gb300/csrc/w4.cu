@@ -9,7 +9,7 @@
 // number 16 q 2^-24, exactly (its subnormal range is linear).  Seven instructions make eight weights (as 1024 + q or 128 + q,
 // minus 1024 + z: nine and eleven).  In the lowest place two less would do, but the tensor cores line their sums up as if a
 // subnormal were 2^-14, and cut off what a small one has too far down: K = 8192, FP16, FP32 results 1.6e-6 of them off
-// instead of 1.8e-7 (16 tokens 30.8 us instead of 31.7, 1 x 16384 x 8192 16.9 instead of 17.6).  The zero comes off afterwards:
+// instead of 1.8e-7 (16 tokens 30.8 us instead of 31.5, 1 x 16384 x 8192 16.9 instead of 17.6).  The zero comes off afterwards:
 //
 //   sum_k (q - z) x = sum_k q x - z sum_k x      over a group, FP32; the sums of x are worked out once per CTA
 //
@@ -24,7 +24,7 @@
 // sums through distributed shared memory, in rank order.  Nothing depends on timing, and nothing needs a workspace.
 //
 // Measured (BF16, groups of 128): 1 x 6144 x 6144 8.7 us, of which the bytes would take 2.9 and launch, staging and joins
-// take 4 to 5; 1 x 16384 x 8192 17.6 us (4.0 TB/s); 8 tokens 23.5 us, 16 tokens 31.7 us (groups of 64: 35.4).  At 16 tokens a step of
+// take 4 to 5; 1 x 16384 x 8192 17.6 us (4.0 TB/s); 8 tokens 23.5 us, 16 tokens 31.5 us (groups of 64: 35.7).  At 16 tokens a step of
 // 16 rows is some 220 warp instructions, which take less than half of the issue slots; the rest is waiting, for the tokens to be
 // staged before the first product, for codes, and at the clusters' joins.  From 17 tokens on w4_tc.cu is faster (its figures
 // are there).

@@ -415,9 +415,9 @@ cudaError_t launch_tokens(const W4Args& a, int splits, cudaStream_t st) {
 
 }  // namespace
 
-// From 17 tokens on.  At 17, w4.cu takes 40.8 / 52.4 / 78.0 us instead of the 33.6 / 40.1 / 68.1 above; at 16 it takes
-// 30.7 / 34.7 / 43.0 where these kernels take 33.3 / 39.5 / 67.3.  (With few rows and a long K they win earlier:
-// 4096 x 14336, 16 tokens, groups of 128, 18.8 us against 22.7.)  Rows of X off 16 bytes go to w4.cu with any number of tokens.
+// From 17 tokens on.  At 17, w4.cu takes 43.4 / 50.1 / 75.8 us instead of the 33.6 / 40.1 / 68.1 above; at 16 it takes
+// 31.5 / 35.7 / 44.0 where these kernels take 33.3 / 39.5 / 67.3.  (With few rows and a long K they win earlier:
+// 4096 x 14336, 16 tokens, groups of 128, 18.8 us against 22.9.)  Rows of X off 16 bytes go to w4.cu with any number of tokens.
 //
 // K is divided as a rough model in ns has it: a step 250, a tile's set-up and store 2500, a cluster's barriers and join 1500 more.
 int w4_tc_splits(const W4Args& a, int num_sms) {
