@@ -420,10 +420,14 @@ __global__ void __launch_bounds__(RW * 32, PER == 16 ? 2 : 3) route_kernel(const
             }
             if (by_score || sums) {
                 const float lo = number(lowest), hi = number(most);
-                // (of each group: 2^-24 of its terms' sizes, and of their sum)
+                // (of each group: 2^-24 of its terms' sizes, and of their sum; an infinity is exact where it is not a sum)
                 size = __int_as_float(__reduce_max_sync(ALL, __float_as_int(size)));
-                const float off = 4.0f * delta + 0x1.8p-23f * (fabsf(lo) + fabsf(hi)) + 0x1.1p-23f * size;
-                if (!unsure && !(lo - hi > off)) {
+                const auto finite = [](float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; };
+                const float off = 4.0f * delta + 0x1.8p-23f * (finite(lo) + finite(hi)) + 0x1.1p-23f * size;
+                const bool sure = lo - hi > off || (!sums && lo == hi && !(fabsf(lo) < INFINITY));
+                if (!unsure && !sure && !(fabsf(lo) < INFINITY)) {
+                    unsure = true;
+                } else if (!unsure && !sure) {
                     // the groups that may go either way, and of each the experts that may be its best (two)
                     const float v = number(its_score);
                     const unsigned open = __ballot_sync(ALL, its_score != NONE && v >= hi - off && v <= lo + off);
