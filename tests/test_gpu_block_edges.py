@@ -135,3 +135,34 @@ def test_two_threads():
     for t in threads:
         t.join()
     assert not bad
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 300, 1000), (40, 129, 333), (300, 400, 520), (600, 1100, 2048)])
+@pytest.mark.parametrize("power", [30, 70, 110, 118, -30, -70, -110])
+def test_fp8_scales_over_their_whole_range(M, N, K, power):
+    # a power of two more on one side and less on the other leaves every bit of the product; blocks of zeros (the least
+    # scale) beside the largest ones
+    r = rng("fp8 range", M, N, K)
+    a, b = (torch.from_numpy(r.standard_normal((n, K)).astype(np.float32)) for n in (M, N))
+    a[:, K // 3: K // 3 + 64], b[:, : 40] = 0, 0
+    a, b = a.cuda(), b.cuda()
+    want = g13.fp8_matmul(g13.fp8_quantize(a), g13.fp8_quantize(b))
+    qa, qb = g13.fp8_quantize(a * 2.0 ** power), g13.fp8_quantize(b * 2.0 ** -power)
+    assert torch.equal(g13.fp8_dequantize(qa), g13.fp8_dequantize(g13.fp8_quantize(a)) * 2.0 ** power)
+    got = g13.fp8_matmul(qa, qb)
+    assert bool(torch.isfinite(got).all()) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("M", [1, 300])
+def test_fp8_products_at_the_ends_of_the_range(M):
+    # scales of 2^-127 whose codes are kept, and terms that leave FP32
+    N, K = 200, 256
+    r = rng("fp8 ends", M)
+    a = torch.from_numpy(r.integers(-7, 8, (M, K)).astype(np.float32)).cuda()
+    b = torch.from_numpy(r.integers(-7, 8, (N, K)).astype(np.float32)).cuda()
+    want = a.double() @ b.double().T
+    qa, qb = g13.fp8_quantize(a * 2.0 ** -126), g13.fp8_quantize(b * 2.0 ** 100)
+    assert bool((qa.scales <= 5).all()) and torch.equal(g13.fp8_dequantize(qa), a * 2.0 ** -126)
+    assert torch.equal(g13.fp8_matmul(qa, qb).double(), want * 2.0 ** -26)
+    big = g13.fp8_matmul(g13.fp8_quantize(a * 2.0 ** 100), qb)
+    assert not bool(torch.isfinite(big).any())  # (terms of both signs beyond FP32: infinities or NaN)
