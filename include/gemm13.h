@@ -519,8 +519,8 @@ int gemm_w4_run(const gemm_w4_desc_t* desc, const void* X, const void* codes, co
  *
  * Experts come in falling order of c, groups and experts that are equal by the lowest index.
  * The order is that of c as a real number: without a bias the logits themselves are compared,
- * and where c in FP32 leaves two in doubt it is computed in 64 bits (what these cannot tell apart, scores below
- * e^-700 among it, counts as equal).  NaN comes last.  Weights are FP32 throughout, and with normalize relative to the
+ * and where c in FP32 leaves two in doubt it is computed in 64 bits, whose rounding is the limit (scores below
+ * e^-700 count as equal).  NaN comes last.  Weights are FP32 throughout, and with normalize relative to the
  * largest of them, so that scores below FP32's range keep their ratios; a token whose logits hold a NaN or +infinity, or
  * none above -infinity, gets NaN weights with softmax (with sigmoid only a chosen NaN does so), and with normalize
  * one whose chosen scores are all exactly 0.
